@@ -307,6 +307,158 @@ int moe_route_noalloc(moe_ctx* ctx, int32_t layer, const float* x_dev, int32_t B
                       float* topk_w_dev, void* stream);
 
 /* ------------------------------------------------------------------ */
+/* operators: group-limited routing, pair sort, microscaled 4-bit floats  */
+/* ------------------------------------------------------------------ */
+/*
+ * A second expert layer's parts, without a context: a router with groups and
+ * a balance bias, the sort of its choices by expert, matrices in microscaled
+ * 4-bit floating point with their product (dense, or grouped by expert), and
+ * the weighted combine.  Inference only.  The Swiftlet pages have no
+ * counterpart of these calls.
+ *
+ * Conventions of this section.
+ *   - Calls run on the current device, asynchronously on `stream`; nothing is
+ *     allocated per call and every buffer (workspace included) is the
+ *     caller's.  They can be captured into a graph; the first moe_mx_product
+ *     of a process on a device sets up a status word and should come before.
+ *   - Strides (`ld`) are in elements between rows; rows are contiguous.
+ *   - moe_last_error(NULL) gives the message of this host thread's last failure.
+ *   - Zero rows or tokens are legal and do what the formula says for none.
+ */
+#define MOE_F32 0  /* element types */
+#define MOE_BF16 1
+
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+
+typedef struct {
+    int32_t n_experts;  /* E, 1..1024 */
+    int32_t top_k;      /* k, 1..32, at most top_groups * (E / n_groups) */
+    int32_t n_groups;   /* G groups of E / G consecutive experts, 1..32, a divisor of E */
+    int32_t top_groups; /* groups that stay in the choice, 1..G */
+    int32_t group_best; /* a group's score: the sum of its best 1 or 2 experts */
+    int32_t score;      /* MOE_SCORE_* */
+    int32_t renorm;     /* 1 = the k weights are divided by their sum */
+    float scale;        /* factor on the weights */
+} moe_route_config;
+
+/*
+ * Routing to experts from given logits [T x E] (logits_type MOE_F32 or
+ * MOE_BF16, row stride ld >= E), per token:
+ *   s_e = softmax(l)_e or 1 / (1 + exp(-l_e));  c_e = s_e + bias_e
+ *   groups: score = sum of the group's best group_best c (of those it has);
+ *           the top_groups best groups stay (ties: the lower group)
+ *   idx = the top_k largest c of the groups that stay (ties: the lower id), descending
+ *   w_j = scale * s_idx[j], divided by sum_j s_idx[j] with renorm
+ * bias_dev: fp32 [E] or NULL; it takes part in the choice only.  Without a
+ * bias c orders as l does, and l is what is compared (a group's score of two
+ * is still the sum of s).  An expert whose logit is NaN or -inf, or whose bias
+ * is NaN or -inf, is out: never chosen, and in no sum.  A logit of +inf counts
+ * as the largest finite number.  Where fewer than top_k experts are left, the
+ * rest of the row is idx -1, w 0.  Weights with renorm are formed relative to
+ * the largest chosen logit, so they do not vanish together.
+ *   idx_dev int32 [T x top_k], w_dev fp32 [T x top_k]
+ */
+int moe_route(const moe_route_config* cfg, const void* logits_dev, int32_t logits_type, int64_t ld,
+              const float* bias_dev, int64_t T, int32_t* idx_dev, float* w_dev, void* stream);
+
+/*
+ * Stable sort of the T x top_k pairs by expert, pairs of one expert in pair
+ * order (token, then slot).  Ids outside 0..n_experts-1 (-1 from moe_route)
+ * are dropped pairs.  1 <= n_experts <= 1024, T * top_k < 2^31.
+ *   offsets_dev      int32 [n_experts + 1]  first row of each expert; the last entry = pairs kept
+ *   row_of_pair_dev  int32 [T x top_k]      sorted row of each pair, -1 if dropped
+ *   token_of_row_dev int32 [T * top_k]      token of each row, -1 past the pairs kept
+ *   group_of_row_dev int32 [T * top_k]      expert of each row, -1 past the pairs kept
+ * workspace_dev: moe_dispatch_workspace() bytes (0: may be NULL), 16-byte aligned, its contents irrelevant.
+ */
+size_t moe_dispatch_workspace(int64_t T, int32_t top_k, int32_t n_experts);
+int moe_dispatch(const int32_t* idx_dev, int64_t T, int32_t top_k, int32_t n_experts, int32_t* offsets_dev,
+                 int32_t* row_of_pair_dev, int32_t* token_of_row_dev, int32_t* group_of_row_dev, void* workspace_dev,
+                 size_t workspace_bytes, void* stream);
+
+/*
+ * A matrix in microscaled 4-bit floating point: e2m1 codes (sign, values
+ * 0 .5 1 1.5 2 3 4 6) with one scale byte per block of consecutive columns.
+ *   MOE_MX_E8M0  blocks of 32, scale 2^(byte - 127), 255 = NaN
+ *   MOE_MX_E4M3  blocks of 16, scale an unsigned e4m3 number, 127 = NaN
+ * Layout: tiles of 128 rows x 256 columns, each 16384 bytes of codes, then
+ * the scales:
+ *   codes   row r: 128 bytes from r * 128; its 16-byte chunk c (32 columns) stands at chunk c ^ (r & 7);
+ *           the even column of a byte in the low nibble
+ *   scales  256 / (4 block) atoms of 512 bytes; block b (0..3) of row r in an atom at
+ *           (r % 32) * 16 + (r / 32) * 4 + b
+ * Tile (row tile i, column tile j) is number i * ceil(cols / 256) + j.
+ * Columns past cols are zero codes with zero scale bytes.  Rows past the last
+ * of a group are never written and never change a result.
+ *   uniform (ragged = 0): `groups` matrices of `rows` rows; matrix g starts at row tile g * ceil(rows / 128)
+ *   ragged  (ragged = 1): `rows` rows in all, sorted by group, group g's rows offsets[g] .. offsets[g+1]-1
+ *           starting at row tile offsets[g] / 128 + g
+ */
+#define MOE_MX_E8M0 0
+#define MOE_MX_E4M3 1
+
+typedef struct {
+    void* data_dev;  /* moe_mx_bytes() bytes, 128-byte aligned, owned by the caller */
+    int64_t rows;    /* uniform: rows of each group; ragged: rows of all groups together */
+    int32_t cols;
+    int32_t groups;  /* 1..4096 */
+    int32_t format;  /* MOE_MX_* */
+    int32_t ragged;  /* 0 or 1 */
+} moe_mx;
+
+/* Bytes of a matrix's data; 0 for a bad descriptor (data_dev is not looked at). */
+size_t moe_mx_bytes(const moe_mx* m);
+
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SWIGLU 1 /* source rows hold cols gate then cols up values: x = gate / (1 + exp(-gate)) * up, in fp32 */
+
+/*
+ * Quantise rows into m.  Per block, with a = max |x| and t = the group's
+ * tensor scale (MOE_MX_E4M3 only; tensor_scale_dev fp32 [groups], NULL = 1):
+ *   E8M0: scale 2^(floor(log2 a) - 2), at least 2^-127;  code = e2m1(x / scale)
+ *   E4M3: scale s = e4m3(a / (6 t)), at most 448;        code = e2m1(x / (s t)), 0 where s is 0
+ * both roundings to nearest even, e2m1 saturating at 6; quotients, 6 t and
+ * s t are fp32.  A block with a NaN or an infinity gets a NaN scale and zero
+ * codes.
+ *   src_dev   rows of src_type (MOE_F32, MOE_BF16), stride src_ld
+ *   src_row_dev  int32 [rows of m]: the source row of each row, -1 leaves the row unwritten; NULL = the same row
+ *   ragged m: offsets_dev int32 [groups + 1] and group_of_row_dev int32 [rows] (negative: the row is left out);
+ *   both are NULL for a uniform m, whose source rows are the groups' rows one after another
+ */
+int moe_mx_quantise(const moe_mx* m, const void* src_dev, int32_t src_type, int64_t src_ld, int32_t act,
+                    const int32_t* src_row_dev, const int32_t* group_of_row_dev, const int32_t* offsets_dev,
+                    const float* tensor_scale_dev, void* stream);
+
+/* The numbers m stands for, in fp32 (exact), times the group's tensor scale if given (fp32), as dst_type; same row order
+ * and same meaning of offsets_dev and group_of_row_dev as moe_mx_quantise.  Rows left out are not written. */
+int moe_mx_dequantise(const moe_mx* m, const int32_t* group_of_row_dev, const int32_t* offsets_dev,
+                      const float* tensor_scale_dev, void* dst_dev, int32_t dst_type, int64_t dst_ld, void* stream);
+
+/*
+ * y[r, n] = alpha_g * sum_c X[r, c] W_g[n, c], g = the group of row r, on the
+ * block-scaled tensor cores with fp32 accumulation; y is rounded once.
+ *   x  uniform with one group (dense; offsets_dev NULL), or ragged with w->groups groups and offsets_dev
+ *      int32 [groups + 1] (ascending, offsets[groups] <= x->rows; rows past it are left alone)
+ *   w  uniform, w->rows = columns of y; same format and cols as x
+ *   alpha_dev fp32 [groups] (tensor scale of x times tensor scale of w) or NULL = 1
+ *   y_dev MOE_F32 or MOE_BF16 [x->rows x w->rows], stride y_ld >= w->rows
+ * A wait inside the kernel that runs out (a second) ends the call's work early; the next moe_mx_product on that device
+ * returns MOE_ETIMEOUT.
+ */
+int moe_mx_product(const moe_mx* x, const moe_mx* w, const int32_t* offsets_dev, const float* alpha_dev, void* y_dev,
+                   int32_t y_type, int64_t y_ld, void* stream);
+
+/*
+ * y[t] = sum_j w[t, j] * rows[row_of_pair[t, j]] in fp32, j ascending; pairs
+ * with row -1 are skipped (a token without pairs gives zeros).  rows_dev of
+ * rows_type, stride rows_ld; y_dev of y_type [T x cols], stride y_ld.
+ */
+int moe_combine(const void* rows_dev, int32_t rows_type, int64_t rows_ld, const int32_t* row_of_pair_dev,
+                const float* w_dev, int64_t T, int32_t top_k, int32_t cols, void* y_dev, int32_t y_type, int64_t y_ld,
+                void* stream);
+
+/* ------------------------------------------------------------------ */
 /* pool introspection                                                   */
 /* ------------------------------------------------------------------ */
 

@@ -21,6 +21,10 @@ from ._build import LIB as _LIB_PATH, build  # noqa: F401
 
 MOE_OK, MOE_EINVAL, MOE_ENOMEM, MOE_ECUDA, MOE_EPOOL, MOE_ETIMEOUT, MOE_ESTATE, MOE_EIO = 0, -1, -2, -3, -4, -5, -6, -7
 MOE_STORE_DIRECT = 0x1
+MOE_F32, MOE_BF16 = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_MX_E8M0, MOE_MX_E4M3 = 0, 1
+MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 MOE_EVICT_LFU_RECENCY, MOE_EVICT_LRU, MOE_EVICT_LFU_PERSIST, MOE_EVICT_LFU_AGED = 0, 1, 2, 3
 MOE_FAULT_PINNED_ALLOC, MOE_FAULT_MISS_COPY, MOE_FAULT_WAIT_TIMEOUT, MOE_FAULT_DEVICE_WAIT = 0x1, 0x2, 0x4, 0x8
 _ERRNAMES = {MOE_EINVAL: "MOE_EINVAL", MOE_ENOMEM: "MOE_ENOMEM", MOE_ECUDA: "MOE_ECUDA", MOE_EPOOL: "MOE_EPOOL",
@@ -31,6 +35,8 @@ EXPORTS = (
     "moe_blob_bytes", "moe_blob_stride", "moe_pack_expert", "moe_create", "moe_destroy", "moe_load_experts",
     "moe_set_router_bias", "moe_set_router_bias_all", "moe_forward_decode", "moe_forward_decode_stack", "moe_forward_prefill",
     "moe_pool_stats", "moe_pool_reset", "moe_pool_trace", "moe_launch_count", "moe_prefill_profile", "moe_prefill_kernel_ms", "moe_route_noalloc", "moe_last_error", "moe_slotpool_create", "moe_slotpool_destroy",
+    "moe_route", "moe_dispatch_workspace", "moe_dispatch", "moe_mx_bytes", "moe_mx_quantise", "moe_mx_dequantise",
+    "moe_mx_product", "moe_combine",
     "moe_slotpool_request", "moe_store_create", "moe_store_write_layer", "moe_store_info", "moe_store_read",
 )
 
@@ -54,6 +60,16 @@ class moe_pool_stats_t(ctypes.Structure):
     _fields_ = [("hits", ctypes.c_uint64), ("misses", ctypes.c_uint64), ("evictions", ctypes.c_uint64),
                 ("h2d_bytes", ctypes.c_uint64), ("h2d_ms", ctypes.c_double), ("resident", ctypes.c_int32),
                 ("calls", ctypes.c_int32)]
+
+
+class moe_route_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_experts", "top_k", "n_groups", "top_groups", "group_best", "score",
+                                              "renorm")] + [("scale", ctypes.c_float)]
+
+
+class moe_mx(ctypes.Structure):
+    _fields_ = [("data_dev", ctypes.c_void_p), ("rows", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("cols", "groups", "format", "ragged")]
 
 
 _lock = threading.Lock()
@@ -103,9 +119,20 @@ def load_library(path: str | None = None):
         lib.moe_store_write_layer.argtypes = [c.c_char_p, i32, vp, sz]
         lib.moe_store_info.argtypes = [c.c_char_p, c.POINTER(c.c_int32), c.POINTER(c.c_uint64)]
         lib.moe_store_read.argtypes = [c.c_char_p, i32, i32, vp, sz]
+        i64, mx = c.c_int64, c.POINTER(moe_mx)
+        lib.moe_route.argtypes = [c.POINTER(moe_route_config), vp, i32, i64, vp, i64, vp, vp, vp]
+        lib.moe_dispatch_workspace.argtypes = [i64, i32, i32]
+        lib.moe_dispatch_workspace.restype = sz
+        lib.moe_dispatch.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+        lib.moe_mx_bytes.argtypes = [mx]
+        lib.moe_mx_bytes.restype = sz
+        lib.moe_mx_quantise.argtypes = [mx, vp, i32, i64, i32, vp, vp, vp, vp, vp]
+        lib.moe_mx_dequantise.argtypes = [mx, vp, vp, vp, vp, i32, i64, vp]
+        lib.moe_mx_product.argtypes = [mx, mx, vp, vp, vp, i32, i64, vp]
+        lib.moe_combine.argtypes = [vp, i32, i64, vp, vp, i64, i32, i32, vp, i32, i64, vp]
         for name in EXPORTS:
             if name not in ("moe_destroy", "moe_slotpool_destroy", "moe_blob_bytes", "moe_blob_stride",
-                            "moe_last_error"):
+                            "moe_last_error", "moe_dispatch_workspace", "moe_mx_bytes"):
                 getattr(lib, name).restype = c.c_int
         _lib = lib
         return lib
@@ -309,6 +336,159 @@ def make_config(n_layers, hidden, n_experts, top_k, inter, shared_inter, bits=4,
                      ctypes.cast(lb, ctypes.POINTER(ctypes.c_int32)) if lb is not None else None)
     cfg._layer_bits = lb  # keeps the array alive with the struct
     return cfg
+
+
+# --------------------------------------------------------------------------
+# operators without a context: CUDA tensors in, shapes and strides taken from
+# them; outputs are the caller's tensors
+# --------------------------------------------------------------------------
+
+_types: dict = {}
+
+
+def _torch_types() -> dict:
+    if not _types:
+        import torch
+        _types.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, "i32": torch.int32, "u8": torch.uint8})
+    return _types
+
+
+def _flat(t, dtype, n: int, what: str):
+    """Address of a contiguous CUDA tensor of at least n elements of the torch dtype; None stays None."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: expected a contiguous CUDA tensor of at least {n} {dtype} elements, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _matrix(t, what: str):
+    """(address, MOE_* type, rows, cols, row stride) of a 2D CUDA tensor whose rows are contiguous."""
+    kind = (_types or _torch_types()).get(t.dtype)
+    if kind is None or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2D CUDA tensor of float32 or bfloat16, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return t.data_ptr(), kind, rows, cols, ld if rows > 1 else cols
+
+
+def make_route_config(n_experts, top_k, n_groups=1, top_groups=1, group_best=1, score=MOE_SCORE_SOFTMAX, renorm=True,
+                      scale=1.0) -> moe_route_config:
+    return moe_route_config(n_experts, top_k, n_groups, top_groups, group_best, score, int(bool(renorm)), scale)
+
+
+def moe_route(cfg: moe_route_config, logits, bias, idx, w, stream=None) -> None:
+    """logits [T, n_experts] fp32 or bf16 (rows may be strided), bias [n_experts] fp32 or None; fills idx [T, top_k]
+    int32 and w [T, top_k] fp32."""
+    ty = _types or _torch_types()
+    p, kind, T, E, ld = _matrix(logits, "logits")
+    if E != cfg.n_experts:
+        raise ValueError(f"logits have {E} columns, the config {cfg.n_experts} experts")
+    n = T * cfg.top_k
+    _check(load_library().moe_route(cfg, p, kind, ld, _scales(bias, E, "bias"), T, _flat(idx, ty["i32"], n, "idx"),
+                                    _scales(w, n, "w"), _stream(stream)))
+
+
+def moe_dispatch_workspace(T: int, top_k: int, n_experts: int) -> int:
+    return int(load_library().moe_dispatch_workspace(T, top_k, n_experts))
+
+
+def moe_dispatch(idx, n_experts: int, offsets, row_of_pair, token_of_row, group_of_row, workspace=None,
+                 stream=None) -> None:
+    """idx [T, top_k] int32 -> offsets [n_experts + 1], row_of_pair [T, top_k], token_of_row and group_of_row
+    [T * top_k], all int32; workspace: uint8, moe_dispatch_workspace() bytes."""
+    i32 = (_types or _torch_types())["i32"]
+    T, k = idx.shape
+    n = T * k
+    ws, size = (None, 0) if workspace is None else (_flat(workspace, _types["u8"], 0, "workspace"), workspace.numel())
+    _check(load_library().moe_dispatch(_flat(idx, i32, n, "idx"), T, k, n_experts,
+                                       _flat(offsets, i32, n_experts + 1, "offsets"),
+                                       _flat(row_of_pair, i32, n, "row_of_pair"),
+                                       _flat(token_of_row, i32, n, "token_of_row"),
+                                       _flat(group_of_row, i32, n, "group_of_row"), ws, size, _stream(stream)))
+
+
+def moe_mx_bytes(m: moe_mx) -> int:
+    return int(load_library().moe_mx_bytes(m))
+
+
+def make_mx(fmt: int, rows: int, cols: int, groups: int = 1, ragged: bool = False, data=None) -> moe_mx:
+    """Descriptor of a microscaled 4-bit matrix (see moe_mx in moe.h) over `data`, a CUDA uint8 tensor of at least
+    moe_mx_bytes() bytes (kept alive by the descriptor; allocated on the current device if None)."""
+    m = moe_mx(None, rows, cols, groups, fmt, int(bool(ragged)))
+    need = moe_mx_bytes(m)
+    if need == 0 and rows > 0:
+        raise ValueError(f"bad matrix shape: format {fmt}, {groups} groups, {rows} rows, {cols} columns")
+    u8 = _torch_types()["u8"]
+    if data is None:
+        import torch
+        data = torch.empty(max(need, 1), dtype=u8, device="cuda")
+    m.data_dev = _flat(data, u8, need, "data")
+    m._data = data
+    return m
+
+
+def moe_mx_quantise(m: moe_mx, src, act: int = MOE_ACT_NONE, src_row=None, group_of_row=None, offsets=None,
+                    tensor_scale=None, stream=None) -> None:
+    """Rows of src (fp32 or bf16, [source rows, cols] or [.., 2 cols] for MOE_ACT_SWIGLU) into m."""
+    ty = _types or _torch_types()
+    p, kind, n, cols, ld = _matrix(src, "src")
+    if cols != (2 * m.cols if act == MOE_ACT_SWIGLU else m.cols):
+        raise ValueError(f"src has {cols} columns, the matrix {m.cols} (activation {act})")
+    rows = m.rows if m.ragged else m.rows * m.groups
+    if src_row is None and n < rows:
+        raise ValueError(f"src has {n} rows, the matrix {rows}")
+    i32 = ty["i32"]
+    _check(load_library().moe_mx_quantise(
+        m, p, kind, ld, act, _flat(src_row, i32, rows, "src_row"), _flat(group_of_row, i32, rows, "group_of_row"),
+        _flat(offsets, i32, m.groups + 1, "offsets"), _scales(tensor_scale, m.groups, "tensor_scale"), _stream(stream)))
+
+
+def _scales(t, n: int, what: str):
+    if t is None:
+        return None
+    if _types.get(t.dtype) != MOE_F32:
+        raise ValueError(f"{what}: expected float32, got {t.dtype}")
+    return _flat(t, t.dtype, n, what)
+
+
+def moe_mx_dequantise(m: moe_mx, dst, group_of_row=None, offsets=None, tensor_scale=None, stream=None) -> None:
+    """The numbers of m into dst [rows, cols], fp32 or bf16."""
+    i32 = (_types or _torch_types())["i32"]
+    p, kind, n, cols, ld = _matrix(dst, "dst")
+    rows = m.rows if m.ragged else m.rows * m.groups
+    if cols != m.cols or n < rows:
+        raise ValueError(f"dst is {n} x {cols}, the matrix {rows} x {m.cols}")
+    _check(load_library().moe_mx_dequantise(m, _flat(group_of_row, i32, rows, "group_of_row"),
+                                            _flat(offsets, i32, m.groups + 1, "offsets"),
+                                            _scales(tensor_scale, m.groups, "tensor_scale"), p, kind, ld,
+                                            _stream(stream)))
+
+
+def moe_mx_product(x: moe_mx, w: moe_mx, y, offsets=None, alpha=None, stream=None) -> None:
+    """y [x.rows, w.rows] (fp32 or bf16) = alpha[group] * X W[group]^T."""
+    i32 = (_types or _torch_types())["i32"]
+    p, kind, n, cols, ld = _matrix(y, "y")
+    if n < x.rows or cols != w.rows:
+        raise ValueError(f"y is {n} x {cols}, the product {x.rows} x {w.rows}")
+    _check(load_library().moe_mx_product(x, w, _flat(offsets, i32, x.groups + 1, "offsets"),
+                                         _scales(alpha, w.groups, "alpha"), p, kind, ld, _stream(stream)))
+
+
+def moe_combine(rows, row_of_pair, w, y, stream=None) -> None:
+    """y [T, cols] = sum_j w[T, k] * rows[row_of_pair[T, k]]; rows and y fp32 or bf16."""
+    i32 = (_types or _torch_types())["i32"]
+    p, kind, _, cols, ld = _matrix(rows, "rows")
+    py, ykind, n, ycols, yld = _matrix(y, "y")
+    T, k = row_of_pair.shape
+    if ycols != cols or n != T:
+        raise ValueError(f"y is {n} x {ycols}, expected {T} x {cols}")
+    _check(load_library().moe_combine(p, kind, ld, _flat(row_of_pair, i32, T * k, "row_of_pair"),
+                                      _scales(w, T * k, "w"), T, k, cols, py, ykind, yld, _stream(stream)))
 
 
 # --------------------------------------------------------------------------

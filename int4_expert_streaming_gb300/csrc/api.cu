@@ -170,6 +170,20 @@ int fail(moe_ctx* c, int code, const char* fmt, ...) {
     return code;
 }
 
+}  // namespace
+
+int moe::fail_global(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_create_error = buf;
+    return code;
+}
+
+namespace {
+
 #define CUDA_TRY(ctx, expr)                                                                          \
     do {                                                                                             \
         cudaError_t e_ = (expr);                                                                     \

@@ -29,6 +29,9 @@ inline cudaError_t smem_limit(const void* kernel, int bytes) {
     return e;
 }
 
+// Records the message that moe_last_error(NULL) gives on this host thread; returns code.
+int fail_global(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+
 // Byte offsets of the six sections of one blob (layout v1, see moe.h).
 struct BlobLayout {
     uint64_t gate_q, up_q, down_q, gate_sb, up_sb, down_sb, bytes;

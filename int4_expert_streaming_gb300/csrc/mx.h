@@ -1,0 +1,66 @@
+// mx.h -- the context-free operators (routing with groups, pair sort,
+// microscaled 4-bit matrices, combine): launchers and the tile layout shared
+// by their kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "moe_internal.h"
+
+namespace moe {
+
+constexpr int kMxTileRows = 128, kMxTileCols = 256;
+constexpr int kMxCodeBytes = 16384;  // codes of one tile
+constexpr int kMxAtomBytes = 512;    // scales of 128 rows x 4 blocks
+
+__host__ __device__ inline int mx_block(int format) { return format == MOE_MX_E8M0 ? 32 : 16; }
+__host__ __device__ inline int mx_tile_bytes(int format) {
+    return kMxCodeBytes + kMxAtomBytes * (kMxTileCols / 4 / mx_block(format));
+}
+__host__ __device__ inline int64_t mx_col_tiles(int cols) { return (cols + kMxTileCols - 1) / kMxTileCols; }
+
+// Where the rows of a matrix stand: row tile and row within it.  Ragged
+// groups start at row tile offsets[g] / 128 + g: consecutive groups then never
+// overlap, because floor((o + n) / 128) + 1 - floor(o / 128) >= ceil(n / 128).
+struct MxRows {
+    const int32_t* group_of_row;  // ragged only
+    const int32_t* offsets;
+    int64_t rows;       // rows to walk
+    int64_t per_group;  // uniform: rows per group
+    __device__ __forceinline__ bool place(int64_t r, int& g, int64_t& tile, int& in) const {
+        int64_t q;
+        if (group_of_row) {
+            g = group_of_row[r];
+            if (g < 0) return false;
+            const int64_t o = offsets[g];
+            q = r - o;
+            tile = o / kMxTileRows + g + q / kMxTileRows;
+        } else {
+            g = (int)(r / per_group);
+            q = r - g * per_group;
+            tile = g * ((per_group + kMxTileRows - 1) / kMxTileRows) + q / kMxTileRows;
+        }
+        in = (int)(q % kMxTileRows);
+        return true;
+    }
+};
+
+// mx_route.cu
+cudaError_t launch_route(const moe_route_config& c, const void* logits, int type, int64_t ld, const float* bias,
+                         int64_t T, int32_t* idx, float* w, cudaStream_t st);
+size_t dispatch_workspace(int64_t pairs, int n_experts);
+cudaError_t launch_dispatch(const int32_t* idx, int64_t pairs, int top_k, int n_experts, int32_t* offsets,
+                            int32_t* row_of_pair, int32_t* token_of_row, int32_t* group_of_row, void* ws,
+                            cudaStream_t st);
+cudaError_t launch_combine(const void* rows, int rows_type, int64_t rows_ld, const int32_t* row_of_pair, const float* w,
+                           int64_t T, int top_k, int cols, void* y, int y_type, int64_t y_ld, cudaStream_t st);
+// mx_quantise.cu
+cudaError_t launch_mx_quantise(const moe_mx& m, const MxRows& rows, const void* src, int type, int64_t ld, int act,
+                               const int32_t* src_row, const float* tscale, cudaStream_t st);
+cudaError_t launch_mx_dequantise(const moe_mx& m, const MxRows& rows, const float* tscale, void* dst, int type,
+                                 int64_t ld, cudaStream_t st);
+// mx_product.cu
+cudaError_t launch_mx_product(const moe_mx& x, const moe_mx& w, const int32_t* offsets, const float* alpha, void* y,
+                              int y_type, int64_t y_ld, cudaStream_t st);
+
+}  // namespace moe
