@@ -402,7 +402,7 @@ typedef struct {
     void* data_dev;  /* moe_mx_bytes() bytes, 128-byte aligned, owned by the caller */
     int64_t rows;    /* uniform: rows of each group; ragged: rows of all groups together */
     int32_t cols;
-    int32_t groups;  /* 1..4096 */
+    int32_t groups;  /* 1..1024 */
     int32_t format;  /* MOE_MX_* */
     int32_t ragged;  /* 0 or 1 */
 } moe_mx;

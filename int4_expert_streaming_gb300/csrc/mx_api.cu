@@ -29,7 +29,7 @@ int launched(cudaError_t e, const char* what) {
 
 // the descriptor's shape, not its address
 bool mx_ok(const moe_mx* m) {
-    return m && m->rows >= 0 && m->cols >= 1 && m->groups >= 1 && m->groups <= 4096 &&
+    return m && m->rows >= 0 && m->cols >= 1 && m->groups >= 1 && m->groups <= 1024 &&
            (m->format == MOE_MX_E8M0 || m->format == MOE_MX_E4M3) && (m->ragged == 0 || m->ragged == 1) &&
            m->rows <= (INT64_C(1) << 31) - 1 && m->cols <= 1 << 24 &&
            (m->ragged ? m->rows : m->rows * m->groups) <= (INT64_C(1) << 40);
@@ -181,8 +181,13 @@ extern "C" int moe_mx_product(const moe_mx* x, const moe_mx* w, const int32_t* o
         if (y_ld < w->rows) return fail_global(MOE_EINVAL, "moe_mx_product: y_ld=%lld below w's rows", (long long)y_ld);
         if (x->rows == 0 || w->rows == 0) return MOE_OK;
         if (!y) return fail_global(MOE_EINVAL, "moe_mx_product: y is required");
-        return launched(launch_mx_product(*x, *w, offsets, alpha, y, type, y_ld, static_cast<cudaStream_t>(stream)),
-                        "moe_mx_product");
+        bool timed_out = false;
+        rc = launched(
+            launch_mx_product(*x, *w, offsets, alpha, y, type, y_ld, static_cast<cudaStream_t>(stream), &timed_out),
+            "moe_mx_product");
+        if (rc == MOE_OK && timed_out)
+            return fail_global(MOE_ETIMEOUT, "moe_mx_product: a wait inside an earlier call's kernel ran out");
+        return rc;
     });
 }
 

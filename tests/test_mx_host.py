@@ -30,8 +30,8 @@ def test_matrix_bytes(lib, fmt, tile):
     assert moe.moe_mx_bytes(m(None, 129, 257, 3, fmt, 0)) == 3 * 2 * 2 * tile
     assert moe.moe_mx_bytes(m(None, 129, 257, 3, fmt, 1)) == (1 + 3) * 2 * tile
     assert moe.moe_mx_bytes(m(None, 0, 256, 4, fmt, 0)) == 0
-    assert moe.moe_mx_bytes(m(None, 1 << 20, 8192, 4096, fmt, 0)) == 4096 * 8192 * 32 * tile  # past 32 bits
-    for bad in (m(None, -1, 1, 1, fmt, 0), m(None, 1, 0, 1, fmt, 0), m(None, 1, 1, 0, fmt, 0), m(None, 1, 1, 4097, fmt, 0),
+    assert moe.moe_mx_bytes(m(None, 1 << 20, 8192, 1024, fmt, 0)) == 1024 * 8192 * 32 * tile  # past 32 bits
+    for bad in (m(None, -1, 1, 1, fmt, 0), m(None, 1, 0, 1, fmt, 0), m(None, 1, 1, 0, fmt, 0), m(None, 1, 1, 1025, fmt, 0),
                 m(None, 1, 1, 1, 2, 0), m(None, 1, 1, 1, fmt, 2)):
         assert moe.moe_mx_bytes(bad) == 0
     assert lib.moe_mx_bytes(None) == 0
