@@ -30,17 +30,21 @@ struct MxRows {
     __device__ __forceinline__ bool place(int64_t r, int& g, int64_t& tile, int& in) const {
         int64_t q;
         if (group_of_row) {
-            g = group_of_row[r];
+            g = __ldg(group_of_row + r);
             if (g < 0) return false;
-            const int64_t o = offsets[g];
+            const int o = __ldg(offsets + g);
             q = r - o;
-            tile = o / kMxTileRows + g + q / kMxTileRows;
+            tile = (o >> 7) + g + (q >> 7);
+        } else if (rows == per_group) {
+            g = 0;
+            q = r;
+            tile = r >> 7;
         } else {
             g = (int)(r / per_group);
             q = r - g * per_group;
-            tile = g * ((per_group + kMxTileRows - 1) / kMxTileRows) + q / kMxTileRows;
+            tile = g * ((per_group + kMxTileRows - 1) >> 7) + (q >> 7);
         }
-        in = (int)(q % kMxTileRows);
+        in = (int)(q & (kMxTileRows - 1));
         return true;
     }
 };

@@ -78,9 +78,18 @@ struct QuantArgs {
     const float* tscale;
     void* dst;
     int64_t ld;
-    int cols, chunks;  // chunks: 16-column chunks of a padded row, a multiple of 16
+    int cols, col_tiles;
     bool wide;
 };
+
+constexpr int kRows = kThreads / 16;  // rows of a block: 16 threads share a row's 256 columns
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // byte offset of a chunk's 8 code bytes in its tile, and of its scale bytes' word
 __device__ __forceinline__ uint32_t code_at(int in, int c16) {
@@ -91,40 +100,41 @@ __device__ __forceinline__ uint32_t scale_at(int in, int atom) {
     return (uint32_t)(kMxCodeBytes + atom * kMxAtomBytes + (in & 31) * 16 + (in >> 5) * 4);
 }
 
-// A thread takes 16 columns of a row, 16 threads one row of a tile: 128 bytes
-// of codes, and the scale bytes of four blocks joined into one word.
+// A block takes 16 rows of one column tile, a thread 16 columns of a row, so
+// 16 threads write one row's 128 bytes of codes, and the scale bytes of four
+// blocks go out as one word.  Row maps and tile addresses need no division.
+//
+// Both formats divide by a scale before the rounding to e2m1.  A power of two
+// is an exact multiply.  The e4m3 scale takes a reciprocal and one residual
+// step: r = x / d to a few units of the last place, then
+// r + (x - r d) / d, the remainder exact in one fma.  Where x / d is itself a
+// short number, as a tie between two codes is, the result is exactly that.
 template <typename T, int FMT, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
-    const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t r = item / a.chunks;
-    const int ck = (int)(item % a.chunks);
+    const int c16 = threadIdx.x & 15;
+    const int64_t r = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 4);
     int g = 0, in = 0;
     int64_t tile = 0;
-    bool live = r < a.rows.rows && a.rows.place(r, g, tile, in);
-    int64_t from = live ? (a.src_row ? a.src_row[r] : r) : -1;
-    live = from >= 0;
+    bool live = r < a.rows.rows;
+    int64_t from = live ? (a.src_row ? __ldg(a.src_row + r) : r) : -1;
+    live = live && a.rows.place(r, g, tile, in) && from >= 0;
     float v[16];
-    const int col = ck * kChunk, n = live ? a.cols - col : 0;
+    const int col = blockIdx.y * kMxTileCols + c16 * kChunk, n = live ? a.cols - col : 0;
     const T* p = static_cast<const T*>(a.src) + (live ? from * a.ld + col : 0);
     load16(p, n, a.wide, v);
     if (SWIGLU) {
         float u[16];
         load16(p + a.cols, n, a.wide, u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * u[i];
+        for (int i = 0; i < 16; ++i) v[i] = silu_mul(v[i], u[i]);
     }
     float amax = 0.0f;
-    bool finite = true;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        amax = fmaxf(amax, fabsf(v[i]));
-        finite = finite && fabsf(v[i]) <= 3.402823466e38f;
-    }
+    for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(v[i]));
+    if (FMT == MOE_MX_E8M0) amax = max_nan(amax, __shfl_xor_sync(kAll, amax, 1));
+    const bool finite = amax <= 3.402823466e38f;
     uint32_t byte;
-    uint32_t out[2];
     if (FMT == MOE_MX_E8M0) {
-        amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
-        finite = finite & (__shfl_xor_sync(kAll, (int)finite, 1) != 0);
         // floor(log2 amax) is the exponent field less 127 (subnormals end at the lower bound either way)
         int e = (int)(__float_as_uint(amax) >> 23) - 127 - 2;
         if (e < -127) e = -127;
@@ -133,14 +143,24 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] *= inv;
     } else {
-        const float t = a.tscale && live ? a.tscale[g] : 1.0f;
+        const float t = a.tscale && live ? __ldg(a.tscale + g) : 1.0f;
         const __nv_fp8_storage_t s =
             __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f * t), __NV_SATFINITE, __NV_E4M3);
         byte = s;
         const float d = __half2float(__half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3))) * t;
+        const float inv = d > 0.0f ? __frcp_rn(d) : 0.0f;
+        if (inv < 1e30f) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = d > 0.0f ? __fdiv_rn(v[i], d) : 0.0f;
+            for (int i = 0; i < 16; ++i) {
+                const float q = v[i] * inv;
+                v[i] = fmaf(fmaf(-q, d, v[i]), inv, q);
+            }
+        } else {  // scales so small that the remainder could be subnormal
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], d);
+        }
     }
+    uint32_t out[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t w = 0;
@@ -161,23 +181,21 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
     word |= __shfl_down_sync(kAll, word, kStep) << 8;
     word |= __shfl_down_sync(kAll, word, 2 * kStep) << 16;
     if (!live) return;
-    uint8_t* base = a.data + (tile * (a.chunks / 16) + (ck >> 4)) * (int64_t)mx_tile_bytes(FMT);
-    const int c16 = ck & 15;
+    uint8_t* base = a.data + (tile * a.col_tiles + blockIdx.y) * (int64_t)mx_tile_bytes(FMT);
     *reinterpret_cast<uint2*>(base + code_at(in, c16)) = make_uint2(out[0], out[1]);
     if (c16 % (4 * kStep) == 0) *reinterpret_cast<uint32_t*>(base + scale_at(in, c16 / (4 * kStep))) = word;
 }
 
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads) dequantise_kernel(const QuantArgs a) {
-    const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t r = item / a.chunks;
-    const int ck = (int)(item % a.chunks);
+    const int c16 = threadIdx.x & 15;
+    const int64_t r = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 4);
     int g, in;
     int64_t tile;
-    const int n = a.cols - ck * kChunk;
+    const int col = blockIdx.y * kMxTileCols + c16 * kChunk, n = a.cols - col;
     if (r >= a.rows.rows || n <= 0 || !a.rows.place(r, g, tile, in)) return;
-    const uint8_t* base = a.data + (tile * (a.chunks / 16) + (ck >> 4)) * (int64_t)mx_tile_bytes(FMT);
-    const int c16 = ck & 15, b = FMT == MOE_MX_E8M0 ? c16 >> 1 : c16;
+    const uint8_t* base = a.data + (tile * a.col_tiles + blockIdx.y) * (int64_t)mx_tile_bytes(FMT);
+    const int b = FMT == MOE_MX_E8M0 ? c16 >> 1 : c16;
     const uint2 q = __ldg(reinterpret_cast<const uint2*>(base + code_at(in, c16)));
     const uint32_t byte = __ldg(base + scale_at(in, b >> 2) + (b & 3));
     float s;
@@ -185,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) dequantise_kernel(const QuantArgs a)
         s = byte == 255 ? __uint_as_float(0x7fffffffu) : byte ? __uint_as_float(byte << 23) : __uint_as_float(0x400000u);
     else
         s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
-    const float t = a.tscale ? a.tscale[g] : 1.0f;
+    const float t = a.tscale ? __ldg(a.tscale + g) : 1.0f;
     float v[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -194,10 +212,10 @@ __global__ void __launch_bounds__(kThreads) dequantise_kernel(const QuantArgs a)
         v[2 * i] = __low2float(h) * s * t;
         v[2 * i + 1] = __high2float(h) * s * t;
     }
-    store16(static_cast<T*>(a.dst) + r * a.ld + ck * kChunk, n, a.wide, v);
+    store16(static_cast<T*>(a.dst) + r * a.ld + col, n, a.wide, v);
 }
 
-unsigned grid_of(const QuantArgs& a) { return (unsigned)((a.rows.rows * a.chunks + kThreads - 1) / kThreads); }
+dim3 grid_of(const QuantArgs& a) { return dim3((unsigned)((a.rows.rows + kRows - 1) / kRows), (unsigned)a.col_tiles); }
 
 template <typename T, int FMT>
 void quantise_act(const QuantArgs& a, int act, cudaStream_t st) {
@@ -225,9 +243,9 @@ cudaError_t launch_mx_quantise(const moe_mx& m, const MxRows& rows, const void* 
     a.tscale = tscale;
     a.ld = ld;
     a.cols = m.cols;
-    a.chunks = (int)mx_col_tiles(m.cols) * 16;
+    a.col_tiles = (int)mx_col_tiles(m.cols);
     a.wide = wide_ok(src, ld, act == MOE_ACT_SWIGLU ? m.cols : 0, type);
-    if ((rows.rows * a.chunks + kThreads - 1) / kThreads > INT32_MAX) return cudaErrorInvalidValue;
+    if ((rows.rows + kRows - 1) / kRows > INT32_MAX || a.col_tiles > 65535) return cudaErrorInvalidValue;
     if (type == MOE_F32) {
         if (m.format == MOE_MX_E8M0) quantise_act<float, MOE_MX_E8M0>(a, act, st);
         else quantise_act<float, MOE_MX_E4M3>(a, act, st);
@@ -247,9 +265,9 @@ cudaError_t launch_mx_dequantise(const moe_mx& m, const MxRows& rows, const floa
     a.dst = dst;
     a.ld = ld;
     a.cols = m.cols;
-    a.chunks = (int)mx_col_tiles(m.cols) * 16;
+    a.col_tiles = (int)mx_col_tiles(m.cols);
     a.wide = wide_ok(dst, ld, 0, type);
-    if ((rows.rows * a.chunks + kThreads - 1) / kThreads > INT32_MAX) return cudaErrorInvalidValue;
+    if ((rows.rows + kRows - 1) / kRows > INT32_MAX || a.col_tiles > 65535) return cudaErrorInvalidValue;
     if (type == MOE_F32) {
         if (m.format == MOE_MX_E8M0) dequantise_kernel<float, MOE_MX_E8M0><<<grid_of(a), kThreads, 0, st>>>(a);
         else dequantise_kernel<float, MOE_MX_E4M3><<<grid_of(a), kThreads, 0, st>>>(a);
