@@ -31,7 +31,7 @@ int launched(cudaError_t e, const char* what) {
 bool mx_ok(const moe_mx* m) {
     return m && m->rows >= 0 && m->cols >= 1 && m->groups >= 1 && m->groups <= 1024 &&
            (m->format == MOE_MX_E8M0 || m->format == MOE_MX_E4M3) && (m->ragged == 0 || m->ragged == 1) &&
-           m->rows <= (INT64_C(1) << 31) - 1 && m->cols <= 1 << 24 &&
+           m->rows <= (INT64_C(1) << 31) - 1 && m->cols <= 1 << 23 &&
            (m->ragged ? m->rows : m->rows * m->groups) <= (INT64_C(1) << 40);
 }
 
@@ -195,7 +195,7 @@ extern "C" int moe_combine(const void* rows, int32_t rows_type, int64_t rows_ld,
                            const float* w, int64_t T, int32_t top_k, int32_t cols, void* y, int32_t y_type,
                            int64_t y_ld, void* stream) {
     return guarded([&]() -> int {
-        if (T < 0 || T > INT32_MAX || top_k < 1 || cols < 1 || T * top_k > INT32_MAX)
+        if (T < 0 || T > INT32_MAX || top_k < 1 || cols < 1 || cols > 1 << 22 || T * top_k > INT32_MAX)
             return fail_global(MOE_EINVAL, "moe_combine: T=%lld, top_k=%d or cols=%d out of range", (long long)T, top_k,
                                cols);
         if (!type_ok(rows_type) || !type_ok(y_type)) return fail_global(MOE_EINVAL, "moe_combine: unknown element type");

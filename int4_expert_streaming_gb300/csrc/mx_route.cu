@@ -1,8 +1,12 @@
 // mx_route.cu -- routing with groups and a balance bias, the stable sort of
 // the chosen pairs by expert, and the weighted combine of the experts' rows.
+#include <cooperative_groups.h>
+
 #include <cfloat>
 
 #include "mx.h"
+
+namespace cg = cooperative_groups;
 
 namespace moe {
 namespace {
@@ -41,67 +45,84 @@ struct RouteArgs {
 
 constexpr int kRouteWarps = 4;
 
-__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+// 1 / (1 + exp(-l)), within a few units of the last place
+__device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+
+// per-warp scratch: the scores on their way to the group sums, then the
+// candidates of the choice
+template <int NV>
+union RouteScratch {
+    float score[NV * 33];
+    struct {
+        uint32_t key[32];
+        int e[32];
+        float l[32];
+        int order[32];
+    } cand;
+};
 
 // One warp per token; lane l holds the experts l, l + 32, ...: the row is read
-// once, coalesced, and every statistic is a warp reduction on registers.  The
-// top-k takes k rounds of (largest key, then lowest id) over the warp.
+// once, coalesced, and every statistic is a warp reduction on registers.
+//
+// The choice: no expert below t, the top_k-th largest of the 32 lanes' maxima,
+// can be chosen, because top_k lanes hold one at or above t.  What is left
+// (top_k to about twice as many) goes to shared memory, one candidate per
+// lane, and each counts the candidates before it.  A row with more than 32
+// left (equal logits) takes top_k rounds of (largest key, then lowest id)
+// instead; rounds for every row, each rescanning the winner's NV keys, took
+// 840 cycles a round at 512 experts.
 template <typename T, int NV>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a) {
-    __shared__ float buf_s[kRouteWarps][NV * 33];
+    __shared__ RouteScratch<NV> scratch[kRouteWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     if (t >= a.T) return;
+    RouteScratch<NV>& sh = scratch[warp];
     const moe_route_config& c = a.c;
     const int E = c.n_experts;
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
 
     float l[NV], ch[NV];  // logits (-inf: out) and what the choice compares
-    float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = i * 32 + lane;
-        float v = e < E ? to_f32(row[e]) : -INFINITY;
-        if (!(v > -INFINITY)) v = -INFINITY;
-        if (a.bias && e < E) {
-            const float b = a.bias[e];
-            if (!(b > -INFINITY)) v = -INFINITY;
-        }
-        l[i] = fminf(v, FLT_MAX);
+        l[i] = e < E ? to_f32(row[e]) : -INFINITY;
+        ch[i] = a.bias && e < E ? a.bias[e] : 0.0f;
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        l[i] = l[i] > -INFINITY && ch[i] > -INFINITY ? fminf(l[i], FLT_MAX) : -INFINITY;
         m = fmaxf(m, l[i]);
     }
     m = warp_max(m);
     const bool softmax = c.score == MOE_SCORE_SOFTMAX;
     const bool sums = c.top_groups < c.n_groups && c.group_best == 2;
-    float total = 1.0f;
+    float inv_total = 1.0f;
     if (softmax && (a.bias || !c.renorm)) {
-        total = 0.0f;
+        float total = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) total += l[i] > -INFINITY ? expf(l[i] - m) : 0.0f;
-        total = warp_sum(total);
+        inv_total = 1.0f / warp_sum(total);
     }
-    auto score = [&](float v) { return softmax ? expf(v - m) / total : sigmoid(v); };
+    auto score = [&](float v) { return softmax ? expf(v - m) * inv_total : sigmoid(v); };
     // a score relative to exp(ref), which only scales all of them: sigmoid(v) exp(-ref) for ref <= 0 is
     // exp(v - ref) / (1 + exp(v)), and does not vanish where every logit is far below zero
     auto relative = [&](float v, float ref) {
         return softmax ? expf(v - ref) : v > 0.0f ? sigmoid(v) : expf(v - ref) / (1.0f + expf(v));
     };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = i * 32 + lane;
-        ch[i] = l[i];
-        if (a.bias && l[i] > -INFINITY) ch[i] = score(l[i]) + a.bias[e];
-    }
+    for (int i = 0; i < NV; ++i)
+        ch[i] = l[i] > -INFINITY && a.bias ? score(l[i]) + ch[i] : l[i];
 
     if (c.top_groups < c.n_groups) {
         // each group's score by `per` lanes over shared memory, then its rank among the groups
         const int S = E / c.n_groups, G = c.n_groups;
-        float* buf = buf_s[warp];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float v = ch[i];
             if (sums && !a.bias && v > -INFINITY) v = relative(v, softmax ? m : fminf(m, 0.0f));
-            buf[i * 33 + lane] = v;
+            sh.score[i * 33 + lane] = v;
         }
         __syncwarp();
         int per = 1;
@@ -109,9 +130,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         const int g = lane / per, sub = lane % per;
         float b1 = -INFINITY, b2 = -INFINITY;
         if (g < G)
+#pragma unroll 4
             for (int j = sub; j < S; j += per) {
                 const int e = g * S + j;
-                const float v = buf[e + (e >> 5)];
+                const float v = sh.score[e + (e >> 5)];
                 b2 = fmaxf(b2, fminf(b1, v));
                 b1 = fmaxf(b1, v);
             }
@@ -122,6 +144,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         }
         const float gs = b1 + (c.group_best == 2 && b2 > -INFINITY ? b2 : 0.0f);
         int rank = 0;
+#pragma unroll 4
         for (int q = 0; q < G; ++q) {
             const float os = __shfl_sync(kAll, gs, q * per);
             rank += os > gs || (os == gs && q < g);
@@ -133,38 +156,85 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
             const int ge = (int)(((uint32_t)e * a.inv_group) >> 20);
             if (e < E && !((kept_lane >> (ge * per)) & 1)) ch[i] = -INFINITY;
         }
-    }
-
-    // top-k: lane j keeps the j-th choice
-    const uint32_t none = ordered(-INFINITY);
-    uint32_t best = none;
-    int at = INT_MAX;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const uint32_t k = ordered(ch[i]);
-        if (k > best) best = k, at = i * 32 + lane;
-    }
-    int mine = -1;
-    for (int j = 0; j < c.top_k; ++j) {
-        const uint32_t top = __reduce_max_sync(kAll, best);
-        if (top == none) break;
-        const int win = __reduce_min_sync(kAll, best == top ? at : INT_MAX);
-        if (lane == j) mine = win;
-        if ((win & 31) == lane) {
-            best = none;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (i == win >> 5) ch[i] = -INFINITY;
-                const uint32_t k = ordered(ch[i]);
-                if (k > best) best = k, at = i * 32 + lane;
-            }
-        }
         __syncwarp();
     }
 
+    const uint32_t none = ordered(-INFINITY);
+    uint32_t key[NV], best = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        key[i] = ordered(ch[i]);
+        best = max(best, key[i]);
+    }
+    int before = 0;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+        const uint32_t o = __shfl_sync(kAll, best, q);
+        before += o > best || (o == best && q < lane);
+    }
+    // at least none + 1: what is out is no candidate
+    const uint32_t floor_key =
+        max(__shfl_sync(kAll, best, __ffs(__ballot_sync(kAll, before == c.top_k - 1)) - 1), none + 1);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) n += key[i] >= floor_key;
+    int at = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(kAll, at, o);
+        if (lane >= o) at += v;
+    }
+    const int local = n;
+    n = __shfl_sync(kAll, at, 31);
+    int mine = -1;     // lane j: the j-th choice
+    float v = -INFINITY;  // and its logit
+    if (n <= 32) {
+        at -= local;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (key[i] >= floor_key) {
+                sh.cand.key[at] = key[i];
+                sh.cand.e[at] = i * 32 + lane;
+                sh.cand.l[at] = l[i];
+                ++at;
+            }
+        __syncwarp();
+        const uint32_t k0 = lane < n ? sh.cand.key[lane] : 0;
+        const int e0 = lane < n ? sh.cand.e[lane] : INT_MAX;
+        int rank = 0;
+#pragma unroll 4
+        for (int q = 0; q < n; ++q) {
+            const uint32_t kq = sh.cand.key[q];
+            rank += kq > k0 || (kq == k0 && sh.cand.e[q] < e0);
+        }
+        if (lane < n) sh.cand.order[rank] = lane;
+        __syncwarp();
+        if (lane < n && lane < c.top_k) {
+            const int q = sh.cand.order[lane];
+            mine = sh.cand.e[q];
+            v = sh.cand.l[q];
+        }
+    } else {
+        for (int j = 0; j < c.top_k; ++j) {
+            const uint32_t top = __reduce_max_sync(kAll, best);
+            if (top == none) break;
+            int first = INT_MAX;
+#pragma unroll
+            for (int i = NV - 1; i >= 0; --i)
+                if (key[i] == top) first = i * 32 + lane;
+            const int win = __reduce_min_sync(kAll, first);
+            if (lane == j) mine = win;
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i * 32 + lane == win) key[i] = none;
+                best = max(best, key[i]);
+            }
+        }
+        if (mine >= 0) v = fminf(to_f32(row[mine]), FLT_MAX);
+    }
+
     // weights, relative to the largest chosen logit where they are renormalised
-    float v = -INFINITY;
-    if (mine >= 0) v = fminf(to_f32(row[mine]), FLT_MAX);
     float wt = 0.0f;
     if (c.renorm) {
         const float ref = softmax ? warp_max(v) : fminf(warp_max(v), 0.0f);
@@ -195,36 +265,72 @@ cudaError_t route_typed(const RouteArgs& a, cudaStream_t st) {
 // dispatch
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kKeep = 8;  // rounds whose ranks stay in registers between the two passes
 
-// One CTA.  Warp w owns a run of consecutive pairs; 32 pairs at a time it
-// finds equal experts by a warp match, so that a pair's rank among its
-// expert's pairs is (counts of earlier warps) + (its warp's earlier rounds) +
-// (lower lanes): stable, and free of atomics.
+// CTAs of one cluster take consecutive runs of the pairs, and each warp a run
+// of its CTA's.  32 pairs at a time a warp finds equal experts by a match, so
+// that a pair's rank among its expert's pairs is (earlier CTAs) + (earlier
+// warps) + (earlier rounds) + (lower lanes): stable, and free of atomics.  The
+// CTAs read each other's counts per expert through distributed shared memory.
+// The match is what bounds it (about 45 cycles of an SM each, one per 32
+// pairs and pass), hence the spread over 16 SMs and the ranks kept.
 __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* idx, int n, int top_k, int E,
                                                                 int32_t* offsets, int32_t* row_of_pair,
                                                                 int32_t* token_of_row, int32_t* group_of_row) {
-    extern __shared__ int cnt[];  // [kSortWarps][E]
+    extern __shared__ int cnt[];  // [kSortWarps][E] per warp, then [E] of the CTA
     __shared__ int warp_tot[kSortWarps];
+    int* const cta_cnt = cnt + kSortWarps * E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     for (int i = tid; i < kSortWarps * E; i += kSortThreads) cnt[i] = 0;
     __syncthreads();
-    const int64_t seg = ((int64_t)n + kSortThreads - 1) / kSortThreads * 32;
-    const int64_t p0 = warp * seg, p1 = p0 + seg < n ? p0 + seg : n;
+    const int64_t seg = ((int64_t)n + (int64_t)ctas * kSortThreads - 1) / ((int64_t)ctas * kSortThreads) * 32;
+    const int64_t p0 = ((int64_t)rank * kSortWarps + warp) * seg, p1 = p0 + seg < n ? p0 + seg : n;
+    const bool keep = seg <= 32 * kKeep;
     int* mine = cnt + warp * E;
-    for (int64_t p = p0 + lane; p - lane < p1; p += 32) {
+    int key_r[kKeep], rank_r[kKeep];
+    auto key_at = [&](int64_t p) {
         const int e = p < p1 ? idx[p] : -1;
-        const int key = e >= 0 && e < E ? e : -1;
+        return e >= 0 && e < E ? e : -1;
+    };
+    // rank among the warp's pairs of this expert so far; counts them
+    auto take = [&](int key) {
         const unsigned peers = __match_any_sync(kAll, key);
+        int r = -1;
+        if (key >= 0) r = mine[key] + __popc(peers & ((1u << lane) - 1));
+        __syncwarp();
         if (key >= 0 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
         __syncwarp();
+        return r;
+    };
+    if (keep) {
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j) key_r[j] = key_at(p0 + 32 * j + lane);
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+            if (p0 + 32 * j < p1) rank_r[j] = take(key_r[j]);
+    } else {
+        for (int64_t p = p0 + lane; p - lane < p1; p += 32) take(key_at(p));
     }
     __syncthreads();
-    int total = 0;
-    if (tid < E)
+    int own = 0;
+    if (tid < E) {
+#pragma unroll 8
         for (int w = 0; w < kSortWarps; ++w) {
             const int c = cnt[w * E + tid];
-            cnt[w * E + tid] = total;
+            cnt[w * E + tid] = own;
+            own += c;
+        }
+        cta_cnt[tid] = own;
+    }
+    cluster.sync();
+    int total = 0, earlier = 0;  // of this expert: all CTAs, CTAs before this one
+    if (tid < E)
+        for (int r = 0; r < ctas; ++r) {
+            const int c = cluster.map_shared_rank(cta_cnt, r)[tid];
             total += c;
+            if (r < rank) earlier += c;
         }
     int incl = total;
 #pragma unroll
@@ -233,35 +339,44 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
         if (lane >= o) incl += v;
     }
     if (lane == 31) warp_tot[warp] = incl;
-    __syncthreads();
+    cluster.sync();  // also: no CTA leaves while its counts are read
     int before = 0, kept = 0;
+#pragma unroll 8
     for (int w = 0; w < kSortWarps; ++w) {
         if (w < warp) before += warp_tot[w];
         kept += warp_tot[w];
     }
-    const int first = before + incl - total;
     if (tid < E) {
-        offsets[tid] = first;
-        for (int w = 0; w < kSortWarps; ++w) cnt[w * E + tid] += first;
+        const int first = before + incl - total;
+        if (rank == 0) offsets[tid] = first;
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) cnt[w * E + tid] += first + earlier;
     }
-    if (tid == 0) offsets[E] = kept;
+    if (tid == 0 && rank == 0) offsets[E] = kept;
     __syncthreads();
-    for (int64_t p = p0 + lane; p - lane < p1; p += 32) {
-        const int e = p < p1 ? idx[p] : -1;
-        const int key = e >= 0 && e < E ? e : -1;
-        const unsigned peers = __match_any_sync(kAll, key);
-        int row = -1;
+    auto put = [&](int64_t p, int key, int row) {
+        if (p >= p1) return;
+        row_of_pair[p] = row;
         if (key >= 0) {
-            row = mine[key] + __popc(peers & ((1u << lane) - 1));
-            token_of_row[row] = (int)(p / top_k);
+            token_of_row[row] = (int)((uint32_t)p / (uint32_t)top_k);
             group_of_row[row] = key;
         }
-        if (p < p1) row_of_pair[p] = row;
-        __syncwarp();
-        if (key >= 0 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
-        __syncwarp();
+    };
+    if (keep) {
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j)
+            if (p0 + 32 * j < p1) {
+                const int key = key_r[j];
+                // the rank counted from the warp's own zero: its count here is the warp's first row
+                put(p0 + 32 * j + lane, key, key >= 0 ? mine[key] + rank_r[j] : -1);
+            }
+    } else {
+        for (int64_t p = p0 + lane; p - lane < p1; p += 32) {
+            const int key = key_at(p);
+            put(p, key, take(key));
+        }
     }
-    for (int r = kept + tid; r < n; r += kSortThreads) {
+    for (int64_t r = kept + (int64_t)rank * kSortThreads + tid; r < n; r += (int64_t)ctas * kSortThreads) {
         token_of_row[r] = -1;
         group_of_row[r] = -1;
     }
@@ -270,30 +385,99 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
 // ---------------------------------------------------------------------------
 // combine
 // ---------------------------------------------------------------------------
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(256) combine_kernel(const TI* rows, int64_t rows_ld, const int32_t* row_of_pair,
-                                                      const float* w, int64_t T, int top_k, int cols, TO* y,
-                                                      int64_t y_ld) {
-    const int per = (cols + 255) / 256;
-    for (int64_t b = blockIdx.x; b < T * per; b += gridDim.x) {
-        const int64_t t = b / per;
-        const int col = (int)(b % per) * 256 + threadIdx.x;
-        if (col >= cols) continue;
-        float acc = 0.0f;
-        for (int j = 0; j < top_k; ++j) {
-            const int r = row_of_pair[t * top_k + j];
-            if (r >= 0) acc += w[t * top_k + j] * to_f32(rows[r * rows_ld + col]);
-        }
-        y[t * y_ld + col] = (TO)acc;
+constexpr int kCombineThreads = 128;
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A CTA takes 8 x 128 columns of one token, a thread 8 of them: memory-bound,
+// so the loads are 16 bytes wide and four rows' are in flight at a time.
+// WIDE = false: any alignment, 128 columns of a token per CTA.
+template <typename TI, typename TO, bool WIDE>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const TI* rows, int64_t rows_ld,
+                                                                  const int32_t* row_of_pair, const float* w, int top_k,
+                                                                  int cols, TO* y, int64_t y_ld) {
+    constexpr int V = WIDE ? 8 : 1;
+    const int64_t t = blockIdx.x;
+    const int col = (blockIdx.y * kCombineThreads + threadIdx.x) * V;
+    if (col >= cols) return;
+    row_of_pair += t * top_k;
+    w += t * top_k;
+    float acc[V] = {};
+    int j = 0;
+    auto add = [&](int n) {  // n <= 4 rows from j on
+        float v[4][V], wj[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i < n ? __ldg(row_of_pair + j + i) : -1;
+            wj[i] = i < n ? __ldg(w + j + i) : 0.0f;
+#pragma unroll
+            for (int q = 0; q < V; ++q) v[i][q] = 0.0f;
+            if (r >= 0) {
+                const TI* p = rows + r * rows_ld + col;
+                if constexpr (WIDE) load8(p, v[i]);
+                else v[i][0] = to_f32(*p);
+            } else {
+                wj[i] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < V; ++q) acc[q] = fmaf(wj[i], v[i][q], acc[q]);
+        j += n;
+    };
+    while (top_k - j >= 4) add(4);
+    if (j < top_k) add(top_k - j);
+    TO* out = y + t * y_ld + col;
+    if constexpr (WIDE) store8(out, acc);
+    else *out = (TO)acc[0];
+}
+
+// 8 columns at a time need whole, aligned 16-byte pieces in every row of both
+template <typename T>
+bool wide_rows(const void* p, int64_t ld, int cols) {
+    return cols % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
 }
 
 template <typename TI, typename TO>
 cudaError_t combine_typed(const void* rows, int64_t rows_ld, const int32_t* row_of_pair, const float* w, int64_t T,
                           int top_k, int cols, void* y, int64_t y_ld, cudaStream_t st) {
-    const int64_t blocks = T * ((cols + 255) / 256);
-    combine_kernel<TI, TO><<<(unsigned)(blocks < 1 << 20 ? blocks : 1 << 20), 256, 0, st>>>(
-        static_cast<const TI*>(rows), rows_ld, row_of_pair, w, T, top_k, cols, static_cast<TO*>(y), y_ld);
+    const bool wide = wide_rows<TI>(rows, rows_ld, cols) && wide_rows<TO>(y, y_ld, cols);
+    const int per = kCombineThreads * (wide ? 8 : 1);
+    const int64_t chunks = ((int64_t)cols + per - 1) / per;
+    if (chunks > 65535) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)T, (unsigned)chunks);
+    const TI* in = static_cast<const TI*>(rows);
+    TO* out = static_cast<TO*>(y);
+    if (wide)
+        combine_kernel<TI, TO, true><<<grid, kCombineThreads, 0, st>>>(in, rows_ld, row_of_pair, w, top_k, cols, out, y_ld);
+    else
+        combine_kernel<TI, TO, false><<<grid, kCombineThreads, 0, st>>>(in, rows_ld, row_of_pair, w, top_k, cols, out, y_ld);
     return cudaGetLastError();
 }
 
@@ -311,12 +495,26 @@ size_t dispatch_workspace(int64_t, int) { return 0; }
 cudaError_t launch_dispatch(const int32_t* idx, int64_t pairs, int top_k, int n_experts, int32_t* offsets,
                             int32_t* row_of_pair, int32_t* token_of_row, int32_t* group_of_row, void*,
                             cudaStream_t st) {
-    const int smem = kSortWarps * n_experts * (int)sizeof(int);
-    cudaError_t e = smem_limit(reinterpret_cast<const void*>(dispatch_kernel), smem);
+    const int smem = (kSortWarps + 1) * n_experts * (int)sizeof(int);
+    const void* kernel = reinterpret_cast<const void*>(dispatch_kernel);
+    cudaError_t e = smem_limit(kernel, smem);
     if (e != cudaSuccess) return e;
-    dispatch_kernel<<<1, kSortThreads, smem, st>>>(idx, (int)pairs, top_k, n_experts, offsets, row_of_pair,
-                                                   token_of_row, group_of_row);
-    return cudaGetLastError();
+    // one CTA up to 2048 pairs (two rounds a warp), else 16: the largest cluster, past the portable 8
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = pairs <= 2048 ? 1 : 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    if (pairs > 2048 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = attr[0].val.clusterDim.x;
+    cfg.blockDim = kSortThreads;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, dispatch_kernel, idx, (int)pairs, top_k, n_experts, offsets, row_of_pair,
+                              token_of_row, group_of_row);
 }
 
 cudaError_t launch_combine(const void* rows, int rows_type, int64_t rows_ld, const int32_t* row_of_pair, const float* w,
