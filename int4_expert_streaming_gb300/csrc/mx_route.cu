@@ -3,6 +3,7 @@
 #include <cooperative_groups.h>
 
 #include <cfloat>
+#include <utility>
 
 #include "mx.h"
 
@@ -48,17 +49,13 @@ constexpr int kRouteWarps = 4;
 // 1 / (1 + exp(-l)), within a few units of the last place
 __device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
 
-// per-warp scratch: the scores on their way to the group sums, then the
-// candidates of the choice
+// per-warp scratch: a score of every expert (expert e at e + e / 32, so that
+// lanes a row apart do not share a bank), and the candidates of the choice
 template <int NV>
-union RouteScratch {
+struct RouteScratch {
     float score[NV * 33];
-    struct {
-        uint32_t key[32];
-        int e[32];
-        float l[32];
-        int order[32];
-    } cand;
+    int cand[32];
+    int order[32];
 };
 
 // One warp per token; lane l holds the experts l, l + 32, ...: the row is read
@@ -66,11 +63,13 @@ union RouteScratch {
 //
 // The choice: no expert below t, the top_k-th largest of the 32 lanes' maxima,
 // can be chosen, because top_k lanes hold one at or above t.  What is left
-// (top_k to about twice as many) goes to shared memory, one candidate per
-// lane, and each counts the candidates before it.  A row with more than 32
-// left (equal logits) takes top_k rounds of (largest key, then lowest id)
-// instead; rounds for every row, each rescanning the winner's NV keys, took
-// 840 cycles a round at 512 experts.
+// (top_k to about twice as many) becomes one candidate per lane, and each
+// counts the candidates before it.  A row with more than 32 left (equal
+// logits) takes top_k rounds of (largest key, then lowest id) instead; rounds
+// for every row, each rescanning the winner's NV keys, took 840 cycles a round
+// at 512 experts.  With one token the kernel is a chain of dependent steps on
+// a cold instruction cache, so the code is kept short; with thousands it is
+// bound by the instructions issued.
 template <typename T, int NV>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a) {
     __shared__ RouteScratch<NV> scratch[kRouteWarps];
@@ -163,57 +162,46 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
     uint32_t key[NV], best = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+        sh.score[i * 33 + lane] = ch[i];
         key[i] = ordered(ch[i]);
         best = max(best, key[i]);
     }
-    int before = 0;
-#pragma unroll
-    for (int q = 0; q < 32; ++q) {
-        const uint32_t o = __shfl_sync(kAll, best, q);
-        before += o > best || (o == best && q < lane);
+    // the top_k-th distinct largest lane maximum (equal ones count once, which can only lower it), and at least
+    // none + 1: what is out is no candidate
+    uint32_t floor_key = none + 1;
+    uint32_t rest = best;
+    for (int j = 0; j < c.top_k; ++j) {
+        const uint32_t top = __reduce_max_sync(kAll, rest);
+        floor_key = top;
+        if (top <= none) break;
+        if (rest == top) rest = 0;
     }
-    // at least none + 1: what is out is no candidate
-    const uint32_t floor_key =
-        max(__shfl_sync(kAll, best, __ffs(__ballot_sync(kAll, before == c.top_k - 1)) - 1), none + 1);
-    int n = 0;
+    floor_key = max(floor_key, none + 1);
+    uint32_t left = 0;  // bit i: key[i] is a candidate
 #pragma unroll
-    for (int i = 0; i < NV; ++i) n += key[i] >= floor_key;
-    int at = n;
+    for (int i = 0; i < NV; ++i) left |= (uint32_t)(key[i] >= floor_key) << i;
+    int at = __popc(left);
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const int v = __shfl_up_sync(kAll, at, o);
         if (lane >= o) at += v;
     }
-    const int local = n;
-    n = __shfl_sync(kAll, at, 31);
-    int mine = -1;     // lane j: the j-th choice
-    float v = -INFINITY;  // and its logit
+    const int n = __shfl_sync(kAll, at, 31);
+    int mine = -1;  // lane j: the j-th choice
     if (n <= 32) {
-        at -= local;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (key[i] >= floor_key) {
-                sh.cand.key[at] = key[i];
-                sh.cand.e[at] = i * 32 + lane;
-                sh.cand.l[at] = l[i];
-                ++at;
-            }
+        for (at -= __popc(left); left; left &= left - 1) sh.cand[at++] = (__ffs(left) - 1) * 32 + lane;
         __syncwarp();
-        const uint32_t k0 = lane < n ? sh.cand.key[lane] : 0;
-        const int e0 = lane < n ? sh.cand.e[lane] : INT_MAX;
+        const int e0 = lane < n ? sh.cand[lane] : E;
+        const float s0 = lane < n ? sh.score[e0 + (e0 >> 5)] : -INFINITY;
         int rank = 0;
-#pragma unroll 4
         for (int q = 0; q < n; ++q) {
-            const uint32_t kq = sh.cand.key[q];
-            rank += kq > k0 || (kq == k0 && sh.cand.e[q] < e0);
+            const float sq = __shfl_sync(kAll, s0, q);
+            const int eq = __shfl_sync(kAll, e0, q);
+            rank += sq > s0 || (sq == s0 && eq < e0);
         }
-        if (lane < n) sh.cand.order[rank] = lane;
+        if (lane < n) sh.order[rank] = e0;
         __syncwarp();
-        if (lane < n && lane < c.top_k) {
-            const int q = sh.cand.order[lane];
-            mine = sh.cand.e[q];
-            v = sh.cand.l[q];
-        }
+        if (lane < n && lane < c.top_k) mine = sh.order[lane];
     } else {
         for (int j = 0; j < c.top_k; ++j) {
             const uint32_t top = __reduce_max_sync(kAll, best);
@@ -231,8 +219,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
                 best = max(best, key[i]);
             }
         }
-        if (mine >= 0) v = fminf(to_f32(row[mine]), FLT_MAX);
     }
+    const float v = mine >= 0 ? fminf(to_f32(row[mine]), FLT_MAX) : -INFINITY;
 
     // weights, relative to the largest chosen logit where they are renormalised
     float wt = 0.0f;
@@ -264,17 +252,89 @@ cudaError_t route_typed(const RouteArgs& a, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // dispatch
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCtas = 16;
 constexpr int kKeep = 8;  // rounds whose ranks stay in registers between the two passes
 
-// CTAs of one cluster take consecutive runs of the pairs, and each warp a run
-// of its CTA's.  32 pairs at a time a warp finds equal experts by a match, so
-// that a pair's rank among its expert's pairs is (earlier CTAs) + (earlier
-// warps) + (earlier rounds) + (lower lanes): stable, and free of atomics.  The
-// CTAs read each other's counts per expert through distributed shared memory.
-// The match is what bounds it (about 45 cycles of an SM each, one per 32
-// pairs and pass), hence the spread over 16 SMs and the ranks kept.
-__global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* idx, int n, int top_k, int E,
+// Lanes of the warp with the same key (0 <= key < 2^bits), by one ballot a
+// bit.  A match instruction does the same, but takes about 65 cycles of an SM.
+__device__ __forceinline__ unsigned peers_of(int key, int bits) {
+    unsigned peers = kAll;
+    for (int b = 0; b < bits; ++b) {
+        const unsigned set = __ballot_sync(kAll, key >> b & 1);
+        peers &= key >> b & 1 ? set : ~set;
+    }
+    return peers;
+}
+
+// inclusive sum over a warp
+__device__ __forceinline__ int warp_scan(int v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int u = __shfl_up_sync(kAll, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Up to 1024 pairs, one a thread: one CTA, counts per (warp, expert) in bytes.
+// A chain of short steps between five barriers; latency is all there is.
+__global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(const int32_t* idx, int n, int top_k, int E,
+                                                                      int bits, int32_t* offsets, int32_t* row_of_pair,
+                                                                      int32_t* token_of_row, int32_t* group_of_row) {
+    extern __shared__ uint4 cnt_raw[];  // [warps with pairs][E] bytes, then [E] first rows
+    __shared__ int warp_tot[kSortWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rows = (n + 31) / 32, bytes = (rows * E + 15) & ~15;
+    uint8_t* cnt = reinterpret_cast<uint8_t*>(cnt_raw);
+    int* first = reinterpret_cast<int*>(cnt + bytes);
+    for (int i = tid; i < bytes / 16; i += blockDim.x) cnt_raw[i] = make_uint4(0, 0, 0, 0);
+    int key = tid < n ? idx[tid] : -1;
+    if (key < 0 || key >= E) key = -1;
+    __syncthreads();
+    int rank = 0;
+    if (warp < rows) {
+        const unsigned peers = peers_of(key < 0 ? E : key, bits);
+        rank = __popc(peers & ((1u << lane) - 1));
+        if (key >= 0 && rank == 0) cnt[warp * E + key] = (uint8_t)__popc(peers);
+    }
+    __syncthreads();
+    int total = 0;
+    if (tid < E)
+        for (int w = 0; w < rows; ++w) total += cnt[w * E + tid];
+    if (key >= 0)
+        for (int w = 0; w < warp; ++w) rank += cnt[w * E + key];
+    const int incl = warp_scan(total, lane);
+    if (lane == 31) warp_tot[warp] = incl;
+    __syncthreads();
+    if (warp == 0) warp_tot[lane] = warp_scan(lane < (int)blockDim.x / 32 ? warp_tot[lane] : 0, lane);
+    __syncthreads();
+    const int kept = warp_tot[blockDim.x / 32 - 1];
+    const int at = (warp ? warp_tot[warp - 1] : 0) + incl - total;
+    if (tid < E) {
+        first[tid] = at;
+        offsets[tid] = at;
+    }
+    if (tid == 0) offsets[E] = kept;
+    __syncthreads();
+    if (tid >= n) return;
+    const int row = key >= 0 ? first[key] + rank : -1;
+    row_of_pair[tid] = row;
+    if (key >= 0) {
+        token_of_row[row] = tid / top_k;
+        group_of_row[row] = key;
+    }
+    if (tid >= kept) {
+        token_of_row[tid] = -1;
+        group_of_row[tid] = -1;
+    }
+}
+
+// More pairs: the CTAs of one cluster take consecutive runs of them, and each
+// warp a run of its CTA's, so that a pair's rank among its expert's pairs is
+// (earlier CTAs) + (earlier warps) + (earlier rounds) + (lower lanes): stable,
+// and free of atomics.  The CTAs read each other's counts per expert through
+// distributed shared memory.
+__global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* idx, int n, int top_k, int E, int bits,
                                                                 int32_t* offsets, int32_t* row_of_pair,
                                                                 int32_t* token_of_row, int32_t* group_of_row) {
     extern __shared__ int cnt[];  // [kSortWarps][E] per warp, then [E] of the CTA
@@ -282,11 +342,9 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
     int* const cta_cnt = cnt + kSortWarps * E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    for (int i = tid; i < kSortWarps * E; i += kSortThreads) cnt[i] = 0;
-    __syncthreads();
-    const int64_t seg = ((int64_t)n + (int64_t)ctas * kSortThreads - 1) / ((int64_t)ctas * kSortThreads) * 32;
-    const int64_t p0 = ((int64_t)rank * kSortWarps + warp) * seg, p1 = p0 + seg < n ? p0 + seg : n;
+    const int me = (int)cluster.block_rank();
+    const int64_t seg = ((int64_t)n + kSortCtas * kSortThreads - 1) / (kSortCtas * kSortThreads) * 32;
+    const int64_t p0 = ((int64_t)me * kSortWarps + warp) * seg, p1 = p0 + seg < n ? p0 + seg : n;
     const bool keep = seg <= 32 * kKeep;
     int* mine = cnt + warp * E;
     int key_r[kKeep], rank_r[kKeep];
@@ -296,17 +354,19 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
     };
     // rank among the warp's pairs of this expert so far; counts them
     auto take = [&](int key) {
-        const unsigned peers = __match_any_sync(kAll, key);
-        int r = -1;
-        if (key >= 0) r = mine[key] + __popc(peers & ((1u << lane) - 1));
+        const unsigned peers = peers_of(key < 0 ? E : key, bits);
+        const int r = key >= 0 ? mine[key] : 0, lower = __popc(peers & ((1u << lane) - 1));
         __syncwarp();
-        if (key >= 0 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
+        if (key >= 0 && lower == 0) mine[key] = r + __popc(peers);
         __syncwarp();
-        return r;
+        return r + lower;
     };
-    if (keep) {
+    if (keep)
 #pragma unroll
         for (int j = 0; j < kKeep; ++j) key_r[j] = key_at(p0 + 32 * j + lane);
+    for (int i = lane; i < E; i += 32) mine[i] = 0;
+    __syncwarp();
+    if (keep) {
 #pragma unroll
         for (int j = 0; j < kKeep; ++j)
             if (p0 + 32 * j < p1) rank_r[j] = take(key_r[j]);
@@ -326,37 +386,34 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
     }
     cluster.sync();
     int total = 0, earlier = 0;  // of this expert: all CTAs, CTAs before this one
-    if (tid < E)
-        for (int r = 0; r < ctas; ++r) {
-            const int c = cluster.map_shared_rank(cta_cnt, r)[tid];
-            total += c;
-            if (r < rank) earlier += c;
-        }
-    int incl = total;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int v = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) warp_tot[warp] = incl;
-    cluster.sync();  // also: no CTA leaves while its counts are read
-    int before = 0, kept = 0;
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) {
-        if (w < warp) before += warp_tot[w];
-        kept += warp_tot[w];
-    }
     if (tid < E) {
-        const int first = before + incl - total;
-        if (rank == 0) offsets[tid] = first;
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) cnt[w * E + tid] += first + earlier;
+        int c[kSortCtas];  // all loads in flight: a remote one takes several hundred cycles
+#pragma unroll
+        for (int r = 0; r < kSortCtas; ++r) c[r] = cluster.map_shared_rank(cta_cnt, r)[tid];
+#pragma unroll
+        for (int r = 0; r < kSortCtas; ++r) {
+            total += c[r];
+            if (r < me) earlier += c[r];
+        }
     }
-    if (tid == 0 && rank == 0) offsets[E] = kept;
+    auto counts_read = cluster.barrier_arrive();
+    const int incl = warp_scan(total, lane);
+    if (lane == 31) warp_tot[warp] = incl;
+    __syncthreads();
+    if (warp == 0) warp_tot[lane] = warp_scan(warp_tot[lane], lane);
+    __syncthreads();
+    const int kept = warp_tot[kSortWarps - 1];
+    if (tid < E) {
+        const int at = (warp ? warp_tot[warp - 1] : 0) + incl - total;
+        if (me == 0) offsets[tid] = at;
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) cnt[w * E + tid] += at + earlier;
+    }
+    if (tid == 0 && me == 0) offsets[E] = kept;
     __syncthreads();
     auto put = [&](int64_t p, int key, int row) {
         if (p >= p1) return;
-        row_of_pair[p] = row;
+        row_of_pair[p] = key >= 0 ? row : -1;
         if (key >= 0) {
             token_of_row[row] = (int)((uint32_t)p / (uint32_t)top_k);
             group_of_row[row] = key;
@@ -367,7 +424,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
         for (int j = 0; j < kKeep; ++j)
             if (p0 + 32 * j < p1) {
                 const int key = key_r[j];
-                // the rank counted from the warp's own zero: its count here is the warp's first row
+                // the rank was counted from the warp's own zero: its count here is the warp's first row
                 put(p0 + 32 * j + lane, key, key >= 0 ? mine[key] + rank_r[j] : -1);
             }
     } else {
@@ -376,10 +433,11 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
             put(p, key, take(key));
         }
     }
-    for (int64_t r = kept + (int64_t)rank * kSortThreads + tid; r < n; r += (int64_t)ctas * kSortThreads) {
+    for (int64_t r = kept + (int64_t)me * kSortThreads + tid; r < n; r += kSortCtas * kSortThreads) {
         token_of_row[r] = -1;
         group_of_row[r] = -1;
     }
+    cluster.barrier_wait(std::move(counts_read));  // no CTA leaves while its counts are read
 }
 
 // ---------------------------------------------------------------------------
@@ -495,25 +553,35 @@ size_t dispatch_workspace(int64_t, int) { return 0; }
 cudaError_t launch_dispatch(const int32_t* idx, int64_t pairs, int top_k, int n_experts, int32_t* offsets,
                             int32_t* row_of_pair, int32_t* token_of_row, int32_t* group_of_row, void*,
                             cudaStream_t st) {
+    int bits = 1;  // ids 0 .. n_experts, the last for a dropped pair
+    while ((n_experts >> bits) != 0) ++bits;
+    cudaError_t e;
+    if (pairs <= kSortThreads) {
+        const int n = (int)pairs, rows = (n + 31) / 32;
+        const int smem = ((rows * n_experts + 15) & ~15) + n_experts * (int)sizeof(int);
+        if ((e = smem_limit(reinterpret_cast<const void*>(dispatch_small_kernel), smem)) != cudaSuccess) return e;
+        const int threads = ((n > n_experts ? n : n_experts) + 31) & ~31;
+        dispatch_small_kernel<<<1, threads, smem, st>>>(idx, n, top_k, n_experts, bits, offsets, row_of_pair,
+                                                        token_of_row, group_of_row);
+        return cudaGetLastError();
+    }
     const int smem = (kSortWarps + 1) * n_experts * (int)sizeof(int);
     const void* kernel = reinterpret_cast<const void*>(dispatch_kernel);
-    cudaError_t e = smem_limit(kernel, smem);
-    if (e != cudaSuccess) return e;
-    // one CTA up to 2048 pairs (two rounds a warp), else 16: the largest cluster, past the portable 8
+    if ((e = smem_limit(kernel, smem)) != cudaSuccess) return e;
+    // 16 CTAs are past the portable cluster size of 8
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = pairs <= 2048 ? 1 : 16;
+    attr[0].val.clusterDim.x = kSortCtas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    if (pairs > 2048 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-        return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = attr[0].val.clusterDim.x;
+    cfg.gridDim = kSortCtas;
     cfg.blockDim = kSortThreads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dispatch_kernel, idx, (int)pairs, top_k, n_experts, offsets, row_of_pair,
+    return cudaLaunchKernelEx(&cfg, dispatch_kernel, idx, (int)pairs, top_k, n_experts, bits, offsets, row_of_pair,
                               token_of_row, group_of_row);
 }
 
