@@ -10,18 +10,26 @@
 //
 // Both operands are stored as the tensor core wants them in shared memory, so
 // a step is plain bulk copies: one for a whole w tile (codes and scales), two
-// per x row tile (its used rows' codes, its scales).  The scale atoms go on to
-// tensor memory with tcgen05.cp, replicated to the four lane quarters: row r
-// of an atom lands in lane r % 32, column r / 32, four scale bytes a column.
+// per x row tile (its used rows' codes, its scales).  The MMA reads the scales
+// from tensor memory: row r of a 128 x 4 scale atom in lane r % 32, column
+// r / 32, the same in all four lane quarters.  Four warps put them there, an
+// atom being one 16-byte shared load and four columns per lane; tcgen05.cp can
+// do it too, but at about 50 cycles an atom in the MMA's own queue: 12 atoms
+// against 512 cycles of MMA in the largest step.
 //
 // Warp roles of a persistent CTA (one per SM):
-//   warp 0     one thread issues the copies, kStages steps ahead
-//   warp 1     one thread issues scale copies, MMAs and commits
-//   warps 2-5  epilogue: tensor memory -> registers -> y; warp w reads the
-//              lanes of quarter w % 4
+//   warp 0      copies, kStages steps ahead; each lane issues one of a step's
+//   warp 1      one thread issues MMAs and commits
+//   warps 2-5   scales: shared memory -> tensor memory, lane quarter w % 4
+//   warps 6-13  epilogue: tensor memory -> registers -> y; lane quarter w % 4,
+//               two warps per quarter take the halves of the columns
+// The loops of warps 0 and 1 are chains of dependent instructions, and a step
+// with few rows lasts about as long as one of them; so they run warp-wide
+// (uniform registers), keep running counters instead of divisions, and only
+// warp 0 searches the groups for a tile.
 // The accumulator region holds 256 columns as two slots of 128: a tile of at
-// most 128 rows takes one slot, so that its epilogue overlaps the next tile's
-// MMAs; a larger one takes both.
+// most 128 rows takes one slot, a larger one both.  A slot is free again as
+// soon as it has been read into registers.
 // Every wait is bounded; one that runs out sets a status word in mapped host
 // memory, and the CTA drains its MMAs and copies and frees its tensor memory.
 #include <mutex>
@@ -35,8 +43,10 @@ namespace {
 using namespace umma;
 using namespace gemmc;
 
-constexpr int kThreads = 192;
-constexpr int kEpiWarp0 = 2, kEpiWarps = 4;
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kScaleWarp0 = 2, kEpiWarp0 = 6, kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kTileRing = 16;  // rows of the tiles between the copies and the MMAs: more than kStages
 constexpr int kTmemCols = 512;
 constexpr int kScaleBufs = 4;    // steps whose scales are in tensor memory at a time
 constexpr int kScaleCol = 256;   // first scale column, behind the accumulators
@@ -50,7 +60,6 @@ struct ProductArgs {
     void* y;
     int64_t y_ld, x_rows, w_rows;
     int groups, steps, w_tiles;  // steps: column tiles; w_tiles: row tiles of one group of w
-    int y_f32;
     int* status;
 };
 
@@ -72,14 +81,35 @@ struct Cfg {
     static_assert(kStages >= 4, "shared memory");
 };
 
-// no-swizzle shared memory descriptor of a scale atom: 32 rows of 16 bytes,
-// 8-row groups 128 bytes apart
-__device__ __forceinline__ uint64_t atom_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+// 16 or 8 consecutive columns of the warp's lane quarter
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
-__device__ __forceinline__ void copy_atom(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
+template <int N>
+__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&v)[N]) {
+    if constexpr (N == 8) {
+        tmem_st(taddr, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 16) {
+            uint32_t u[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) u[j] = v[i + j];
+            tmem_st(taddr + i, u);
+        }
+    }
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // instruction descriptor of the block-scaled kinds: e2m1 A and B, fp32 D, both
 // K-major; scale type e8m0 or e4m3; `id`: first scale byte used of a column
@@ -88,21 +118,21 @@ __device__ __forceinline__ uint32_t idesc_mx(int N, uint32_t id) {
     return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((FMT == MOE_MX_E8M0 ? 1u : 0u) << 23) |
            (1u << 27) | (id << 29);
 }
+// D (+)= A * B^T, the descriptors given as low words and one high word
 template <int FMT>
-__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t alo, uint32_t blo, uint32_t dhi, uint32_t idesc, uint32_t sa,
+                                       uint32_t sb, uint32_t accumulate) {
     if (FMT == MOE_MX_E8M0)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            "{\n .reg .pred p;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n setp.ne.b32 p, %7, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], ad, bd, %4, [%5], [%6], p;\n}" ::"r"(d),
+            "r"(alo), "r"(blo), "r"(dhi), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-                d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            "{\n .reg .pred p;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n setp.ne.b32 p, %7, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], ad, bd, %4, [%5], [%6], p;\n}" ::"r"(d),
+            "r"(alo), "r"(blo), "r"(dhi), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
             : "memory");
 }
 
@@ -110,17 +140,22 @@ __device__ __forceinline__ void fail(const ProductArgs& a, volatile int* abort) 
     *abort = 1;
     *(volatile int*)a.status = 1;
 }
+// bounded wait of a whole warp, the same answer in every lane
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+    if (__all_sync(kAll, bar_try_wait(b, parity))) return true;
+    return __all_sync(kAll, bar_wait(b, parity, kTimeoutNs, abort));
+}
 
 struct Tile {
-    int g, n, wt;      // group, rows, w row tile
-    int64_t row0;      // first row of x and y
-    int64_t xt;        // first x row tile
+    int g, n, wt;  // group, rows, w row tile
+    int64_t row0;  // first row of x and y
+    int64_t xt;    // first x row tile
 };
 
-// tile t of the CTA's walk: row tile t / w_tiles, found by bisection in the
-// groups' running counts, and w row tile t % w_tiles
+// tile t, by a whole warp: row tile t / w_tiles, found in the groups' running
+// counts (the last g with cum[g] <= it) by two ballots, and w row tile t % w_tiles
 template <int NT>
-__device__ __forceinline__ Tile find_tile(const ProductArgs& a, const int* cum, int t) {
+__device__ __forceinline__ Tile find_tile(const ProductArgs& a, const int* cum, int t, int lane) {
     Tile ti;
     int q = t / a.w_tiles;
     ti.wt = t - q * a.w_tiles;
@@ -128,22 +163,32 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs& a, const int* cum, 
     int64_t o = 0, n = a.x_rows;
     ti.xt = 0;
     if (a.offsets) {
-        int lo = 0, hi = a.groups - 1;  // the last g with cum[g] <= q
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cum[mid] <= q) lo = mid;
-            else hi = mid - 1;
-        }
-        ti.g = lo;
-        q -= cum[lo];
-        o = __ldg(a.offsets + lo);
-        n = __ldg(a.offsets + lo + 1) - o;
-        ti.xt = o / kMxTileRows + lo;
+        const int blk = 32 * (__popc(__ballot_sync(kAll, lane * 32 < a.groups && cum[min(lane * 32, a.groups - 1)] <= q)) - 1);
+        const int i = blk + lane;
+        ti.g = blk + __popc(__ballot_sync(kAll, i < a.groups && cum[min(i, a.groups - 1)] <= q)) - 1;
+        q -= cum[ti.g];
+        const int o0 = __ldg(a.offsets + ti.g), o1 = __ldg(a.offsets + ti.g + 1);
+        o = o0;
+        n = o1 - o0;
+        ti.xt = (o0 >> 7) + ti.g;
     }
     ti.row0 = o + (int64_t)q * NT;
-    ti.n = (int)(n - (int64_t)q * NT < NT ? n - (int64_t)q * NT : NT);
+    ti.n = (int)min(n - (int64_t)q * NT, (int64_t)NT);
     ti.xt += (int64_t)q * ((NT + kMxTileRows - 1) / kMxTileRows);  // NT < 128: q is 0, the product has at most NT rows
     return ti;
+}
+
+// one thread of a converged warp, the same at every call
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+
+// row j of a piece: fp32 bits, or bf16 pairs
+__device__ __forceinline__ void put(float* y, const uint32_t (&v)[16], int j) { *y = __uint_as_float(v[j]); }
+__device__ __forceinline__ void put(__nv_bfloat16* y, const uint32_t (&v)[8], int j) {
+    *reinterpret_cast<uint16_t*>(y) = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
 }
 
 // which accumulator slots a tile uses, and how often each has been used
@@ -157,14 +202,14 @@ struct Slots {
     }
 };
 
-template <int FMT, int NT>
+template <int FMT, int NT, typename TY>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs a) {
     using C = Cfg<FMT, NT>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], scales_full[kScaleBufs], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tmem_s;
     __shared__ volatile int abort_s, never_s;
-    __shared__ int warp_sum[kThreads / 32];
+    __shared__ int warp_sum[kThreads / 32], tile_n[kTileRing];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -175,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             bar_init(&full[s], 1);
             bar_init(&empty[s], 1);
         }
+        for (int s = 0; s < kScaleBufs; ++s) bar_init(&scales_full[s], 4);
         for (int s = 0; s < 2; ++s) {
             bar_init(&acc_full[s], 1);
             bar_init(&acc_empty[s], kEpiWarps);
@@ -218,147 +264,217 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = tmem_s;
+    const int my_tiles = (n_tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // <= 0: none
 
     if (warp == 0) {
         // ---------------------------------------------------------------- copies
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-                const Tile ti = find_tile<NT>(a, cum, t);
-                const uint8_t* wp = a.w + ((int64_t)ti.g * a.w_tiles + ti.wt) * a.steps * C::kTile;
-                const uint8_t* xp = a.x + ti.xt * a.steps * C::kTile;
-                const int n0 = min(ti.n, 128), n1 = ti.n - n0;
-                const uint32_t b0 = (uint32_t)((n0 + 7) & ~7) * 128u, b1 = (uint32_t)((n1 + 7) & ~7) * 128u;
-                const uint32_t bytes = C::kTile + b0 + b1 + (n1 > 0 ? 2u : 1u) * C::kScaleBytes;
-                for (int k = 0; k < a.steps; ++k, ++it) {
-                    const uint32_t s = it % C::kStages;
-                    if (it >= C::kStages &&
-                        !bar_wait(&empty[s], (it / C::kStages - 1) & 1u, kTimeoutNs, &abort_s)) {
-                        fail(a, &abort_s);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = smem0 + s * C::kStage;
-                    bar_arrive_expect_tx(&full[s], bytes);
-                    bulk_g2s(st, wp + (int64_t)k * C::kTile, C::kTile, &full[s]);
-                    const uint8_t* x0 = xp + (int64_t)k * C::kTile;
-                    bulk_g2s(st + C::kOffX, x0, b0, &full[s]);
-                    bulk_g2s(st + C::kOffXs, x0 + kMxCodeBytes, C::kScaleBytes, &full[s]);
-                    if (NT > 128 && n1 > 0) {
-                        const uint8_t* x1 = x0 + (int64_t)a.steps * C::kTile;
-                        bulk_g2s(st + C::kOffX + 128 * 128, x1, b1, &full[s]);
-                        bulk_g2s(st + C::kOffXs + C::kScaleBytes, x1 + kMxCodeBytes, C::kScaleBytes, &full[s]);
-                    }
-                }
+        uint32_t s = 0, ph = 1, filled = 0;  // stage, parity of its release, steps begun
+        bool ok = true;
+        for (int i = 0; i < my_tiles && ok; ++i) {
+            const Tile ti = find_tile<NT>(a, cum, (int)blockIdx.x + i * (int)gridDim.x, lane);
+            const int n0 = min(ti.n, 128), n1 = ti.n - n0;
+            // lane 0: the w tile; 1, 2: codes and scales of the first x row tile; 3, 4: of the second
+            const uint32_t b0 = (uint32_t)((n0 + 7) & ~7) * 128u, b1 = (uint32_t)((n1 + 7) & ~7) * 128u;
+            const uint32_t total = C::kTile + b0 + b1 + (n1 > 0 ? 2u : 1u) * C::kScaleBytes;
+            const uint8_t* src;
+            uint32_t dst, bytes;
+            if (lane == 0) {
+                src = a.w + ((int64_t)ti.g * a.w_tiles + ti.wt) * a.steps * C::kTile;
+                dst = 0;
+                bytes = C::kTile;
+            } else {
+                const int second = (lane - 1) >> 1, scales = (lane - 1) & 1;
+                src = a.x + (ti.xt + second) * a.steps * C::kTile + scales * kMxCodeBytes;
+                dst = scales ? C::kOffXs + second * C::kScaleBytes : C::kOffX + second * kMxCodeBytes;
+                bytes = second && n1 <= 0 ? 0u : scales ? C::kScaleBytes : second ? b1 : b0;
+                if (lane > 4 || (NT <= 128 && lane > 2)) bytes = 0;
             }
-            // copies still in flight land before the CTA exits
-            for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
-                bar_wait(&full[i % C::kStages], (i / C::kStages) & 1u, kTimeoutNs, &never_s);
+            if (lane == 0) tile_n[i % kTileRing] = ti.n;
+            dst += smem0;
+            for (int k = 0; k < a.steps; ++k) {
+                if (!warp_wait(&empty[s], ph, &abort_s)) {
+                    fail(a, &abort_s);
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) bar_arrive_expect_tx(&full[s], total);
+                __syncwarp();
+                if (bytes) bulk_g2s(dst + s * C::kStage, src, bytes, &full[s]);
+                src += C::kTile;
+                ++filled;
+                if (++s == C::kStages) s = 0, ph ^= 1;
+            }
         }
+        // copies still in flight land before the CTA exits
+        for (uint32_t i = filled > C::kStages ? filled - C::kStages : 0; i < filled; ++i)
+            bar_wait(&full[i % C::kStages], (i / C::kStages) & 1u, kTimeoutNs, &never_s);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA
-        if (lane == 0) {
-            uint32_t it = 0;
-            Slots slots;
-            bool ok = true;
-            for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-                const Tile ti = find_tile<NT>(a, cum, t);
-                const uint32_t m = slots.mask(ti.n);
-                for (int s = 0; s < 2 && ok; ++s)
-                    if ((m >> s & 1) && !bar_wait(&acc_empty[s], (slots.use[s] & 1u) ^ 1u, kTimeoutNs, &abort_s)) ok = false;
+        const bool leader = elect_one();
+        uint32_t s = 0, ph = 0, buf = 0, bph = 0;
+        Slots slots;
+        bool ok = true;
+        const uint32_t dhi = (uint32_t)(sdesc(smem0) >> 32);  // the same for every operand tile
+        const uint32_t w_lo = (uint32_t)sdesc(smem0), x_lo = (uint32_t)sdesc(smem0 + C::kOffX);
+        for (int i = 0; i < my_tiles && ok; ++i) {
+            uint32_t d = 0, idesc = 0, m = 0;
+            for (int k = 0; k < a.steps; ++k) {
+                ok = warp_wait(&full[s], ph, &abort_s) && warp_wait(&scales_full[buf], bph, &abort_s);
+                if (k == 0 && ok) {
+                    const int n = tile_n[i % kTileRing];
+                    m = slots.mask(n);
+                    if (m & 1) ok = warp_wait(&acc_empty[0], (slots.use[0] & 1u) ^ 1u, &abort_s);
+                    if ((m & 2) && ok) ok = warp_wait(&acc_empty[1], (slots.use[1] & 1u) ^ 1u, &abort_s);
+                    d = tmem + (m == 2 ? 128u : 0u);
+                    idesc = idesc_mx<FMT>((n + 15) & ~15, 0);
+                }
                 if (!ok) {
                     fail(a, &abort_s);
                     break;
                 }
                 fence_after_sync();
-                const uint32_t d = tmem + (m == 2 ? 128u : 0u);
-                const int N = (ti.n + 15) & ~15;
-                for (int k = 0; k < a.steps; ++k, ++it) {
-                    const uint32_t s = it % C::kStages;
-                    if (!bar_wait(&full[s], (it / C::kStages) & 1u, kTimeoutNs, &abort_s) ||
-                        // the scale buffer was last read by the MMAs of step it - kScaleBufs
-                        (it >= kScaleBufs &&
-                         !bar_wait(&empty[(it - kScaleBufs) % C::kStages], ((it - kScaleBufs) / C::kStages) & 1u, kTimeoutNs,
-                                   &abort_s))) {
-                        fail(a, &abort_s);
-                        ok = false;
-                        break;
-                    }
-                    fence_after_sync();
-                    const uint32_t st = smem0 + s * C::kStage;
-                    const uint32_t sc = tmem + kScaleCol + (it % kScaleBufs) * C::kStepCols;
-#pragma unroll
-                    for (int q = 0; q < C::kAtoms; ++q) {
-                        copy_atom(sc + 4 * q, atom_desc(st + kMxCodeBytes + q * kMxAtomBytes));
-                        copy_atom(sc + C::kWCols + q * 4 * C::kXTiles, atom_desc(st + C::kOffXs + q * kMxAtomBytes));
-                        if (NT > 128 && ti.n > 128)
-                            copy_atom(sc + C::kWCols + q * 4 * C::kXTiles + 4,
-                                      atom_desc(st + C::kOffXs + C::kScaleBytes + q * kMxAtomBytes));
-                    }
-                    const uint64_t wd = sdesc(st), xd = sdesc(st + C::kOffX);
+                if (leader) {
+                    const uint32_t wd = w_lo + s * (C::kStage >> 4), xd = x_lo + s * (C::kStage >> 4);
+                    const uint32_t sc = tmem + kScaleCol + buf * C::kStepCols;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         // a column holds the scales of 64 (e4m3) or 128 (e8m0) matrix columns
                         const int atom = FMT == MOE_MX_E8M0 ? q >> 1 : q;
                         const uint32_t id = FMT == MOE_MX_E8M0 ? (q & 1) * 2 : 0;
-                        mma_mx<FMT>(d, wd + 2 * q, xd + 2 * q, idesc_mx<FMT>(N, id), sc + 4 * atom,
-                                    sc + C::kWCols + atom * 4 * C::kXTiles, (k | q) ? 1u : 0u);
+                        mma_mx<FMT>(d, wd + 2 * q, xd + 2 * q, dhi, idesc | id << 4 | id << 29, sc + 4 * atom,
+                                    sc + C::kWCols + atom * 4 * C::kXTiles, q ? 1u : (uint32_t)k);
                     }
                     mma_commit(&empty[s]);
                 }
-                if (!ok) break;
-                for (int s = 0; s < 2; ++s)
-                    if (m >> s & 1) mma_commit(&acc_full[s]);
-                slots.advance(m);
+                __syncwarp();
+                if (++s == C::kStages) s = 0, ph ^= 1;
+                if (++buf == kScaleBufs) buf = 0, bph ^= 1;
             }
-            // everything issued above has completed once this commit arrives
+            if (!ok) break;
+            if (leader) {
+                if (m & 1) mma_commit(&acc_full[0]);
+                if (m & 2) mma_commit(&acc_full[1]);
+            }
+            __syncwarp();
+            slots.advance(m);
+        }
+        // everything issued above has completed once this commit arrives
+        if (leader) {
             mma_commit(&drain);
             if (!bar_wait(&drain, 0, kTimeoutNs, &never_s)) fail(a, &abort_s);
         }
         __syncwarp();
+    } else if (warp < kEpiWarp0) {
+        // --------------------------------------------------------------- scales
+        const uint32_t quarter = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        uint32_t s = 0, ph = 0, buf = 0;
+        uint32_t fs = 0, fph = 0;  // the step kScaleBufs back, whose MMAs read the buffer last
+        const int steps = my_tiles * a.steps;
+        for (int it = 0; it < steps; ++it) {
+            if (!warp_wait(&full[s], ph, &abort_s)) {
+                fail(a, &abort_s);
+                break;
+            }
+            uint32_t wv[C::kWCols], xv[C::kXCols];
+            const uint32_t st = smem0 + s * C::kStage + lane * 16;
+#pragma unroll
+            for (int q = 0; q < C::kAtoms; ++q) {
+                const uint4 v = lds128(st + kMxCodeBytes + q * kMxAtomBytes);
+                wv[4 * q] = v.x, wv[4 * q + 1] = v.y, wv[4 * q + 2] = v.z, wv[4 * q + 3] = v.w;
+#pragma unroll
+                for (int h = 0; h < C::kXTiles; ++h) {
+                    const uint4 u = lds128(st + C::kOffXs + h * C::kScaleBytes + q * kMxAtomBytes);
+                    const int c = 4 * (q * C::kXTiles + h);
+                    xv[c] = u.x, xv[c + 1] = u.y, xv[c + 2] = u.z, xv[c + 3] = u.w;
+                }
+            }
+            if (it >= kScaleBufs) {
+                if (!warp_wait(&empty[fs], fph, &abort_s)) {
+                    fail(a, &abort_s);
+                    break;
+                }
+                if (++fs == C::kStages) fs = 0, fph ^= 1;
+                fence_after_sync();
+            }
+            const uint32_t sc = quarter + kScaleCol + buf * C::kStepCols;
+            store_columns(sc, wv);
+            store_columns(sc + C::kWCols, xv);
+            tmem_st_wait();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&scales_full[buf]);
+            if (++s == C::kStages) s = 0, ph ^= 1;
+            if (++buf == kScaleBufs) buf = 0;
+        }
     } else {
         // ------------------------------------------------------------- epilogue
-        const int q = warp & 3;
+        const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
         const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
         Slots slots;
-        for (int t = blockIdx.x; t < n_tiles; t += gridDim.x) {
-            const Tile ti = find_tile<NT>(a, cum, t);
+        for (int i = 0; i < my_tiles; ++i) {
+            const Tile ti = find_tile<NT>(a, cum, (int)blockIdx.x + i * (int)gridDim.x, lane);
+            const float alpha = a.alpha ? __ldg(a.alpha + ti.g) : 1.0f;
             const uint32_t m = slots.mask(ti.n);
-            int ok = 1;
-            if (lane == 0)
-                for (int s = 0; s < 2; ++s)
-                    if ((m >> s & 1) && !bar_wait(&acc_full[s], slots.use[s] & 1u, kTimeoutNs, &abort_s)) ok = 0;
-            if (!__shfl_sync(0xffffffffu, ok, 0)) {
+            bool ok = true;
+            if (m & 1) ok = warp_wait(&acc_full[0], slots.use[0] & 1u, &abort_s);
+            if ((m & 2) && ok) ok = warp_wait(&acc_full[1], slots.use[1] & 1u, &abort_s);
+            if (!ok) {
                 fail(a, &abort_s);
                 break;
             }
             fence_after_sync();
-            const float alpha = a.alpha ? __ldg(a.alpha + ti.g) : 1.0f;
+            // 16-column pieces 2 p + half of the tile's rows, up to 8 of them, kept in the output's type
+            constexpr int kPieces = (NT + 31) / 32;
+            constexpr int kRegs = sizeof(TY) == 2 ? 8 : 16;
+            const uint32_t src = trow + (m == 2 ? 128u : 0u) + 16 * half;
             const int64_t col = (int64_t)ti.wt * 128 + 32 * q + lane;
-            const uint32_t src = trow + (m == 2 ? 128u : 0u);
-            for (int c0 = 0; c0 < ti.n; c0 += 16) {
-                uint32_t v[16];
-                tmem_ld16(src + c0, v);
-                tmem_ld_wait();
-                if (col < a.w_rows) {
+            TY* const y = static_cast<TY*>(a.y) + (ti.row0 + 16 * half) * a.y_ld + col;
+            const int left = ti.n - 16 * half;  // rows from this warp's first on
+            const bool in = col < a.w_rows;
+            constexpr int kBatch = sizeof(TY) == 2 ? kPieces : (kPieces > 4 ? 4 : kPieces);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c0 + j < ti.n) {
-                            const float f = __uint_as_float(v[j]) * alpha;
-                            const int64_t at = (ti.row0 + c0 + j) * a.y_ld + col;
-                            if (a.y_f32) static_cast<float*>(a.y)[at] = f;
-                            else static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(f);
+            for (int p0 = 0; p0 < kPieces; p0 += kBatch) {
+                uint32_t v[kBatch][kRegs];
+#pragma unroll
+                for (int p = 0; p < kBatch; ++p)
+                    if (32 * (p0 + p) < left) {
+                        uint32_t raw[16];
+                        tmem_ld16(src + 32 * (p0 + p), raw);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < kRegs; ++j) {
+                            if constexpr (sizeof(TY) == 2)
+                                v[p][j] = pack_bf16(__uint_as_float(raw[2 * j]) * alpha, __uint_as_float(raw[2 * j + 1]) * alpha);
+                            else
+                                v[p][j] = __float_as_uint(__uint_as_float(raw[j]) * alpha);
                         }
+                    }
+                if (p0 + kBatch >= kPieces) {  // all read: the slots may be overwritten
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (m & 1) bar_arrive(&acc_empty[0]);
+                        if (m & 2) bar_arrive(&acc_empty[1]);
+                    }
+                }
+                if (in) {
+#pragma unroll
+                    for (int p = 0; p < kBatch; ++p) {
+                        TY* yp = y + (int64_t)(32 * (p0 + p)) * a.y_ld;
+                        const int rows = left - 32 * (p0 + p);
+                        if (rows >= 16) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j, yp += a.y_ld) put(yp, v[p], j);
+                        } else if (rows > 0) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j, yp += a.y_ld)
+                                if (j < rows) put(yp, v[p], j);
+                        }
+                    }
                 }
                 __syncwarp();
             }
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                for (int s = 0; s < 2; ++s)
-                    if (m >> s & 1) bar_arrive(&acc_empty[s]);
             slots.advance(m);
         }
     }
@@ -402,18 +518,24 @@ cudaError_t device_state(DeviceState& out) {
     return cudaSuccess;
 }
 
-template <int FMT, int NT>
+template <int FMT, int NT, typename TY>
 cudaError_t launch_typed(ProductArgs& a, int sms, cudaStream_t st) {
     using C = Cfg<FMT, NT>;
     const int smem = C::kStages * C::kStage + 1024 + (a.offsets ? a.groups * 4 : 0);
-    cudaError_t e = smem_limit(reinterpret_cast<const void*>(product_kernel<FMT, NT>), smem);
+    cudaError_t e = smem_limit(reinterpret_cast<const void*>(product_kernel<FMT, NT, TY>), smem);
     if (e != cudaSuccess) return e;
     const int64_t row_tiles = a.offsets ? a.x_rows / NT + (a.groups < a.x_rows ? a.groups : a.x_rows)
                                         : (a.x_rows + NT - 1) / NT;
     const int64_t tiles = row_tiles * a.w_tiles;
-    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    product_kernel<FMT, NT><<<(unsigned)(tiles < sms ? tiles : sms), kThreads, smem, st>>>(a);
+    if (tiles > INT32_MAX || tiles / sms * a.steps > INT32_MAX / 2) return cudaErrorInvalidValue;
+    product_kernel<FMT, NT, TY><<<(unsigned)(tiles < sms ? tiles : sms), kThreads, smem, st>>>(a);
     return cudaGetLastError();
+}
+
+// few rows: a short row tile leaves shared memory for more steps in flight
+template <int FMT, typename TY>
+cudaError_t launch_rows(ProductArgs& a, int sms, cudaStream_t st) {
+    return a.x_rows <= 64 ? launch_typed<FMT, 64, TY>(a, sms, st) : launch_typed<FMT, 256, TY>(a, sms, st);
 }
 
 }  // namespace
@@ -441,13 +563,12 @@ cudaError_t launch_mx_product(const moe_mx& x, const moe_mx& w, const int32_t* o
     a.groups = w.groups;
     a.steps = (int)mx_col_tiles(x.cols);
     a.w_tiles = (int)((w.rows + kMxTileRows - 1) / kMxTileRows);
-    a.y_f32 = y_type == MOE_F32;
     a.status = ds.dev;
-    // few rows: a short row tile leaves shared memory for more steps in flight
-    const bool few = x.rows <= 64;
     if (x.format == MOE_MX_E8M0)
-        return few ? launch_typed<MOE_MX_E8M0, 64>(a, ds.sms, st) : launch_typed<MOE_MX_E8M0, 256>(a, ds.sms, st);
-    return few ? launch_typed<MOE_MX_E4M3, 64>(a, ds.sms, st) : launch_typed<MOE_MX_E4M3, 256>(a, ds.sms, st);
+        return y_type == MOE_F32 ? launch_rows<MOE_MX_E8M0, float>(a, ds.sms, st)
+                                 : launch_rows<MOE_MX_E8M0, __nv_bfloat16>(a, ds.sms, st);
+    return y_type == MOE_F32 ? launch_rows<MOE_MX_E4M3, float>(a, ds.sms, st)
+                             : launch_rows<MOE_MX_E4M3, __nv_bfloat16>(a, ds.sms, st);
 }
 
 }  // namespace moe
