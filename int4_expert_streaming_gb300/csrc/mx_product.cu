@@ -18,7 +18,7 @@
 // against 512 cycles of MMA in the largest step.
 //
 // Warp roles of a persistent CTA (one per SM):
-//   warp 0      copies, kStages steps ahead; each lane issues one of a step's
+//   warp 0      one thread issues the copies, kStages steps ahead
 //   warp 1      one thread issues MMAs and commits
 //   warps 2-5   scales: shared memory -> tensor memory, lane quarter w % 4
 //   warps 6-13  epilogue: tensor memory -> registers -> y; lane quarter w % 4,
@@ -44,11 +44,11 @@ using namespace umma;
 using namespace gemmc;
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kScaleWarp0 = 2, kEpiWarp0 = 6, kEpiWarps = 8;
+constexpr int kEpiWarp0 = 6, kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kPer = (1024 + kThreads - 1) / kThreads;  // groups per thread
 constexpr int kTileRing = 16;  // rows of the tiles between the copies and the MMAs: more than kStages
 constexpr int kTmemCols = 512;
-constexpr int kScaleBufs = 4;    // steps whose scales are in tensor memory at a time
 constexpr int kScaleCol = 256;   // first scale column, behind the accumulators
 constexpr unsigned long long kTimeoutNs = 1000000000ull;
 
@@ -77,8 +77,10 @@ struct Cfg {
     // scale columns of a step: kAtoms x 4 for w, then kAtoms x (4 per 128 rows) for x
     static constexpr int kWCols = kAtoms * 4, kXCols = kAtoms * 4 * kXTiles;
     static constexpr int kStepCols = kWCols + kXCols;
+    // steps whose scales are in tensor memory at a time: no more than stages
+    static constexpr int kScaleBufs = NT <= 128 ? 7 : 4;
     static_assert(kScaleCol + kScaleBufs * kStepCols <= kTmemCols, "tensor memory");
-    static_assert(kStages >= 4, "shared memory");
+    static_assert(kStages >= kScaleBufs, "shared memory");
 };
 
 // 16 or 8 consecutive columns of the warp's lane quarter
@@ -118,22 +120,49 @@ __device__ __forceinline__ uint32_t idesc_mx(int N, uint32_t id) {
     return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((FMT == MOE_MX_E8M0 ? 1u : 0u) << 23) |
            (1u << 27) | (id << 29);
 }
+// The issuing instructions below take effect in the one thread whose `on` is
+// set.  They are predicated rather than branched around: the warp stays
+// converged, so their operands are uniform registers computed once for all.
+
 // D (+)= A * B^T, the descriptors given as low words and one high word
 template <int FMT>
-__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t alo, uint32_t blo, uint32_t dhi, uint32_t idesc, uint32_t sa,
-                                       uint32_t sb, uint32_t accumulate) {
+__device__ __forceinline__ void mma_mx(uint32_t on, uint32_t d, uint32_t alo, uint32_t blo, uint32_t dhi, uint32_t idesc,
+                                       uint32_t sa, uint32_t sb, uint32_t accumulate) {
     if (FMT == MOE_MX_E8M0)
         asm volatile(
-            "{\n .reg .pred p;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n setp.ne.b32 p, %7, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], ad, bd, %4, [%5], [%6], p;\n}" ::"r"(d),
-            "r"(alo), "r"(blo), "r"(dhi), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            "{\n .reg .pred p, q;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n"
+            " setp.ne.b32 p, %7, 0;\n setp.ne.b32 q, %8, 0;\n"
+            " @q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], ad, bd, %4, [%5], [%6], p;\n}" ::"r"(d),
+            "r"(alo), "r"(blo), "r"(dhi), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(on)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n setp.ne.b32 p, %7, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], ad, bd, %4, [%5], [%6], p;\n}" ::"r"(d),
-            "r"(alo), "r"(blo), "r"(dhi), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            "{\n .reg .pred p, q;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n"
+            " setp.ne.b32 p, %7, 0;\n setp.ne.b32 q, %8, 0;\n"
+            " @q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], ad, bd, %4, [%5], [%6], p;\n}" ::"r"(d),
+            "r"(alo), "r"(blo), "r"(dhi), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(on)
             : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+        "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void expect_if(uint32_t on, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n .reg .pred q;\n .reg .b64 st;\n setp.ne.b32 q, %2, 0;\n"
+        " @q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 st, [%0], %1;\n}" ::"r"(bar),
+        "r"(bytes), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void copy_if(uint32_t on, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %4, 0;\n"
+        " @q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "r"(on)
+        : "memory");
 }
 
 __device__ __forceinline__ void fail(const ProductArgs& a, volatile int* abort) {
@@ -155,7 +184,7 @@ struct Tile {
 // tile t, by a whole warp: row tile t / w_tiles, found in the groups' running
 // counts (the last g with cum[g] <= it) by two ballots, and w row tile t % w_tiles
 template <int NT>
-__device__ __forceinline__ Tile find_tile(const ProductArgs& a, const int* cum, int t, int lane) {
+__device__ __forceinline__ Tile find_tile(const ProductArgs& a, const int* cum, const int* offs, int t, int lane) {
     Tile ti;
     int q = t / a.w_tiles;
     ti.wt = t - q * a.w_tiles;
@@ -167,7 +196,7 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs& a, const int* cum, 
         const int i = blk + lane;
         ti.g = blk + __popc(__ballot_sync(kAll, i < a.groups && cum[min(i, a.groups - 1)] <= q)) - 1;
         q -= cum[ti.g];
-        const int o0 = __ldg(a.offsets + ti.g), o1 = __ldg(a.offsets + ti.g + 1);
+        const int o0 = offs[ti.g], o1 = offs[ti.g + 1];
         o = o0;
         n = o1 - o0;
         ti.xt = (o0 >> 7) + ti.g;
@@ -206,7 +235,7 @@ template <int FMT, int NT, typename TY>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs a) {
     using C = Cfg<FMT, NT>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], scales_full[kScaleBufs], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], scales_full[C::kScaleBufs], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tmem_s;
     __shared__ volatile int abort_s, never_s;
     __shared__ int warp_sum[kThreads / 32], tile_n[kTileRing];
@@ -214,13 +243,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     int* cum = reinterpret_cast<int*>(smem_raw + (smem0 - smem_u32(smem_raw)) + C::kStages * C::kStage);
+    int* offs = cum + a.groups;
 
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             bar_init(&full[s], 1);
             bar_init(&empty[s], 1);
         }
-        for (int s = 0; s < kScaleBufs; ++s) bar_init(&scales_full[s], 4);
+        for (int s = 0; s < C::kScaleBufs; ++s) bar_init(&scales_full[s], 4);
         for (int s = 0; s < 2; ++s) {
             bar_init(&acc_full[s], 1);
             bar_init(&acc_empty[s], kEpiWarps);
@@ -233,15 +263,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     if (warp == 1) tmem_alloc(&tmem_s, kTmemCols);
     int row_tiles;
     if (a.offsets) {
-        // running counts of the groups' row tiles
+        // running counts of the groups' row tiles; a thread has at most kPer groups
         const int per = (a.groups + kThreads - 1) / kThreads;
-        const int g0 = tid * per, g1 = min(g0 + per, a.groups);
-        int sum = 0;
-        for (int g = g0; g < g1; ++g) sum += (a.offsets[g + 1] - a.offsets[g] + NT - 1) / NT;
+        const int g0 = tid * per;
+        int first[kPer + 1], sum = 0;
+#pragma unroll
+        for (int j = 0; j <= kPer; ++j)
+            if (j <= per) first[j] = __ldg(a.offsets + min(g0 + j, a.groups));
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (j < per) sum += (first[j + 1] - first[j] + NT - 1) / NT;
         int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            const int v = __shfl_up_sync(kAll, incl, o);
             if (lane >= o) incl += v;
         }
         if (lane == 31) warp_sum[warp] = incl;
@@ -252,10 +287,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             if (w < warp) at += warp_sum[w];
             row_tiles += warp_sum[w];
         }
-        for (int g = g0; g < g1; ++g) {
-            cum[g] = at;
-            at += (a.offsets[g + 1] - a.offsets[g] + NT - 1) / NT;
-        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (j < per && g0 + j < a.groups) {
+                cum[g0 + j] = at;
+                offs[g0 + j] = first[j];
+                at += (first[j + 1] - first[j] + NT - 1) / NT;
+                if (g0 + j == a.groups - 1) offs[a.groups] = first[j + 1];
+            }
     } else {
         row_tiles = (int)((a.x_rows + NT - 1) / NT);
     }
@@ -268,39 +307,36 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
 
     if (warp == 0) {
         // ---------------------------------------------------------------- copies
+        const uint32_t leader = elect_one(), full0 = smem_u32(full);
         uint32_t s = 0, ph = 1, filled = 0;  // stage, parity of its release, steps begun
         bool ok = true;
         for (int i = 0; i < my_tiles && ok; ++i) {
-            const Tile ti = find_tile<NT>(a, cum, (int)blockIdx.x + i * (int)gridDim.x, lane);
+            const Tile ti = find_tile<NT>(a, cum, offs, (int)blockIdx.x + i * (int)gridDim.x, lane);
             const int n0 = min(ti.n, 128), n1 = ti.n - n0;
-            // lane 0: the w tile; 1, 2: codes and scales of the first x row tile; 3, 4: of the second
             const uint32_t b0 = (uint32_t)((n0 + 7) & ~7) * 128u, b1 = (uint32_t)((n1 + 7) & ~7) * 128u;
             const uint32_t total = C::kTile + b0 + b1 + (n1 > 0 ? 2u : 1u) * C::kScaleBytes;
-            const uint8_t* src;
-            uint32_t dst, bytes;
-            if (lane == 0) {
-                src = a.w + ((int64_t)ti.g * a.w_tiles + ti.wt) * a.steps * C::kTile;
-                dst = 0;
-                bytes = C::kTile;
-            } else {
-                const int second = (lane - 1) >> 1, scales = (lane - 1) & 1;
-                src = a.x + (ti.xt + second) * a.steps * C::kTile + scales * kMxCodeBytes;
-                dst = scales ? C::kOffXs + second * C::kScaleBytes : C::kOffX + second * kMxCodeBytes;
-                bytes = second && n1 <= 0 ? 0u : scales ? C::kScaleBytes : second ? b1 : b0;
-                if (lane > 4 || (NT <= 128 && lane > 2)) bytes = 0;
-            }
+            const uint8_t* wp = a.w + ((int64_t)ti.g * a.w_tiles + ti.wt) * a.steps * C::kTile;
+            const uint8_t* x0 = a.x + ti.xt * a.steps * C::kTile;
+            const uint8_t* x1 = x0 + (int64_t)a.steps * C::kTile;
             if (lane == 0) tile_n[i % kTileRing] = ti.n;
-            dst += smem0;
             for (int k = 0; k < a.steps; ++k) {
                 if (!warp_wait(&empty[s], ph, &abort_s)) {
                     fail(a, &abort_s);
                     ok = false;
                     break;
                 }
-                if (lane == 0) bar_arrive_expect_tx(&full[s], total);
-                __syncwarp();
-                if (bytes) bulk_g2s(dst + s * C::kStage, src, bytes, &full[s]);
-                src += C::kTile;
+                const uint32_t st = smem0 + s * C::kStage, bar = full0 + 8 * s;
+                expect_if(leader, bar, total);
+                copy_if(leader, st, wp, C::kTile, bar);
+                copy_if(leader, st + C::kOffX, x0, b0, bar);
+                copy_if(leader, st + C::kOffXs, x0 + kMxCodeBytes, C::kScaleBytes, bar);
+                if (NT > 128 && n1 > 0) {
+                    copy_if(leader, st + C::kOffX + kMxCodeBytes, x1, b1, bar);
+                    copy_if(leader, st + C::kOffXs + C::kScaleBytes, x1 + kMxCodeBytes, C::kScaleBytes, bar);
+                }
+                wp += C::kTile;
+                x0 += C::kTile;
+                x1 += C::kTile;
                 ++filled;
                 if (++s == C::kStages) s = 0, ph ^= 1;
             }
@@ -311,16 +347,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA
-        const bool leader = elect_one();
-        uint32_t s = 0, ph = 0, buf = 0, bph = 0;
+        const uint32_t leader = elect_one();
+        uint32_t s = 0, buf = 0, bph = 0;
         Slots slots;
         bool ok = true;
         const uint32_t dhi = (uint32_t)(sdesc(smem0) >> 32);  // the same for every operand tile
-        const uint32_t w_lo = (uint32_t)sdesc(smem0), x_lo = (uint32_t)sdesc(smem0 + C::kOffX);
+        const uint32_t w_lo = (uint32_t)sdesc(smem0), empty0 = smem_u32(empty), acc0 = smem_u32(acc_full);
+        uint32_t wd = w_lo, sc = tmem + kScaleCol;
         for (int i = 0; i < my_tiles && ok; ++i) {
             uint32_t d = 0, idesc = 0, m = 0;
             for (int k = 0; k < a.steps; ++k) {
-                ok = warp_wait(&full[s], ph, &abort_s) && warp_wait(&scales_full[buf], bph, &abort_s);
+                // the scales' warps have seen the step's copies land before they arrive here
+                ok = warp_wait(&scales_full[buf], bph, &abort_s);
                 if (k == 0 && ok) {
                     const int n = tile_n[i % kTileRing];
                     m = slots.mask(n);
@@ -334,29 +372,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                     break;
                 }
                 fence_after_sync();
-                if (leader) {
-                    const uint32_t wd = w_lo + s * (C::kStage >> 4), xd = x_lo + s * (C::kStage >> 4);
-                    const uint32_t sc = tmem + kScaleCol + buf * C::kStepCols;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        // a column holds the scales of 64 (e4m3) or 128 (e8m0) matrix columns
-                        const int atom = FMT == MOE_MX_E8M0 ? q >> 1 : q;
-                        const uint32_t id = FMT == MOE_MX_E8M0 ? (q & 1) * 2 : 0;
-                        mma_mx<FMT>(d, wd + 2 * q, xd + 2 * q, dhi, idesc | id << 4 | id << 29, sc + 4 * atom,
-                                    sc + C::kWCols + atom * 4 * C::kXTiles, q ? 1u : (uint32_t)k);
-                    }
-                    mma_commit(&empty[s]);
+                for (int q = 0; q < 4; ++q) {
+                    // a column holds the scales of 64 (e4m3) or 128 (e8m0) matrix columns
+                    const int atom = FMT == MOE_MX_E8M0 ? q >> 1 : q;
+                    const uint32_t id = FMT == MOE_MX_E8M0 ? (q & 1) * 2 : 0;
+                    mma_mx<FMT>(leader, d, wd + 2 * q, wd + (C::kOffX >> 4) + 2 * q, dhi, idesc | id << 4 | id << 29,
+                                sc + 4 * atom, sc + C::kWCols + atom * 4 * C::kXTiles, q ? 1u : (uint32_t)k);
                 }
-                __syncwarp();
-                if (++s == C::kStages) s = 0, ph ^= 1;
-                if (++buf == kScaleBufs) buf = 0, bph ^= 1;
+                commit_if(leader, empty0 + 8 * s);
+                wd += C::kStage >> 4;
+                sc += C::kStepCols;
+                if (++s == C::kStages) s = 0, wd = w_lo;
+                if (++buf == C::kScaleBufs) buf = 0, bph ^= 1, sc = tmem + kScaleCol;
             }
             if (!ok) break;
-            if (leader) {
-                if (m & 1) mma_commit(&acc_full[0]);
-                if (m & 2) mma_commit(&acc_full[1]);
-            }
-            __syncwarp();
+            if (m & 1) commit_if(leader, acc0);
+            if (m & 2) commit_if(leader, acc0 + 8);
             slots.advance(m);
         }
         // everything issued above has completed once this commit arrives
@@ -389,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                     xv[c] = u.x, xv[c + 1] = u.y, xv[c + 2] = u.z, xv[c + 3] = u.w;
                 }
             }
-            if (it >= kScaleBufs) {
+            if (it >= C::kScaleBufs) {
                 if (!warp_wait(&empty[fs], fph, &abort_s)) {
                     fail(a, &abort_s);
                     break;
@@ -405,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             __syncwarp();
             if (lane == 0) bar_arrive(&scales_full[buf]);
             if (++s == C::kStages) s = 0, ph ^= 1;
-            if (++buf == kScaleBufs) buf = 0;
+            if (++buf == C::kScaleBufs) buf = 0;
         }
     } else {
         // ------------------------------------------------------------- epilogue
@@ -413,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
         Slots slots;
         for (int i = 0; i < my_tiles; ++i) {
-            const Tile ti = find_tile<NT>(a, cum, (int)blockIdx.x + i * (int)gridDim.x, lane);
+            const Tile ti = find_tile<NT>(a, cum, offs, (int)blockIdx.x + i * (int)gridDim.x, lane);
             const float alpha = a.alpha ? __ldg(a.alpha + ti.g) : 1.0f;
             const uint32_t m = slots.mask(ti.n);
             bool ok = true;
@@ -521,7 +553,7 @@ cudaError_t device_state(DeviceState& out) {
 template <int FMT, int NT, typename TY>
 cudaError_t launch_typed(ProductArgs& a, int sms, cudaStream_t st) {
     using C = Cfg<FMT, NT>;
-    const int smem = C::kStages * C::kStage + 1024 + (a.offsets ? a.groups * 4 : 0);
+    const int smem = C::kStages * C::kStage + 1024 + (a.offsets ? a.groups * 8 + 4 : 0);
     cudaError_t e = smem_limit(reinterpret_cast<const void*>(product_kernel<FMT, NT, TY>), smem);
     if (e != cudaSuccess) return e;
     const int64_t row_tiles = a.offsets ? a.x_rows / NT + (a.groups < a.x_rows ? a.groups : a.x_rows)
