@@ -59,29 +59,63 @@ struct ProductArgs {
     const float* alpha;
     void* y;
     int64_t y_ld, x_rows, w_rows;
-    int groups, steps, w_tiles;  // steps: column tiles; w_tiles: row tiles of one group of w
+    int groups, steps, w_tiles, w_units;  // steps: column tiles; w_tiles: row tiles of one group of w; w_units: tiles or pairs
     int* status;
 };
 
+// NT = 256: a pair of CTAs (M = 256); NT = 64: one CTA
 template <int FMT, int NT>
 struct Cfg {
+    static constexpr bool kPair = NT == 256;
     static constexpr int kAtoms = FMT == MOE_MX_E8M0 ? 2 : 4;  // scale atoms of a 128 x 256 tile
     static constexpr int kScaleBytes = kAtoms * kMxAtomBytes;
     static constexpr int kTile = kMxCodeBytes + kScaleBytes;
     static constexpr int kXTiles = (NT + 127) / 128;
-    // stage: w tile (codes, scales), x codes, x scales, each part 1024-byte aligned
+    // stage: w tile (codes, scales), x codes (half of the rows in each CTA of a pair), x scales; 1024-byte aligned parts
     static constexpr int kOffX = (kTile + 1023) / 1024 * 1024;
-    static constexpr int kOffXs = kOffX + NT * 128;
+    static constexpr int kOffXs = kOffX + (kPair ? NT / 2 : NT) * 128;
     static constexpr int kStage = (kOffXs + kXTiles * kScaleBytes + 1023) / 1024 * 1024;
-    static constexpr int kStages = (222 * 1024 / kStage) < 8 ? (222 * 1024 / kStage) : 8;
+    static constexpr int kStages = (220 * 1024 / kStage) < 7 ? (220 * 1024 / kStage) : 7;
     // scale columns of a step: kAtoms x 4 for w, then kAtoms x (4 per 128 rows) for x
     static constexpr int kWCols = kAtoms * 4, kXCols = kAtoms * 4 * kXTiles;
     static constexpr int kStepCols = kWCols + kXCols;
-    // steps whose scales are in tensor memory at a time: no more than stages
-    static constexpr int kScaleBufs = NT <= 128 ? 7 : 4;
-    static_assert(kScaleCol + kScaleBufs * kStepCols <= kTmemCols, "tensor memory");
-    static_assert(kStages >= kScaleBufs, "shared memory");
+    static_assert(kScaleCol + kStages * kStepCols <= kTmemCols, "tensor memory");
 };
+
+// ---------------------------------------------------------------------------
+// forms for one CTA and for a pair
+// ---------------------------------------------------------------------------
+template <bool PAIR>
+__device__ __forceinline__ void alloc_columns(uint32_t* dst, uint32_t ncols) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(dst, ncols);
+    }
+}
+template <bool PAIR>
+__device__ __forceinline__ void free_columns(uint32_t taddr, uint32_t ncols) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+    else
+        tmem_dealloc(taddr, ncols);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the same shared-memory offset in CTA 0 of the pair
+__device__ __forceinline__ uint32_t leader_addr(uint32_t saddr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(saddr));
+    return r;
+}
 
 // 16 or 8 consecutive columns of the warp's lane quarter
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -116,19 +150,33 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // instruction descriptor of the block-scaled kinds: e2m1 A and B, fp32 D, both
 // K-major; scale type e8m0 or e4m3; `id`: first scale byte used of a column
 template <int FMT>
-__device__ __forceinline__ uint32_t idesc_mx(int N, uint32_t id) {
+__device__ __forceinline__ uint32_t idesc_mx(int M, int N, uint32_t id) {
     return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((FMT == MOE_MX_E8M0 ? 1u : 0u) << 23) |
-           (1u << 27) | (id << 29);
+           ((uint32_t)(M >> 7) << 27) | (id << 29);
 }
 // The issuing instructions below take effect in the one thread whose `on` is
 // set.  They are predicated rather than branched around: the warp stays
 // converged, so their operands are uniform registers computed once for all.
 
 // D (+)= A * B^T, the descriptors given as low words and one high word
-template <int FMT>
+template <int FMT, bool PAIR>
 __device__ __forceinline__ void mma_mx(uint32_t on, uint32_t d, uint32_t alo, uint32_t blo, uint32_t dhi, uint32_t idesc,
                                        uint32_t sa, uint32_t sb, uint32_t accumulate) {
-    if (FMT == MOE_MX_E8M0)
+    if constexpr (PAIR && FMT == MOE_MX_E8M0)
+        asm volatile(
+            "{\n .reg .pred p, q;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n"
+            " setp.ne.b32 p, %7, 0;\n setp.ne.b32 q, %8, 0;\n"
+            " @q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], ad, bd, %4, [%5], [%6], p;\n}" ::"r"(d),
+            "r"(alo), "r"(blo), "r"(dhi), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(on)
+            : "memory");
+    else if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred p, q;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n"
+            " setp.ne.b32 p, %7, 0;\n setp.ne.b32 q, %8, 0;\n"
+            " @q tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], ad, bd, %4, [%5], [%6], p;\n}" ::"r"(d),
+            "r"(alo), "r"(blo), "r"(dhi), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(on)
+            : "memory");
+    else if constexpr (FMT == MOE_MX_E8M0)
         asm volatile(
             "{\n .reg .pred p, q;\n .reg .b64 ad, bd;\n mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n"
             " setp.ne.b32 p, %7, 0;\n setp.ne.b32 q, %8, 0;\n"
@@ -143,12 +191,22 @@ __device__ __forceinline__ void mma_mx(uint32_t on, uint32_t d, uint32_t alo, ui
             "r"(alo), "r"(blo), "r"(dhi), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(on)
             : "memory");
 }
+// arrive, in both CTAs of a pair, once every MMA issued so far by this thread has completed
+template <bool PAIR>
 __device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
-        "r"(on)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred q;\n .reg .b16 both;\n setp.ne.b32 q, %1, 0;\n mov.b16 both, 3;\n"
+            " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n}" ::"r"(
+                bar),
+            "r"(on)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+            " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+            "r"(on)
+            : "memory");
 }
 __device__ __forceinline__ void expect_if(uint32_t on, uint32_t bar, uint32_t bytes) {
     asm volatile(
@@ -169,25 +227,46 @@ __device__ __forceinline__ void fail(const ProductArgs& a, volatile int* abort) 
     *abort = 1;
     *(volatile int*)a.status = 1;
 }
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// arrival on a barrier of another CTA of the cluster
+__device__ __forceinline__ void remote_arrive_relaxed(uint32_t addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
 // bounded wait of a whole warp, the same answer in every lane
 __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
     if (__all_sync(kAll, bar_try_wait(b, parity))) return true;
     return __all_sync(kAll, bar_wait(b, parity, kTimeoutNs, abort));
 }
+// the same on a barrier that the other CTA of a pair arrives on too
+template <bool PAIR>
+__device__ __forceinline__ bool pair_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+    const bool ok = warp_wait(b, parity, abort);
+    if (PAIR) try_wait_cluster(b, parity);  // complete: orders what follows after the other CTA's arrival
+    return ok;
+}
 
 struct Tile {
-    int g, n, wt;  // group, rows, w row tile
+    int g, n, wt;  // group, rows, w row tile (a pair: the first of two)
     int64_t row0;  // first row of x and y
     int64_t xt;    // first x row tile
 };
 
-// tile t, by a whole warp: row tile t / w_tiles, found in the groups' running
-// counts (the last g with cum[g] <= it) by two ballots, and w row tile t % w_tiles
+// tile t, by a whole warp: row tile t / w_units, found in the groups' running
+// counts (the last g with cum[g] <= it) by two ballots, and w row tile (or pair
+// of them) t % w_units
 template <int NT>
 __device__ __forceinline__ Tile find_tile(const ProductArgs& a, const int* cum, const int* offs, int t, int lane) {
     Tile ti;
-    int q = t / a.w_tiles;
-    ti.wt = t - q * a.w_tiles;
+    int q = t / a.w_units;
+    ti.wt = (t - q * a.w_units) * (NT == 256 ? 2 : 1);
     ti.g = 0;
     int64_t o = 0, n = a.x_rows;
     ti.xt = 0;
@@ -234,8 +313,9 @@ struct Slots {
 template <int FMT, int NT, typename TY>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs a) {
     using C = Cfg<FMT, NT>;
+    constexpr bool PAIR = C::kPair;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], scales_full[C::kScaleBufs], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], scales_full[C::kStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tmem_s;
     __shared__ volatile int abort_s, never_s;
     __shared__ int warp_sum[kThreads / 32], tile_n[kTileRing];
@@ -245,22 +325,25 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     int* cum = reinterpret_cast<int*>(smem_raw + (smem0 - smem_u32(smem_raw)) + C::kStages * C::kStage);
     int* offs = cum + a.groups;
 
+    const uint32_t rank = PAIR ? cluster_rank() : 0;  // CTA 0 issues a pair's MMAs
+
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             bar_init(&full[s], 1);
             bar_init(&empty[s], 1);
         }
-        for (int s = 0; s < C::kScaleBufs; ++s) bar_init(&scales_full[s], 4);
+        // the four scale warps, and in CTA 0 of a pair CTA 1's forwarded
+        for (int s = 0; s < C::kStages; ++s) bar_init(&scales_full[s], PAIR && rank == 0 ? 5 : 4);
         for (int s = 0; s < 2; ++s) {
             bar_init(&acc_full[s], 1);
-            bar_init(&acc_empty[s], kEpiWarps);
+            bar_init(&acc_empty[s], PAIR ? 2 * kEpiWarps : kEpiWarps);
         }
         bar_init(&drain, 1);
         abort_s = 0;
         never_s = 0;
         fence_barrier_init();
     }
-    if (warp == 1) tmem_alloc(&tmem_s, kTmemCols);
+    if (warp == 1) alloc_columns<PAIR>(&tmem_s, kTmemCols);
     int row_tiles;
     if (a.offsets) {
         // running counts of the groups' row tiles; a thread has at most kPer groups
@@ -298,12 +381,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     } else {
         row_tiles = (int)((a.x_rows + NT - 1) / NT);
     }
-    const int n_tiles = row_tiles * a.w_tiles;
+    const int n_tiles = row_tiles * a.w_units;
     fence_before_sync();
-    __syncthreads();
+    if (PAIR) cluster_sync();  // the barriers of both CTAs are ready
+    else __syncthreads();
     fence_after_sync();
     const uint32_t tmem = tmem_s;
-    const int my_tiles = (n_tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // <= 0: none
+    const int unit = (int)blockIdx.x / (PAIR ? 2 : 1), units = (int)gridDim.x / (PAIR ? 2 : 1);
+    const int my_tiles = (n_tiles - unit + units - 1) / units;  // <= 0: none
+
+    // Arrival at the CTA that issues the MMAs.  From CTA 1 it is relaxed: what it announces are accesses to tensor
+    // memory, which the fences before and after it order, and copies that have already landed in shared memory.  A
+    // release at cluster scope would also wait for this SM's stores of y (1800 cycles a step measured).
+    auto arrive_at_leader = [&](uint64_t* b) {
+        if (PAIR && rank == 1) remote_arrive_relaxed(leader_addr(smem_u32(b)));
+        else bar_arrive(b);
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- copies
@@ -311,14 +404,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         uint32_t s = 0, ph = 1, filled = 0;  // stage, parity of its release, steps begun
         bool ok = true;
         for (int i = 0; i < my_tiles && ok; ++i) {
-            const Tile ti = find_tile<NT>(a, cum, offs, (int)blockIdx.x + i * (int)gridDim.x, lane);
-            const int n0 = min(ti.n, 128), n1 = ti.n - n0;
-            const uint32_t b0 = (uint32_t)((n0 + 7) & ~7) * 128u, b1 = (uint32_t)((n1 + 7) & ~7) * 128u;
-            const uint32_t total = C::kTile + b0 + b1 + (n1 > 0 ? 2u : 1u) * C::kScaleBytes;
-            const uint8_t* wp = a.w + ((int64_t)ti.g * a.w_tiles + ti.wt) * a.steps * C::kTile;
+            const Tile ti = find_tile<NT>(a, cum, offs, unit + i * units, lane);
+            // this CTA's rows of x: all, or its half of the MMA's N; r0 .. r1 may lie in two row tiles
+            const int n8 = (ti.n + 7) & ~7, half = PAIR ? ((ti.n + 31) & ~31) / 2 : 0;
+            const int r0 = (int)rank * half, r1 = PAIR && rank == 0 ? min(half, n8) : n8;
+            const uint32_t b0 = (uint32_t)max(min(r1, 128) - r0, 0) * 128u, b1 = (uint32_t)max(r1 - max(r0, 128), 0) * 128u;
+            const uint32_t total = C::kTile + b0 + b1 + (ti.n > 128 ? 2u : 1u) * C::kScaleBytes;
+            const int wt = min(ti.wt + (int)rank, a.w_tiles - 1);  // an odd last tile: CTA 1 repeats it, and stores nothing
+            const uint8_t* wp = a.w + ((int64_t)ti.g * a.w_tiles + wt) * a.steps * C::kTile;
             const uint8_t* x0 = a.x + ti.xt * a.steps * C::kTile;
             const uint8_t* x1 = x0 + (int64_t)a.steps * C::kTile;
-            if (lane == 0) tile_n[i % kTileRing] = ti.n;
+            if (leader) tile_n[i % kTileRing] = ti.n;
             for (int k = 0; k < a.steps; ++k) {
                 if (!warp_wait(&empty[s], ph, &abort_s)) {
                     fail(a, &abort_s);
@@ -328,10 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                 const uint32_t st = smem0 + s * C::kStage, bar = full0 + 8 * s;
                 expect_if(leader, bar, total);
                 copy_if(leader, st, wp, C::kTile, bar);
-                copy_if(leader, st + C::kOffX, x0, b0, bar);
+                if (!PAIR || b0) copy_if(leader, st + C::kOffX, x0 + r0 * 128, b0, bar);
                 copy_if(leader, st + C::kOffXs, x0 + kMxCodeBytes, C::kScaleBytes, bar);
-                if (NT > 128 && n1 > 0) {
-                    copy_if(leader, st + C::kOffX + kMxCodeBytes, x1, b1, bar);
+                if (PAIR && ti.n > 128) {
+                    if (b1) copy_if(leader, st + C::kOffX + b0, x1 + max(r0 - 128, 0) * 128, b1, bar);
                     copy_if(leader, st + C::kOffXs + C::kScaleBytes, x1 + kMxCodeBytes, C::kScaleBytes, bar);
                 }
                 wp += C::kTile;
@@ -345,10 +441,24 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         for (uint32_t i = filled > C::kStages ? filled - C::kStages : 0; i < filled; ++i)
             bar_wait(&full[i % C::kStages], (i / C::kStages) & 1u, kTimeoutNs, &never_s);
         __syncwarp();
+    } else if (warp == 1 && rank == 1) {
+        // -------------- CTA 1 of a pair: forwards its scale warps' arrivals, and so spares them the remote access
+        uint32_t s = 0, ph = 0;
+        const int steps = my_tiles * a.steps;
+        for (int it = 0; it < steps; ++it) {
+            if (!warp_wait(&scales_full[s], ph, &abort_s)) {
+                fail(a, &abort_s);
+                break;
+            }
+            if (lane == 0) arrive_at_leader(&scales_full[s]);
+            __syncwarp();
+            if (++s == C::kStages) s = 0, ph ^= 1;
+        }
+        warp_wait(&drain, 0, &never_s);  // CTA 0's last arrival here
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA
         const uint32_t leader = elect_one();
-        uint32_t s = 0, buf = 0, bph = 0;
+        uint32_t s = 0, ph = 0;
         Slots slots;
         bool ok = true;
         const uint32_t dhi = (uint32_t)(sdesc(smem0) >> 32);  // the same for every operand tile
@@ -358,14 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             uint32_t d = 0, idesc = 0, m = 0;
             for (int k = 0; k < a.steps; ++k) {
                 // the scales' warps have seen the step's copies land before they arrive here
-                ok = warp_wait(&scales_full[buf], bph, &abort_s);
+                ok = pair_wait<PAIR>(&scales_full[s], ph, &abort_s);
                 if (k == 0 && ok) {
                     const int n = tile_n[i % kTileRing];
                     m = slots.mask(n);
-                    if (m & 1) ok = warp_wait(&acc_empty[0], (slots.use[0] & 1u) ^ 1u, &abort_s);
-                    if ((m & 2) && ok) ok = warp_wait(&acc_empty[1], (slots.use[1] & 1u) ^ 1u, &abort_s);
+                    if (m & 1) ok = pair_wait<PAIR>(&acc_empty[0], (slots.use[0] & 1u) ^ 1u, &abort_s);
+                    if ((m & 2) && ok) ok = pair_wait<PAIR>(&acc_empty[1], (slots.use[1] & 1u) ^ 1u, &abort_s);
                     d = tmem + (m == 2 ? 128u : 0u);
-                    idesc = idesc_mx<FMT>((n + 15) & ~15, 0);
+                    idesc = PAIR ? idesc_mx<FMT>(256, (n + 31) & ~31, 0) : idesc_mx<FMT>(128, (n + 15) & ~15, 0);
                 }
                 if (!ok) {
                     fail(a, &abort_s);
@@ -377,31 +487,26 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                     // a column holds the scales of 64 (e4m3) or 128 (e8m0) matrix columns
                     const int atom = FMT == MOE_MX_E8M0 ? q >> 1 : q;
                     const uint32_t id = FMT == MOE_MX_E8M0 ? (q & 1) * 2 : 0;
-                    mma_mx<FMT>(leader, d, wd + 2 * q, wd + (C::kOffX >> 4) + 2 * q, dhi, idesc | id << 4 | id << 29,
+                    mma_mx<FMT, PAIR>(leader, d, wd + 2 * q, wd + (C::kOffX >> 4) + 2 * q, dhi, idesc | id << 4 | id << 29,
                                 sc + 4 * atom, sc + C::kWCols + atom * 4 * C::kXTiles, q ? 1u : (uint32_t)k);
                 }
-                commit_if(leader, empty0 + 8 * s);
+                commit_if<PAIR>(leader, empty0 + 8 * s);
                 wd += C::kStage >> 4;
                 sc += C::kStepCols;
-                if (++s == C::kStages) s = 0, wd = w_lo;
-                if (++buf == C::kScaleBufs) buf = 0, bph ^= 1, sc = tmem + kScaleCol;
+                if (++s == C::kStages) s = 0, ph ^= 1, wd = w_lo, sc = tmem + kScaleCol;
             }
             if (!ok) break;
-            if (m & 1) commit_if(leader, acc0);
-            if (m & 2) commit_if(leader, acc0 + 8);
+            if (m & 1) commit_if<PAIR>(leader, acc0);
+            if (m & 2) commit_if<PAIR>(leader, acc0 + 8);
             slots.advance(m);
         }
         // everything issued above has completed once this commit arrives
-        if (leader) {
-            mma_commit(&drain);
-            if (!bar_wait(&drain, 0, kTimeoutNs, &never_s)) fail(a, &abort_s);
-        }
-        __syncwarp();
+        commit_if<PAIR>(leader, smem_u32(&drain));
+        if (!warp_wait(&drain, 0, &never_s)) fail(a, &abort_s);
     } else if (warp < kEpiWarp0) {
         // --------------------------------------------------------------- scales
         const uint32_t quarter = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        uint32_t s = 0, ph = 0, buf = 0;
-        uint32_t fs = 0, fph = 0;  // the step kScaleBufs back, whose MMAs read the buffer last
+        uint32_t s = 0, ph = 0;
         const int steps = my_tiles * a.steps;
         for (int it = 0; it < steps; ++it) {
             if (!warp_wait(&full[s], ph, &abort_s)) {
@@ -421,23 +526,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                     xv[c] = u.x, xv[c + 1] = u.y, xv[c + 2] = u.z, xv[c + 3] = u.w;
                 }
             }
-            if (it >= C::kScaleBufs) {
-                if (!warp_wait(&empty[fs], fph, &abort_s)) {
-                    fail(a, &abort_s);
-                    break;
-                }
-                if (++fs == C::kStages) fs = 0, fph ^= 1;
-                fence_after_sync();
-            }
-            const uint32_t sc = quarter + kScaleCol + buf * C::kStepCols;
+            // the MMAs that read this stage's columns last are done: the copies into the stage waited for them
+            fence_after_sync();
+            const uint32_t sc = quarter + kScaleCol + s * C::kStepCols;
             store_columns(sc, wv);
             store_columns(sc + C::kWCols, xv);
             tmem_st_wait();
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) bar_arrive(&scales_full[buf]);
+            if (lane == 0) bar_arrive(&scales_full[s]);
             if (++s == C::kStages) s = 0, ph ^= 1;
-            if (++buf == C::kScaleBufs) buf = 0;
         }
     } else {
         // ------------------------------------------------------------- epilogue
@@ -445,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
         Slots slots;
         for (int i = 0; i < my_tiles; ++i) {
-            const Tile ti = find_tile<NT>(a, cum, offs, (int)blockIdx.x + i * (int)gridDim.x, lane);
+            const Tile ti = find_tile<NT>(a, cum, offs, unit + i * units, lane);
             const float alpha = a.alpha ? __ldg(a.alpha + ti.g) : 1.0f;
             const uint32_t m = slots.mask(ti.n);
             bool ok = true;
@@ -460,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             constexpr int kPieces = (NT + 31) / 32;
             constexpr int kRegs = sizeof(TY) == 2 ? 8 : 16;
             const uint32_t src = trow + (m == 2 ? 128u : 0u) + 16 * half;
-            const int64_t col = (int64_t)ti.wt * 128 + 32 * q + lane;
+            const int64_t col = (int64_t)(ti.wt + (int)rank) * 128 + 32 * q + lane;
             TY* const y = static_cast<TY*>(a.y) + (ti.row0 + 16 * half) * a.y_ld + col;
             const int left = ti.n - 16 * half;  // rows from this warp's first on
             const bool in = col < a.w_rows;
@@ -486,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                     fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
-                        if (m & 1) bar_arrive(&acc_empty[0]);
-                        if (m & 2) bar_arrive(&acc_empty[1]);
+                        if (m & 1) arrive_at_leader(&acc_empty[0]);
+                        if (m & 2) arrive_at_leader(&acc_empty[1]);
                     }
                 }
                 if (in) {
@@ -512,9 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     }
 
     fence_before_sync();
-    __syncthreads();
+    if (PAIR) cluster_sync();  // nothing of the other CTA's is under way here any more
+    else __syncthreads();
     fence_after_sync();
-    if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+    if (warp == 1) free_columns<PAIR>(tmem, kTmemCols);
 }
 
 // The kernel's status word of each device, pinned and mapped, set up once.
@@ -558,9 +657,25 @@ cudaError_t launch_typed(ProductArgs& a, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t row_tiles = a.offsets ? a.x_rows / NT + (a.groups < a.x_rows ? a.groups : a.x_rows)
                                         : (a.x_rows + NT - 1) / NT;
-    const int64_t tiles = row_tiles * a.w_tiles;
-    if (tiles > INT32_MAX || tiles / sms * a.steps > INT32_MAX / 2) return cudaErrorInvalidValue;
-    product_kernel<FMT, NT, TY><<<(unsigned)(tiles < sms ? tiles : sms), kThreads, smem, st>>>(a);
+    a.w_units = C::kPair ? (a.w_tiles + 1) / 2 : a.w_tiles;
+    const int64_t tiles = row_tiles * a.w_units, units = C::kPair ? sms / 2 : sms;
+    if (tiles > INT32_MAX || tiles / units * a.steps > INT32_MAX / 2) return cudaErrorInvalidValue;
+    const unsigned n = (unsigned)(tiles < units ? tiles : units);
+    if constexpr (C::kPair) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = 2 * n;
+        cfg.blockDim = kThreads;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, product_kernel<FMT, NT, TY>, (const ProductArgs)a);
+    }
+    product_kernel<FMT, NT, TY><<<n, kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
