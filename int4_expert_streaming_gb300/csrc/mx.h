@@ -19,6 +19,35 @@ __host__ __device__ inline int mx_tile_bytes(int format) {
 }
 __host__ __device__ inline int64_t mx_col_tiles(int cols) { return (cols + kMxTileCols - 1) / kMxTileCols; }
 
+// Launches are programmatic dependents of the kernel before them on the
+// stream: a kernel's CTAs may be set up while that one still runs, and wait
+// (after_previous) before they touch memory; every thread that does so waits.
+// Memory is read by plain loads: the read-only path may not be used for data
+// that changes during the kernel's life.  let_next_start allows the same to the
+// kernel after it.  Between two small
+// kernels this hides most of the launch.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, unsigned cluster,
+                   const A&... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = threads;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Where the rows of a matrix stand: row tile and row within it.  Ragged
 // groups start at row tile offsets[g] / 128 + g: consecutive groups then never
 // overlap, because floor((o + n) / 128) + 1 - floor(o / 128) >= ceil(n / 128).
@@ -30,9 +59,9 @@ struct MxRows {
     __device__ __forceinline__ bool place(int64_t r, int& g, int64_t& tile, int& in) const {
         int64_t q;
         if (group_of_row) {
-            g = __ldg(group_of_row + r);
+            g = group_of_row[r];
             if (g < 0) return false;
-            const int o = __ldg(offsets + g);
+            const int o = offsets[g];
             q = r - o;
             tile = (o >> 7) + g + (q >> 7);
         } else if (rows == per_group) {

@@ -248,8 +248,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile
 // the same on a barrier that the other CTA of a pair arrives on too
 template <bool PAIR>
 __device__ __forceinline__ bool pair_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
-    const bool ok = warp_wait(b, parity, abort);
-    if (PAIR) try_wait_cluster(b, parity);  // complete: orders what follows after the other CTA's arrival
+    if constexpr (!PAIR) return warp_wait(b, parity, abort);
+    if (__all_sync(kAll, try_wait_cluster(b, parity))) return true;
+    const bool ok = __all_sync(kAll, bar_wait(b, parity, kTimeoutNs, abort));
+    try_wait_cluster(b, parity);  // complete: orders what follows after the other CTA's arrival
     return ok;
 }
 
@@ -344,6 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         fence_barrier_init();
     }
     if (warp == 1) alloc_columns<PAIR>(&tmem_s, kTmemCols);
+    let_next_start();
+    after_previous();
     int row_tiles;
     if (a.offsets) {
         // running counts of the groups' row tiles; a thread has at most kPer groups
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         int first[kPer + 1], sum = 0;
 #pragma unroll
         for (int j = 0; j <= kPer; ++j)
-            if (j <= per) first[j] = __ldg(a.offsets + min(g0 + j, a.groups));
+            if (j <= per) first[j] = a.offsets[min(g0 + j, a.groups)];
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
             if (j < per) sum += (first[j + 1] - first[j] + NT - 1) / NT;
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         Slots slots;
         for (int i = 0; i < my_tiles; ++i) {
             const Tile ti = find_tile<NT>(a, cum, offs, unit + i * units, lane);
-            const float alpha = a.alpha ? __ldg(a.alpha + ti.g) : 1.0f;
+            const float alpha = a.alpha ? a.alpha[ti.g] : 1.0f;
             const uint32_t m = slots.mask(ti.n);
             bool ok = true;
             if (m & 1) ok = warp_wait(&acc_full[0], slots.use[0] & 1u, &abort_s);
@@ -661,22 +665,7 @@ cudaError_t launch_typed(ProductArgs& a, int sms, cudaStream_t st) {
     const int64_t tiles = row_tiles * a.w_units, units = C::kPair ? sms / 2 : sms;
     if (tiles > INT32_MAX || tiles / units * a.steps > INT32_MAX / 2) return cudaErrorInvalidValue;
     const unsigned n = (unsigned)(tiles < units ? tiles : units);
-    if constexpr (C::kPair) {
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = 2 * n;
-        cfg.blockDim = kThreads;
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = st;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, product_kernel<FMT, NT, TY>, (const ProductArgs)a);
-    }
-    product_kernel<FMT, NT, TY><<<n, kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch(product_kernel<FMT, NT, TY>, C::kPair ? 2 * n : n, kThreads, smem, st, C::kPair ? 2 : 1, a);
 }
 
 // few rows: a short row tile leaves shared memory for more steps in flight

@@ -15,7 +15,7 @@ __device__ __forceinline__ void load16(const float* p, int n, bool wide, float (
     if (wide && n >= 16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
+            const float4 q = reinterpret_cast<const float4*>(p)[i];
             v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
         }
     } else {
@@ -27,7 +27,7 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, int n, bool wide,
     if (wide && n >= 16) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            const uint4 q = reinterpret_cast<const uint4*>(p)[i];
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -111,12 +111,14 @@ __device__ __forceinline__ uint32_t scale_at(int in, int atom) {
 // short number, as a tie between two codes is, the result is exactly that.
 template <typename T, int FMT, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
+    after_previous();
+    let_next_start();
     const int c16 = threadIdx.x & 15;
     const int64_t r = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 4);
     int g = 0, in = 0;
     int64_t tile = 0;
     bool live = r < a.rows.rows;
-    int64_t from = live ? (a.src_row ? __ldg(a.src_row + r) : r) : -1;
+    int64_t from = live ? (a.src_row ? a.src_row[r] : r) : -1;
     live = live && a.rows.place(r, g, tile, in) && from >= 0;
     float v[16];
     const int col = blockIdx.y * kMxTileCols + c16 * kChunk, n = live ? a.cols - col : 0;
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] *= inv;
     } else {
-        const float t = a.tscale && live ? __ldg(a.tscale + g) : 1.0f;
+        const float t = a.tscale && live ? a.tscale[g] : 1.0f;
         const __nv_fp8_storage_t s =
             __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f * t), __NV_SATFINITE, __NV_E4M3);
         byte = s;
@@ -188,6 +190,8 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
 
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads) dequantise_kernel(const QuantArgs a) {
+    after_previous();
+    let_next_start();
     const int c16 = threadIdx.x & 15;
     const int64_t r = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 4);
     int g, in;
@@ -196,14 +200,14 @@ __global__ void __launch_bounds__(kThreads) dequantise_kernel(const QuantArgs a)
     if (r >= a.rows.rows || n <= 0 || !a.rows.place(r, g, tile, in)) return;
     const uint8_t* base = a.data + (tile * a.col_tiles + blockIdx.y) * (int64_t)mx_tile_bytes(FMT);
     const int b = FMT == MOE_MX_E8M0 ? c16 >> 1 : c16;
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(base + code_at(in, c16)));
-    const uint32_t byte = __ldg(base + scale_at(in, b >> 2) + (b & 3));
+    const uint2 q = *reinterpret_cast<const uint2*>(base + code_at(in, c16));
+    const uint32_t byte = base[scale_at(in, b >> 2) + (b & 3)];
     float s;
     if (FMT == MOE_MX_E8M0)
         s = byte == 255 ? __uint_as_float(0x7fffffffu) : byte ? __uint_as_float(byte << 23) : __uint_as_float(0x400000u);
     else
         s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
-    const float t = a.tscale ? __ldg(a.tscale + g) : 1.0f;
+    const float t = a.tscale ? a.tscale[g] : 1.0f;
     float v[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -218,11 +222,9 @@ __global__ void __launch_bounds__(kThreads) dequantise_kernel(const QuantArgs a)
 dim3 grid_of(const QuantArgs& a) { return dim3((unsigned)((a.rows.rows + kRows - 1) / kRows), (unsigned)a.col_tiles); }
 
 template <typename T, int FMT>
-void quantise_act(const QuantArgs& a, int act, cudaStream_t st) {
-    if (act == MOE_ACT_SWIGLU)
-        quantise_kernel<T, FMT, true><<<grid_of(a), kThreads, 0, st>>>(a);
-    else
-        quantise_kernel<T, FMT, false><<<grid_of(a), kThreads, 0, st>>>(a);
+cudaError_t quantise_act(const QuantArgs& a, int act, cudaStream_t st) {
+    if (act == MOE_ACT_SWIGLU) return launch(quantise_kernel<T, FMT, true>, grid_of(a), kThreads, 0, st, 1, a);
+    return launch(quantise_kernel<T, FMT, false>, grid_of(a), kThreads, 0, st, 1, a);
 }
 
 // whole 16-byte loads or stores need every 16-column chunk of every row aligned
@@ -247,13 +249,11 @@ cudaError_t launch_mx_quantise(const moe_mx& m, const MxRows& rows, const void* 
     a.wide = wide_ok(src, ld, act == MOE_ACT_SWIGLU ? m.cols : 0, type);
     if ((rows.rows + kRows - 1) / kRows > INT32_MAX || a.col_tiles > 65535) return cudaErrorInvalidValue;
     if (type == MOE_F32) {
-        if (m.format == MOE_MX_E8M0) quantise_act<float, MOE_MX_E8M0>(a, act, st);
-        else quantise_act<float, MOE_MX_E4M3>(a, act, st);
-    } else {
-        if (m.format == MOE_MX_E8M0) quantise_act<__nv_bfloat16, MOE_MX_E8M0>(a, act, st);
-        else quantise_act<__nv_bfloat16, MOE_MX_E4M3>(a, act, st);
+        if (m.format == MOE_MX_E8M0) return quantise_act<float, MOE_MX_E8M0>(a, act, st);
+        return quantise_act<float, MOE_MX_E4M3>(a, act, st);
     }
-    return cudaGetLastError();
+    if (m.format == MOE_MX_E8M0) return quantise_act<__nv_bfloat16, MOE_MX_E8M0>(a, act, st);
+    return quantise_act<__nv_bfloat16, MOE_MX_E4M3>(a, act, st);
 }
 
 cudaError_t launch_mx_dequantise(const moe_mx& m, const MxRows& rows, const float* tscale, void* dst, int type,
@@ -269,13 +269,12 @@ cudaError_t launch_mx_dequantise(const moe_mx& m, const MxRows& rows, const floa
     a.wide = wide_ok(dst, ld, 0, type);
     if ((rows.rows + kRows - 1) / kRows > INT32_MAX || a.col_tiles > 65535) return cudaErrorInvalidValue;
     if (type == MOE_F32) {
-        if (m.format == MOE_MX_E8M0) dequantise_kernel<float, MOE_MX_E8M0><<<grid_of(a), kThreads, 0, st>>>(a);
-        else dequantise_kernel<float, MOE_MX_E4M3><<<grid_of(a), kThreads, 0, st>>>(a);
-    } else {
-        if (m.format == MOE_MX_E8M0) dequantise_kernel<__nv_bfloat16, MOE_MX_E8M0><<<grid_of(a), kThreads, 0, st>>>(a);
-        else dequantise_kernel<__nv_bfloat16, MOE_MX_E4M3><<<grid_of(a), kThreads, 0, st>>>(a);
+        if (m.format == MOE_MX_E8M0) return launch(dequantise_kernel<float, MOE_MX_E8M0>, grid_of(a), kThreads, 0, st, 1, a);
+        return launch(dequantise_kernel<float, MOE_MX_E4M3>, grid_of(a), kThreads, 0, st, 1, a);
     }
-    return cudaGetLastError();
+    if (m.format == MOE_MX_E8M0)
+        return launch(dequantise_kernel<__nv_bfloat16, MOE_MX_E8M0>, grid_of(a), kThreads, 0, st, 1, a);
+    return launch(dequantise_kernel<__nv_bfloat16, MOE_MX_E4M3>, grid_of(a), kThreads, 0, st, 1, a);
 }
 
 }  // namespace moe

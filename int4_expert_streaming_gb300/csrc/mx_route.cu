@@ -73,6 +73,8 @@ struct RouteScratch {
 template <typename T, int NV>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a) {
     __shared__ RouteScratch<NV> scratch[kRouteWarps];
+    after_previous();
+    let_next_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     if (t >= a.T) return;
@@ -242,11 +244,10 @@ template <typename T>
 cudaError_t route_typed(const RouteArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
     const int E = a.c.n_experts;
-    if (E <= 128) route_kernel<T, 4><<<grid, 32 * kRouteWarps, 0, st>>>(a);
-    else if (E <= 256) route_kernel<T, 8><<<grid, 32 * kRouteWarps, 0, st>>>(a);
-    else if (E <= 512) route_kernel<T, 16><<<grid, 32 * kRouteWarps, 0, st>>>(a);
-    else route_kernel<T, 32><<<grid, 32 * kRouteWarps, 0, st>>>(a);
-    return cudaGetLastError();
+    if (E <= 128) return launch(route_kernel<T, 4>, grid, 32 * kRouteWarps, 0, st, 1, a);
+    if (E <= 256) return launch(route_kernel<T, 8>, grid, 32 * kRouteWarps, 0, st, 1, a);
+    if (E <= 512) return launch(route_kernel<T, 16>, grid, 32 * kRouteWarps, 0, st, 1, a);
+    return launch(route_kernel<T, 32>, grid, 32 * kRouteWarps, 0, st, 1, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -283,11 +284,13 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(const int3
                                                                       int32_t* token_of_row, int32_t* group_of_row) {
     extern __shared__ uint4 cnt_raw[];  // [warps with pairs][E] bytes, then [E] first rows
     __shared__ int warp_tot[kSortWarps];
+    let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rows = (n + 31) / 32, bytes = (rows * E + 15) & ~15;
     uint8_t* cnt = reinterpret_cast<uint8_t*>(cnt_raw);
     int* first = reinterpret_cast<int*>(cnt + bytes);
     for (int i = tid; i < bytes / 16; i += blockDim.x) cnt_raw[i] = make_uint4(0, 0, 0, 0);
+    after_previous();
     int key = tid < n ? idx[tid] : -1;
     if (key < 0 || key >= E) key = -1;
     __syncthreads();
@@ -339,6 +342,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
                                                                 int32_t* token_of_row, int32_t* group_of_row) {
     extern __shared__ int cnt[];  // [kSortWarps][E] per warp, then [E] of the CTA
     __shared__ int warp_tot[kSortWarps];
+    let_next_start();
     int* const cta_cnt = cnt + kSortWarps * E;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     cg::cluster_group cluster = cg::this_cluster();
@@ -361,6 +365,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
         __syncwarp();
         return r + lower;
     };
+    after_previous();
     if (keep)
 #pragma unroll
         for (int j = 0; j < kKeep; ++j) key_r[j] = key_at(p0 + 32 * j + lane);
@@ -446,11 +451,11 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
 constexpr int kCombineThreads = 128;
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = *reinterpret_cast<const float4*>(p), b = reinterpret_cast<const float4*>(p)[1];
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -480,6 +485,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const TI* rows
                                                                   const int32_t* row_of_pair, const float* w, int top_k,
                                                                   int cols, TO* y, int64_t y_ld) {
     constexpr int V = WIDE ? 8 : 1;
+    after_previous();
+    let_next_start();
     const int64_t t = blockIdx.x;
     const int col = (blockIdx.y * kCombineThreads + threadIdx.x) * V;
     if (col >= cols) return;
@@ -491,8 +498,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const TI* rows
         float v[4][V], wj[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = i < n ? __ldg(row_of_pair + j + i) : -1;
-            wj[i] = i < n ? __ldg(w + j + i) : 0.0f;
+            const int r = i < n ? row_of_pair[j + i] : -1;
+            wj[i] = i < n ? w[j + i] : 0.0f;
 #pragma unroll
             for (int q = 0; q < V; ++q) v[i][q] = 0.0f;
             if (r >= 0) {
@@ -532,11 +539,8 @@ cudaError_t combine_typed(const void* rows, int64_t rows_ld, const int32_t* row_
     const dim3 grid((unsigned)T, (unsigned)chunks);
     const TI* in = static_cast<const TI*>(rows);
     TO* out = static_cast<TO*>(y);
-    if (wide)
-        combine_kernel<TI, TO, true><<<grid, kCombineThreads, 0, st>>>(in, rows_ld, row_of_pair, w, top_k, cols, out, y_ld);
-    else
-        combine_kernel<TI, TO, false><<<grid, kCombineThreads, 0, st>>>(in, rows_ld, row_of_pair, w, top_k, cols, out, y_ld);
-    return cudaGetLastError();
+    return launch(wide ? combine_kernel<TI, TO, true> : combine_kernel<TI, TO, false>, grid, kCombineThreads, 0, st, 1, in,
+                  rows_ld, row_of_pair, w, top_k, cols, out, y_ld);
 }
 
 }  // namespace
@@ -561,28 +565,16 @@ cudaError_t launch_dispatch(const int32_t* idx, int64_t pairs, int top_k, int n_
         const int smem = ((rows * n_experts + 15) & ~15) + n_experts * (int)sizeof(int);
         if ((e = smem_limit(reinterpret_cast<const void*>(dispatch_small_kernel), smem)) != cudaSuccess) return e;
         const int threads = ((n > n_experts ? n : n_experts) + 31) & ~31;
-        dispatch_small_kernel<<<1, threads, smem, st>>>(idx, n, top_k, n_experts, bits, offsets, row_of_pair,
-                                                        token_of_row, group_of_row);
-        return cudaGetLastError();
+        return launch(dispatch_small_kernel, 1, threads, smem, st, 1, idx, n, top_k, n_experts, bits, offsets,
+                      row_of_pair, token_of_row, group_of_row);
     }
     const int smem = (kSortWarps + 1) * n_experts * (int)sizeof(int);
     const void* kernel = reinterpret_cast<const void*>(dispatch_kernel);
     if ((e = smem_limit(kernel, smem)) != cudaSuccess) return e;
     // 16 CTAs are past the portable cluster size of 8
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kSortCtas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = kSortCtas;
-    cfg.blockDim = kSortThreads;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dispatch_kernel, idx, (int)pairs, top_k, n_experts, bits, offsets, row_of_pair,
-                              token_of_row, group_of_row);
+    return launch(dispatch_kernel, kSortCtas, kSortThreads, smem, st, kSortCtas, idx, (int)pairs, top_k, n_experts, bits,
+                  offsets, row_of_pair, token_of_row, group_of_row);
 }
 
 cudaError_t launch_combine(const void* rows, int rows_type, int64_t rows_ld, const int32_t* row_of_pair, const float* w,
