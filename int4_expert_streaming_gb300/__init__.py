@@ -1,8 +1,9 @@
 """Python binding of libmoe.so -- the routed sparse-MoE layer with expert
 streaming on one GB300 (sm_103a).
 
-Argument marshalling only: every step of the layer runs in the library's CUDA
-kernels.  The names mirror the C ABI in ``include/moe.h``.  Device buffers are
+Argument marshalling only (ctypes, and the small C module _call for the
+operators without a context): every step of the layer runs in the library's
+CUDA kernels.  The names mirror the C ABI in ``include/moe.h``.  Device buffers are
 passed as CUDA torch tensors (fp32 / int32, contiguous) or raw integer device
 addresses; streams as ``torch.cuda.Stream`` or raw ``cudaStream_t`` integers.
 
@@ -12,6 +13,7 @@ built ``libmoe.so`` and raises if it is missing -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -340,40 +342,23 @@ def make_config(n_layers, hidden, n_experts, top_k, inter, shared_inter, bits=4,
 
 # --------------------------------------------------------------------------
 # operators without a context: CUDA tensors in, shapes and strides taken from
-# them; outputs are the caller's tensors
+# them; outputs are the caller's tensors.  _call (csrc/binding.c) takes the
+# tensors apart; one that does not fit raises ValueError.
 # --------------------------------------------------------------------------
 
-_types: dict = {}
+_ops = None
 
 
-def _torch_types() -> dict:
-    if not _types:
+def _binding():
+    global _ops
+    if _ops is None:
+        load_library()
         import torch
-        _types.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, "i32": torch.int32, "u8": torch.uint8})
-    return _types
 
-
-def _flat(t, dtype, n: int, what: str):
-    """Address of a contiguous CUDA tensor of at least n elements of the torch dtype; None stays None."""
-    if t is None:
-        return None
-    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what}: expected a contiguous CUDA tensor of at least {n} {dtype} elements, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    return t.data_ptr()
-
-
-def _matrix(t, what: str):
-    """(address, MOE_* type, rows, cols, row stride) of a 2D CUDA tensor whose rows are contiguous."""
-    kind = (_types or _torch_types()).get(t.dtype)
-    if kind is None or not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{what}: expected a 2D CUDA tensor of float32 or bfloat16, got {tuple(t.shape)} {t.dtype} "
-                         f"on {t.device}")
-    rows, cols = t.shape
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{what}: rows must be contiguous")
-    return t.data_ptr(), kind, rows, cols, ld if rows > 1 else cols
+        mod = importlib.import_module("._call", __name__)  # built beside libmoe.so
+        mod.dtypes(torch.float32, torch.bfloat16, torch.int32, torch.uint8)
+        _ops = mod
+    return _ops
 
 
 def make_route_config(n_experts, top_k, n_groups=1, top_groups=1, group_best=1, score=MOE_SCORE_SOFTMAX, renorm=True,
@@ -384,13 +369,9 @@ def make_route_config(n_experts, top_k, n_groups=1, top_groups=1, group_best=1, 
 def moe_route(cfg: moe_route_config, logits, bias, idx, w, stream=None) -> None:
     """logits [T, n_experts] fp32 or bf16 (rows may be strided), bias [n_experts] fp32 or None; fills idx [T, top_k]
     int32 and w [T, top_k] fp32."""
-    ty = _types or _torch_types()
-    p, kind, T, E, ld = _matrix(logits, "logits")
-    if E != cfg.n_experts:
-        raise ValueError(f"logits have {E} columns, the config {cfg.n_experts} experts")
-    n = T * cfg.top_k
-    _check(load_library().moe_route(cfg, p, kind, ld, _scales(bias, E, "bias"), T, _flat(idx, ty["i32"], n, "idx"),
-                                    _scales(w, n, "w"), _stream(stream)))
+    rc = (_ops or _binding()).route(cfg, logits, bias, idx, w, stream)
+    if rc:
+        _check(rc)
 
 
 def moe_dispatch_workspace(T: int, top_k: int, n_experts: int) -> int:
@@ -401,15 +382,9 @@ def moe_dispatch(idx, n_experts: int, offsets, row_of_pair, token_of_row, group_
                  stream=None) -> None:
     """idx [T, top_k] int32 -> offsets [n_experts + 1], row_of_pair [T, top_k], token_of_row and group_of_row
     [T * top_k], all int32; workspace: uint8, moe_dispatch_workspace() bytes."""
-    i32 = (_types or _torch_types())["i32"]
-    T, k = idx.shape
-    n = T * k
-    ws, size = (None, 0) if workspace is None else (_flat(workspace, _types["u8"], 0, "workspace"), workspace.numel())
-    _check(load_library().moe_dispatch(_flat(idx, i32, n, "idx"), T, k, n_experts,
-                                       _flat(offsets, i32, n_experts + 1, "offsets"),
-                                       _flat(row_of_pair, i32, n, "row_of_pair"),
-                                       _flat(token_of_row, i32, n, "token_of_row"),
-                                       _flat(group_of_row, i32, n, "group_of_row"), ws, size, _stream(stream)))
+    rc = (_ops or _binding()).dispatch(idx, n_experts, offsets, row_of_pair, token_of_row, group_of_row, workspace, stream)
+    if rc:
+        _check(rc)
 
 
 def moe_mx_bytes(m: moe_mx) -> int:
@@ -417,17 +392,20 @@ def moe_mx_bytes(m: moe_mx) -> int:
 
 
 def make_mx(fmt: int, rows: int, cols: int, groups: int = 1, ragged: bool = False, data=None) -> moe_mx:
-    """Descriptor of a microscaled 4-bit matrix (see moe_mx in moe.h) over `data`, a CUDA uint8 tensor of at least
-    moe_mx_bytes() bytes (kept alive by the descriptor; allocated on the current device if None)."""
+    """Descriptor of a microscaled 4-bit matrix (see moe_mx in moe.h) over `data`, a contiguous CUDA uint8 tensor of at
+    least moe_mx_bytes() bytes (kept alive by the descriptor; allocated on the current device if None)."""
+    import torch
+
     m = moe_mx(None, rows, cols, groups, fmt, int(bool(ragged)))
     need = moe_mx_bytes(m)
-    if need == 0 and rows > 0:
+    if need == 0 and rows != 0:
         raise ValueError(f"bad matrix shape: format {fmt}, {groups} groups, {rows} rows, {cols} columns")
-    u8 = _torch_types()["u8"]
     if data is None:
-        import torch
-        data = torch.empty(max(need, 1), dtype=u8, device="cuda")
-    m.data_dev = _flat(data, u8, need, "data")
+        data = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    if not data.is_cuda or data.dtype is not torch.uint8 or not data.is_contiguous() or data.numel() < need:
+        raise ValueError(f"data: expected a contiguous CUDA tensor of at least {need} uint8, got {tuple(data.shape)} "
+                         f"{data.dtype} on {data.device}")
+    m.data_dev = data.data_ptr()
     m._data = data
     return m
 
@@ -435,60 +413,30 @@ def make_mx(fmt: int, rows: int, cols: int, groups: int = 1, ragged: bool = Fals
 def moe_mx_quantise(m: moe_mx, src, act: int = MOE_ACT_NONE, src_row=None, group_of_row=None, offsets=None,
                     tensor_scale=None, stream=None) -> None:
     """Rows of src (fp32 or bf16, [source rows, cols] or [.., 2 cols] for MOE_ACT_SWIGLU) into m."""
-    ty = _types or _torch_types()
-    p, kind, n, cols, ld = _matrix(src, "src")
-    if cols != (2 * m.cols if act == MOE_ACT_SWIGLU else m.cols):
-        raise ValueError(f"src has {cols} columns, the matrix {m.cols} (activation {act})")
-    rows = m.rows if m.ragged else m.rows * m.groups
-    if src_row is None and n < rows:
-        raise ValueError(f"src has {n} rows, the matrix {rows}")
-    i32 = ty["i32"]
-    _check(load_library().moe_mx_quantise(
-        m, p, kind, ld, act, _flat(src_row, i32, rows, "src_row"), _flat(group_of_row, i32, rows, "group_of_row"),
-        _flat(offsets, i32, m.groups + 1, "offsets"), _scales(tensor_scale, m.groups, "tensor_scale"), _stream(stream)))
-
-
-def _scales(t, n: int, what: str):
-    if t is None:
-        return None
-    if _types.get(t.dtype) != MOE_F32:
-        raise ValueError(f"{what}: expected float32, got {t.dtype}")
-    return _flat(t, t.dtype, n, what)
+    rc = (_ops or _binding()).quantise(m, src, act, src_row, group_of_row, offsets, tensor_scale, stream)
+    if rc:
+        _check(rc)
 
 
 def moe_mx_dequantise(m: moe_mx, dst, group_of_row=None, offsets=None, tensor_scale=None, stream=None) -> None:
     """The numbers of m into dst [rows, cols], fp32 or bf16."""
-    i32 = (_types or _torch_types())["i32"]
-    p, kind, n, cols, ld = _matrix(dst, "dst")
-    rows = m.rows if m.ragged else m.rows * m.groups
-    if cols != m.cols or n < rows:
-        raise ValueError(f"dst is {n} x {cols}, the matrix {rows} x {m.cols}")
-    _check(load_library().moe_mx_dequantise(m, _flat(group_of_row, i32, rows, "group_of_row"),
-                                            _flat(offsets, i32, m.groups + 1, "offsets"),
-                                            _scales(tensor_scale, m.groups, "tensor_scale"), p, kind, ld,
-                                            _stream(stream)))
+    rc = (_ops or _binding()).dequantise(m, dst, group_of_row, offsets, tensor_scale, stream)
+    if rc:
+        _check(rc)
 
 
 def moe_mx_product(x: moe_mx, w: moe_mx, y, offsets=None, alpha=None, stream=None) -> None:
     """y [x.rows, w.rows] (fp32 or bf16) = alpha[group] * X W[group]^T."""
-    i32 = (_types or _torch_types())["i32"]
-    p, kind, n, cols, ld = _matrix(y, "y")
-    if n < x.rows or cols != w.rows:
-        raise ValueError(f"y is {n} x {cols}, the product {x.rows} x {w.rows}")
-    _check(load_library().moe_mx_product(x, w, _flat(offsets, i32, x.groups + 1, "offsets"),
-                                         _scales(alpha, w.groups, "alpha"), p, kind, ld, _stream(stream)))
+    rc = (_ops or _binding()).product(x, w, y, offsets, alpha, stream)
+    if rc:
+        _check(rc)
 
 
 def moe_combine(rows, row_of_pair, w, y, stream=None) -> None:
     """y [T, cols] = sum_j w[T, k] * rows[row_of_pair[T, k]]; rows and y fp32 or bf16."""
-    i32 = (_types or _torch_types())["i32"]
-    p, kind, _, cols, ld = _matrix(rows, "rows")
-    py, ykind, n, ycols, yld = _matrix(y, "y")
-    T, k = row_of_pair.shape
-    if ycols != cols or n != T:
-        raise ValueError(f"y is {n} x {ycols}, expected {T} x {cols}")
-    _check(load_library().moe_combine(p, kind, ld, _flat(row_of_pair, i32, T * k, "row_of_pair"),
-                                      _scales(w, T * k, "w"), T, k, cols, py, ykind, yld, _stream(stream)))
+    rc = (_ops or _binding()).combine(rows, row_of_pair, w, y, stream)
+    if rc:
+        _check(rc)
 
 
 # --------------------------------------------------------------------------

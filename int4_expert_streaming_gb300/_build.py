@@ -1,7 +1,9 @@
 """Build libmoe.so in-tree with nvcc for sm_103a (no torch extension machinery).
 
 Each translation unit compiles in parallel into _build/, then one nvcc link
-produces int4_expert_streaming_gb300/libmoe.so (static CUDA runtime).
+produces int4_expert_streaming_gb300/libmoe.so (static CUDA runtime).  gcc
+builds _call.so beside it, the Python module that marshals the arguments of
+the operators without a context (csrc/binding.c, linked against libmoe.so).
 """
 from __future__ import annotations
 
@@ -10,12 +12,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
+CALL = os.path.join(PKG, "_call.so")
+BINDING = os.path.join(CSRC, "binding.c")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -31,14 +36,14 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "moe.h"),
+    return sources() + [BINDING] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "moe.h"),
                                                                os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -72,7 +77,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_binding()
     return LIB
+
+
+def _build_binding() -> None:
+    tmp = CALL + f".tmp{os.getpid()}"
+    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
+           "-I" + os.path.join(ROOT, "include"), BINDING, "-o", tmp, "-L" + PKG, "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
 
 
 if __name__ == "__main__":
