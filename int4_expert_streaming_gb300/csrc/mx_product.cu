@@ -18,7 +18,10 @@
 // against 512 cycles of MMA in the largest step.
 //
 // Warp roles of a persistent CTA (one per SM):
-//   warp 0      one thread issues the copies, kStages steps ahead
+//   warps 0, 14, 15  one thread each issues the copies of w, of x's codes and of
+//               x's scales, kStages steps ahead; a copy costs its thread about
+//               80 cycles, and one thread for all of a step's five was slower
+//               than the step's MMAs
 //   warp 1      one thread issues MMAs and commits
 //   warps 2-5   scales: shared memory -> tensor memory, lane quarter w % 4
 //   warps 6-13  epilogue: tensor memory -> registers -> y; lane quarter w % 4,
@@ -45,7 +48,8 @@ using namespace gemmc;
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kEpiWarp0 = 6, kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kXWarp = kEpiWarp0 + kEpiWarps, kCopyWarps = 3;  // warps 0, kXWarp, kXWarp + 1
+constexpr int kThreads = 32 * (kXWarp + 2);
 constexpr int kPer = (1024 + kThreads - 1) / kThreads;  // groups per thread
 constexpr int kTileRing = 16;  // rows of the tiles between the copies and the MMAs: more than kStages
 constexpr int kTmemCols = 512;
@@ -227,15 +231,6 @@ __device__ __forceinline__ void fail(const ProductArgs& a, volatile int* abort) 
     *abort = 1;
     *(volatile int*)a.status = 1;
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_u32(b)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // arrival on a barrier of another CTA of the cluster
 __device__ __forceinline__ void remote_arrive_relaxed(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
@@ -245,16 +240,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile
     if (__all_sync(kAll, bar_try_wait(b, parity))) return true;
     return __all_sync(kAll, bar_wait(b, parity, kTimeoutNs, abort));
 }
-// the same on a barrier that the other CTA of a pair arrives on too
-template <bool PAIR>
-__device__ __forceinline__ bool pair_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
-    if constexpr (!PAIR) return warp_wait(b, parity, abort);
-    if (__all_sync(kAll, try_wait_cluster(b, parity))) return true;
-    const bool ok = __all_sync(kAll, bar_wait(b, parity, kTimeoutNs, abort));
-    try_wait_cluster(b, parity);  // complete: orders what follows after the other CTA's arrival
-    return ok;
-}
-
 struct Tile {
     int g, n, wt;  // group, rows, w row tile (a pair: the first of two)
     int64_t row0;  // first row of x and y
@@ -296,8 +281,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // row j of a piece: fp32 bits, or bf16 pairs
-__device__ __forceinline__ void put(float* y, const uint32_t (&v)[16], int j) { *y = __uint_as_float(v[j]); }
-__device__ __forceinline__ void put(__nv_bfloat16* y, const uint32_t (&v)[8], int j) {
+__device__ __forceinline__ void put(float* y, const uint32_t (&v)[32], int j) { *y = __uint_as_float(v[j]); }
+__device__ __forceinline__ void put(__nv_bfloat16* y, const uint32_t (&v)[16], int j) {
     *reinterpret_cast<uint16_t*>(y) = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
 }
 
@@ -331,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
 
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            bar_init(&full[s], 1);
+            bar_init(&full[s], kCopyWarps);
             bar_init(&empty[s], 1);
         }
         // the four scale warps, and in CTA 0 of a pair CTA 1's forwarded
@@ -402,23 +387,44 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         else bar_arrive(b);
     };
 
-    if (warp == 0) {
+    if (warp == 0 || warp >= kXWarp) {
         // ---------------------------------------------------------------- copies
         const uint32_t leader = elect_one(), full0 = smem_u32(full);
         uint32_t s = 0, ph = 1, filled = 0;  // stage, parity of its release, steps begun
         bool ok = true;
         for (int i = 0; i < my_tiles && ok; ++i) {
             const Tile ti = find_tile<NT>(a, cum, offs, unit + i * units, lane);
-            // this CTA's rows of x: all, or its half of the MMA's N; r0 .. r1 may lie in two row tiles
-            const int n8 = (ti.n + 7) & ~7, half = PAIR ? ((ti.n + 31) & ~31) / 2 : 0;
-            const int r0 = (int)rank * half, r1 = PAIR && rank == 0 ? min(half, n8) : n8;
-            const uint32_t b0 = (uint32_t)max(min(r1, 128) - r0, 0) * 128u, b1 = (uint32_t)max(r1 - max(r0, 128), 0) * 128u;
-            const uint32_t total = C::kTile + b0 + b1 + (ti.n > 128 ? 2u : 1u) * C::kScaleBytes;
-            const int wt = min(ti.wt + (int)rank, a.w_tiles - 1);  // an odd last tile: CTA 1 repeats it, and stores nothing
-            const uint8_t* wp = a.w + ((int64_t)ti.g * a.w_tiles + wt) * a.steps * C::kTile;
-            const uint8_t* x0 = a.x + ti.xt * a.steps * C::kTile;
-            const uint8_t* x1 = x0 + (int64_t)a.steps * C::kTile;
-            if (leader) tile_n[i % kTileRing] = ti.n;
+            // this warp's one or two copies of a step: sizes, first sources, places in the stage
+            uint32_t b0, b1 = 0, d0, d1 = 0;
+            const uint8_t *p0, *p1 = nullptr;
+            if (warp == 0) {
+                if (leader) tile_n[i % kTileRing] = ti.n;
+                const int wt = min(ti.wt + (int)rank, a.w_tiles - 1);  // an odd last tile: CTA 1 repeats it, and stores nothing
+                p0 = a.w + ((int64_t)ti.g * a.w_tiles + wt) * a.steps * C::kTile;
+                b0 = C::kTile;
+                d0 = 0;
+            } else {
+                const uint8_t* x0 = a.x + ti.xt * a.steps * C::kTile;
+                const uint8_t* x1 = x0 + (int64_t)a.steps * C::kTile;
+                if (warp == kXWarp) {
+                    // all rows, or this CTA's half of the MMA's N; r0 .. r1 may lie in two row tiles
+                    const int n8 = (ti.n + 7) & ~7, half = PAIR ? ((ti.n + 31) & ~31) / 2 : 0;
+                    const int r0 = (int)rank * half, r1 = PAIR && rank == 0 ? min(half, n8) : n8;
+                    b0 = (uint32_t)max(min(r1, 128) - r0, 0) * 128u;
+                    b1 = (uint32_t)max(r1 - max(r0, 128), 0) * 128u;
+                    p0 = x0 + r0 * 128;
+                    p1 = x1 + max(r0 - 128, 0) * 128;
+                    d0 = C::kOffX;
+                    d1 = C::kOffX + b0;
+                } else {
+                    p0 = x0 + kMxCodeBytes;
+                    p1 = x1 + kMxCodeBytes;
+                    b0 = C::kScaleBytes;
+                    b1 = ti.n > 128 ? C::kScaleBytes : 0;
+                    d0 = C::kOffXs;
+                    d1 = C::kOffXs + C::kScaleBytes;
+                }
+            }
             for (int k = 0; k < a.steps; ++k) {
                 if (!warp_wait(&empty[s], ph, &abort_s)) {
                     fail(a, &abort_s);
@@ -426,17 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                     break;
                 }
                 const uint32_t st = smem0 + s * C::kStage, bar = full0 + 8 * s;
-                expect_if(leader, bar, total);
-                copy_if(leader, st, wp, C::kTile, bar);
-                if (!PAIR || b0) copy_if(leader, st + C::kOffX, x0 + r0 * 128, b0, bar);
-                copy_if(leader, st + C::kOffXs, x0 + kMxCodeBytes, C::kScaleBytes, bar);
-                if (PAIR && ti.n > 128) {
-                    if (b1) copy_if(leader, st + C::kOffX + b0, x1 + max(r0 - 128, 0) * 128, b1, bar);
-                    copy_if(leader, st + C::kOffXs + C::kScaleBytes, x1 + kMxCodeBytes, C::kScaleBytes, bar);
-                }
-                wp += C::kTile;
-                x0 += C::kTile;
-                x1 += C::kTile;
+                expect_if(leader, bar, b0 + b1);
+                if (b0) copy_if(leader, st + d0, p0, b0, bar);
+                if (PAIR && b1) copy_if(leader, st + d1, p1, b1, bar);
+                p0 += C::kTile;
+                if (PAIR) p1 += C::kTile;
                 ++filled;
                 if (++s == C::kStages) s = 0, ph ^= 1;
             }
@@ -472,12 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             uint32_t d = 0, idesc = 0, m = 0;
             for (int k = 0; k < a.steps; ++k) {
                 // the scales' warps have seen the step's copies land before they arrive here
-                ok = pair_wait<PAIR>(&scales_full[s], ph, &abort_s);
+                ok = warp_wait(&scales_full[s], ph, &abort_s);
                 if (k == 0 && ok) {
                     const int n = tile_n[i % kTileRing];
                     m = slots.mask(n);
-                    if (m & 1) ok = pair_wait<PAIR>(&acc_empty[0], (slots.use[0] & 1u) ^ 1u, &abort_s);
-                    if ((m & 2) && ok) ok = pair_wait<PAIR>(&acc_empty[1], (slots.use[1] & 1u) ^ 1u, &abort_s);
+                    if (m & 1) ok = warp_wait(&acc_empty[0], (slots.use[0] & 1u) ^ 1u, &abort_s);
+                    if ((m & 2) && ok) ok = warp_wait(&acc_empty[1], (slots.use[1] & 1u) ^ 1u, &abort_s);
                     d = tmem + (m == 2 ? 128u : 0u);
                     idesc = PAIR ? idesc_mx<FMT>(256, (n + 31) & ~31, 0) : idesc_mx<FMT>(128, (n + 15) & ~15, 0);
                 }
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         // everything issued above has completed once this commit arrives
         commit_if<PAIR>(leader, smem_u32(&drain));
         if (!warp_wait(&drain, 0, &never_s)) fail(a, &abort_s);
-    } else if (warp < kEpiWarp0) {
+    } else if (warp >= 2 && warp < kEpiWarp0) {
         // --------------------------------------------------------------- scales
         const uint32_t quarter = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         uint32_t s = 0, ph = 0;
@@ -558,23 +558,25 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                 break;
             }
             fence_after_sync();
-            // 16-column pieces 2 p + half of the tile's rows, up to 8 of them, kept in the output's type
-            constexpr int kPieces = (NT + 31) / 32;
-            constexpr int kRegs = sizeof(TY) == 2 ? 8 : 16;
-            const uint32_t src = trow + (m == 2 ? 128u : 0u) + 16 * half;
+            // Pieces of 32 columns, kept in the output's type until all of the tile has been read.  A large tile's slots
+            // are the halves; in a small one each half has 64 columns of the slot.
+            constexpr int kPieces = NT > 128 ? 4 : 1;
+            constexpr int kRegs = sizeof(TY) == 2 ? 16 : 32;
+            constexpr int kBatch = sizeof(TY) == 2 ? kPieces : (kPieces > 2 ? 2 : kPieces);
+            const int first = half * (ti.n > 128 ? 128 : NT > 128 ? 64 : 32);
+            const int mine = min(ti.n - first, ti.n > 128 ? 128 : NT > 128 ? 64 : 32);  // this warp's rows, if any
+            const uint32_t src = trow + (m == 2 ? 128u : 0u) + first;
             const int64_t col = (int64_t)(ti.wt + (int)rank) * 128 + 32 * q + lane;
-            TY* const y = static_cast<TY*>(a.y) + (ti.row0 + 16 * half) * a.y_ld + col;
-            const int left = ti.n - 16 * half;  // rows from this warp's first on
+            TY* const y = static_cast<TY*>(a.y) + (ti.row0 + first) * a.y_ld + col;
             const bool in = col < a.w_rows;
-            constexpr int kBatch = sizeof(TY) == 2 ? kPieces : (kPieces > 4 ? 4 : kPieces);
 #pragma unroll
             for (int p0 = 0; p0 < kPieces; p0 += kBatch) {
                 uint32_t v[kBatch][kRegs];
 #pragma unroll
                 for (int p = 0; p < kBatch; ++p)
-                    if (32 * (p0 + p) < left) {
-                        uint32_t raw[16];
-                        tmem_ld16(src + 32 * (p0 + p), raw);
+                    if (32 * (p0 + p) < mine) {
+                        uint32_t raw[32];
+                        tmem_ld32(src + 32 * (p0 + p), raw);
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < kRegs; ++j) {
@@ -596,13 +598,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
 #pragma unroll
                     for (int p = 0; p < kBatch; ++p) {
                         TY* yp = y + (int64_t)(32 * (p0 + p)) * a.y_ld;
-                        const int rows = left - 32 * (p0 + p);
-                        if (rows >= 16) {
+                        const int rows = mine - 32 * (p0 + p);
+                        if (rows >= 32) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j, yp += a.y_ld) put(yp, v[p], j);
+                            for (int j = 0; j < 32; ++j, yp += a.y_ld) put(yp, v[p], j);
                         } else if (rows > 0) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j, yp += a.y_ld)
+                            for (int j = 0; j < 32; ++j, yp += a.y_ld)
                                 if (j < rows) put(yp, v[p], j);
                         }
                     }
