@@ -1,13 +1,8 @@
 // mx_route.cu -- routing with groups and a balance bias, the stable sort of
 // the chosen pairs by expert, and the weighted combine of the experts' rows.
-#include <cooperative_groups.h>
-
 #include <cfloat>
-#include <utility>
 
 #include "mx.h"
-
-namespace cg = cooperative_groups;
 
 namespace moe {
 namespace {
@@ -28,12 +23,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
-}
-
 struct RouteArgs {
     const void* logits;
     const float* bias;
@@ -42,12 +31,24 @@ struct RouteArgs {
     int64_t ld, T;
     moe_route_config c;
     uint32_t inv_group;  // e / group size = (e * inv_group) >> 20 for e < 1024
+    int group_size, lanes_log2;  // lanes that share a group's score: the largest power of two with n_groups of it in a warp
 };
 
-constexpr int kRouteWarps = 4;
+constexpr int kRouteWarps = 16;  // at most, per block
 
-// 1 / (1 + exp(-l)), within a few units of the last place
-__device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ float warp_max(float v) { return from_ordered(__reduce_max_sync(kAll, ordered(v))); }
+
+// 1 / (1 + exp(-l)), exp(-l) = 2^(-l log2 e), to about 2^-21 relative for |l| < 16: the choice compares fp32 sums of
+// it anyway, and a short form halves this part of the kernel.  The weights take expf.
+__device__ __forceinline__ float sigmoid_fast(float l) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * l));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
 
 // per-warp scratch: a score of every expert (expert e at e + e / 32, so that
 // lanes a row apart do not share a bank), and the candidates of the choice
@@ -72,13 +73,13 @@ struct RouteScratch {
 // bound by the instructions issued.
 template <typename T, int NV>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a) {
-    __shared__ RouteScratch<NV> scratch[kRouteWarps];
+    extern __shared__ float scratch[];  // a RouteScratch per warp
     after_previous();
     let_next_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
     if (t >= a.T) return;
-    RouteScratch<NV>& sh = scratch[warp];
+    RouteScratch<NV>& sh = reinterpret_cast<RouteScratch<NV>*>(scratch)[warp];
     const moe_route_config& c = a.c;
     const int E = c.n_experts;
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
@@ -96,9 +97,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         l[i] = l[i] > -INFINITY && ch[i] > -INFINITY ? fminf(l[i], FLT_MAX) : -INFINITY;
         m = fmaxf(m, l[i]);
     }
-    m = warp_max(m);
     const bool softmax = c.score == MOE_SCORE_SOFTMAX;
     const bool sums = c.top_groups < c.n_groups && c.group_best == 2;
+    m = warp_max(m);
     float inv_total = 1.0f;
     if (softmax && (a.bias || !c.renorm)) {
         float total = 0.0f;
@@ -106,11 +107,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         for (int i = 0; i < NV; ++i) total += l[i] > -INFINITY ? expf(l[i] - m) : 0.0f;
         inv_total = 1.0f / warp_sum(total);
     }
-    auto score = [&](float v) { return softmax ? expf(v - m) * inv_total : sigmoid(v); };
+    auto score = [&](float v) { return softmax ? expf(v - m) * inv_total : sigmoid_fast(v); };
     // a score relative to exp(ref), which only scales all of them: sigmoid(v) exp(-ref) for ref <= 0 is
     // exp(v - ref) / (1 + exp(v)), and does not vanish where every logit is far below zero
     auto relative = [&](float v, float ref) {
-        return softmax ? expf(v - ref) : v > 0.0f ? sigmoid(v) : expf(v - ref) / (1.0f + expf(v));
+        const float e = expf(softmax || v <= 0.0f ? v - ref : -v);
+        return softmax ? e : v > 0.0f ? 1.0f / (1.0f + e) : e / (1.0f + expf(v));
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
 
     if (c.top_groups < c.n_groups) {
         // each group's score by `per` lanes over shared memory, then its rank among the groups
-        const int S = E / c.n_groups, G = c.n_groups;
+        const int S = a.group_size, G = c.n_groups, log2 = a.lanes_log2, per = 1 << log2;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float v = ch[i];
@@ -126,9 +128,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
             sh.score[i * 33 + lane] = v;
         }
         __syncwarp();
-        int per = 1;
-        while (2 * per * G <= 32) per *= 2;
-        const int g = lane / per, sub = lane % per;
+        const int g = lane >> log2, sub = lane & (per - 1);
         float b1 = -INFINITY, b2 = -INFINITY;
         if (g < G)
 #pragma unroll 4
@@ -147,15 +147,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         int rank = 0;
 #pragma unroll 4
         for (int q = 0; q < G; ++q) {
-            const float os = __shfl_sync(kAll, gs, q * per);
+            const float os = __shfl_sync(kAll, gs, q << log2);
             rank += os > gs || (os == gs && q < g);
         }
         const unsigned kept_lane = __ballot_sync(kAll, g < G && sub == 0 && rank < c.top_groups);
+        const bool whole = (S & 31) == 0;  // a row of 32 experts lies in one group: the test is the warp's
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = i * 32 + lane;
+            const int e = whole ? i * 32 : i * 32 + lane;
             const int ge = (int)(((uint32_t)e * a.inv_group) >> 20);
-            if (e < E && !((kept_lane >> (ge * per)) & 1)) ch[i] = -INFINITY;
+            if (e < E && !((kept_lane >> (ge << log2)) & 1)) ch[i] = -INFINITY;
         }
         __syncwarp();
     }
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
         const float sum = warp_sum(wt);
         if (mine >= 0) wt = wt / sum * c.scale;
     } else if (mine >= 0) {
-        wt = score(v) * c.scale;
+        wt = (softmax ? expf(v - m) * inv_total : 1.0f / (1.0f + expf(-v))) * c.scale;
     }
     if (lane < c.top_k) {
         a.idx[t * c.top_k + lane] = mine;
@@ -240,20 +241,29 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
     }
 }
 
+template <typename T, int NV>
+cudaError_t route_rows(const RouteArgs& a, cudaStream_t st) {
+    // Blocks of 16 warps once they fill the GPU: starting 1000 blocks of 4 costs more than their work (4001 tokens of
+    // 256 experts 7.7 -> 6.3 us); below that 4, to spread over the SMs.
+    constexpr int kMost = NV == 32 ? kRouteWarps / 2 : kRouteWarps;  // within 48 KB of scratch
+    const int warps = a.T >= 16 * 128 ? kMost : 4;
+    return launch(route_kernel<T, NV>, (unsigned)((a.T + warps - 1) / warps), 32 * warps, warps * sizeof(RouteScratch<NV>),
+                  st, 1, a);
+}
+
 template <typename T>
 cudaError_t route_typed(const RouteArgs& a, cudaStream_t st) {
-    const unsigned grid = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
     const int E = a.c.n_experts;
-    if (E <= 128) return launch(route_kernel<T, 4>, grid, 32 * kRouteWarps, 0, st, 1, a);
-    if (E <= 256) return launch(route_kernel<T, 8>, grid, 32 * kRouteWarps, 0, st, 1, a);
-    if (E <= 512) return launch(route_kernel<T, 16>, grid, 32 * kRouteWarps, 0, st, 1, a);
-    return launch(route_kernel<T, 32>, grid, 32 * kRouteWarps, 0, st, 1, a);
+    if (E <= 128) return route_rows<T, 4>(a, st);
+    if (E <= 256) return route_rows<T, 8>(a, st);
+    if (E <= 512) return route_rows<T, 16>(a, st);
+    return route_rows<T, 32>(a, st);
 }
 
 // ---------------------------------------------------------------------------
 // dispatch
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCtas = 16;
+constexpr int kSortThreads = 1024, kSortWarps = 32, kSortCtas = 128;
 constexpr int kKeep = 8;  // rounds whose ranks stay in registers between the two passes
 
 // Lanes of the warp with the same key (0 <= key < 2^bits), by one ballot a
@@ -332,43 +342,66 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(const int3
     }
 }
 
-// More pairs: the CTAs of one cluster take consecutive runs of them, and each
-// warp a run of its CTA's, so that a pair's rank among its expert's pairs is
-// (earlier CTAs) + (earlier warps) + (earlier rounds) + (lower lanes): stable,
-// and free of atomics.  The CTAs read each other's counts per expert through
-// distributed shared memory.
-__global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* idx, int n, int top_k, int E, int bits,
-                                                                int32_t* offsets, int32_t* row_of_pair,
-                                                                int32_t* token_of_row, int32_t* group_of_row) {
-    extern __shared__ int cnt[];  // [kSortWarps][E] per warp, then [E] of the CTA
+// More pairs, two kernels: up to kSortCtas CTAs take consecutive runs of the
+// pairs, and each warp a run of its CTA's.  The first counts each CTA's pairs
+// per expert.  In the second a pair's place is (earlier CTAs) + (earlier warps)
+// + (earlier rounds) + (lower lanes): stable, whatever runs first.  Its ranks
+// within the CTA need nothing of the first kernel, so they are formed before it
+// has finished; after that come the sums over the CTAs' counts and the
+// scattered stores (a sector each, about one a cycle of an SM: the reason for
+// many CTAs.  One cluster of 16 took 9.6 us for 40960 pairs, these 7.7).
+struct SortArgs {
+    const int32_t* idx;
+    int n, top_k, E, bits, ctas;
+    int64_t seg;  // pairs of a warp, a multiple of 32
+    int32_t *offsets, *row_of_pair, *token_of_row, *group_of_row;
+    int32_t* counts;  // [ctas][E]
+};
+
+__device__ __forceinline__ int sort_key(const SortArgs& a, int64_t p, int64_t end) {
+    const int e = p < end ? a.idx[p] : -1;
+    return e >= 0 && e < a.E ? e : -1;
+}
+
+__global__ void __launch_bounds__(kSortThreads) dispatch_count_kernel(const SortArgs a) {
+    extern __shared__ int hist[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < a.E; e += kSortThreads) hist[e] = 0;
+    after_previous();
+    let_next_start();  // after the wait: the next kernel may read idx at once
+    const int64_t p0 = ((int64_t)blockIdx.x * kSortWarps + warp) * a.seg, p1 = min(p0 + a.seg, (int64_t)a.n);
+    __syncthreads();
+    for (int64_t p = p0 + lane; p - lane < p1; p += 32) {
+        const int key = sort_key(a, p, p1);
+        const unsigned peers = peers_of(key < 0 ? a.E : key, a.bits);
+        if (key >= 0 && lane == __ffs(peers) - 1) atomicAdd(hist + key, __popc(peers));  // a sum: order does not matter
+    }
+    __syncthreads();
+    for (int e = tid; e < a.E; e += kSortThreads) a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
+}
+
+__global__ void __launch_bounds__(kSortThreads) dispatch_place_kernel(const SortArgs a) {
+    extern __shared__ int cnt[];  // [kSortWarps][E] per warp, then [2][parts][E] sums of the counts
     __shared__ int warp_tot[kSortWarps];
     let_next_start();
-    int* const cta_cnt = cnt + kSortWarps * E;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int me = (int)cluster.block_rank();
-    const int64_t seg = ((int64_t)n + kSortCtas * kSortThreads - 1) / (kSortCtas * kSortThreads) * 32;
-    const int64_t p0 = ((int64_t)me * kSortWarps + warp) * seg, p1 = p0 + seg < n ? p0 + seg : n;
-    const bool keep = seg <= 32 * kKeep;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.E;
+    int* const sums = cnt + kSortWarps * E;
+    const int64_t p0 = ((int64_t)blockIdx.x * kSortWarps + warp) * a.seg, p1 = min(p0 + a.seg, (int64_t)a.n);
+    const bool keep = a.seg <= 32 * kKeep;
     int* mine = cnt + warp * E;
     int key_r[kKeep], rank_r[kKeep];
-    auto key_at = [&](int64_t p) {
-        const int e = p < p1 ? idx[p] : -1;
-        return e >= 0 && e < E ? e : -1;
-    };
     // rank among the warp's pairs of this expert so far; counts them
     auto take = [&](int key) {
-        const unsigned peers = peers_of(key < 0 ? E : key, bits);
+        const unsigned peers = peers_of(key < 0 ? E : key, a.bits);
         const int r = key >= 0 ? mine[key] : 0, lower = __popc(peers & ((1u << lane) - 1));
         __syncwarp();
         if (key >= 0 && lower == 0) mine[key] = r + __popc(peers);
         __syncwarp();
         return r + lower;
     };
-    after_previous();
     if (keep)
 #pragma unroll
-        for (int j = 0; j < kKeep; ++j) key_r[j] = key_at(p0 + 32 * j + lane);
+        for (int j = 0; j < kKeep; ++j) key_r[j] = sort_key(a, p0 + 32 * j + lane, p1);
     for (int i = lane; i < E; i += 32) mine[i] = 0;
     __syncwarp();
     if (keep) {
@@ -376,52 +409,61 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
         for (int j = 0; j < kKeep; ++j)
             if (p0 + 32 * j < p1) rank_r[j] = take(key_r[j]);
     } else {
-        for (int64_t p = p0 + lane; p - lane < p1; p += 32) take(key_at(p));
+        for (int64_t p = p0 + lane; p - lane < p1; p += 32) take(sort_key(a, p, p1));
     }
     __syncthreads();
-    int own = 0;
-    if (tid < E) {
+    if (tid < E) {  // the warps' first places within the CTA
+        int own = 0;
 #pragma unroll 8
         for (int w = 0; w < kSortWarps; ++w) {
             const int c = cnt[w * E + tid];
             cnt[w * E + tid] = own;
             own += c;
         }
-        cta_cnt[tid] = own;
     }
-    cluster.sync();
-    int total = 0, earlier = 0;  // of this expert: all CTAs, CTAs before this one
-    if (tid < E) {
-        int c[kSortCtas];  // all loads in flight: a remote one takes several hundred cycles
-#pragma unroll
-        for (int r = 0; r < kSortCtas; ++r) c[r] = cluster.map_shared_rank(cta_cnt, r)[tid];
-#pragma unroll
-        for (int r = 0; r < kSortCtas; ++r) {
-            total += c[r];
-            if (r < me) earlier += c[r];
+    after_previous();
+    // each expert's pairs in all CTAs and in those before this one, by `parts` threads per expert
+    int parts = 1;
+    while (2 * parts * E <= kSortThreads) parts *= 2;
+    const int part = tid / E, e = tid - part * E;
+    if (part < parts) {
+        int total = 0, earlier = 0;
+#pragma unroll 8
+        for (int r = part; r < a.ctas; r += parts) {
+            const int c = a.counts[(int64_t)r * E + e];
+            total += c;
+            earlier += r < (int)blockIdx.x ? c : 0;
         }
+        sums[part * E + e] = total;
+        sums[(parts + part) * E + e] = earlier;
     }
-    auto counts_read = cluster.barrier_arrive();
+    __syncthreads();
+    int total = 0, earlier = 0;
+    if (tid < E)
+        for (int q = 0; q < parts; ++q) {
+            total += sums[q * E + tid];
+            earlier += sums[(parts + q) * E + tid];
+        }
     const int incl = warp_scan(total, lane);
     if (lane == 31) warp_tot[warp] = incl;
     __syncthreads();
     if (warp == 0) warp_tot[lane] = warp_scan(warp_tot[lane], lane);
     __syncthreads();
     const int kept = warp_tot[kSortWarps - 1];
+    int* const base = sums;  // the CTA's first place of each expert
     if (tid < E) {
         const int at = (warp ? warp_tot[warp - 1] : 0) + incl - total;
-        if (me == 0) offsets[tid] = at;
-#pragma unroll 8
-        for (int w = 0; w < kSortWarps; ++w) cnt[w * E + tid] += at + earlier;
+        base[tid] = at + earlier;
+        if (blockIdx.x == 0) a.offsets[tid] = at;
     }
-    if (tid == 0 && me == 0) offsets[E] = kept;
+    if (tid == 0 && blockIdx.x == 0) a.offsets[E] = kept;
     __syncthreads();
     auto put = [&](int64_t p, int key, int row) {
         if (p >= p1) return;
-        row_of_pair[p] = key >= 0 ? row : -1;
+        a.row_of_pair[p] = key >= 0 ? row : -1;
         if (key >= 0) {
-            token_of_row[row] = (int)((uint32_t)p / (uint32_t)top_k);
-            group_of_row[row] = key;
+            a.token_of_row[row] = (int)((uint32_t)p / (uint32_t)a.top_k);
+            a.group_of_row[row] = key;
         }
     };
     if (keep) {
@@ -429,20 +471,20 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const int32_t* i
         for (int j = 0; j < kKeep; ++j)
             if (p0 + 32 * j < p1) {
                 const int key = key_r[j];
-                // the rank was counted from the warp's own zero: its count here is the warp's first row
-                put(p0 + 32 * j + lane, key, key >= 0 ? mine[key] + rank_r[j] : -1);
+                // the rank was counted from the warp's own zero: its count here is the warp's first place
+                put(p0 + 32 * j + lane, key, key >= 0 ? base[key] + mine[key] + rank_r[j] : -1);
             }
     } else {
         for (int64_t p = p0 + lane; p - lane < p1; p += 32) {
-            const int key = key_at(p);
-            put(p, key, take(key));
+            const int key = sort_key(a, p, p1);
+            const int r = take(key);
+            put(p, key, key >= 0 ? base[key] + r : -1);
         }
     }
-    for (int64_t r = kept + (int64_t)me * kSortThreads + tid; r < n; r += kSortCtas * kSortThreads) {
-        token_of_row[r] = -1;
-        group_of_row[r] = -1;
+    for (int64_t r = kept + (int64_t)blockIdx.x * kSortThreads + tid; r < a.n; r += (int64_t)gridDim.x * kSortThreads) {
+        a.token_of_row[r] = -1;
+        a.group_of_row[r] = -1;
     }
-    cluster.barrier_wait(std::move(counts_read));  // no CTA leaves while its counts are read
 }
 
 // ---------------------------------------------------------------------------
@@ -548,14 +590,24 @@ cudaError_t combine_typed(const void* rows, int64_t rows_ld, const int32_t* row_
 cudaError_t launch_route(const moe_route_config& c, const void* logits, int type, int64_t ld, const float* bias,
                          int64_t T, int32_t* idx, float* w, cudaStream_t st) {
     const int S = c.n_experts / c.n_groups;
-    RouteArgs a{logits, bias, idx, w, ld, T, c, (uint32_t)(((1 << 20) + S - 1) / S)};
+    int log2 = 0;
+    while ((2 << log2) * c.n_groups <= 32) ++log2;
+    RouteArgs a{logits, bias, idx, w, ld, T, c, (uint32_t)(((1 << 20) + S - 1) / S), S, log2};
     return type == MOE_F32 ? route_typed<float>(a, st) : route_typed<__nv_bfloat16>(a, st);
 }
 
-size_t dispatch_workspace(int64_t, int) { return 0; }
+// CTAs of the two-kernel sort: at least one round of 32 pairs per warp each
+static int sort_ctas(int64_t pairs) {
+    const int64_t n = (pairs + kSortThreads - 1) / kSortThreads;
+    return (int)(n < kSortCtas ? n : kSortCtas);
+}
+
+size_t dispatch_workspace(int64_t pairs, int n_experts) {
+    return pairs <= kSortThreads ? 0 : (size_t)sort_ctas(pairs) * n_experts * sizeof(int32_t);
+}
 
 cudaError_t launch_dispatch(const int32_t* idx, int64_t pairs, int top_k, int n_experts, int32_t* offsets,
-                            int32_t* row_of_pair, int32_t* token_of_row, int32_t* group_of_row, void*,
+                            int32_t* row_of_pair, int32_t* token_of_row, int32_t* group_of_row, void* ws,
                             cudaStream_t st) {
     int bits = 1;  // ids 0 .. n_experts, the last for a dropped pair
     while ((n_experts >> bits) != 0) ++bits;
@@ -568,13 +620,15 @@ cudaError_t launch_dispatch(const int32_t* idx, int64_t pairs, int top_k, int n_
         return launch(dispatch_small_kernel, 1, threads, smem, st, 1, idx, n, top_k, n_experts, bits, offsets,
                       row_of_pair, token_of_row, group_of_row);
     }
-    const int smem = (kSortWarps + 1) * n_experts * (int)sizeof(int);
-    const void* kernel = reinterpret_cast<const void*>(dispatch_kernel);
-    if ((e = smem_limit(kernel, smem)) != cudaSuccess) return e;
-    // 16 CTAs are past the portable cluster size of 8
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-    return launch(dispatch_kernel, kSortCtas, kSortThreads, smem, st, kSortCtas, idx, (int)pairs, top_k, n_experts, bits,
-                  offsets, row_of_pair, token_of_row, group_of_row);
+    SortArgs a{idx, (int)pairs, top_k, n_experts, bits, sort_ctas(pairs), 0, offsets, row_of_pair, token_of_row, group_of_row,
+               static_cast<int32_t*>(ws)};
+    a.seg = (pairs + (int64_t)a.ctas * kSortThreads - 1) / ((int64_t)a.ctas * kSortThreads) * 32;
+    int parts = 1;
+    while (2 * parts * n_experts <= kSortThreads) parts *= 2;
+    const int smem = (kSortWarps + 2 * parts) * n_experts * (int)sizeof(int);
+    if ((e = smem_limit(reinterpret_cast<const void*>(dispatch_place_kernel), smem)) != cudaSuccess) return e;
+    e = launch(dispatch_count_kernel, a.ctas, kSortThreads, n_experts * sizeof(int), st, 1, a);
+    return e != cudaSuccess ? e : launch(dispatch_place_kernel, a.ctas, kSortThreads, smem, st, 1, a);
 }
 
 cudaError_t launch_combine(const void* rows, int rows_type, int64_t rows_ld, const int32_t* row_of_pair, const float* w,

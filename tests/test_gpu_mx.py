@@ -141,8 +141,8 @@ def test_route_masks_and_extremes(score, biased):
     np.testing.assert_allclose(got_w[live].sum(1), 1, rtol=1e-6)
 
 
-def test_route_of_many_tokens_is_the_route_of_each():
-    E, k = 512, 10
+@pytest.mark.parametrize("E,k", [(512, 10), (1024, 32), (100, 3)])
+def test_route_of_many_tokens_is_the_route_of_each(E, k):
     torch.manual_seed(0)
     logits = torch.randn(5003, E, device="cuda")
     cfg = moe.make_route_config(E, k)
