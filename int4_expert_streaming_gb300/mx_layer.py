@@ -1,0 +1,107 @@
+"""A routed expert layer in microscaled 4-bit floats, out of the operators without a context:
+
+  logits -> moe_route -> moe_dispatch -> moe_mx_quantise (token rows, in expert order) -> moe_mx_product (gate and up)
+         -> moe_mx_quantise (SwiGLU) -> moe_mx_product (down) -> moe_combine
+
+``python -m int4_expert_streaming_gb300.mx_layer`` runs one layer of the 512-expert shapes on random weights and prints
+its time; ``MxLayer`` is the same as a class, and an example of how the calls go together: what is laid out once, what
+is sized by the largest batch, and what each call is given.
+"""
+from __future__ import annotations
+
+import torch
+
+import int4_expert_streaming_gb300 as moe
+
+
+def quantise_weights(w, fmt: int):
+    """w [groups, rows, cols] (fp32 or bf16, CUDA) -> (matrix, tensor scales [groups] or None).  An e4m3 scale has a
+    narrow range, so each group's largest weight is brought to the largest product of code and scale, 6 * 448."""
+    E, N, K = w.shape
+    m = moe.make_mx(fmt, N, K, groups=E)
+    t = (w.abs().amax((1, 2)).float() / (6 * 448)).clamp(min=1e-30) if fmt == moe.MOE_MX_E4M3 else None
+    moe.moe_mx_quantise(m, w.reshape(E * N, K), tensor_scale=t, stream=torch.cuda.current_stream())
+    return m, t
+
+
+class MxLayer:
+    """gate_up [E, 2 * inter, hidden] (gate rows, then up rows of each expert), down [E, hidden, inter]; cfg as of
+    make_route_config; max_tokens sizes the buffers.  One call at a time per object."""
+
+    def __init__(self, gate_up, down, cfg: moe.moe_route_config, max_tokens: int, router_bias=None,
+                 fmt: int = moe.MOE_MX_E4M3):
+        E, two_inter, hidden = gate_up.shape
+        if down.shape != (E, hidden, two_inter // 2) or cfg.n_experts != E:
+            raise ValueError(f"gate_up {tuple(gate_up.shape)}, down {tuple(down.shape)} and {cfg.n_experts} experts do "
+                             "not go together")
+        self.cfg, self.fmt, self.max_tokens, self.bias = cfg, fmt, max_tokens, router_bias
+        self.E, self.hidden, self.inter = E, hidden, two_inter // 2
+        self.gate_up, self.alpha_up = quantise_weights(gate_up, fmt)
+        self.down, self.alpha_down = quantise_weights(down, fmt)
+        pairs, k = max_tokens * cfg.top_k, cfg.top_k
+
+        def i32(*shape):
+            return torch.empty(shape, dtype=torch.int32, device="cuda")
+        self.idx, self.w = i32(max_tokens, k), torch.empty((max_tokens, k), device="cuda")
+        self.offsets, self.row_of_pair = i32(E + 1), i32(max_tokens, k)
+        self.token_of_row, self.group_of_row = i32(pairs), i32(pairs)
+        # a smaller batch needs no more CTAs than the largest one
+        self.workspace = torch.empty(max(1, moe.moe_dispatch_workspace(max_tokens, k, E)), dtype=torch.uint8, device="cuda")
+        self.x = moe.make_mx(fmt, pairs, hidden, groups=E, ragged=True)
+        self.h = moe.make_mx(fmt, pairs, self.inter, groups=E, ragged=True)
+        self.up = torch.empty((pairs, two_inter), dtype=torch.bfloat16, device="cuda")
+        self.out = torch.empty((pairs, hidden), dtype=torch.bfloat16, device="cuda")
+
+    def forward(self, x, logits, y):
+        """x [T, hidden] and logits [T, E] (fp32 or bf16) -> y [T, hidden] (fp32 or bf16), on the current stream."""
+        T, k, st = x.shape[0], self.cfg.top_k, torch.cuda.current_stream()
+        n = T * k
+        if T > self.max_tokens:
+            raise ValueError(f"{T} tokens, room for {self.max_tokens}")
+        idx, w, rop = self.idx[:T], self.w[:T], self.row_of_pair[:T]
+        tor, gor = self.token_of_row[:n], self.group_of_row[:n]
+        moe.moe_route(self.cfg, logits, self.bias, idx, w, st)
+        moe.moe_dispatch(idx, self.E, self.offsets, rop, tor, gor, self.workspace, st)
+        mx, mh = self._batch(self.x, n), self._batch(self.h, n)
+        moe.moe_mx_quantise(mx, x, src_row=tor, group_of_row=gor, offsets=self.offsets, stream=st)
+        moe.moe_mx_product(mx, self.gate_up, self.up[:n], offsets=self.offsets, alpha=self.alpha_up, stream=st)
+        moe.moe_mx_quantise(mh, self.up[:n], act=moe.MOE_ACT_SWIGLU, group_of_row=gor, offsets=self.offsets, stream=st)
+        moe.moe_mx_product(mh, self.down, self.out[:n], offsets=self.offsets, alpha=self.alpha_down, stream=st)
+        moe.moe_combine(self.out[:n], rop, w, y, st)
+        return y
+
+    @staticmethod
+    def _batch(m: moe.moe_mx, rows: int) -> moe.moe_mx:
+        """The same data, for a batch of fewer rows."""
+        return moe.moe_mx(m.data_dev, rows, m.cols, m.groups, m.format, m.ragged)
+
+
+def main() -> None:
+    E, k, hidden, inter = 512, 10, 2048, 512
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def normal(*shape, sigma=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * sigma).to(torch.bfloat16)
+    layer = MxLayer(normal(E, 2 * inter, hidden, sigma=0.02), normal(E, hidden, inter, sigma=0.02),
+                    moe.make_route_config(E, k), max_tokens=4096)
+    for T in (1, 8, 64, 4096):
+        x, logits = normal(T, hidden), normal(T, E).float()
+        y = torch.empty((T, hidden), device="cuda")
+        for _ in range(3):
+            layer.forward(x, logits, y)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            layer.forward(x, logits, y)
+        graph.replay()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(50):
+            graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        print(f"{T} tokens: {a.elapsed_time(b) * 20:.1f} us a layer")
+
+
+if __name__ == "__main__":
+    main()
