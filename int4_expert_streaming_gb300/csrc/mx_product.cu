@@ -67,7 +67,7 @@ struct ProductArgs {
     int* status;
 };
 
-// NT = 256: a pair of CTAs (M = 256); NT = 64: one CTA
+// NT, the most rows of a tile: 256 a pair of CTAs (M = 256), 128 and 64 one CTA
 template <int FMT, int NT>
 struct Cfg {
     static constexpr bool kPair = NT == 256;
@@ -560,11 +560,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             fence_after_sync();
             // Pieces of 32 columns, kept in the output's type until all of the tile has been read.  A large tile's slots
             // are the halves; in a small one each half has 64 columns of the slot.
-            constexpr int kPieces = NT > 128 ? 4 : 1;
+            constexpr int kHalf = (NT < 128 ? NT : 128) / 2, kPieces = PAIR ? 4 : kHalf / 32;
             constexpr int kRegs = sizeof(TY) == 2 ? 16 : 32;
             constexpr int kBatch = sizeof(TY) == 2 ? kPieces : (kPieces > 2 ? 2 : kPieces);
-            const int first = half * (ti.n > 128 ? 128 : NT > 128 ? 64 : 32);
-            const int mine = min(ti.n - first, ti.n > 128 ? 128 : NT > 128 ? 64 : 32);  // this warp's rows, if any
+            const int first = half * (ti.n > 128 ? 128 : kHalf);
+            const int mine = min(ti.n - first, ti.n > 128 ? 128 : kHalf);  // this warp's rows, if any
             const uint32_t src = trow + (m == 2 ? 128u : 0u) + first;
             const int64_t col = (int64_t)(ti.wt + (int)rank) * 128 + 32 * q + lane;
             TY* const y = static_cast<TY*>(a.y) + (ti.row0 + first) * a.y_ld + col;
@@ -655,25 +655,39 @@ cudaError_t device_state(DeviceState& out) {
     return cudaSuccess;
 }
 
+// Row tiles of an upper bound: a group's rows are known to the GPU only.
+int64_t most_row_tiles(const ProductArgs& a, int nt) {
+    if (!a.offsets) return (a.x_rows + nt - 1) / nt;
+    return a.x_rows / nt + (a.groups < a.x_rows ? a.groups : a.x_rows);
+}
+
 template <int FMT, int NT, typename TY>
 cudaError_t launch_typed(ProductArgs& a, int sms, cudaStream_t st) {
     using C = Cfg<FMT, NT>;
     const int smem = C::kStages * C::kStage + 1024 + (a.offsets ? a.groups * 8 + 4 : 0);
     cudaError_t e = smem_limit(reinterpret_cast<const void*>(product_kernel<FMT, NT, TY>), smem);
     if (e != cudaSuccess) return e;
-    const int64_t row_tiles = a.offsets ? a.x_rows / NT + (a.groups < a.x_rows ? a.groups : a.x_rows)
-                                        : (a.x_rows + NT - 1) / NT;
     a.w_units = C::kPair ? (a.w_tiles + 1) / 2 : a.w_tiles;
-    const int64_t tiles = row_tiles * a.w_units, units = C::kPair ? sms / 2 : sms;
+    const int64_t tiles = most_row_tiles(a, NT) * a.w_units, units = C::kPair ? sms / 2 : sms;
     if (tiles > INT32_MAX || tiles / units * a.steps > INT32_MAX / 2) return cudaErrorInvalidValue;
     const unsigned n = (unsigned)(tiles < units ? tiles : units);
     return launch(product_kernel<FMT, NT, TY>, C::kPair ? 2 * n : n, kThreads, smem, st, C::kPair ? 2 : 1, a);
 }
 
-// few rows: a short row tile leaves shared memory for more steps in flight
+// The variant, by sizes alone (times in us, E4M3, bf16 y; pair | one CTA):
+//   - A pair's tile (256 features x 256 rows) feeds the tensor cores best: groups of 512 rows x 1024 x 2048
+//     70.8 | 81.4, of 200 76.1 | 83.5.
+//   - It needs more than 64 rows a group on average (a mixed batch of 80 rows a group 75.0 | 78.9, of 40 59.1 | 58.9),
+//   - at least 4 steps, because its tiles cost more to begin and end (80 rows a group x 2048 x 512 91.9 | 71.0),
+//   - and enough tiles for most of the SMs (512 x 4096 x 4096: 32 pairs 11.5 | 8.9; 1024 rows: 64 pairs 12.4 | 13.7).
+//   - Up to 64 rows in all, a shorter row tile leaves shared memory for one more step in flight: 80 experts of one
+//     row 15.6 instead of 16.2.
 template <int FMT, typename TY>
 cudaError_t launch_rows(ProductArgs& a, int sms, cudaStream_t st) {
-    return a.x_rows <= 64 ? launch_typed<FMT, 64, TY>(a, sms, st) : launch_typed<FMT, 256, TY>(a, sms, st);
+    if (a.x_rows <= 64) return launch_typed<FMT, 64, TY>(a, sms, st);
+    const bool pair = a.steps >= 4 && a.x_rows > 64 * (int64_t)a.groups &&
+                      most_row_tiles(a, 256) * ((a.w_tiles + 1) / 2) * 8 >= 3 * sms;
+    return pair ? launch_typed<FMT, 256, TY>(a, sms, st) : launch_typed<FMT, 128, TY>(a, sms, st);
 }
 
 }  // namespace

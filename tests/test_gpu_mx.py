@@ -398,6 +398,20 @@ def test_dense_product_matches_definition(fmt, R, N, K, ydt):
 
 
 @pytest.mark.parametrize("fmt", [E8, E4])
+@pytest.mark.parametrize("R,N,K", [(1300, 4000, 1100), (2049, 8192 - 3, 1024), (700, 12000, 1024), (769, 3000, 2048)])
+def test_large_dense_product_matches_definition(fmt, R, N, K):
+    """Enough tiles for pairs of CTAs, an odd last feature tile, row tiles of every remainder."""
+    check_product(fmt, R, N, K, torch.bfloat16, alpha=True)
+
+
+@pytest.mark.parametrize("fmt", [E8, E4])
+@pytest.mark.parametrize("sizes", [[400, 0, 1, 255, 256, 257, 129, 128, 127, 700, 33, 16, 0, 512], [300] * 9])
+@pytest.mark.parametrize("ydt", [torch.float32, torch.bfloat16])
+def test_large_groups_match_definition(fmt, sizes, ydt):
+    check_product(fmt, sizes, 1500, 1024, ydt, alpha=True, extra_rows=3)
+
+
+@pytest.mark.parametrize("fmt", [E8, E4])
 @pytest.mark.parametrize("pad", [1, 4, 8])
 def test_product_into_strided_rows(fmt, pad):
     check_product(fmt, 70, 200, 320, torch.bfloat16, pad=pad)
