@@ -26,6 +26,9 @@
 //   warps 2-5   scales: shared memory -> tensor memory, lane quarter w % 4
 //   warps 6-13  epilogue: tensor memory -> registers -> y; lane quarter w % 4,
 //               two warps per quarter take the halves of the columns
+// Where the tiles are too few for the SMs, a cluster shares one tile: each CTA
+// takes a run of its steps, and at the end every CTA adds up a part of the
+// results from all of the cluster's shared memories, in CTA order.
 // The loops of warps 0 and 1 are chains of dependent instructions, and a step
 // with few rows lasts about as long as one of them; so they run warp-wide
 // (uniform registers), keep running counters instead of divisions, and only
@@ -113,6 +116,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+// four floats at a shared-memory offset of CTA `rank` of the cluster
+__device__ __forceinline__ float4 load_remote(uint32_t saddr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(saddr), "r"(rank)
+        : "memory");
+    return v;
 }
 // the same shared-memory offset in CTA 0 of the pair
 __device__ __forceinline__ uint32_t leader_addr(uint32_t saddr) {
@@ -297,10 +315,11 @@ struct Slots {
     }
 };
 
-template <int FMT, int NT, typename TY>
+template <int FMT, int NT, typename TY, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs a) {
     using C = Cfg<FMT, NT>;
     constexpr bool PAIR = C::kPair;
+    static_assert(!(PAIR && SPLIT), "a pair's tile is not split");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t full[C::kStages], empty[C::kStages], scales_full[C::kStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tmem_s;
@@ -376,8 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     else __syncthreads();
     fence_after_sync();
     const uint32_t tmem = tmem_s;
-    const int unit = (int)blockIdx.x / (PAIR ? 2 : 1), units = (int)gridDim.x / (PAIR ? 2 : 1);
-    const int my_tiles = (n_tiles - unit + units - 1) / units;  // <= 0: none
+    const int parts = SPLIT ? (int)cluster_size() : 1, part = SPLIT ? (int)cluster_rank() : 0;
+    const int unit = (int)blockIdx.x / (PAIR ? 2 : parts), units = (int)gridDim.x / (PAIR ? 2 : parts);
+    const int my_tiles = (n_tiles - unit + units - 1) / units;  // <= 0: none; a split has at most one
+    // this CTA's steps of a tile
+    const int k_first = SPLIT ? (int)((int64_t)a.steps * part / parts) : 0;
+    const int k_count = (SPLIT ? (int)((int64_t)a.steps * (part + 1) / parts) : a.steps) - k_first;
 
     // Arrival at the CTA that issues the MMAs.  From CTA 1 it is relaxed: what it announces are accesses to tensor
     // memory, which the fences before and after it order, and copies that have already landed in shared memory.  A
@@ -425,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                     d1 = C::kOffXs + C::kScaleBytes;
                 }
             }
-            for (int k = 0; k < a.steps; ++k) {
+            if (SPLIT) p0 += (int64_t)k_first * C::kTile;
+            for (int k = 0; k < k_count; ++k) {
                 if (!warp_wait(&empty[s], ph, &abort_s)) {
                     fail(a, &abort_s);
                     ok = false;
@@ -448,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     } else if (warp == 1 && rank == 1) {
         // -------------- CTA 1 of a pair: forwards its scale warps' arrivals, and so spares them the remote access
         uint32_t s = 0, ph = 0;
-        const int steps = my_tiles * a.steps;
+        const int steps = my_tiles * k_count;
         for (int it = 0; it < steps; ++it) {
             if (!warp_wait(&scales_full[s], ph, &abort_s)) {
                 fail(a, &abort_s);
@@ -470,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         uint32_t wd = w_lo, sc = tmem + kScaleCol;
         for (int i = 0; i < my_tiles && ok; ++i) {
             uint32_t d = 0, idesc = 0, m = 0;
-            for (int k = 0; k < a.steps; ++k) {
+            for (int k = 0; k < k_count; ++k) {
                 // the scales' warps have seen the step's copies land before they arrive here
                 ok = warp_wait(&scales_full[s], ph, &abort_s);
                 if (k == 0 && ok) {
@@ -511,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         // --------------------------------------------------------------- scales
         const uint32_t quarter = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         uint32_t s = 0, ph = 0;
-        const int steps = my_tiles * a.steps;
+        const int steps = my_tiles * k_count;
         for (int it = 0; it < steps; ++it) {
             if (!warp_wait(&full[s], ph, &abort_s)) {
                 fail(a, &abort_s);
@@ -566,6 +590,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             const int first = half * (ti.n > 128 ? 128 : kHalf);
             const int mine = min(ti.n - first, ti.n > 128 ? 128 : kHalf);  // this warp's rows, if any
             const uint32_t src = trow + (m == 2 ? 128u : 0u) + first;
+            if constexpr (SPLIT) {
+                // the ring is idle: the part's sums to shared memory as [row][128 features]
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p)
+                    if (32 * p < mine) {
+                        uint32_t raw[32];
+                        tmem_ld32(src + 32 * p, raw);
+                        tmem_ld_wait();
+                        const uint32_t to = smem0 + ((first + 32 * p) * 128 + 32 * q + lane) * 4;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + j * 512), "r"(raw[j]) : "memory");
+                    }
+                continue;
+            }
             const int64_t col = (int64_t)(ti.wt + (int)rank) * 128 + 32 * q + lane;
             TY* const y = static_cast<TY*>(a.y) + (ti.row0 + first) * a.y_ld + col;
             const bool in = col < a.w_rows;
@@ -615,8 +654,31 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         }
     }
 
+    if constexpr (SPLIT) {
+        // four features of a row a thread, a run of them for each CTA
+        __syncwarp();
+        cluster_sync();
+        if (my_tiles > 0) {
+            const Tile ti = find_tile<NT>(a, cum, offs, unit, lane);
+            const float alpha = a.alpha ? a.alpha[ti.g] : 1.0f;
+            const int end = ti.n * 32 * (part + 1) / parts;
+            for (int i = ti.n * 32 * part / parts + tid; i < end; i += kThreads) {
+                float4 sum = load_remote(smem0 + i * 16, 0);
+                for (int r = 1; r < parts; ++r) {
+                    const float4 v = load_remote(smem0 + i * 16, (uint32_t)r);
+                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                }
+                const float v[4] = {sum.x * alpha, sum.y * alpha, sum.z * alpha, sum.w * alpha};
+                const int64_t col = (int64_t)ti.wt * 128 + (i & 31) * 4;
+                TY* const y = static_cast<TY*>(a.y) + (ti.row0 + (i >> 5)) * a.y_ld + col;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (col + j < a.w_rows) y[j] = (TY)v[j];
+            }
+        }
+    }
     fence_before_sync();
-    if (PAIR) cluster_sync();  // nothing of the other CTA's is under way here any more
+    if (PAIR || SPLIT) cluster_sync();  // nothing of the other CTAs' is under way here any more, nor read
     else __syncthreads();
     fence_after_sync();
     if (warp == 1) free_columns<PAIR>(tmem, kTmemCols);
@@ -661,17 +723,19 @@ int64_t most_row_tiles(const ProductArgs& a, int nt) {
     return a.x_rows / nt + (a.groups < a.x_rows ? a.groups : a.x_rows);
 }
 
-template <int FMT, int NT, typename TY>
-cudaError_t launch_typed(ProductArgs& a, int sms, cudaStream_t st) {
+// parts > 1: clusters of that many CTAs share a tile, one tile each
+template <int FMT, int NT, typename TY, bool SPLIT = false>
+cudaError_t launch_typed(ProductArgs& a, int sms, cudaStream_t st, unsigned parts = 1) {
     using C = Cfg<FMT, NT>;
     const int smem = C::kStages * C::kStage + 1024 + (a.offsets ? a.groups * 8 + 4 : 0);
-    cudaError_t e = smem_limit(reinterpret_cast<const void*>(product_kernel<FMT, NT, TY>), smem);
+    cudaError_t e = smem_limit(reinterpret_cast<const void*>(product_kernel<FMT, NT, TY, SPLIT>), smem);
     if (e != cudaSuccess) return e;
     a.w_units = C::kPair ? (a.w_tiles + 1) / 2 : a.w_tiles;
     const int64_t tiles = most_row_tiles(a, NT) * a.w_units, units = C::kPair ? sms / 2 : sms;
     if (tiles > INT32_MAX || tiles / units * a.steps > INT32_MAX / 2) return cudaErrorInvalidValue;
     const unsigned n = (unsigned)(tiles < units ? tiles : units);
-    return launch(product_kernel<FMT, NT, TY>, C::kPair ? 2 * n : n, kThreads, smem, st, C::kPair ? 2 : 1, a);
+    const unsigned cluster = C::kPair ? 2 : parts;
+    return launch(product_kernel<FMT, NT, TY, SPLIT>, n * cluster, kThreads, smem, st, cluster, a);
 }
 
 // The variant, by sizes alone (times in us, E4M3, bf16 y; pair | one CTA):
@@ -680,10 +744,19 @@ cudaError_t launch_typed(ProductArgs& a, int sms, cudaStream_t st) {
 //   - It needs more than 64 rows a group on average (a mixed batch of 80 rows a group 75.0 | 78.9, of 40 59.1 | 58.9),
 //   - at least 4 steps, because its tiles cost more to begin and end (80 rows a group x 2048 x 512 91.9 | 71.0),
 //   - and enough tiles for most of the SMs (512 x 4096 x 4096: 32 pairs 11.5 | 8.9; 1024 rows: 64 pairs 12.4 | 13.7).
+//   - Long rows and few tiles: a cluster of 2, 4 or 8 CTAs splits a tile's steps.  That costs 1.4 us, so it takes 16
+//     steps (1 row x 4096 x 4096 6.5 unsplit, 5.7 with 4) or 24 (128 rows x 1024 x 8192 12.2, 8.6; 1 row 9.9, 5.4 with
+//     8; at 8 steps 4.5, 4.9).  Clusters of 8 do not fill the GPU, since an SM group holds two: 16 of them took two
+//     rounds.
 //   - Up to 64 rows in all, a shorter row tile leaves shared memory for one more step in flight: 80 experts of one
 //     row 15.6 instead of 16.2.
 template <int FMT, typename TY>
 cudaError_t launch_rows(ProductArgs& a, int sms, cudaStream_t st) {
+    if (a.steps >= (a.x_rows <= 32 ? 16 : 24)) {
+        const int64_t tiles = most_row_tiles(a, 128) * a.w_tiles;
+        const int parts = tiles * 8 <= sms / 2 ? 8 : tiles * 4 <= sms ? 4 : tiles * 2 <= sms ? 2 : 1;
+        if (parts > 1) return launch_typed<FMT, 128, TY, true>(a, sms, st, parts);
+    }
     if (a.x_rows <= 64) return launch_typed<FMT, 64, TY>(a, sms, st);
     const bool pair = a.steps >= 4 && a.x_rows > 64 * (int64_t)a.groups &&
                       most_row_tiles(a, 256) * ((a.w_tiles + 1) / 2) * 8 >= 3 * sms;

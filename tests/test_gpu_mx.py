@@ -405,6 +405,15 @@ def test_large_dense_product_matches_definition(fmt, R, N, K):
 
 
 @pytest.mark.parametrize("fmt", [E8, E4])
+@pytest.mark.parametrize("sizes,N,K", [(1, 1024, 8192), (1, 300, 4096), (7, 4096, 4100), (33, 1000, 6400), (128, 1024, 8192),
+                                       (200, 130, 6300), (300, 1024, 6144 + 255), ([1, 0, 3], 500, 8000), ([40, 90], 127, 7000)])
+@pytest.mark.parametrize("ydt", [torch.float32, torch.bfloat16])
+def test_long_rows_split_over_a_cluster(fmt, sizes, N, K, ydt):
+    """Few tiles and many steps: clusters of 2, 4 and 8 CTAs share a tile, with steps that do not divide evenly."""
+    check_product(fmt, sizes, N, K, ydt, alpha=True, pad=3)
+
+
+@pytest.mark.parametrize("fmt", [E8, E4])
 @pytest.mark.parametrize("sizes", [[400, 0, 1, 255, 256, 257, 129, 128, 127, 700, 33, 16, 0, 512], [300] * 9])
 @pytest.mark.parametrize("ydt", [torch.float32, torch.bfloat16])
 def test_large_groups_match_definition(fmt, sizes, ydt):
