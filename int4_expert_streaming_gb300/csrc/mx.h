@@ -56,13 +56,15 @@ struct MxRows {
     const int32_t* offsets;
     int64_t rows;       // rows to walk
     int64_t per_group;  // uniform: rows per group
+    int groups;
     __device__ __forceinline__ bool place(int64_t r, int& g, int64_t& tile, int& in) const {
         int64_t q;
         if (group_of_row) {
             g = group_of_row[r];
-            if (g < 0) return false;
+            if (g < 0 || g >= groups) return false;
             const int o = offsets[g];
             q = r - o;
+            if (o < 0 || q < 0) return false;  // maps that do not belong together: nothing is written out of range
             tile = (o >> 7) + g + (q >> 7);
         } else if (rows == per_group) {
             g = 0;

@@ -48,6 +48,7 @@ MxRows rows_of(const moe_mx* m, const int32_t* group_of_row, const int32_t* offs
     r.offsets = offsets;
     r.rows = m->ragged ? m->rows : m->rows * m->groups;
     r.per_group = m->rows;
+    r.groups = m->groups;
     return r;
 }
 

@@ -358,8 +358,9 @@ struct SortArgs {
     int32_t* counts;  // [ctas][E]
 };
 
+// read past L1: the second kernel reads idx before it has waited for the first
 __device__ __forceinline__ int sort_key(const SortArgs& a, int64_t p, int64_t end) {
-    const int e = p < end ? a.idx[p] : -1;
+    const int e = p < end ? __ldcg(a.idx + p) : -1;
     return e >= 0 && e < a.E ? e : -1;
 }
 
