@@ -10,29 +10,39 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kChunk = 16;  // columns of a thread: one E4M3 block, half an E8M0 block
 
-// 16 consecutive columns as they were loaded: unpacked only when they are
-// needed, so that several rows' loads can be under way
-template <typename T>
+// 16 consecutive columns of a row for each of 16 threads, as they were loaded:
+// unpacked only when they are needed, so that the next row's loads can be under
+// way.  Rows that are not aligned for 16-byte loads are loaded value by value,
+// thread c taking columns c, c + 16, ..., so that the threads' loads share
+// sectors, and change hands in shared memory (pitch 17: no bank conflicts).
+// 16384 rows of 2047 columns to e8m0: bf16 31 us, fp32 27 (of 2048: 15 and 24).
+constexpr int kSwap = 16 * 17;  // floats of a row
+
+template <typename T, bool WIDE>
 struct Raw {
-    uint4 q[sizeof(T)];  // 4 x fp32 quads, 2 x bf16 octets
-    __device__ __forceinline__ void load(const T* p, int n, bool wide) {
+    uint4 q[sizeof(T)];  // 16 values
+    // p: column 0 of the 256; n: of them in the row (256 or fewer); c: this thread's place
+    __device__ __forceinline__ void load(const T* p, int n, int c) {
         constexpr int kPer = 16 / (int)sizeof(T);  // values of a quad
-        if (wide && n >= 16) {
+        if (WIDE && n >= 16 * c + 16) {
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(T); ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
+            for (int i = 0; i < (int)sizeof(T); ++i) q[i] = reinterpret_cast<const uint4*>(p + 16 * c)[i];
         } else {
 #pragma unroll
             for (int i = 0; i < (int)sizeof(T); ++i) {
                 T t[kPer];
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) t[j] = i * kPer + j < n ? p[i * kPer + j] : (T)0.0f;
+                for (int j = 0; j < kPer; ++j) {
+                    const int col = WIDE ? 16 * c + i * kPer + j : 16 * (i * kPer + j) + c;
+                    t[j] = col < n ? p[col] : (T)0.0f;
+                }
                 memcpy(&q[i], t, 16);
             }
         }
     }
-    __device__ __forceinline__ void get(float (&v)[16]) const {
+    // swap: the row's kSwap floats, used where the loads were not wide (by all 16 threads)
+    __device__ __forceinline__ void get(float (&v)[16], int c, float* swap) const {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T); ++i) {
             const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
@@ -46,11 +56,19 @@ struct Raw {
                 }
             }
         }
+        if constexpr (!WIDE) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) swap[17 * j + c] = v[j];
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = swap[17 * c + j];
+        }
     }
 };
 
-__device__ __forceinline__ void store8(float* p, int n, bool wide, const float (&v)[8]) {
-    if (wide && n >= 8) {
+__device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
+    if (n >= 8) {
         reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
         reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
@@ -59,8 +77,8 @@ __device__ __forceinline__ void store8(float* p, int n, bool wide, const float (
             if (i < n) p[i] = v[i];
     }
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int n, bool wide, const float (&v)[8]) {
-    if (wide && n >= 8) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int n, const float (&v)[8]) {
+    if (n >= 8) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -141,15 +159,17 @@ __device__ __forceinline__ uint32_t scale_at(int in, int atom) {
 // step: r = x / d to a few units of the last place, then
 // r + (x - r d) / d, the remainder exact in one fma.  Where x / d is itself a
 // short number, as a tie between two codes is, the result is exactly that.
-template <typename T, int FMT, bool SWIGLU>
+template <typename T, int FMT, bool SWIGLU, bool WIDE>
 __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
     after_previous();
     let_next_start();
+    __shared__ float swap_s[WIDE ? 1 : kRows * kSwap];
     const int c16 = threadIdx.x & 15;
-    const int col = blockIdx.y * kMxTileCols + c16 * kChunk;
+    float* const swap = swap_s + (WIDE ? 0 : (threadIdx.x >> 4) * kSwap);
+    const int col = blockIdx.y * kMxTileCols;
     const int64_t stride = (int64_t)gridDim.x * kRows, first = (int64_t)blockIdx.x * kRows;
     int64_t r = first + (threadIdx.x >> 4);
-    Raw<T> x, up;
+    Raw<T, WIDE> x, up;
     bool live;
     // the row's values: they do not wait for its place in the tiles
     auto fetch = [&](int64_t row) {
@@ -157,8 +177,8 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
         live = from >= 0;
         const int n = live ? a.cols - col : 0;
         const T* p = static_cast<const T*>(a.src) + (live ? from * a.ld + col : 0);
-        x.load(p, n, a.wide);
-        if (SWIGLU) up.load(p + a.cols, n, a.wide);
+        x.load(p, n, c16);
+        if (SWIGLU) up.load(p + a.cols, n, c16);
     };
     fetch(r);
     for (int64_t at = first; at < a.rows.rows; at += stride, r += stride) {
@@ -166,10 +186,10 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
         int64_t tile = 0;
         const bool mine = live && a.rows.place(r, g, tile, in);
         float v[16];
-        x.get(v);
+        x.get(v, c16, swap);
         if (SWIGLU) {
             float u[16];
-            up.get(u);
+            up.get(u, c16, swap);
             if (at + stride < a.rows.rows) fetch(r + stride);
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = silu_mul(v[j], u[j]);
@@ -235,11 +255,15 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
 // the first is needed.  Eight rows a warp where that still fills the GPU
 // (40960 x 512 to bf16: 11.5 us, with two 14.1), else one (64 rows of 2048
 // columns: 1.7 us instead of 2.9).
+__device__ __forceinline__ __half2 e2m1_pair(uint32_t byte) {
+    return __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(byte & 0xffu), __NV_E2M1));
+}
+
 template <typename T, int FMT, int ROWS>
 __global__ void __launch_bounds__(kThreads) dequantise_kernel(const QuantArgs a) {
     after_previous();
     let_next_start();
-    const int lane = threadIdx.x & 31, col = blockIdx.y * kMxTileCols + 8 * lane, n = a.cols - col;
+    const int lane = threadIdx.x & 31, col = blockIdx.y * kMxTileCols, n = a.cols - col;  // columns of the row from here on
     const int64_t r0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * ROWS;
     const int b = FMT == MOE_MX_E8M0 ? lane >> 2 : lane >> 1;
     int g = 0, in = 0;
@@ -252,7 +276,8 @@ __global__ void __launch_bounds__(kThreads) dequantise_kernel(const QuantArgs a)
     for (int i = 0; i < ROWS; ++i) {
         const int in_i = __shfl_sync(kAll, in, i);
         const int64_t tile_i = __shfl_sync(kAll, tile, i);
-        if (!(live >> i & 1) || n <= 0) continue;
+        codes[i] = byte[i] = 0;
+        if (!(live >> i & 1)) continue;
         const uint8_t* base = a.data + (tile_i * a.col_tiles + blockIdx.y) * (int64_t)mx_tile_bytes(FMT);
         codes[i] = *reinterpret_cast<const uint32_t*>(base + in_i * 128 + (((lane >> 2) ^ (in_i & 7)) << 4) + (lane & 3) * 4);
         byte[i] = base[scale_at(in_i, b >> 2) + (b & 3)];
@@ -260,25 +285,37 @@ __global__ void __launch_bounds__(kThreads) dequantise_kernel(const QuantArgs a)
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const float t = __shfl_sync(kAll, t_own, i);
-        if (!(live >> i & 1) || n <= 0) continue;
+        if (!(live >> i & 1)) continue;
         float s;
         if (FMT == MOE_MX_E8M0)
             s = byte[i] == 255 ? __uint_as_float(0x7fffffffu)
                                : byte[i] ? __uint_as_float(byte[i] << 23) : __uint_as_float(0x400000u);
         else
             s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte[i], __NV_E4M3)));
-        float v[8];
+        T* const row = static_cast<T*>(a.dst) + (r0 + i) * a.ld + col;
+        if (a.wide) {
+            float v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __half2 h =
-                __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(codes[i] >> (8 * j) & 0xffu), __NV_E2M1));
-            v[2 * j] = __low2float(h) * s;
-            v[2 * j + 1] = __high2float(h) * s;
+            for (int j = 0; j < 4; ++j) {
+                const __half2 h = e2m1_pair(codes[i] >> (8 * j));
+                v[2 * j] = __low2float(h) * s;
+                v[2 * j + 1] = __high2float(h) * s;
+            }
+            if (a.tscale)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= t;
+            store8(row + 8 * lane, n - 8 * lane, v);
+        } else {
+            // columns 32 j + lane, from the lane that holds them: stores of neighbours share sectors
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int from = 4 * j + (lane >> 3), c = 32 * j + lane;
+                const uint32_t word = __shfl_sync(kAll, codes[i], from);
+                const float sj = __shfl_sync(kAll, s, from);
+                const float v = __low2float(e2m1_pair(word >> (4 * (lane & 7)) & 15u)) * sj;
+                if (c < n) row[c] = (T)(a.tscale ? v * t : v);
+            }
         }
-        if (a.tscale)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= t;
-        store8(static_cast<T*>(a.dst) + (r0 + i) * a.ld + col, n, a.wide, v);
     }
 }
 
@@ -291,10 +328,12 @@ int sm_count() {
         return 1;  // the launch itself will say what is wrong
     return sms;
 }
-// about as many blocks as fit the GPU at a time (four of 256 threads on an SM)
-dim3 walk_grid(const QuantArgs& a) {
+// Blocks that stay and walk: four of 256 threads on an SM with SwiGLU, as many as fit at a time (40960 x 512: 19.5 us,
+// with six 23.5); eight without, where less work hides less of the loads (16384 x 2048 bf16 to e8m0: 15.2 us, with
+// four 18.5).
+dim3 walk_grid(const QuantArgs& a, bool swiglu) {
     dim3 g = grid_of(a, kRows);
-    const unsigned most = (unsigned)((4 * sm_count() + a.col_tiles - 1) / a.col_tiles);
+    const unsigned most = (unsigned)(((swiglu ? 4 : 8) * sm_count() + a.col_tiles - 1) / a.col_tiles);
     if (g.x > most) g.x = most;
     return g;
 }
@@ -309,8 +348,10 @@ cudaError_t dequantise_rows(const QuantArgs& a, cudaStream_t st) {
 
 template <typename T, int FMT>
 cudaError_t quantise_act(const QuantArgs& a, int act, cudaStream_t st) {
-    if (act == MOE_ACT_SWIGLU) return launch(quantise_kernel<T, FMT, true>, walk_grid(a), kThreads, 0, st, 1, a);
-    return launch(quantise_kernel<T, FMT, false>, walk_grid(a), kThreads, 0, st, 1, a);
+    const bool swiglu = act == MOE_ACT_SWIGLU;
+    return launch(a.wide ? (swiglu ? quantise_kernel<T, FMT, true, true> : quantise_kernel<T, FMT, false, true>)
+                         : (swiglu ? quantise_kernel<T, FMT, true, false> : quantise_kernel<T, FMT, false, false>),
+                  walk_grid(a, swiglu), kThreads, 0, st, 1, a);
 }
 
 // whole 16-byte loads or stores need every 16-column chunk of every row aligned

@@ -493,97 +493,126 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_place_kernel(const Sort
 // ---------------------------------------------------------------------------
 constexpr int kCombineThreads = 128;
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// V consecutive values by one load or store of at most 16 bytes (eight fp32: two)
+template <int V>
+__device__ __forceinline__ void load_v(const float* p, float* v) {
+    if constexpr (V == 8) {
+        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else if constexpr (V == 2) {
+        const float2 a = *reinterpret_cast<const float2*>(p);
+        v[0] = a.x, v[1] = a.y;
+    } else {
+        v[0] = *p;
     }
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+template <int V>
+__device__ __forceinline__ void load_v(const __nv_bfloat16* p, float* v) {
+    uint32_t w[(V + 1) / 2];
+    if constexpr (V == 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else if constexpr (V == 2) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+        w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+}
+template <int V>
+__device__ __forceinline__ void store_v(float* p, const float* v) {
+    if constexpr (V == 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    } else {
+        *p = v[0];
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_v(__nv_bfloat16* p, const float* v) {
+    uint32_t w[(V + 1) / 2];
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[i], i + 1 < V ? v[i + 1] : 0.0f);
+        w[i / 2] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
 }
 
-// A CTA takes 8 x 128 columns of one token, a thread 8 of them: memory-bound,
-// so the loads are 16 bytes wide and four rows' are in flight at a time.
-// WIDE = false: any alignment, 128 columns of a token per CTA.
-template <typename TI, typename TO, bool WIDE>
+// A thread takes kPieces<V> pieces of V columns of one token, V as the alignment
+// allows: memory-bound, so loads are wide and four rows'
+// are in flight at a time.  4096 tokens of 10 rows of 2048 bf16: 32.8 us with
+// V = 8 (6.1 TB/s); of 2046 with 2 43.6, of 2047 with 1 50.7.
+template <int V>
+constexpr int kPieces = V == 8 ? 1 : V == 2 ? 2 : 4;
+
+template <typename TI, typename TO, int V>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const TI* rows, int64_t rows_ld,
                                                                   const int32_t* row_of_pair, const float* w, int top_k,
                                                                   int cols, TO* y, int64_t y_ld) {
-    constexpr int V = WIDE ? 8 : 1;
+    constexpr int U = kPieces<V>, W = U * V;
     after_previous();
     let_next_start();
     const int64_t t = blockIdx.x;
-    const int col = (blockIdx.y * kCombineThreads + threadIdx.x) * V;
+    const int col = blockIdx.y * (W * kCombineThreads) + threadIdx.x * V;  // pieces kCombineThreads * V apart
     if (col >= cols) return;
     row_of_pair += t * top_k;
     w += t * top_k;
-    float acc[V] = {};
+    float acc[W] = {};
     int j = 0;
     auto add = [&](int n) {  // n <= 4 rows from j on
-        float v[4][V], wj[4];
+        float v[4][W], wj[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = i < n ? row_of_pair[j + i] : -1;
-            wj[i] = i < n ? w[j + i] : 0.0f;
+            wj[i] = r >= 0 ? w[j + i] : 0.0f;
+            const TI* p = rows + (r >= 0 ? r * rows_ld : 0) + col;
 #pragma unroll
-            for (int q = 0; q < V; ++q) v[i][q] = 0.0f;
-            if (r >= 0) {
-                const TI* p = rows + r * rows_ld + col;
-                if constexpr (WIDE) load8(p, v[i]);
-                else v[i][0] = to_f32(*p);
-            } else {
-                wj[i] = 0.0f;
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int q = 0; q < V; ++q) v[i][u * V + q] = 0.0f;
+                if (r >= 0 && col + u * kCombineThreads * V < cols) load_v<V>(p + u * kCombineThreads * V, v[i] + u * V);
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int q = 0; q < V; ++q) acc[q] = fmaf(wj[i], v[i][q], acc[q]);
+            for (int q = 0; q < W; ++q) acc[q] = fmaf(wj[i], v[i][q], acc[q]);
         j += n;
     };
     while (top_k - j >= 4) add(4);
     if (j < top_k) add(top_k - j);
     TO* out = y + t * y_ld + col;
-    if constexpr (WIDE) store8(out, acc);
-    else *out = (TO)acc[0];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (col + u * kCombineThreads * V < cols) store_v<V>(out + u * kCombineThreads * V, acc + u * V);
 }
 
-// 8 columns at a time need whole, aligned 16-byte pieces in every row of both
+// pieces of V need whole, aligned ones in every row
 template <typename T>
-bool wide_rows(const void* p, int64_t ld, int cols) {
-    return cols % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
+bool pieces_ok(const void* p, int64_t ld, int cols, int V) {
+    const int64_t bytes = V * (int64_t)sizeof(T) < 16 ? V * (int64_t)sizeof(T) : 16;
+    return cols % V == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * (int64_t)sizeof(T) % bytes == 0;
 }
 
 template <typename TI, typename TO>
 cudaError_t combine_typed(const void* rows, int64_t rows_ld, const int32_t* row_of_pair, const float* w, int64_t T,
                           int top_k, int cols, void* y, int64_t y_ld, cudaStream_t st) {
-    const bool wide = wide_rows<TI>(rows, rows_ld, cols) && wide_rows<TO>(y, y_ld, cols);
-    const int per = kCombineThreads * (wide ? 8 : 1);
-    const int64_t chunks = ((int64_t)cols + per - 1) / per;
-    if (chunks > 65535) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)T, (unsigned)chunks);
-    const TI* in = static_cast<const TI*>(rows);
-    TO* out = static_cast<TO*>(y);
-    return launch(wide ? combine_kernel<TI, TO, true> : combine_kernel<TI, TO, false>, grid, kCombineThreads, 0, st, 1, in,
-                  rows_ld, row_of_pair, w, top_k, cols, out, y_ld);
+    auto both = [&](int V) { return pieces_ok<TI>(rows, rows_ld, cols, V) && pieces_ok<TO>(y, y_ld, cols, V); };
+    auto run = [&](auto kernel, int per) {
+        const int64_t chunks = ((int64_t)cols + per * kCombineThreads - 1) / (per * kCombineThreads);
+        if (chunks > 65535) return cudaErrorInvalidValue;
+        return launch(kernel, dim3((unsigned)T, (unsigned)chunks), kCombineThreads, 0, st, 1, static_cast<const TI*>(rows),
+                      rows_ld, row_of_pair, w, top_k, cols, static_cast<TO*>(y), y_ld);
+    };
+    if (both(8)) return run(combine_kernel<TI, TO, 8>, 8 * kPieces<8>);
+    if (both(2)) return run(combine_kernel<TI, TO, 2>, 2 * kPieces<2>);
+    return run(combine_kernel<TI, TO, 1>, kPieces<1>);
 }
 
 }  // namespace
