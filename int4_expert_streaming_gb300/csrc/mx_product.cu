@@ -762,15 +762,14 @@ cudaError_t launch_typed(ProductArgs& a, int sms, cudaStream_t st, unsigned part
 //   - and enough tiles for most of the SMs (512 x 4096 x 4096: 32 pairs 11.5 | 8.9; 1024 rows: 64 pairs 12.4 | 13.7).
 //   - Long rows and few tiles: a cluster of 2, 4 or 8 CTAs splits a tile's steps.  That costs 1.4 us, so it takes 16
 //     steps (1 row x 4096 x 4096 6.5 unsplit, 5.7 with 4) or 24 (128 rows x 1024 x 8192 12.2, 8.6; 1 row 9.9, 5.4 with
-//     8; at 8 steps 4.5, 4.9).  Clusters of 8 do not fill the GPU, since an SM group holds two: 16 of them took two
-//     rounds.
+//     8; at 8 steps 4.5, 4.9).  Clusters of 8 and 4 do not fill the GPU (15 and 36 fit at a time: the bounds on tiles).
 //   - Up to 64 rows in all, a shorter row tile leaves shared memory for one more step in flight: 80 experts of one
 //     row 15.6 instead of 16.2.
 template <int FMT, typename TY>
 cudaError_t launch_rows(ProductArgs& a, int sms, cudaStream_t st) {
     if (a.steps >= (a.x_rows <= 32 ? 16 : 24)) {
         const int64_t tiles = most_row_tiles(a, 128) * a.w_tiles;
-        const int parts = tiles * 8 <= sms / 2 ? 8 : tiles * 4 <= sms ? 4 : tiles * 2 <= sms ? 2 : 1;
+        const int parts = tiles * 8 <= sms / 2 ? 8 : tiles * 4 * 10 <= sms * 9 ? 4 : tiles * 2 <= sms ? 2 : 1;
         if (parts > 1) return launch_typed<FMT, 128, TY, true>(a, sms, st, parts);
     }
     if (a.x_rows <= 64) return launch_typed<FMT, 64, TY>(a, sms, st);

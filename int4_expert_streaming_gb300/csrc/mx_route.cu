@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_place_kernel(const Sort
     const int part = tid / E, e = tid - part * E;
     if (part < parts) {
         int total = 0, earlier = 0;
-#pragma unroll 8
+#pragma unroll 20
         for (int r = part; r < a.ctas; r += parts) {
             const int c = a.counts[(int64_t)r * E + e];
             total += c;
