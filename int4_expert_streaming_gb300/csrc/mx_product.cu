@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             }
             if (SPLIT) p0 += (int64_t)k_first * C::kTile;
             for (int k = 0; k < k_count; ++k) {
-                if (!warp_wait(&empty[s], ph, &abort_s)) {
+                if (filled >= C::kStages && !warp_wait(&empty[s], ph, &abort_s)) {  // at first every stage is free
                     fail(a, &abort_s);
                     ok = false;
                     break;
@@ -650,19 +650,24 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                     }
                 }
                 if (in) {
+                    // runs of eight rows for small tiles, where few rows then take few instructions (1 row: 0.2 us);
+                    // a pair's tiles are mostly full, and longer runs keep more stores going (8 rows: 79 us, not 73)
+                    constexpr int kRun = PAIR ? 32 : 8;
 #pragma unroll
-                    for (int p = 0; p < kBatch; ++p) {
-                        TY* yp = y + (int64_t)(32 * (p0 + p)) * a.y_ld;
-                        const int rows = mine - 32 * (p0 + p);
-                        if (rows >= 32) {
+                    for (int p = 0; p < kBatch; ++p)
 #pragma unroll
-                            for (int j = 0; j < 32; ++j, yp += a.y_ld) put(yp, v[p], j);
-                        } else if (rows > 0) {
+                        for (int c = 0; c < 32; c += kRun) {
+                            const int rows = mine - 32 * (p0 + p) - c;
+                            TY* yp = y + (int64_t)(32 * (p0 + p) + c) * a.y_ld;
+                            if (rows >= kRun) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j, yp += a.y_ld)
-                                if (j < rows) put(yp, v[p], j);
+                                for (int j = 0; j < kRun; ++j, yp += a.y_ld) put(yp, v[p], c + j);
+                            } else if (rows > 0) {
+#pragma unroll
+                                for (int j = 0; j < kRun; ++j, yp += a.y_ld)
+                                    if (j < rows) put(yp, v[p], c + j);
+                            }
                         }
-                    }
                 }
                 __syncwarp();
             }
