@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             }
             if (SPLIT) p0 += (int64_t)k_first * C::kTile;
             for (int k = 0; k < k_count; ++k) {
-                if (filled >= C::kStages && !warp_wait(&empty[s], ph, &abort_s)) {  // at first every stage is free
+                if (!warp_wait(&empty[s], ph, &abort_s)) {
                     fail(a, &abort_s);
                     ok = false;
                     break;
@@ -627,19 +627,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
 #pragma unroll
             for (int p0 = 0; p0 < kPieces; p0 += kBatch) {
                 uint32_t v[kBatch][kRegs];
+                constexpr int kTwo = PAIR && kBatch > 1 ? 2 : 1;  // pieces read at a time
 #pragma unroll
-                for (int p = 0; p < kBatch; ++p)
+                for (int p = 0; p < kBatch; p += kTwo)
                     if (32 * (p0 + p) < mine) {
-                        uint32_t raw[32];
-                        tmem_ld32(src + 32 * (p0 + p), raw);
+                        uint32_t raw[kTwo][32];
+#pragma unroll
+                        for (int t = 0; t < kTwo; ++t) tmem_ld32(src + 32 * (p0 + p + t), raw[t]);  // within the slots
                         tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < kRegs; ++j) {
-                            if constexpr (sizeof(TY) == 2)
-                                v[p][j] = pack_bf16(__uint_as_float(raw[2 * j]) * alpha, __uint_as_float(raw[2 * j + 1]) * alpha);
-                            else
-                                v[p][j] = __float_as_uint(__uint_as_float(raw[j]) * alpha);
-                        }
+                        for (int t = 0; t < kTwo; ++t)
+#pragma unroll
+                            for (int j = 0; j < kRegs; ++j) {
+                                if constexpr (sizeof(TY) == 2)
+                                    v[p + t][j] = pack_bf16(__uint_as_float(raw[t][2 * j]) * alpha, __uint_as_float(raw[t][2 * j + 1]) * alpha);
+                                else
+                                    v[p + t][j] = __float_as_uint(__uint_as_float(raw[t][j]) * alpha);
+                            }
                     }
                 if (p0 + kBatch >= kPieces) {  // all read: the slots may be overwritten
                     fence_before_sync();
@@ -650,9 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                     }
                 }
                 if (in) {
-                    // runs of eight rows for small tiles, where few rows then take few instructions (1 row: 0.2 us);
-                    // a pair's tiles are mostly full, and longer runs keep more stores going (8 rows: 79 us, not 73)
-                    constexpr int kRun = PAIR ? 32 : 8;
+                    // Rows are stored in runs of 32: the longest keeps most stores going (512 groups of 80 rows x 2048 x
+                    // 512: 73 us, runs of 8 82).  Where the whole product has at most 64 rows, runs of 8: few rows then
+                    // take few instructions (1 row x 1024 x 256: 3.0 us, not 3.2).
+                    constexpr int kRun = NT == 64 ? 8 : 32;
 #pragma unroll
                     for (int p = 0; p < kBatch; ++p)
 #pragma unroll
