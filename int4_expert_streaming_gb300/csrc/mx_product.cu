@@ -37,14 +37,16 @@
 // most 128 rows takes one slot, a larger one both.  A slot is free again as
 // soon as it has been read into registers.
 // Measured (random codes, bf16 y):
-//   7937 x 8192 x 8192   160 us, 6.7 PFLOP/s; with neither copies nor stores the
-//               MMAs alone take 137: a pair's step is 590 cycles of MMA against
-//               512 at the nominal rate, shared memory moving 68 KB in it; long
-//               runs are also held by the power limit
+//   7937 x 8192 x 8192   160 us, 6.7 PFLOP/s (145 in a CUDA graph of 21 calls);
+//               without copies and stores an earlier build of the pair took 138:
+//               a step is about 590 cycles of MMA against 512 at the nominal
+//               rate, probably because shared memory moves 68 KB in it; long
+//               runs are probably held by the power limit as well
 //   40960 rows of 206 experts of mixed sizes x 1024 x 2048 (E4M3)   73 us for
-//               374 MB; the copies alone take 60: 634 MB from L2 to the SMs, at
-//               low reuse, and a large tile's eight steps are followed by 1000
-//               cycles in which its accumulators are read
+//               374 MB: 634 MB from L2 to the SMs at low reuse (without MMAs and
+//               stores 60 in an earlier build that took 78), and a large tile's
+//               eight steps are followed by 1000 cycles in which its
+//               accumulators are read
 //   64 rows of 58 experts x 1024 x 2048 (E8M0)   15 us for 65 MB: 4 us to begin
 //               and end, the rest at 6.1 TB/s
 // Every wait is bounded; one that runs out sets a status word in mapped host

@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(const int3
 // within the CTA need nothing of the first kernel, so they are formed before it
 // has finished; after that come the sums over the CTAs' counts and the
 // scattered stores (a sector each, about one a cycle of an SM: the reason for
-// many CTAs.  One cluster of 16 took 9.6 us for 40960 pairs, these 7.7).
+// many CTAs.  One cluster of 16 took 9.6 us for 40960 pairs, these 7.1).
 struct SortArgs {
     const int32_t* idx;
     int n, top_k, E, bits, ctas;
