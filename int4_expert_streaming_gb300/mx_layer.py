@@ -100,6 +100,9 @@ class MxLayer:
         """x [T, hidden] and logits [T, E] (fp32 or bf16) -> y [T, hidden] (fp32 or bf16), on the current stream."""
         T, k, st = x.shape[0], self.cfg.top_k, torch.cuda.current_stream()
         n = T * k
+        if tuple(x.shape) != (T, self.hidden) or tuple(logits.shape) != (T, self.E) or tuple(y.shape) != (T, self.hidden):
+            raise ValueError(f"x {tuple(x.shape)}, logits {tuple(logits.shape)} and y {tuple(y.shape)} do not go together "
+                             f"in a layer of {self.E} experts and width {self.hidden}")
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens, room for {self.max_tokens}")
         idx, w, rop = self.idx[:T], self.w[:T], self.row_of_pair[:T]
