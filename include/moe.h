@@ -415,9 +415,9 @@ size_t moe_mx_bytes(const moe_mx* m);
 
 /*
  * Quantise rows into m.  Per block, with a = max |x| and t = the group's
- * tensor scale (MOE_MX_E4M3 only; tensor_scale_dev fp32 [groups], NULL = 1):
+ * tensor scale (MOE_MX_E4M3 only; tensor_scale_dev fp32 [groups], not negative, NULL = 1):
  *   E8M0: scale 2^(floor(log2 a) - 2), at least 2^-127;  code = e2m1(x / scale)
- *   E4M3: scale s = e4m3(a / (6 t)), at most 448;        code = e2m1(x / (s t)), 0 where s is 0
+ *   E4M3: scale s = e4m3(a / (6 t)), at most 448, 0 for a block of zeros;  code = e2m1(x / (s t)), 0 where s t is 0
  * both roundings to nearest even, e2m1 saturating at 6; quotients, 6 t and
  * s t are fp32.  A block with a NaN or an infinity gets a NaN scale and zero
  * codes.

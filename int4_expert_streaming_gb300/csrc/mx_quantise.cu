@@ -212,8 +212,9 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
             for (int j = 0; j < 16; ++j) v[j] *= inv;
         } else {
             const float t = a.tscale && mine ? a.tscale[g] : 1.0f;
+            // a block of zeros has scale 0 also where t is 0
             const __nv_fp8_storage_t s =
-                __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f * t), __NV_SATFINITE, __NV_E4M3);
+                __nv_cvt_float_to_fp8(__fdiv_rn(amax, amax > 0.0f ? 6.0f * t : 1.0f), __NV_SATFINITE, __NV_E4M3);
             byte = s;
             const float d = __half2float(__half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3))) * t;
             const float inv = d > 0.0f ? __frcp_rn(d) : 0.0f;
