@@ -218,18 +218,18 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
             byte = s;
             const float d = __half2float(__half(__nv_cvt_fp8_to_halfraw(s, __NV_E4M3))) * t;
             const float inv = d > 0.0f ? __frcp_rn(d) : 0.0f;
-            if (SWIGLU) {  // the activation is not exact to the last place either
+            if (inv >= 1e30f) {  // scales so small that a remainder could be subnormal, or the reciprocal infinite
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __fdiv_rn(v[j], d);
+            } else if (SWIGLU) {  // the activation is not exact to the last place either
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] *= inv;
-            } else if (inv < 1e30f) {
+            } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float q = v[j] * inv;
                     v[j] = fmaf(fmaf(-q, d, v[j]), inv, q);
                 }
-            } else {  // scales so small that the remainder could be subnormal
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = __fdiv_rn(v[j], d);
             }
         }
         uint32_t out[2] = {codes8(v), codes8(v + 8)};

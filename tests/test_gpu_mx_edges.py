@@ -1,4 +1,4 @@
-"""The operators without a context at the edges of what they take: tensor scales of zero."""
+"""The operators without a context at the edges of what they take: tensor scales of zero and next to zero."""
 import numpy as np
 import pytest
 
@@ -53,3 +53,17 @@ def test_a_tensor_scale_of_zero_gives_no_nan(cols, dtype):
     y = torch.full((3, 5), 7.0, device="cuda")
     moe.moe_mx_product(x, m, y, offsets=cuda(np.arange(4, dtype=np.int32)), alpha=t)
     assert (y[0] == 0).all() and (y[2] == 0).all() and y.isfinite().all()
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_swiglu_zeros_stay_zeros_at_the_smallest_scales(dtype):
+    """A block whose scale times the tensor scale has no reciprocal in fp32."""
+    cols, t = 48, 2.0 ** -120
+    src = np.zeros((1, 2 * cols), np.float32)
+    src[0, :cols] = 2.0 ** -63
+    src[0, cols:] = np.where(np.arange(cols) % 3 == 0, 2.0 ** -63, 0)  # silu(g) u = 2^-127, or 0
+    m = moe.make_mx(moe.MOE_MX_E4M3, 1, cols)
+    moe.moe_mx_quantise(m, cuda(src).to(dtype), act=moe.MOE_ACT_SWIGLU, tensor_scale=cuda(np.array([t], np.float32)))
+    code, byte = rows_of(m, 1, 1, cols)
+    # a / (6 t) = 2^-7 / 6, two thirds of the smallest scale 2^-9: the scale is 2^-9, the values 2^-127 / 2^-129 = 4
+    assert (byte[0, :3] == 1).all()
+    assert np.array_equal(code[0, :cols] & 7, np.where(np.arange(cols) % 3 == 0, 6, 0))
