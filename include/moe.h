@@ -320,7 +320,7 @@ int moe_route_noalloc(moe_ctx* ctx, int32_t layer, const float* x_dev, int32_t B
  *   - Calls run on the current device, asynchronously on `stream`; nothing is
  *     allocated per call and every buffer (workspace included) is the
  *     caller's.  They can be captured into a graph; the first moe_mx_product
- *     of a process on a device sets up a status word and should come before.
+ *     of a process on a device sets up a count and should come before.
  *   - Strides (`ld`) are in elements between rows; rows are contiguous.
  *   - moe_last_error(NULL) gives the message of this host thread's last failure.
  *   - Zero rows or tokens are legal and do what the formula says for none.
@@ -443,11 +443,26 @@ int moe_mx_dequantise(const moe_mx* m, const int32_t* group_of_row_dev, const in
  *   w  uniform, w->rows = columns of y; same format and cols as x
  *   alpha_dev fp32 [groups] (tensor scale of x times tensor scale of w) or NULL = 1
  *   y_dev MOE_F32 or MOE_BF16 [x->rows x w->rows], stride y_ld >= w->rows
- * A wait inside the kernel that runs out (a second) ends the call's work early; the next moe_mx_product on that device
- * returns MOE_ETIMEOUT.
+ * Waits inside the kernel are bounded (a second).  Where one runs out, y stays incomplete although the call has
+ * returned: moe_mx_timeouts tells.
  */
 int moe_mx_product(const moe_mx* x, const moe_mx* w, const int32_t* offsets_dev, const float* alpha_dev, void* y_dev,
                    int32_t y_type, int64_t y_ld, void* stream);
+
+/*
+ * How often a product on the current device was cut short since the process began: *count is larger than at an earlier
+ * reading if and only if a wait of a moe_mx_product ran out in between, in a call or in the replay of a graph.  To be
+ * read once the stream in question has been synchronised; no reading changes it, and no call is refused because of it.
+ * A device's first moe_mx_timeouts or moe_mx_product sets up the count.
+ */
+int moe_mx_timeouts(uint64_t* count);
+
+/*
+ * Fault injection for tests, for the calls of this host thread from now on: with MOE_FAULT_DEVICE_WAIT every
+ * moe_mx_product with more than one step (256 columns of one tile) contains a wait that nothing ends, and its waits are
+ * bounded by 1 ms.  The kernel ends normally.  0 ends it.
+ */
+int moe_mx_set_fault(uint32_t fault_flags);
 
 /*
  * y[t] = sum_j w[t, j] * rows[row_of_pair[t, j]] in fp32, j ascending; pairs

@@ -38,7 +38,7 @@ EXPORTS = (
     "moe_set_router_bias", "moe_set_router_bias_all", "moe_forward_decode", "moe_forward_decode_stack", "moe_forward_prefill",
     "moe_pool_stats", "moe_pool_reset", "moe_pool_trace", "moe_launch_count", "moe_prefill_profile", "moe_prefill_kernel_ms", "moe_route_noalloc", "moe_last_error", "moe_slotpool_create", "moe_slotpool_destroy",
     "moe_route", "moe_dispatch_workspace", "moe_dispatch", "moe_mx_bytes", "moe_mx_quantise", "moe_mx_dequantise",
-    "moe_mx_product", "moe_combine",
+    "moe_mx_product", "moe_mx_timeouts", "moe_mx_set_fault", "moe_combine",
     "moe_slotpool_request", "moe_store_create", "moe_store_write_layer", "moe_store_info", "moe_store_read",
 )
 
@@ -131,6 +131,8 @@ def load_library(path: str | None = None):
         lib.moe_mx_quantise.argtypes = [mx, vp, i32, i64, i32, vp, vp, vp, vp, vp]
         lib.moe_mx_dequantise.argtypes = [mx, vp, vp, vp, vp, i32, i64, vp]
         lib.moe_mx_product.argtypes = [mx, mx, vp, vp, vp, i32, i64, vp]
+        lib.moe_mx_timeouts.argtypes = [c.POINTER(c.c_uint64)]
+        lib.moe_mx_set_fault.argtypes = [c.c_uint32]
         lib.moe_combine.argtypes = [vp, i32, i64, vp, vp, i64, i32, i32, vp, i32, i64, vp]
         for name in EXPORTS:
             if name not in ("moe_destroy", "moe_slotpool_destroy", "moe_blob_bytes", "moe_blob_stride",
@@ -430,6 +432,19 @@ def moe_mx_product(x: moe_mx, w: moe_mx, y, offsets=None, alpha=None, stream=Non
     rc = (_ops or _binding()).product(x, w, y, offsets, alpha, stream)
     if rc:
         _check(rc)
+
+
+def moe_mx_timeouts() -> int:
+    """Grows when a wait inside a product on the current device has run out and left its y incomplete; read it after a
+    synchronise and compare."""
+    n = ctypes.c_uint64()
+    _check(load_library().moe_mx_timeouts(n))
+    return n.value
+
+
+def moe_mx_set_fault(fault_flags: int) -> None:
+    """Tests only: this thread's products get a wait that nothing ends (MOE_FAULT_DEVICE_WAIT), or none (0)."""
+    _check(load_library().moe_mx_set_fault(fault_flags))
 
 
 def moe_combine(rows, row_of_pair, w, y, stream=None) -> None:

@@ -94,8 +94,9 @@ cudaError_t launch_mx_quantise(const moe_mx& m, const MxRows& rows, const void* 
                                const int32_t* src_row, const float* tscale, cudaStream_t st);
 cudaError_t launch_mx_dequantise(const moe_mx& m, const MxRows& rows, const float* tscale, void* dst, int type,
                                  int64_t ld, cudaStream_t st);
-// mx_product.cu; *timed_out: an earlier call's wait ran out, and nothing was launched
+// mx_product.cu; fault: with a wait that nothing ends, and short limits
 cudaError_t launch_mx_product(const moe_mx& x, const moe_mx& w, const int32_t* offsets, const float* alpha, void* y,
-                              int y_type, int64_t y_ld, cudaStream_t st, bool* timed_out);
+                              int y_type, int64_t y_ld, cudaStream_t st, bool fault);
+cudaError_t mx_timeouts(uint64_t* count);  // of the current device
 
 }  // namespace moe

@@ -8,6 +8,8 @@
 namespace moe {
 namespace {
 
+thread_local bool g_fault = false;  // moe_mx_set_fault
+
 bool type_ok(int t) { return t == MOE_F32 || t == MOE_BF16; }
 
 // an entry's body: no C++ exception leaves the C interface
@@ -182,13 +184,25 @@ extern "C" int moe_mx_product(const moe_mx* x, const moe_mx* w, const int32_t* o
         if (y_ld < w->rows) return fail_global(MOE_EINVAL, "moe_mx_product: y_ld=%lld below w's rows", (long long)y_ld);
         if (x->rows == 0 || w->rows == 0) return MOE_OK;
         if (!y) return fail_global(MOE_EINVAL, "moe_mx_product: y is required");
-        bool timed_out = false;
-        rc = launched(
-            launch_mx_product(*x, *w, offsets, alpha, y, type, y_ld, static_cast<cudaStream_t>(stream), &timed_out),
+        return launched(
+            launch_mx_product(*x, *w, offsets, alpha, y, type, y_ld, static_cast<cudaStream_t>(stream), g_fault),
             "moe_mx_product");
-        if (rc == MOE_OK && timed_out)
-            return fail_global(MOE_ETIMEOUT, "moe_mx_product: a wait inside an earlier call's kernel ran out");
-        return rc;
+    });
+}
+
+extern "C" int moe_mx_timeouts(uint64_t* count) {
+    return guarded([&]() -> int {
+        if (!count) return fail_global(MOE_EINVAL, "moe_mx_timeouts: count is NULL");
+        return launched(mx_timeouts(count), "moe_mx_timeouts");
+    });
+}
+
+extern "C" int moe_mx_set_fault(uint32_t fault_flags) {
+    return guarded([&]() -> int {
+        if (fault_flags & ~MOE_FAULT_DEVICE_WAIT)
+            return fail_global(MOE_EINVAL, "moe_mx_set_fault: only MOE_FAULT_DEVICE_WAIT applies");
+        g_fault = fault_flags != 0;
+        return MOE_OK;
     });
 }
 

@@ -49,8 +49,8 @@
 //               accumulators are read
 //   64 rows of 58 experts x 1024 x 2048 (E8M0)   15 us for 65 MB: 4 us to begin
 //               and end, the rest at 6.1 TB/s
-// Every wait is bounded; one that runs out sets a status word in mapped host
-// memory, and the CTA drains its MMAs and copies and frees its tensor memory.
+// Every wait is bounded; where one runs out, the CTA counts that in mapped host
+// memory, drains its MMAs and copies, and frees its tensor memory.
 #include <mutex>
 
 #include "gemm_common.cuh"
@@ -80,7 +80,9 @@ struct ProductArgs {
     void* y;
     int64_t y_ld, x_rows, w_rows;
     int groups, steps, w_tiles, w_units;  // steps: column tiles; w_tiles: row tiles of one group of w; w_units: tiles or pairs
-    int* status;
+    unsigned long long* timeouts;  // mapped host memory: CTAs that gave up
+    unsigned long long limit_ns;   // of a wait
+    int fault;                     // tests: the second stage's scales never count as complete
 };
 
 // NT, the most rows of a tile: 256 a pair of CTAs (M = 256), 128 and 64 one CTA
@@ -258,18 +260,19 @@ __device__ __forceinline__ void copy_if(uint32_t on, uint32_t dst, const void* s
         : "memory");
 }
 
+// by a whole warp; counted once a CTA
 __device__ __forceinline__ void fail(const ProductArgs& a, volatile int* abort) {
-    *abort = 1;
-    *(volatile int*)a.status = 1;
+    if ((threadIdx.x & 31) == 0 && atomicExch(const_cast<int*>(abort), 1) == 0) atomicAdd_system(a.timeouts, 1ull);
+    __syncwarp();
 }
 // arrival on a barrier of another CTA of the cluster
 __device__ __forceinline__ void remote_arrive_relaxed(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // bounded wait of a whole warp, the same answer in every lane
-__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit_ns) {
     if (__all_sync(kAll, bar_try_wait(b, parity))) return true;
-    return __all_sync(kAll, bar_wait(b, parity, kTimeoutNs, abort));
+    return __all_sync(kAll, bar_wait(b, parity, limit_ns, abort));
 }
 struct Tile {
     int g, n, wt;  // group, rows, w row tile (a pair: the first of two)
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             bar_init(&empty[s], 1);
         }
         // the four scale warps, and in CTA 0 of a pair CTA 1's forwarded
-        for (int s = 0; s < C::kStages; ++s) bar_init(&scales_full[s], PAIR && rank == 0 ? 5 : 4);
+        for (int s = 0; s < C::kStages; ++s) bar_init(&scales_full[s], (PAIR && rank == 0 ? 5 : 4) + (s == 1 && a.fault));
         for (int s = 0; s < 2; ++s) {
             bar_init(&acc_full[s], 1);
             bar_init(&acc_empty[s], PAIR ? 2 * kEpiWarps : kEpiWarps);
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             }
             if (SPLIT) p0 += (int64_t)k_first * C::kTile;
             for (int k = 0; k < k_count; ++k) {
-                if (!warp_wait(&empty[s], ph, &abort_s)) {
+                if (!warp_wait(&empty[s], ph, &abort_s, a.limit_ns)) {
                     fail(a, &abort_s);
                     ok = false;
                     break;
@@ -483,16 +486,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                 if (++s == C::kStages) s = 0, ph ^= 1;
             }
         }
-        // copies still in flight land before the CTA exits
+        // copies still in flight land before the CTA exits; a stage that another copy warp gave up before filling never
+        // counts as full, but after that second everything has landed
         for (uint32_t i = filled > C::kStages ? filled - C::kStages : 0; i < filled; ++i)
-            bar_wait(&full[i % C::kStages], (i / C::kStages) & 1u, kTimeoutNs, &never_s);
+            if (!bar_wait(&full[i % C::kStages], (i / C::kStages) & 1u, kTimeoutNs, &never_s)) break;
         __syncwarp();
     } else if (warp == 1 && rank == 1) {
         // -------------- CTA 1 of a pair: forwards its scale warps' arrivals, and so spares them the remote access
         uint32_t s = 0, ph = 0;
         const int steps = my_tiles * k_count;
         for (int it = 0; it < steps; ++it) {
-            if (!warp_wait(&scales_full[s], ph, &abort_s)) {
+            if (!warp_wait(&scales_full[s], ph, &abort_s, a.limit_ns)) {
                 fail(a, &abort_s);
                 break;
             }
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             __syncwarp();
             if (++s == C::kStages) s = 0, ph ^= 1;
         }
-        warp_wait(&drain, 0, &never_s);  // CTA 0's last arrival here
+        warp_wait(&drain, 0, &never_s, kTimeoutNs);  // CTA 0's last arrival here
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA
         const uint32_t leader = elect_one();
@@ -514,12 +518,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             uint32_t d = 0, idesc = 0, m = 0;
             for (int k = 0; k < k_count; ++k) {
                 // the scales' warps have seen the step's copies land before they arrive here
-                ok = warp_wait(&scales_full[s], ph, &abort_s);
+                ok = warp_wait(&scales_full[s], ph, &abort_s, a.limit_ns);
                 if (k == 0 && ok) {
                     const int n = tile_n[i % kTileRing];
                     m = slots.mask(n);
-                    if (m & 1) ok = warp_wait(&acc_empty[0], (slots.use[0] & 1u) ^ 1u, &abort_s);
-                    if ((m & 2) && ok) ok = warp_wait(&acc_empty[1], (slots.use[1] & 1u) ^ 1u, &abort_s);
+                    if (m & 1) ok = warp_wait(&acc_empty[0], (slots.use[0] & 1u) ^ 1u, &abort_s, a.limit_ns);
+                    if ((m & 2) && ok) ok = warp_wait(&acc_empty[1], (slots.use[1] & 1u) ^ 1u, &abort_s, a.limit_ns);
                     d = tmem + (m == 2 ? 128u : 0u);
                     idesc = PAIR ? idesc_mx<FMT>(256, (n + 31) & ~31, 0) : idesc_mx<FMT>(128, (n + 15) & ~15, 0);
                 }
@@ -548,14 +552,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
         }
         // everything issued above has completed once this commit arrives
         commit_if<PAIR>(leader, smem_u32(&drain));
-        if (!warp_wait(&drain, 0, &never_s)) fail(a, &abort_s);
+        if (!warp_wait(&drain, 0, &never_s, kTimeoutNs)) fail(a, &abort_s);
     } else if (warp >= 2 && warp < kEpiWarp0) {
         // --------------------------------------------------------------- scales
         const uint32_t quarter = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         uint32_t s = 0, ph = 0;
         const int steps = my_tiles * k_count;
         for (int it = 0; it < steps; ++it) {
-            if (!warp_wait(&full[s], ph, &abort_s)) {
+            if (!warp_wait(&full[s], ph, &abort_s, a.limit_ns)) {
                 fail(a, &abort_s);
                 break;
             }
@@ -593,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
             const float alpha = a.alpha ? a.alpha[ti.g] : 1.0f;
             const uint32_t m = slots.mask(ti.n);
             bool ok = true;
-            if (m & 1) ok = warp_wait(&acc_full[0], slots.use[0] & 1u, &abort_s);
-            if ((m & 2) && ok) ok = warp_wait(&acc_full[1], slots.use[1] & 1u, &abort_s);
+            if (m & 1) ok = warp_wait(&acc_full[0], slots.use[0] & 1u, &abort_s, a.limit_ns);
+            if ((m & 2) && ok) ok = warp_wait(&acc_full[1], slots.use[1] & 1u, &abort_s, a.limit_ns);
             if (!ok) {
                 fail(a, &abort_s);
                 break;
@@ -712,10 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     if (warp == 1) free_columns<PAIR>(tmem, kTmemCols);
 }
 
-// The kernel's status word of each device, pinned and mapped, set up once.
+// The kernel's count of each device, pinned and mapped, set up once.
 struct DeviceState {
-    int* host = nullptr;
-    int* dev = nullptr;
+    unsigned long long* host = nullptr;
+    unsigned long long* dev = nullptr;
     int sms = 0;
 };
 
@@ -729,10 +733,10 @@ cudaError_t device_state(DeviceState& out) {
     std::lock_guard<std::mutex> lock(mu);
     DeviceState& s = states[id];
     if (!s.host) {
-        int* p = nullptr;
+        unsigned long long* p = nullptr;
         int sms = 0;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, id)) != cudaSuccess) return e;
-        if ((e = cudaHostAlloc(reinterpret_cast<void**>(&p), sizeof(int), cudaHostAllocMapped)) != cudaSuccess) return e;
+        if ((e = cudaHostAlloc(reinterpret_cast<void**>(&p), sizeof *p, cudaHostAllocMapped)) != cudaSuccess) return e;
         *p = 0;
         if ((e = cudaHostGetDevicePointer(reinterpret_cast<void**>(&s.dev), p, 0)) != cudaSuccess) {
             cudaFreeHost(p);
@@ -792,17 +796,18 @@ cudaError_t launch_rows(ProductArgs& a, int sms, cudaStream_t st) {
 
 }  // namespace
 
+cudaError_t mx_timeouts(uint64_t* count) {
+    DeviceState ds;
+    const cudaError_t e = device_state(ds);
+    if (e == cudaSuccess) *count = *static_cast<volatile unsigned long long*>(ds.host);
+    return e;
+}
+
 cudaError_t launch_mx_product(const moe_mx& x, const moe_mx& w, const int32_t* offsets, const float* alpha, void* y,
-                              int y_type, int64_t y_ld, cudaStream_t st, bool* timed_out) {
+                              int y_type, int64_t y_ld, cudaStream_t st, bool fault) {
     DeviceState ds;
     cudaError_t e = device_state(ds);
     if (e != cudaSuccess) return e;
-    volatile int* status = ds.host;
-    if (*status) {
-        *status = 0;
-        *timed_out = true;
-        return cudaSuccess;
-    }
     ProductArgs a{};
     a.x = static_cast<const uint8_t*>(x.data_dev);
     a.w = static_cast<const uint8_t*>(w.data_dev);
@@ -815,7 +820,9 @@ cudaError_t launch_mx_product(const moe_mx& x, const moe_mx& w, const int32_t* o
     a.groups = w.groups;
     a.steps = (int)mx_col_tiles(x.cols);
     a.w_tiles = (int)((w.rows + kMxTileRows - 1) / kMxTileRows);
-    a.status = ds.dev;
+    a.timeouts = ds.dev;
+    a.limit_ns = fault ? 1000000ull : kTimeoutNs;
+    a.fault = fault;
     if (x.format == MOE_MX_E8M0)
         return y_type == MOE_F32 ? launch_rows<MOE_MX_E8M0, float>(a, ds.sms, st)
                                  : launch_rows<MOE_MX_E8M0, __nv_bfloat16>(a, ds.sms, st);
