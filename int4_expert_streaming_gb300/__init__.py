@@ -70,6 +70,7 @@ class moe_route_config(ctypes.Structure):
 
 
 class moe_mx(ctypes.Structure):
+    device = -1  # ordinal of the GPU that holds the data; -1: not known, and not checked
     _fields_ = [("data_dev", ctypes.c_void_p), ("rows", ctypes.c_int64)] + [
         (n, ctypes.c_int32) for n in ("cols", "groups", "format", "ragged")]
 
@@ -345,7 +346,8 @@ def make_config(n_layers, hidden, n_experts, top_k, inter, shared_inter, bits=4,
 # --------------------------------------------------------------------------
 # operators without a context: CUDA tensors in, shapes and strides taken from
 # them; outputs are the caller's tensors.  _call (csrc/binding.c) takes the
-# tensors apart; one that does not fit raises ValueError.
+# tensors apart; one that does not fit, or is on another GPU than the current
+# one, raises ValueError.
 # --------------------------------------------------------------------------
 
 _ops = None
@@ -409,6 +411,7 @@ def make_mx(fmt: int, rows: int, cols: int, groups: int = 1, ragged: bool = Fals
                          f"{data.dtype} on {data.device}")
     m.data_dev = data.data_ptr()
     m._data = data
+    m.device = data.get_device()
     return m
 
 

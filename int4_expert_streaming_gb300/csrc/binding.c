@@ -14,7 +14,9 @@
 
 #include "moe.h"
 
-static PyObject *s_is_cuda, *s_dtype, *s_is_contiguous, *s_numel, *s_data_ptr, *s_shape, *s_stride, *s_cuda_stream;
+int moe_binding_device(void); /* the current device, -1 where there is none; not part of the C interface */
+
+static PyObject *s_get_device, *s_device, *s_dtype, *s_is_contiguous, *s_numel, *s_data_ptr, *s_shape, *s_stride, *s_cuda_stream;
 static PyObject *t_f32, *t_bf16, *t_i32, *t_u8; /* torch dtypes */
 
 static int bad(PyObject* t, const char* what, const char* expected) {
@@ -35,12 +37,6 @@ static int bad(PyObject* t, const char* what, const char* expected) {
     return -1;
 }
 
-/* 1 / 0: the attribute is True / is not (or is missing) */
-static int is_true(PyObject* o) {
-    const int yes = o == Py_True;
-    Py_XDECREF(o);
-    return yes;
-}
 static int has_type(PyObject* t, PyObject* type) {
     PyObject* d = PyObject_GetAttr(t, s_dtype);
     const int yes = d == type;
@@ -63,20 +59,39 @@ static int address(PyObject* t, void** out) {
     return PyErr_Occurred() ? -1 : 0;
 }
 
+/*
+ * A call's kernels run on the current device, and everything it is given has
+ * to be there: an address of another GPU would be a fault.  *dev is that
+ * device; where there is none to be told, the first tensor's.
+ */
+static int same_device(long long d, const char* what, int* dev) {
+    if (*dev < 0) *dev = (int)d;
+    if (d == *dev) return 0;
+    PyErr_Format(PyExc_ValueError, "%s: is on GPU %lld, the call is for GPU %d", what, d, *dev);
+    return -1;
+}
+/* 0: a CUDA tensor of that device; -1 and an exception if not */
+static int on_device(PyObject* t, const char* what, const char* expected, int* dev) {
+    const long long d = number(t, s_get_device); /* -1 for a tensor of the host */
+    return d < 0 ? bad(t, what, expected) : same_device(d, what, dev);
+}
+
 /* contiguous CUDA tensor of at least n elements of the type; None gives NULL */
-static int flat(PyObject* t, PyObject* type, long long n, const char* what, const char* expected, void** out) {
+static int flat(PyObject* t, PyObject* type, long long n, const char* what, const char* expected, int* dev, void** out) {
     *out = NULL;
     if (t == Py_None) return 0;
-    if (!is_true(PyObject_GetAttr(t, s_is_cuda)) || !has_type(t, type) ||
-        !is_true(PyObject_CallMethodNoArgs(t, s_is_contiguous)) || number(t, s_numel) < n)
-        return bad(t, what, expected);
+    if (on_device(t, what, expected, dev)) return -1;
+    PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+    const int contiguous = c == Py_True;
+    Py_XDECREF(c);
+    if (!contiguous || !has_type(t, type) || number(t, s_numel) < n) return bad(t, what, expected);
     return address(t, out);
 }
-static int flat_i32(PyObject* t, long long n, const char* what, void** out) {
-    return flat(t, t_i32, n, what, "a contiguous int32 CUDA tensor that is long enough", out);
+static int flat_i32(PyObject* t, long long n, const char* what, int* dev, void** out) {
+    return flat(t, t_i32, n, what, "a contiguous int32 CUDA tensor that is long enough", dev, out);
 }
-static int flat_f32(PyObject* t, long long n, const char* what, void** out) {
-    return flat(t, t_f32, n, what, "a contiguous float32 CUDA tensor that is long enough", out);
+static int flat_f32(PyObject* t, long long n, const char* what, int* dev, void** out) {
+    return flat(t, t_f32, n, what, "a contiguous float32 CUDA tensor that is long enough", dev, out);
 }
 
 typedef struct {
@@ -86,14 +101,15 @@ typedef struct {
 } matrix_t;
 
 /* 2D CUDA tensor of fp32 or bf16 with contiguous rows */
-static int matrix(PyObject* t, const char* what, matrix_t* m) {
+static int matrix(PyObject* t, const char* what, int* dev, matrix_t* m) {
     static const char* expected = "a 2D CUDA tensor of float32 or bfloat16 with contiguous rows";
     PyObject *d = PyObject_GetAttr(t, s_dtype), *shape = NULL, *stride = NULL;
     int rc = -1;
     const int ok = d == t_f32 || d == t_bf16;
     m->type = d == t_f32 ? MOE_F32 : MOE_BF16;
     Py_XDECREF(d);
-    if (!ok || !is_true(PyObject_GetAttr(t, s_is_cuda))) return bad(t, what, expected);
+    if (!ok) return bad(t, what, expected);
+    if (on_device(t, what, expected, dev)) return -1;
     shape = PyObject_GetAttr(t, s_shape);
     if (shape) stride = PyObject_CallMethodNoArgs(t, s_stride);
     if (shape && stride && PyTuple_Check(shape) && PyTuple_Check(stride) && PyTuple_GET_SIZE(shape) == 2 &&
@@ -148,6 +164,16 @@ static int structure(PyObject* o, void* out, size_t size, const char* what) {
     return ok ? 0 : -1;
 }
 
+/* copy of a matrix's descriptor, whose data is on the call's device as far as that is known (attribute device >= 0) */
+static int descriptor(PyObject* o, moe_mx* out, const char* what, int* dev) {
+    if (structure(o, out, sizeof *out, what)) return -1;
+    PyObject* v = PyObject_GetAttr(o, s_device);
+    const long d = v ? PyLong_AsLong(v) : -1;
+    Py_XDECREF(v);
+    if (PyErr_Occurred()) PyErr_Clear(); /* a structure of another make */
+    return d < 0 ? 0 : same_device(d, what, dev);
+}
+
 static int count(Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return 0;
     PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
@@ -175,12 +201,13 @@ static PyObject* route(ARGS) {
     moe_route_config c;
     matrix_t l;
     void *bias, *idx, *w, *st;
+    int dev = moe_binding_device();
     (void)self;
-    if (count(n, 6) || structure(v[0], &c, sizeof c, "cfg") || matrix(v[1], "logits", &l)) return NULL;
+    if (count(n, 6) || structure(v[0], &c, sizeof c, "cfg") || matrix(v[1], "logits", &dev, &l)) return NULL;
     CHECK(l.cols == c.n_experts, "logits have %lld columns, the config %d experts", (long long)l.cols, c.n_experts);
     const long long out = l.rows * (long long)c.top_k;
-    if (flat_f32(v[2], c.n_experts, "bias", &bias) || flat_i32(v[3], out, "idx", &idx) || flat_f32(v[4], out, "w", &w) ||
-        stream_of(v[5], &st))
+    if (flat_f32(v[2], c.n_experts, "bias", &dev, &bias) || flat_i32(v[3], out, "idx", &dev, &idx) ||
+        flat_f32(v[4], out, "w", &dev, &w) || stream_of(v[5], &st))
         return NULL;
     STATUS(moe_route(&c, l.p, l.type, l.ld, bias, l.rows, idx, w, st));
 }
@@ -190,15 +217,16 @@ static PyObject* dispatch(ARGS) {
     int64_t T, k;
     void *idx, *off, *rop, *tor, *gor, *ws, *st;
     long long bytes = 0;
+    int dev = moe_binding_device();
     (void)self;
     if (count(n, 8) || sides(v[0], "idx", &T, &k)) return NULL;
     const long E = PyLong_AsLong(v[1]);
     if (E == -1 && PyErr_Occurred()) return NULL;
     CHECK(k <= INT32_MAX && E >= INT32_MIN && E < INT32_MAX, "idx has too many columns, or n_experts is out of range");
-    if (flat_i32(v[0], T * k, "idx", &idx) || flat_i32(v[2], E + 1, "offsets", &off) ||
-        flat_i32(v[3], T * k, "row_of_pair", &rop) || flat_i32(v[4], T * k, "token_of_row", &tor) ||
-        flat_i32(v[5], T * k, "group_of_row", &gor) ||
-        flat(v[6], t_u8, 0, "workspace", "a contiguous uint8 CUDA tensor", &ws) || stream_of(v[7], &st))
+    if (flat_i32(v[0], T * k, "idx", &dev, &idx) || flat_i32(v[2], E + 1, "offsets", &dev, &off) ||
+        flat_i32(v[3], T * k, "row_of_pair", &dev, &rop) || flat_i32(v[4], T * k, "token_of_row", &dev, &tor) ||
+        flat_i32(v[5], T * k, "group_of_row", &dev, &gor) ||
+        flat(v[6], t_u8, 0, "workspace", "a contiguous uint8 CUDA tensor", &dev, &ws) || stream_of(v[7], &st))
         return NULL;
     if (v[6] != Py_None && (bytes = number(v[6], s_numel)) < 0) return NULL;
     STATUS(moe_dispatch(idx, T, (int32_t)k, (int32_t)E, off, rop, tor, gor, ws, (size_t)bytes, st));
@@ -211,16 +239,17 @@ static PyObject* quantise(ARGS) {
     moe_mx m;
     matrix_t s;
     void *row, *gor, *off, *ts, *st;
+    int dev = moe_binding_device();
     (void)self;
-    if (count(n, 8) || structure(v[0], &m, sizeof m, "m") || matrix(v[1], "src", &s)) return NULL;
+    if (count(n, 8) || descriptor(v[0], &m, "m", &dev) || matrix(v[1], "src", &dev, &s)) return NULL;
     const long act = PyLong_AsLong(v[2]);
     if (act == -1 && PyErr_Occurred()) return NULL;
     const int64_t rows = rows_of(&m), cols = act == MOE_ACT_SWIGLU ? 2 * (int64_t)m.cols : m.cols;
     CHECK(s.cols == cols, "src has %lld columns, the matrix needs %lld", (long long)s.cols, (long long)cols);
     CHECK(v[3] != Py_None || s.rows >= rows, "src has %lld rows, the matrix %lld", (long long)s.rows, (long long)rows);
-    if (flat_i32(v[3], rows, "src_row", &row) || flat_i32(v[4], rows, "group_of_row", &gor) ||
-        flat_i32(v[5], (long long)m.groups + 1, "offsets", &off) || flat_f32(v[6], m.groups, "tensor_scale", &ts) ||
-        stream_of(v[7], &st))
+    if (flat_i32(v[3], rows, "src_row", &dev, &row) || flat_i32(v[4], rows, "group_of_row", &dev, &gor) ||
+        flat_i32(v[5], (long long)m.groups + 1, "offsets", &dev, &off) ||
+        flat_f32(v[6], m.groups, "tensor_scale", &dev, &ts) || stream_of(v[7], &st))
         return NULL;
     STATUS(moe_mx_quantise(&m, s.p, s.type, s.ld, (int32_t)act, row, gor, off, ts, st));
 }
@@ -230,13 +259,14 @@ static PyObject* dequantise(ARGS) {
     moe_mx m;
     matrix_t d;
     void *gor, *off, *ts, *st;
+    int dev = moe_binding_device();
     (void)self;
-    if (count(n, 6) || structure(v[0], &m, sizeof m, "m") || matrix(v[1], "dst", &d)) return NULL;
+    if (count(n, 6) || descriptor(v[0], &m, "m", &dev) || matrix(v[1], "dst", &dev, &d)) return NULL;
     const int64_t rows = rows_of(&m);
     CHECK(d.cols == m.cols && d.rows >= rows, "dst is %lld x %lld, the matrix %lld x %d", (long long)d.rows,
           (long long)d.cols, (long long)rows, m.cols);
-    if (flat_i32(v[2], rows, "group_of_row", &gor) || flat_i32(v[3], (long long)m.groups + 1, "offsets", &off) ||
-        flat_f32(v[4], m.groups, "tensor_scale", &ts) || stream_of(v[5], &st))
+    if (flat_i32(v[2], rows, "group_of_row", &dev, &gor) ||
+        flat_i32(v[3], (long long)m.groups + 1, "offsets", &dev, &off) || flat_f32(v[4], m.groups, "tensor_scale", &dev, &ts) || stream_of(v[5], &st))
         return NULL;
     STATUS(moe_mx_dequantise(&m, gor, off, ts, d.p, d.type, d.ld, st));
 }
@@ -246,13 +276,15 @@ static PyObject* product(ARGS) {
     moe_mx x, w;
     matrix_t y;
     void *off, *alpha, *st;
+    int dev = moe_binding_device();
     (void)self;
-    if (count(n, 6) || structure(v[0], &x, sizeof x, "x") || structure(v[1], &w, sizeof w, "w") || matrix(v[2], "y", &y))
+    if (count(n, 6) || descriptor(v[0], &x, "x", &dev) || descriptor(v[1], &w, "w", &dev) ||
+        matrix(v[2], "y", &dev, &y))
         return NULL;
     CHECK(y.rows >= x.rows && y.cols == w.rows, "y is %lld x %lld, the product %lld x %lld", (long long)y.rows,
           (long long)y.cols, (long long)x.rows, (long long)w.rows);
-    if (flat_i32(v[3], (long long)x.groups + 1, "offsets", &off) || flat_f32(v[4], w.groups, "alpha", &alpha) ||
-        stream_of(v[5], &st))
+    if (flat_i32(v[3], (long long)x.groups + 1, "offsets", &dev, &off) ||
+        flat_f32(v[4], w.groups, "alpha", &dev, &alpha) || stream_of(v[5], &st))
         return NULL;
     STATUS(moe_mx_product(&x, &w, off, alpha, y.p, y.type, y.ld, st));
 }
@@ -262,12 +294,17 @@ static PyObject* combine(ARGS) {
     matrix_t r, y;
     int64_t T, k;
     void *rop, *w, *st;
+    int dev = moe_binding_device();
     (void)self;
-    if (count(n, 5) || matrix(v[0], "rows", &r) || sides(v[1], "row_of_pair", &T, &k) || matrix(v[3], "y", &y)) return NULL;
+    if (count(n, 5) || matrix(v[0], "rows", &dev, &r) || sides(v[1], "row_of_pair", &T, &k) ||
+        matrix(v[3], "y", &dev, &y))
+        return NULL;
     CHECK(y.cols == r.cols && y.rows == T, "y is %lld x %lld, expected %lld x %lld", (long long)y.rows, (long long)y.cols,
           (long long)T, (long long)r.cols);
     CHECK(k <= INT32_MAX && r.cols <= INT32_MAX, "row_of_pair or rows has too many columns");
-    if (flat_i32(v[1], T * k, "row_of_pair", &rop) || flat_f32(v[2], T * k, "w", &w) || stream_of(v[4], &st)) return NULL;
+    if (flat_i32(v[1], T * k, "row_of_pair", &dev, &rop) || flat_f32(v[2], T * k, "w", &dev, &w) ||
+        stream_of(v[4], &st))
+        return NULL;
     STATUS(moe_combine(r.p, r.type, r.ld, rop, w, T, (int32_t)k, (int32_t)r.cols, y.p, y.type, y.ld, st));
 }
 
@@ -292,9 +329,9 @@ PyMODINIT_FUNC PyInit__call(void) {
     struct {
         PyObject** at;
         const char* name;
-    } names[] = {{&s_is_cuda, "is_cuda"}, {&s_dtype, "dtype"},       {&s_is_contiguous, "is_contiguous"},
-                 {&s_numel, "numel"},     {&s_data_ptr, "data_ptr"}, {&s_shape, "shape"},
-                 {&s_stride, "stride"},   {&s_cuda_stream, "cuda_stream"}};
+    } names[] = {{&s_get_device, "get_device"}, {&s_device, "device"},     {&s_dtype, "dtype"},
+                 {&s_is_contiguous, "is_contiguous"}, {&s_numel, "numel"}, {&s_data_ptr, "data_ptr"},
+                 {&s_shape, "shape"}, {&s_stride, "stride"}, {&s_cuda_stream, "cuda_stream"}};
     for (size_t i = 0; i < sizeof names / sizeof names[0]; ++i)
         if (!(*names[i].at = PyUnicode_InternFromString(names[i].name))) return NULL;
     return PyModule_Create(&module);

@@ -223,3 +223,9 @@ extern "C" int moe_combine(const void* rows, int32_t rows_type, int64_t rows_ld,
                         "moe_combine");
     });
 }
+
+// The device that a call made now would run on, -1 where there is none; for the Python module, which compares tensors with it.
+extern "C" int moe_binding_device(void) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}

@@ -129,7 +129,9 @@ class MxLayer:
     @staticmethod
     def _batch(m: moe.moe_mx, rows: int) -> moe.moe_mx:
         """The same data, for a batch of fewer rows."""
-        return moe.moe_mx(m.data_dev, rows, m.cols, m.groups, m.format, m.ragged)
+        b = moe.moe_mx(m.data_dev, rows, m.cols, m.groups, m.format, m.ragged)
+        b.device = m.device
+        return b
 
 
 def main() -> None:
