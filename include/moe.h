@@ -422,13 +422,19 @@ size_t moe_mx_bytes(const moe_mx* m);
  * s t are fp32.  A block with a NaN or an infinity gets a NaN scale and zero
  * codes.
  *   src_dev   rows of src_type (MOE_F32, MOE_BF16), stride src_ld
- *   src_row_dev  int32 [rows of m]: the source row of each row, -1 leaves the row unwritten; NULL = the same row
+ *   src_row_dev  int32 [rows of m]: the source row of each row, -1 leaves the row unwritten; NULL = the same row.  Has to
+ *   stay within the source, whose rows this call does not know: moe_mx_quantise_rows is told
  *   ragged m: offsets_dev int32 [groups + 1] and group_of_row_dev int32 [rows] (negative: the row is left out);
  *   both are NULL for a uniform m, whose source rows are the groups' rows one after another
  */
 int moe_mx_quantise(const moe_mx* m, const void* src_dev, int32_t src_type, int64_t src_ld, int32_t act,
                     const int32_t* src_row_dev, const int32_t* group_of_row_dev, const int32_t* offsets_dev,
                     const float* tensor_scale_dev, void* stream);
+
+/* The same from a source of src_rows rows: a row whose source row is outside 0..src_rows-1 is left unwritten. */
+int moe_mx_quantise_rows(const moe_mx* m, const void* src_dev, int64_t src_rows, int32_t src_type, int64_t src_ld,
+                         int32_t act, const int32_t* src_row_dev, const int32_t* group_of_row_dev,
+                         const int32_t* offsets_dev, const float* tensor_scale_dev, void* stream);
 
 /* The numbers m stands for, in fp32 (exact), times the group's tensor scale if given (fp32), as dst_type; same row order
  * and same meaning of offsets_dev and group_of_row_dev as moe_mx_quantise.  Rows left out are not written. */
@@ -467,11 +473,17 @@ int moe_mx_set_fault(uint32_t fault_flags);
 /*
  * y[t] = sum_j w[t, j] * rows[row_of_pair[t, j]] in fp32, j ascending; pairs
  * with row -1 are skipped (a token without pairs gives zeros).  rows_dev of
- * rows_type, stride rows_ld; y_dev of y_type [T x cols], stride y_ld.
+ * rows_type, stride rows_ld; y_dev of y_type [T x cols], stride y_ld.  row_of_pair has to stay within rows_dev, whose
+ * length this call does not know: moe_combine_rows is told.
  */
 int moe_combine(const void* rows_dev, int32_t rows_type, int64_t rows_ld, const int32_t* row_of_pair_dev,
                 const float* w_dev, int64_t T, int32_t top_k, int32_t cols, void* y_dev, int32_t y_type, int64_t y_ld,
                 void* stream);
+
+/* The same of n_rows rows: pairs with a row outside 0..n_rows-1 are skipped. */
+int moe_combine_rows(const void* rows_dev, int64_t n_rows, int32_t rows_type, int64_t rows_ld,
+                     const int32_t* row_of_pair_dev, const float* w_dev, int64_t T, int32_t top_k, int32_t cols,
+                     void* y_dev, int32_t y_type, int64_t y_ld, void* stream);
 
 /* ------------------------------------------------------------------ */
 /* pool introspection                                                   */

@@ -38,7 +38,7 @@ EXPORTS = (
     "moe_set_router_bias", "moe_set_router_bias_all", "moe_forward_decode", "moe_forward_decode_stack", "moe_forward_prefill",
     "moe_pool_stats", "moe_pool_reset", "moe_pool_trace", "moe_launch_count", "moe_prefill_profile", "moe_prefill_kernel_ms", "moe_route_noalloc", "moe_last_error", "moe_slotpool_create", "moe_slotpool_destroy",
     "moe_route", "moe_dispatch_workspace", "moe_dispatch", "moe_mx_bytes", "moe_mx_quantise", "moe_mx_dequantise",
-    "moe_mx_product", "moe_mx_timeouts", "moe_mx_set_fault", "moe_combine",
+    "moe_mx_product", "moe_mx_timeouts", "moe_mx_set_fault", "moe_combine", "moe_mx_quantise_rows", "moe_combine_rows",
     "moe_slotpool_request", "moe_store_create", "moe_store_write_layer", "moe_store_info", "moe_store_read",
 )
 
@@ -132,6 +132,8 @@ def load_library(path: str | None = None):
         lib.moe_mx_quantise.argtypes = [mx, vp, i32, i64, i32, vp, vp, vp, vp, vp]
         lib.moe_mx_dequantise.argtypes = [mx, vp, vp, vp, vp, i32, i64, vp]
         lib.moe_mx_product.argtypes = [mx, mx, vp, vp, vp, i32, i64, vp]
+        lib.moe_mx_quantise_rows.argtypes = [mx, vp, i64, i32, i64, i32, vp, vp, vp, vp, vp]
+        lib.moe_combine_rows.argtypes = [vp, i64, i32, i64, vp, vp, i64, i32, i32, vp, i32, i64, vp]
         lib.moe_mx_timeouts.argtypes = [c.POINTER(c.c_uint64)]
         lib.moe_mx_set_fault.argtypes = [c.c_uint32]
         lib.moe_combine.argtypes = [vp, i32, i64, vp, vp, i64, i32, i32, vp, i32, i64, vp]
@@ -417,7 +419,8 @@ def make_mx(fmt: int, rows: int, cols: int, groups: int = 1, ragged: bool = Fals
 
 def moe_mx_quantise(m: moe_mx, src, act: int = MOE_ACT_NONE, src_row=None, group_of_row=None, offsets=None,
                     tensor_scale=None, stream=None) -> None:
-    """Rows of src (fp32 or bf16, [source rows, cols] or [.., 2 cols] for MOE_ACT_SWIGLU) into m."""
+    """Rows of src (fp32 or bf16, [source rows, cols] or [.., 2 cols] for MOE_ACT_SWIGLU) into m; a src_row that is none
+    of them leaves its row unwritten."""
     rc = (_ops or _binding()).quantise(m, src, act, src_row, group_of_row, offsets, tensor_scale, stream)
     if rc:
         _check(rc)
@@ -451,7 +454,8 @@ def moe_mx_set_fault(fault_flags: int) -> None:
 
 
 def moe_combine(rows, row_of_pair, w, y, stream=None) -> None:
-    """y [T, cols] = sum_j w[T, k] * rows[row_of_pair[T, k]]; rows and y fp32 or bf16."""
+    """y [T, cols] = sum_j w[T, k] * rows[row_of_pair[T, k]]; rows and y fp32 or bf16.  Pairs whose row is none of rows
+    are skipped."""
     rc = (_ops or _binding()).combine(rows, row_of_pair, w, y, stream)
     if rc:
         _check(rc)

@@ -251,7 +251,7 @@ static PyObject* quantise(ARGS) {
         flat_i32(v[5], (long long)m.groups + 1, "offsets", &dev, &off) ||
         flat_f32(v[6], m.groups, "tensor_scale", &dev, &ts) || stream_of(v[7], &st))
         return NULL;
-    STATUS(moe_mx_quantise(&m, s.p, s.type, s.ld, (int32_t)act, row, gor, off, ts, st));
+    STATUS(moe_mx_quantise_rows(&m, s.p, s.rows, s.type, s.ld, (int32_t)act, row, gor, off, ts, st));
 }
 
 /* m, dst, group_of_row, offsets, tensor_scale, stream */
@@ -305,7 +305,7 @@ static PyObject* combine(ARGS) {
     if (flat_i32(v[1], T * k, "row_of_pair", &dev, &rop) || flat_f32(v[2], T * k, "w", &dev, &w) ||
         stream_of(v[4], &st))
         return NULL;
-    STATUS(moe_combine(r.p, r.type, r.ld, rop, w, T, (int32_t)k, (int32_t)r.cols, y.p, y.type, y.ld, st));
+    STATUS(moe_combine_rows(r.p, r.rows, r.type, r.ld, rop, w, T, (int32_t)k, (int32_t)r.cols, y.p, y.type, y.ld, st));
 }
 
 /* the torch dtypes float32, bfloat16, int32, uint8 */

@@ -87,11 +87,11 @@ size_t dispatch_workspace(int64_t pairs, int n_experts);
 cudaError_t launch_dispatch(const int32_t* idx, int64_t pairs, int top_k, int n_experts, int32_t* offsets,
                             int32_t* row_of_pair, int32_t* token_of_row, int32_t* group_of_row, void* ws,
                             cudaStream_t st);
-cudaError_t launch_combine(const void* rows, int rows_type, int64_t rows_ld, const int32_t* row_of_pair, const float* w,
-                           int64_t T, int top_k, int cols, void* y, int y_type, int64_t y_ld, cudaStream_t st);
+cudaError_t launch_combine(const void* rows, int64_t n_rows, int rows_type, int64_t rows_ld, const int32_t* row_of_pair,
+                           const float* w, int64_t T, int top_k, int cols, void* y, int y_type, int64_t y_ld, cudaStream_t st);
 // mx_quantise.cu
-cudaError_t launch_mx_quantise(const moe_mx& m, const MxRows& rows, const void* src, int type, int64_t ld, int act,
-                               const int32_t* src_row, const float* tscale, cudaStream_t st);
+cudaError_t launch_mx_quantise(const moe_mx& m, const MxRows& rows, const void* src, int64_t src_rows, int type,
+                               int64_t ld, int act, const int32_t* src_row, const float* tscale, cudaStream_t st);
 cudaError_t launch_mx_dequantise(const moe_mx& m, const MxRows& rows, const float* tscale, void* dst, int type,
                                  int64_t ld, cudaStream_t st);
 // mx_product.cu; fault: with a wait that nothing ends, and short limits

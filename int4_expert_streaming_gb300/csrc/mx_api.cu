@@ -130,9 +130,9 @@ static int check_maps(const moe_mx* m, const int32_t* group_of_row, const int32_
     return MOE_OK;
 }
 
-extern "C" int moe_mx_quantise(const moe_mx* m, const void* src, int32_t type, int64_t ld, int32_t act,
-                               const int32_t* src_row, const int32_t* group_of_row, const int32_t* offsets,
-                               const float* tscale, void* stream) {
+extern "C" int moe_mx_quantise_rows(const moe_mx* m, const void* src, int64_t src_rows, int32_t type, int64_t ld,
+                                    int32_t act, const int32_t* src_row, const int32_t* group_of_row,
+                                    const int32_t* offsets, const float* tscale, void* stream) {
     return guarded([&]() -> int {
         int rc = check_mx(m, "moe_mx_quantise");
         if (rc || (rc = check_maps(m, group_of_row, offsets, "moe_mx_quantise"))) return rc;
@@ -143,13 +143,20 @@ extern "C" int moe_mx_quantise(const moe_mx* m, const void* src, int32_t type, i
             return fail_global(MOE_EINVAL, "moe_mx_quantise: src_ld=%lld is shorter than a source row", (long long)ld);
         if (tscale && m->format != MOE_MX_E4M3)
             return fail_global(MOE_EINVAL, "moe_mx_quantise: tensor scales go with MOE_MX_E4M3");
+        if (src_rows < 0) return fail_global(MOE_EINVAL, "moe_mx_quantise: src_rows=%lld", (long long)src_rows);
         const MxRows rows = rows_of(m, group_of_row, offsets);
         if (rows.rows == 0) return MOE_OK;
-        if (!src) return fail_global(MOE_EINVAL, "moe_mx_quantise: src is required");
-        return launched(
-            launch_mx_quantise(*m, rows, src, type, ld, act, src_row, tscale, static_cast<cudaStream_t>(stream)),
-            "moe_mx_quantise");
+        if (!src && src_rows > 0) return fail_global(MOE_EINVAL, "moe_mx_quantise: src is required");
+        return launched(launch_mx_quantise(*m, rows, src, src_rows, type, ld, act, src_row, tscale,
+                                           static_cast<cudaStream_t>(stream)),
+                        "moe_mx_quantise");
     });
+}
+
+extern "C" int moe_mx_quantise(const moe_mx* m, const void* src, int32_t type, int64_t ld, int32_t act,
+                               const int32_t* src_row, const int32_t* group_of_row, const int32_t* offsets,
+                               const float* tscale, void* stream) {
+    return moe_mx_quantise_rows(m, src, INT64_MAX, type, ld, act, src_row, group_of_row, offsets, tscale, stream);
 }
 
 extern "C" int moe_mx_dequantise(const moe_mx* m, const int32_t* group_of_row, const int32_t* offsets,
@@ -206,22 +213,29 @@ extern "C" int moe_mx_set_fault(uint32_t fault_flags) {
     });
 }
 
-extern "C" int moe_combine(const void* rows, int32_t rows_type, int64_t rows_ld, const int32_t* row_of_pair,
-                           const float* w, int64_t T, int32_t top_k, int32_t cols, void* y, int32_t y_type,
-                           int64_t y_ld, void* stream) {
+extern "C" int moe_combine_rows(const void* rows, int64_t n_rows, int32_t rows_type, int64_t rows_ld,
+                                const int32_t* row_of_pair, const float* w, int64_t T, int32_t top_k, int32_t cols,
+                                void* y, int32_t y_type, int64_t y_ld, void* stream) {
     return guarded([&]() -> int {
         if (T < 0 || T > INT32_MAX || top_k < 1 || cols < 1 || cols > 1 << 22 || T * top_k > INT32_MAX)
             return fail_global(MOE_EINVAL, "moe_combine: T=%lld, top_k=%d or cols=%d out of range", (long long)T, top_k,
                                cols);
         if (!type_ok(rows_type) || !type_ok(y_type)) return fail_global(MOE_EINVAL, "moe_combine: unknown element type");
         if (rows_ld < cols || y_ld < cols) return fail_global(MOE_EINVAL, "moe_combine: a stride is shorter than a row");
+        if (n_rows < 0) return fail_global(MOE_EINVAL, "moe_combine: n_rows=%lld", (long long)n_rows);
         if (T == 0) return MOE_OK;
-        if (!rows || !row_of_pair || !w || !y)
+        if ((!rows && n_rows > 0) || !row_of_pair || !w || !y)
             return fail_global(MOE_EINVAL, "moe_combine: rows, row_of_pair, w and y are required");
-        return launched(launch_combine(rows, rows_type, rows_ld, row_of_pair, w, T, top_k, cols, y, y_type, y_ld,
+        return launched(launch_combine(rows, n_rows, rows_type, rows_ld, row_of_pair, w, T, top_k, cols, y, y_type, y_ld,
                                        static_cast<cudaStream_t>(stream)),
                         "moe_combine");
     });
+}
+
+extern "C" int moe_combine(const void* rows, int32_t rows_type, int64_t rows_ld, const int32_t* row_of_pair,
+                           const float* w, int64_t T, int32_t top_k, int32_t cols, void* y, int32_t y_type,
+                           int64_t y_ld, void* stream) {
+    return moe_combine_rows(rows, INT64_MAX, rows_type, rows_ld, row_of_pair, w, T, top_k, cols, y, y_type, y_ld, stream);
 }
 
 // The device that a call made now would run on, -1 where there is none; for the Python module, which compares tensors with it.

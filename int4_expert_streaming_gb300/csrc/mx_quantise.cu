@@ -100,7 +100,7 @@ struct QuantArgs {
     const int32_t* src_row;
     const float* tscale;
     void* dst;
-    int64_t ld;
+    int64_t ld, src_rows;
     int cols, col_tiles;
     bool wide;
 };
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
     // the row's values: they do not wait for its place in the tiles
     auto fetch = [&](int64_t row) {
         const int64_t from = row < a.rows.rows ? (a.src_row ? a.src_row[row] : row) : -1;
-        live = from >= 0;
+        live = (uint64_t)from < (uint64_t)a.src_rows;  // -1 is not
         const int n = live ? a.cols - col : 0;
         const T* p = static_cast<const T*>(a.src) + (live ? from * a.ld + col : 0);
         x.load(p, n, c16);
@@ -363,12 +363,13 @@ bool wide_ok(const void* p, int64_t ld, int64_t second, int type) {
 
 }  // namespace
 
-cudaError_t launch_mx_quantise(const moe_mx& m, const MxRows& rows, const void* src, int type, int64_t ld, int act,
-                               const int32_t* src_row, const float* tscale, cudaStream_t st) {
+cudaError_t launch_mx_quantise(const moe_mx& m, const MxRows& rows, const void* src, int64_t src_rows, int type,
+                               int64_t ld, int act, const int32_t* src_row, const float* tscale, cudaStream_t st) {
     QuantArgs a{};
     a.data = static_cast<uint8_t*>(m.data_dev);
     a.rows = rows;
     a.src = src;
+    a.src_rows = src_rows;
     a.src_row = src_row;
     a.tscale = tscale;
     a.ld = ld;

@@ -552,9 +552,9 @@ template <int V>
 constexpr int kPieces = V == 8 ? 1 : V == 2 ? 2 : 4;
 
 template <typename TI, typename TO, int V>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const TI* rows, int64_t rows_ld,
-                                                                  const int32_t* row_of_pair, const float* w, int top_k,
-                                                                  int cols, TO* y, int64_t y_ld) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const TI* rows, uint32_t n_rows,
+                                                                  int64_t rows_ld, const int32_t* row_of_pair,
+                                                                  const float* w, int top_k, int cols, TO* y, int64_t y_ld) {
     constexpr int U = kPieces<V>, W = U * V;
     after_previous();
     let_next_start();
@@ -570,13 +570,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const TI* rows
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = i < n ? row_of_pair[j + i] : -1;
-            wj[i] = r >= 0 ? w[j + i] : 0.0f;
-            const TI* p = rows + (r >= 0 ? r * rows_ld : 0) + col;
+            const bool there = (uint32_t)r < n_rows;  // -1 is not
+            wj[i] = there ? w[j + i] : 0.0f;
+            const TI* p = rows + (there ? r * rows_ld : 0) + col;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int q = 0; q < V; ++q) v[i][u * V + q] = 0.0f;
-                if (r >= 0 && col + u * kCombineThreads * V < cols) load_v<V>(p + u * kCombineThreads * V, v[i] + u * V);
+                if (there && col + u * kCombineThreads * V < cols) load_v<V>(p + u * kCombineThreads * V, v[i] + u * V);
             }
         }
 #pragma unroll
@@ -601,14 +602,14 @@ bool pieces_ok(const void* p, int64_t ld, int cols, int V) {
 }
 
 template <typename TI, typename TO>
-cudaError_t combine_typed(const void* rows, int64_t rows_ld, const int32_t* row_of_pair, const float* w, int64_t T,
-                          int top_k, int cols, void* y, int64_t y_ld, cudaStream_t st) {
+cudaError_t combine_typed(const void* rows, uint32_t n_rows, int64_t rows_ld, const int32_t* row_of_pair,
+                          const float* w, int64_t T, int top_k, int cols, void* y, int64_t y_ld, cudaStream_t st) {
     auto both = [&](int V) { return pieces_ok<TI>(rows, rows_ld, cols, V) && pieces_ok<TO>(y, y_ld, cols, V); };
     auto run = [&](auto kernel, int per) {
         const int64_t chunks = ((int64_t)cols + per * kCombineThreads - 1) / (per * kCombineThreads);
         if (chunks > 65535) return cudaErrorInvalidValue;
         return launch(kernel, dim3((unsigned)T, (unsigned)chunks), kCombineThreads, 0, st, 1, static_cast<const TI*>(rows),
-                      rows_ld, row_of_pair, w, top_k, cols, static_cast<TO*>(y), y_ld);
+                      n_rows, rows_ld, row_of_pair, w, top_k, cols, static_cast<TO*>(y), y_ld);
     };
     if (both(8)) return run(combine_kernel<TI, TO, 8>, 8 * kPieces<8>);
     if (both(2)) return run(combine_kernel<TI, TO, 2>, 2 * kPieces<2>);
@@ -661,15 +662,16 @@ cudaError_t launch_dispatch(const int32_t* idx, int64_t pairs, int top_k, int n_
     return e != cudaSuccess ? e : launch(dispatch_place_kernel, a.ctas, kSortThreads, smem, st, 1, a);
 }
 
-cudaError_t launch_combine(const void* rows, int rows_type, int64_t rows_ld, const int32_t* row_of_pair, const float* w,
-                           int64_t T, int top_k, int cols, void* y, int y_type, int64_t y_ld, cudaStream_t st) {
+cudaError_t launch_combine(const void* rows, int64_t n_rows, int rows_type, int64_t rows_ld, const int32_t* row_of_pair,
+                           const float* w, int64_t T, int top_k, int cols, void* y, int y_type, int64_t y_ld, cudaStream_t st) {
     using bf = __nv_bfloat16;
+    const uint32_t n = n_rows > INT32_MAX ? 1u << 31 : (uint32_t)n_rows;  // an index has no more than 31 bits
     if (rows_type == MOE_F32)
         return y_type == MOE_F32
-                   ? combine_typed<float, float>(rows, rows_ld, row_of_pair, w, T, top_k, cols, y, y_ld, st)
-                   : combine_typed<float, bf>(rows, rows_ld, row_of_pair, w, T, top_k, cols, y, y_ld, st);
-    return y_type == MOE_F32 ? combine_typed<bf, float>(rows, rows_ld, row_of_pair, w, T, top_k, cols, y, y_ld, st)
-                             : combine_typed<bf, bf>(rows, rows_ld, row_of_pair, w, T, top_k, cols, y, y_ld, st);
+                   ? combine_typed<float, float>(rows, n, rows_ld, row_of_pair, w, T, top_k, cols, y, y_ld, st)
+                   : combine_typed<float, bf>(rows, n, rows_ld, row_of_pair, w, T, top_k, cols, y, y_ld, st);
+    return y_type == MOE_F32 ? combine_typed<bf, float>(rows, n, rows_ld, row_of_pair, w, T, top_k, cols, y, y_ld, st)
+                             : combine_typed<bf, bf>(rows, n, rows_ld, row_of_pair, w, T, top_k, cols, y, y_ld, st);
 }
 
 }  // namespace moe

@@ -102,3 +102,12 @@ def test_counts_and_faults_refuse_what_they_do_not_know():
     lib = moe.load_library()
     assert lib.moe_mx_timeouts(None) == moe.MOE_EINVAL
     assert lib.moe_mx_set_fault(1) == moe.MOE_EINVAL and lib.moe_mx_set_fault(0) == moe.MOE_OK
+
+
+def test_row_counts_below_zero_are_refused():
+    lib, P = moe.load_library(), 1 << 20
+    m = moe.moe_mx(P, 4, 64, 1, moe.MOE_MX_E8M0, 0)
+    assert lib.moe_mx_quantise_rows(m, P, -1, 0, 64, 0, P, None, None, None, None) == moe.MOE_EINVAL
+    assert "src_rows" in moe.moe_last_error(None)
+    assert lib.moe_combine_rows(P, -1, 0, 8, P, P, 2, 2, 8, P, 0, 8, None) == moe.MOE_EINVAL
+    assert "n_rows" in moe.moe_last_error(None)
