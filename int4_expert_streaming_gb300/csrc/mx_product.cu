@@ -265,9 +265,9 @@ __device__ __forceinline__ void fail(const ProductArgs& a, volatile int* abort) 
     if ((threadIdx.x & 31) == 0 && atomicExch(const_cast<int*>(abort), 1) == 0) atomicAdd_system(a.timeouts, 1ull);
     __syncwarp();
 }
-// arrival on a barrier of another CTA of the cluster
-__device__ __forceinline__ void remote_arrive_relaxed(uint32_t addr) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+// arrival on a barrier of another CTA of the cluster, released at CTA scope
+__device__ __forceinline__ void remote_arrive(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // bounded wait of a whole warp, the same answer in every lane
 __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit_ns) {
@@ -423,11 +423,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
     const int k_first = SPLIT ? (int)((int64_t)a.steps * part / parts) : 0;
     const int k_count = (SPLIT ? (int)((int64_t)a.steps * (part + 1) / parts) : a.steps) - k_first;
 
-    // Arrival at the CTA that issues the MMAs.  From CTA 1 it is relaxed: what it announces are accesses to tensor
-    // memory, which the fences before and after it order, and copies that have already landed in shared memory.  A
-    // release at cluster scope would also wait for this SM's stores of y (1800 cycles a step measured).
+    // Arrival at the CTA that issues the MMAs.  CTA 1 announces no memory that another thread reads: accesses to tensor
+    // memory, complete (wait::st, wait::ld) before the fence and the arrival, and copies that have landed in its own
+    // shared memory, where its half of the tensor core reads them.  So it releases at CTA scope, which costs as much as
+    // a relaxed arrival (7937 x 8192 x 8192 147 us in a chain of 21 calls, 4096 tokens of 512 experts 74); at cluster
+    // scope it would also wait for this SM's stores of y (402 and 151).
     auto arrive_at_leader = [&](uint64_t* b) {
-        if (PAIR && rank == 1) remote_arrive_relaxed(leader_addr(smem_u32(b)));
+        if (PAIR && rank == 1) remote_arrive(leader_addr(smem_u32(b)));
         else bar_arrive(b);
     };
 
@@ -500,6 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const ProductArgs 
                 fail(a, &abort_s);
                 break;
             }
+            fence_after_sync();  // what the scales' warps stored is ordered before this warp's arrival as well
+            fence_before_sync();
             if (lane == 0) arrive_at_leader(&scales_full[s]);
             __syncwarp();
             if (++s == C::kStages) s = 0, ph ^= 1;
