@@ -547,7 +547,7 @@ __device__ __forceinline__ void store_v(__nv_bfloat16* p, const float* v) {
 // A thread takes kPieces<V> pieces of V columns of one token, V as the alignment
 // allows: memory-bound, so loads are wide and four rows'
 // are in flight at a time.  4096 tokens of 10 rows of 2048 bf16: 32.8 us with
-// V = 8 (6.1 TB/s); of 2046 with 2 43.6, of 2047 with 1 50.7.
+// V = 8 (6.1 TB/s); of 2046 with 2 38.5, of 2047 with 1 52.2: those wait for narrow loads.
 template <int V>
 constexpr int kPieces = V == 8 ? 1 : V == 2 ? 2 : 4;
 
@@ -569,10 +569,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const TI* rows
         float v[4][W], wj[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = i < n ? row_of_pair[j + i] : -1;
-            const bool there = (uint32_t)r < n_rows;  // -1 is not
+            // Whether there is a row, kept as a condition or, where many single loads hang on it, as the index -1: the
+            // compiler's order of the loads differs.  4096 x 10 bf16 rows to fp32: of 2048 32.8 us as a condition, 33.4
+            // as the index, of 2046 38.5 and 43.9, of 2047 62.7 and 52.2.
+            int r = i < n ? row_of_pair[j + i] : -1;
+            if (V == 1 && (uint32_t)r >= n_rows) r = -1;
+            const bool there = V == 1 ? r >= 0 : (uint32_t)r < n_rows;
             wj[i] = there ? w[j + i] : 0.0f;
-            const TI* p = rows + (there ? r * rows_ld : 0) + col;
+            const TI* p = rows + (V == 1 ? (there ? r * rows_ld : 0) : (int64_t)(there ? r : 0) * rows_ld) + col;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
