@@ -352,7 +352,7 @@ typedef struct {
  *   w_j = scale * s_idx[j], divided by sum_j s_idx[j] with renorm
  * bias_dev: fp32 [E] or NULL; it takes part in the choice only.  Without a
  * bias c orders as l does, and l is what is compared (a group's score of two
- * is still the sum of s).  An expert whose logit is NaN or -inf, or whose bias
+ * is still the sum of s).  With a bias, sigmoid scores are compared to about 2^-21.  An expert whose logit is NaN or -inf, or whose bias
  * is NaN or -inf, is out: never chosen, and in no sum.  A logit of +inf counts
  * as the largest finite number.  Where fewer than top_k experts are left, the
  * rest of the row is idx -1, w 0.  Weights with renorm are formed relative to
@@ -411,7 +411,8 @@ typedef struct {
 size_t moe_mx_bytes(const moe_mx* m);
 
 #define MOE_ACT_NONE 0
-#define MOE_ACT_SWIGLU 1 /* source rows hold cols gate then cols up values: x = gate / (1 + exp(-gate)) * up, in fp32 */
+#define MOE_ACT_SWIGLU 1 /* source rows hold cols gate then cols up values: x = gate / (1 + exp(-gate)) * up, in fp32,
+                            its exp and its reciprocal to about 2^-22 */
 
 /*
  * Quantise rows into m.  Per block, with a = max |x| and t = the group's
@@ -419,8 +420,10 @@ size_t moe_mx_bytes(const moe_mx* m);
  *   E8M0: scale 2^(floor(log2 a) - 2), at least 2^-127;  code = e2m1(x / scale)
  *   E4M3: scale s = e4m3(a / (6 t)), at most 448, 0 for a block of zeros;  code = e2m1(x / (s t)), 0 where s t is 0
  * both roundings to nearest even, e2m1 saturating at 6; quotients, 6 t and
- * s t are fp32.  A block with a NaN or an infinity gets a NaN scale and zero
- * codes.
+ * s t are fp32, and a quotient is exact where it stands half way between two
+ * codes.  Not so after MOE_ACT_SWIGLU with E4M3, where x is multiplied by the
+ * rounded reciprocal of s t: a value next to such a place may take the other
+ * code.  A block with a NaN or an infinity gets a NaN scale and zero codes.
  *   src_dev   rows of src_type (MOE_F32, MOE_BF16), stride src_ld
  *   src_row_dev  int32 [rows of m]: the source row of each row, -1 leaves the row unwritten; NULL = the same row.  Has to
  *   stay within the source, whose rows this call does not know: moe_mx_quantise_rows is told

@@ -349,7 +349,8 @@ def make_config(n_layers, hidden, n_experts, top_k, inter, shared_inter, bits=4,
 # operators without a context: CUDA tensors in, shapes and strides taken from
 # them; outputs are the caller's tensors.  _call (csrc/binding.c) takes the
 # tensors apart; one that does not fit, or is on another GPU than the current
-# one, raises ValueError.
+# one, raises ValueError.  stream=None is the legacy default stream, as in the
+# calls above, not torch's current one: within torch.cuda.stream(s) pass s.
 # --------------------------------------------------------------------------
 
 _ops = None

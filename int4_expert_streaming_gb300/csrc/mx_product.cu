@@ -37,7 +37,7 @@
 // most 128 rows takes one slot, a larger one both.  A slot is free again as
 // soon as it has been read into registers.
 // Measured (random codes, bf16 y):
-//   7937 x 8192 x 8192   160 us, 6.7 PFLOP/s (145 in a CUDA graph of 21 calls);
+//   7937 x 8192 x 8192   160 to 165 us, 6.6 PFLOP/s (147 in a CUDA graph of 21 calls);
 //               without copies and stores an earlier build of the pair took 138:
 //               a step is about 590 cycles of MMA against 512 at the nominal
 //               rate, probably because shared memory moves 68 KB in it; long

@@ -16,7 +16,8 @@ constexpr int kThreads = 256;
 // way.  Rows that are not aligned for 16-byte loads are loaded value by value,
 // thread c taking columns c, c + 16, ..., so that the threads' loads share
 // sectors, and change hands in shared memory (pitch 17: no bank conflicts).
-// 16384 rows of 2047 columns to e8m0: bf16 31 us, fp32 27 (of 2048: 15 and 24).
+// 16384 rows of 2047 columns to e8m0: bf16 23.7 us, fp32 26.5 (of 2048: 15.1 and 24.7), to e4m3 30.3 and 30.0 (19.0 and
+// 25.2; the bf16 form spills 16 bytes).
 constexpr int kSwap = 16 * 17;  // floats of a row
 
 template <typename T, bool WIDE>
@@ -255,7 +256,8 @@ __global__ void __launch_bounds__(kThreads) quantise_kernel(const QuantArgs a) {
 // lanes look their places up together, and all rows' codes are loaded before
 // the first is needed.  Eight rows a warp where that still fills the GPU
 // (40960 x 512 to bf16: 11.5 us, with two 14.1), else one (64 rows of 2048
-// columns: 1.7 us instead of 2.9).
+// columns: 1.7 us instead of 2.9).  Bound by the instructions issued (84 % of
+// the slots at 16384 x 2048, 14.5 us; rows that are not aligned take 32).
 __device__ __forceinline__ __half2 e2m1_pair(uint32_t byte) {
     return __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(byte & 0xffu), __NV_E2M1));
 }

@@ -56,7 +56,8 @@ def largest_of(v, live, parts: int = 1):
 
 class MxLayer:
     """gate_up [E, 2 * inter, hidden] (gate rows, then up rows of each expert), down [E, hidden, inter]; cfg as of
-    make_route_config; max_tokens sizes the buffers.  One call at a time per object.
+    make_route_config; max_tokens sizes the buffers.  One call at a time per object.  From hidden or inter of 3841 on a
+    batch of few rows may sum its products in another order than a large one.
 
     x_scale, h_scale (e4m3 only): tensor scales of the token rows and of the SwiGLU rows.  One that is None is measured
     from each batch, over the rows that have an expert, by about ten small launches; the SwiGLU rows' from the bound
