@@ -489,6 +489,136 @@ int moe_combine_rows(const void* rows_dev, int64_t n_rows, int32_t rows_type, in
                      void* y_dev, int32_t y_type, int64_t y_ld, void* stream);
 
 /* ------------------------------------------------------------------ */
+/* operators: what a hybrid decoder has between two expert layers         */
+/* ------------------------------------------------------------------ */
+/*
+ * The token mixer of a hybrid decoder's linear-attention layers between its
+ * projections, in pieces: a short causal convolution over the channels, norms
+ * of heads (to unit length, or weighted, with the position rotation or a
+ * gate), and the gated delta rule.  Inference only.
+ * [README translation (news.paixiangai.cn), "How it works": three of four
+ *  layers are Gated DeltaNet with a fixed recurrent state, the fourth is
+ *  gated attention; the pages give no formulas, these are this library's.]
+ *
+ * Conventions of the section before hold: current device, the caller's stream
+ * and buffers, nothing allocated, calls can be captured.  Outputs may not
+ * overlap inputs except where a call says so.
+ *
+ * Sequences.  A batch is n sequences whose rows stand one after another:
+ * sequence s has rows offsets[s] .. offsets[s+1]-1 of the call's T rows;
+ * rows outside all sequences are left alone.  Each has a state in a slot of
+ * the state tensor, which the call reads and replaces:
+ *   offsets_dev  int32 [n + 1], ascending, within 0..T; NULL: each row is a sequence (n = T), as in decode
+ *   slot_dev     int32 [n]: slot of each sequence; NULL: sequence s has slot s.  A sequence whose slot is outside
+ *                0..slots-1 (-1: padding) is left out: its rows of the output are not written.  Two sequences with rows
+ *                may not share a slot: what they read and leave there is then not defined
+ *   carry_dev    int32 [n]: 0 = the sequence starts now, from a state of zeros, and what its slot holds is not read;
+ *                NULL: all go on from their slots
+ *   max_len      no sequence has more rows (0: not known); from 1 to 16 moe_delta needs neither its workspace nor its
+ *                kernels for long runs.  Calls stay right, if slow, where it is too small
+ * A sequence without rows leaves its slot as it is.  seqs = NULL: all T rows are one sequence, with slot 0.
+ */
+typedef struct {
+    const int32_t* offsets_dev;
+    const int32_t* slot_dev;
+    const int32_t* carry_dev;
+    int32_t n;       /* 0..2^20 */
+    int32_t max_len;
+} moe_seqs;
+
+#define MOE_ACT_SILU 2 /* x / (1 + exp(-x)), to about 2^-21 */
+
+/*
+ * Short causal convolution, each channel by itself:
+ *   y[t, c] = act(bias[c] + sum_i w[c, i] x[t - (width-1) + i, c]),  i = 0..width-1
+ * in fp32, rounded once; the rows before a sequence's first are its slot's.
+ *   x_dev, y_dev  rows of `type` (MOE_F32, MOE_BF16), strides x_ld, y_ld >= channels
+ *   w_dev         `w_type` [channels x width], contiguous; width 2..4;  bias_dev fp32 [channels] or NULL
+ *   act           MOE_ACT_NONE or MOE_ACT_SILU
+ *   state_dev     `type` [slots x (width-1) x channels]: the last width-1 rows of x, oldest first; NULL: every sequence
+ *                 starts from zeros and leaves nothing behind (slots is then not looked at; slot_dev still leaves out
+ *                 the sequences with a negative slot)
+ */
+int moe_conv(const moe_seqs* seqs, const void* x_dev, int32_t type, int64_t x_ld, int64_t T, int32_t channels,
+             const void* w_dev, int32_t w_type, int32_t width, const float* bias_dev, int32_t act, void* state_dev,
+             int64_t slots, void* y_dev, int64_t y_ld, void* stream);
+
+#define MOE_NORM_NONE 0
+#define MOE_NORM_RMS 1 /* x / sqrt(mean x^2 + eps) */
+#define MOE_NORM_L2 2  /* x / sqrt(sum x^2 + eps) */
+
+#define MOE_ROT_HALVES 0   /* value i of the first rot_dim/2 turns with value i + rot_dim/2 */
+#define MOE_ROT_ADJACENT 1 /* value 2i with value 2i + 1 */
+
+typedef struct {
+    int32_t dim;     /* values of a head, 1..512 */
+    int32_t norm;    /* MOE_NORM_* */
+    int32_t rot_dim; /* the first rot_dim values are rotated, even, 0..dim (0: none) */
+    int32_t pairs;   /* MOE_ROT_* */
+    float eps;           /* >= 0 */
+    float weight_offset; /* a weight counts as weight_offset + weight */
+} moe_head_norm_config;
+
+typedef struct {
+    const void* x_dev;    /* element (t, h, i) at t * x_ld + h * x_head + i */
+    void* y_dev;          /* likewise; may be x_dev itself with the same strides */
+    const void* gate_dev; /* likewise, or NULL: y is multiplied by silu(gate) */
+    const float* weight_dev; /* fp32 [dim] or NULL */
+    int64_t x_ld, x_head, y_ld, y_head, gate_ld, gate_head;
+    int32_t heads; /* 1..65535 */
+    int32_t type;  /* MOE_F32, MOE_BF16: of x, y and gate */
+} moe_heads;
+
+/*
+ * Heads of T tokens (queries, say), and a second tensor's (keys; b may be
+ * NULL) in the same pass; for each head of `dim` values, in fp32, rounded once:
+ *   z = norm(x) * (weight_offset + weight)              (without a weight: norm(x))
+ *   (z_i, z_j) = (z_i cos - z_j sin, z_j cos + z_i sin)  for each pair, angle = pos[t] * inv_freq[pair]
+ *   y = z * silu(gate)
+ * a head of zeros with eps 0 gives NaN, as the formula does.
+ *   pos_dev int32 [T], inv_freq_dev fp32 [rot_dim / 2]: with rot_dim > 0 only.  The angle is reduced in fp64, so
+ *   positions far from 0 lose nothing.
+ */
+int moe_head_norm(const moe_head_norm_config* cfg, const moe_heads* a, const moe_heads* b, const int32_t* pos_dev,
+                  const float* inv_freq_dev, int64_t T, void* stream);
+
+typedef struct {
+    int32_t k_heads; /* heads of q and k, 1..1024 */
+    int32_t v_heads; /* heads of v, o and the state, a multiple of k_heads, up to 1024: head h uses q and k of
+                        h / (v_heads / k_heads) */
+    int32_t k_dim;   /* multiples of 8, 8..128 */
+    int32_t v_dim;
+    float scale;     /* factor on o */
+} moe_delta_config;
+
+/*
+ * The gated delta rule.  Per sequence and head, token by token, S [v_dim x k_dim]:
+ *   S <- exp(g_t) S
+ *   S <- S + beta_t (v_t - S k_t) k_t^T
+ *   o_t = scale S q_t
+ *   q_dev, k_dev  bf16 rows [k_heads x k_dim], v_dev and o_dev bf16 rows [v_heads x v_dim]; strides between tokens
+ *                 q_ld, k_ld, v_ld, o_ld
+ *   g_dev, beta_dev  fp32 [T x v_heads], contiguous; g is the logarithm of a decay: 0 or less (-inf: the state is
+ *                 cleared), and above 0 the result is defined only as far as fp32 holds exp of its sums
+ *   state_dev     fp32 [slots x v_heads x v_dim x k_dim], contiguous, 16-byte aligned; NULL: every sequence starts from
+ *                 zeros and leaves nothing behind
+ * Sequences of up to 16 rows run token by token, with the state in registers
+ * and fp32 throughout.  Longer ones run in chunks of 64 tokens on the tensor
+ * cores: within a chunk the updates come from one triangular system; the
+ * state, the chunk's inverse and the updates enter the products as pairs of
+ * fp16 numbers (each row or column scaled by a power of two; about 2^-22) and
+ * are summed in fp32.  Which of the two a sequence takes depends on its own
+ * length alone (max_len being right), so its results do not depend on its batch.
+ * workspace_dev: moe_delta_workspace() bytes (0: may be NULL), 128-byte aligned, contents irrelevant; two calls that may
+ * run at the same time (or two graphs) need one each.
+ */
+size_t moe_delta_workspace(const moe_delta_config* cfg, int64_t T, int32_t n, int32_t max_len);
+int moe_delta(const moe_delta_config* cfg, const moe_seqs* seqs, const void* q_dev, int64_t q_ld, const void* k_dev,
+              int64_t k_ld, const void* v_dev, int64_t v_ld, const float* g_dev, const float* beta_dev, float* state_dev,
+              int64_t slots, void* o_dev, int64_t o_ld, int64_t T, void* workspace_dev, size_t workspace_bytes,
+              void* stream);
+
+/* ------------------------------------------------------------------ */
 /* pool introspection                                                   */
 /* ------------------------------------------------------------------ */
 

@@ -26,7 +26,9 @@ MOE_STORE_DIRECT = 0x1
 MOE_F32, MOE_BF16 = 0, 1
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_MX_E8M0, MOE_MX_E4M3 = 0, 1
-MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
+MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_ACT_SILU = 0, 1, 2
+MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_L2 = 0, 1, 2
+MOE_ROT_HALVES, MOE_ROT_ADJACENT = 0, 1
 MOE_EVICT_LFU_RECENCY, MOE_EVICT_LRU, MOE_EVICT_LFU_PERSIST, MOE_EVICT_LFU_AGED = 0, 1, 2, 3
 MOE_FAULT_PINNED_ALLOC, MOE_FAULT_MISS_COPY, MOE_FAULT_WAIT_TIMEOUT, MOE_FAULT_DEVICE_WAIT = 0x1, 0x2, 0x4, 0x8
 _ERRNAMES = {MOE_EINVAL: "MOE_EINVAL", MOE_ENOMEM: "MOE_ENOMEM", MOE_ECUDA: "MOE_ECUDA", MOE_EPOOL: "MOE_EPOOL",
@@ -39,6 +41,7 @@ EXPORTS = (
     "moe_pool_stats", "moe_pool_reset", "moe_pool_trace", "moe_launch_count", "moe_prefill_profile", "moe_prefill_kernel_ms", "moe_route_noalloc", "moe_last_error", "moe_slotpool_create", "moe_slotpool_destroy",
     "moe_route", "moe_dispatch_workspace", "moe_dispatch", "moe_mx_bytes", "moe_mx_quantise", "moe_mx_dequantise",
     "moe_mx_product", "moe_mx_timeouts", "moe_mx_set_fault", "moe_combine", "moe_mx_quantise_rows", "moe_combine_rows",
+    "moe_conv", "moe_head_norm", "moe_delta_workspace", "moe_delta",
     "moe_slotpool_request", "moe_store_create", "moe_store_write_layer", "moe_store_info", "moe_store_read",
 )
 
@@ -73,6 +76,27 @@ class moe_mx(ctypes.Structure):
     device = -1  # ordinal of the GPU that holds the data; -1: not known, and not checked
     _fields_ = [("data_dev", ctypes.c_void_p), ("rows", ctypes.c_int64)] + [
         (n, ctypes.c_int32) for n in ("cols", "groups", "format", "ragged")]
+
+
+class moe_seqs(ctypes.Structure):
+    device = -1  # ordinal of the GPU that holds the lists; -1: not known, and not checked
+    _fields_ = [(n, ctypes.c_void_p) for n in ("offsets_dev", "slot_dev", "carry_dev")] + [
+        ("n", ctypes.c_int32), ("max_len", ctypes.c_int32)]
+
+
+class moe_head_norm_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dim", "norm", "rot_dim", "pairs")] + [
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class moe_heads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x_dev", "y_dev", "gate_dev", "weight_dev")] + [
+        (n, ctypes.c_int64) for n in ("x_ld", "x_head", "y_ld", "y_head", "gate_ld", "gate_head")] + [
+        ("heads", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class moe_delta_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("k_heads", "v_heads", "k_dim", "v_dim")] + [("scale", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -137,8 +161,15 @@ def load_library(path: str | None = None):
         lib.moe_mx_timeouts.argtypes = [c.POINTER(c.c_uint64)]
         lib.moe_mx_set_fault.argtypes = [c.c_uint32]
         lib.moe_combine.argtypes = [vp, i32, i64, vp, vp, i64, i32, i32, vp, i32, i64, vp]
+        seqs, heads = c.POINTER(moe_seqs), c.POINTER(moe_heads)
+        lib.moe_conv.argtypes = [seqs, vp, i32, i64, i64, i32, vp, i32, i32, vp, i32, vp, i64, vp, i64, vp]
+        lib.moe_head_norm.argtypes = [c.POINTER(moe_head_norm_config), heads, heads, vp, vp, i64, vp]
+        lib.moe_delta_workspace.argtypes = [c.POINTER(moe_delta_config), i64, i32, i32]
+        lib.moe_delta_workspace.restype = sz
+        lib.moe_delta.argtypes = [c.POINTER(moe_delta_config), seqs, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,
+                                  i64, vp, sz, vp]
         for name in EXPORTS:
-            if name not in ("moe_destroy", "moe_slotpool_destroy", "moe_blob_bytes", "moe_blob_stride",
+            if name not in ("moe_delta_workspace", "moe_destroy", "moe_slotpool_destroy", "moe_blob_bytes", "moe_blob_stride",
                             "moe_last_error", "moe_dispatch_workspace", "moe_mx_bytes"):
                 getattr(lib, name).restype = c.c_int
         _lib = lib
@@ -458,6 +489,62 @@ def moe_combine(rows, row_of_pair, w, y, stream=None) -> None:
     """y [T, cols] = sum_j w[T, k] * rows[row_of_pair[T, k]]; rows and y fp32 or bf16.  Pairs whose row is none of rows
     are skipped."""
     rc = (_ops or _binding()).combine(rows, row_of_pair, w, y, stream)
+    if rc:
+        _check(rc)
+
+
+def make_seqs(n: int, offsets=None, slot=None, carry=None, max_len: int = 0) -> moe_seqs:
+    """Descriptor of a batch of n sequences (see moe_seqs in moe.h): offsets [n + 1] (None: each row is a sequence), slot
+    [n] and carry [n], contiguous int32 CUDA tensors, kept alive by the descriptor."""
+    import torch
+
+    q = moe_seqs(None, None, None, n, max_len)
+    for name, t, need in (("offsets", offsets, n + 1), ("slot", slot, n), ("carry", carry, n)):
+        if t is None:
+            continue
+        if not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < need:
+            raise ValueError(f"{name}: expected a contiguous CUDA tensor of at least {need} int32, got {tuple(t.shape)} "
+                             f"{t.dtype} on {t.device}")
+        if q.device >= 0 and t.get_device() != q.device:
+            raise ValueError(f"{name}: is on GPU {t.get_device()}, another list on GPU {q.device}")
+        q.device = t.get_device()
+        setattr(q, name + "_dev", t.data_ptr())
+    q._lists = (offsets, slot, carry)
+    return q
+
+
+def moe_conv(x, w, y, bias=None, act: int = MOE_ACT_SILU, seqs: moe_seqs | None = None, state=None, stream=None) -> None:
+    """Causal convolution of each column of x [T, channels] by w [channels, width], into y; state [slots, width - 1,
+    channels], of x's type, is read and replaced."""
+    rc = (_ops or _binding()).conv(x, w, y, bias, act, seqs, state, stream)
+    if rc:
+        _check(rc)
+
+
+def make_head_norm_config(norm: int = MOE_NORM_RMS, eps: float = 1e-6, weight_offset: float = 0.0, rot_dim: int = 0,
+                          pairs: int = MOE_ROT_HALVES) -> moe_head_norm_config:
+    """Without the heads' dimension, which a call takes from its tensors."""
+    return moe_head_norm_config(0, norm, rot_dim, pairs, eps, weight_offset)
+
+
+def moe_head_norm(cfg: moe_head_norm_config, x, y, weight=None, gate=None, x2=None, y2=None, weight2=None, pos=None,
+                  inv_freq=None, stream=None) -> None:
+    """Norm of each head of x [T, heads, dim], then the rotation or the gate, into y (which may be x); x2, y2: a second
+    tensor in the same pass.  pos [T] int32, inv_freq [rot_dim / 2] fp32."""
+    rc = (_ops or _binding()).head_norm(cfg, x, y, weight, gate, x2, y2, weight2, pos, inv_freq, stream)
+    if rc:
+        _check(rc)
+
+
+def moe_delta_workspace(T: int, n: int, k_heads: int, v_heads: int, k_dim: int, v_dim: int, max_len: int = 0) -> int:
+    return int(load_library().moe_delta_workspace(moe_delta_config(k_heads, v_heads, k_dim, v_dim, 1.0), T, n, max_len))
+
+
+def moe_delta(q, k, v, g, beta, state, o, scale: float = 1.0, seqs: moe_seqs | None = None, workspace=None,
+              stream=None) -> None:
+    """The gated delta rule: q, k [T, k_heads, k_dim], v, o [T, v_heads, v_dim] bf16, g, beta [T, v_heads] fp32, state
+    [slots, v_heads, v_dim, k_dim] fp32 (read and replaced) or None; workspace: uint8, moe_delta_workspace() bytes."""
+    rc = (_ops or _binding()).delta(q, k, v, g, beta, state, o, scale, seqs, workspace, stream)
     if rc:
         _check(rc)
 

@@ -125,6 +125,42 @@ static int matrix(PyObject* t, const char* what, int* dev, matrix_t* m) {
     return rc ? bad(t, what, expected) : 0;
 }
 
+typedef struct {
+    void* p;
+    int32_t type;
+    int64_t n, heads, dim, ld, head; /* element (t, h, i) at t * ld + h * head + i */
+} heads_t;
+
+/* 3D CUDA tensor [tokens, heads, values] of fp32 or bf16, its values contiguous */
+static int heads_of(PyObject* t, const char* what, int* dev, heads_t* m) {
+    static const char* expected = "a 3D CUDA tensor of float32 or bfloat16 with contiguous heads";
+    PyObject *d = PyObject_GetAttr(t, s_dtype), *shape = NULL, *stride = NULL;
+    int rc = -1;
+    const int ok = d == t_f32 || d == t_bf16;
+    m->type = d == t_f32 ? MOE_F32 : MOE_BF16;
+    Py_XDECREF(d);
+    if (!ok) return bad(t, what, expected);
+    if (on_device(t, what, expected, dev)) return -1;
+    shape = PyObject_GetAttr(t, s_shape);
+    if (shape) stride = PyObject_CallMethodNoArgs(t, s_stride);
+    if (shape && stride && PyTuple_Check(shape) && PyTuple_Check(stride) && PyTuple_GET_SIZE(shape) == 3 &&
+        PyTuple_GET_SIZE(stride) == 3) {
+        m->n = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
+        m->heads = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 1));
+        m->dim = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 2));
+        m->ld = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 0));
+        m->head = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 1));
+        if (m->heads <= 1) m->head = m->dim; /* one head's or token's stride means nothing */
+        if (m->n <= 1) m->ld = m->heads * m->dim;
+        if (m->heads <= INT32_MAX && m->dim <= INT32_MAX &&
+            (m->dim <= 1 || PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 2)) == 1))
+            rc = address(t, &m->p);
+    }
+    Py_XDECREF(shape);
+    Py_XDECREF(stride);
+    return rc ? bad(t, what, expected) : 0;
+}
+
 /* rows and columns of a 2D tensor */
 static int sides(PyObject* t, const char* what, int64_t* rows, int64_t* cols) {
     PyObject* shape = PyObject_GetAttr(t, s_shape);
@@ -308,6 +344,152 @@ static PyObject* combine(ARGS) {
     STATUS(moe_combine_rows(r.p, r.rows, r.type, r.ld, rop, w, T, (int32_t)k, (int32_t)r.cols, y.p, y.type, y.ld, st));
 }
 
+/* copy of a batch's descriptor, its lists on the call's device; None gives NULL */
+static int batch(PyObject* o, moe_seqs* out, const moe_seqs** p, int* dev) {
+    *p = NULL;
+    if (o == Py_None) return 0;
+    if (structure(o, out, sizeof *out, "seqs")) return -1;
+    PyObject* v = PyObject_GetAttr(o, s_device);
+    const long d = v ? PyLong_AsLong(v) : -1;
+    Py_XDECREF(v);
+    if (PyErr_Occurred()) PyErr_Clear();
+    *p = out;
+    return d < 0 ? 0 : same_device(d, "seqs", dev);
+}
+
+/* the tensor's extent along its first dimension; -1 and an exception if it has none */
+static long long first_extent(PyObject* t, const char* what) {
+    long long n = -1;
+    PyObject* shape = PyObject_GetAttr(t, s_shape);
+    if (shape && PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) >= 1)
+        n = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
+    Py_XDECREF(shape);
+    if (n < 0) bad(t, what, "a tensor with slots along its first dimension");
+    return n;
+}
+
+/* x, w, y, bias, act, seqs, state, stream */
+static PyObject* conv(ARGS) {
+    matrix_t x, w, y;
+    moe_seqs q;
+    const moe_seqs* qp;
+    void *bias, *state = NULL, *st;
+    long long slots = 0;
+    int dev = moe_binding_device();
+    (void)self;
+    if (count(n, 8) || matrix(v[0], "x", &dev, &x) || matrix(v[1], "w", &dev, &w) || matrix(v[2], "y", &dev, &y))
+        return NULL;
+    const long act = PyLong_AsLong(v[4]);
+    if (act == -1 && PyErr_Occurred()) return NULL;
+    CHECK(x.cols <= INT32_MAX && w.rows == x.cols && w.cols <= INT32_MAX && w.ld == w.cols,
+          "w is %lld x %lld, expected contiguous rows of each of %lld channels", (long long)w.rows, (long long)w.cols,
+          (long long)x.cols);
+    CHECK(y.cols == x.cols && y.rows >= x.rows && y.type == x.type, "y is %lld x %lld, x %lld x %lld, of one type",
+          (long long)y.rows, (long long)y.cols, (long long)x.rows, (long long)x.cols);
+    if (flat_f32(v[3], x.cols, "bias", &dev, &bias) || batch(v[5], &q, &qp, &dev) || stream_of(v[7], &st)) return NULL;
+    if (v[6] != Py_None) {
+        static const char* expected = "a contiguous CUDA tensor [slots, width - 1, channels] of x's type";
+        if ((slots = first_extent(v[6], "state")) < 0) return NULL;
+        if (flat(v[6], x.type == MOE_F32 ? t_f32 : t_bf16, slots * (w.cols - 1) * x.cols, "state", expected, &dev, &state))
+            return NULL;
+        /* a state of no slots still is one: every sequence is left out */
+        if (!slots) Py_RETURN_NONE;
+    }
+    STATUS(moe_conv(qp, x.p, x.type, x.ld, x.rows, (int32_t)x.cols, w.p, w.type, (int32_t)w.cols, bias, (int32_t)act,
+                    state, slots, y.p, y.ld, st));
+}
+
+/* cfg, x, y, weight, gate, x2, y2, weight2, pos, inv_freq, stream; cfg.dim is x's */
+static PyObject* head_norm(ARGS) {
+    moe_head_norm_config c;
+    moe_heads t[2];
+    heads_t x, y, gate;
+    void *pos, *freq, *weight, *st;
+    int dev = moe_binding_device();
+    (void)self;
+    if (count(n, 11) || structure(v[0], &c, sizeof c, "cfg")) return NULL;
+    const int second = v[5] != Py_None;
+    CHECK(second || v[6] == Py_None, "y2 goes with x2");
+    memset(t, 0, sizeof t);
+    long long tokens = 0;
+    for (int i = 0; i <= second; ++i) {
+        const char *xn = i ? "x2" : "x", *yn = i ? "y2" : "y";
+        if (heads_of(v[i ? 5 : 1], xn, &dev, &x) || heads_of(v[i ? 6 : 2], yn, &dev, &y)) return NULL;
+        if (!i) {
+            tokens = x.n;
+            c.dim = (int32_t)x.dim;
+        }
+        CHECK(x.n == tokens && x.dim == c.dim, "%s is %lld x %lld x %lld, expected %lld tokens and heads of %d", xn,
+              (long long)x.n, (long long)x.heads, (long long)x.dim, tokens, c.dim);
+        CHECK(y.n == x.n && y.heads == x.heads && y.dim == x.dim && y.type == x.type,
+              "%s is %lld x %lld x %lld, expected %lld x %lld x %lld of %s's type", yn, (long long)y.n, (long long)y.heads,
+              (long long)y.dim, (long long)x.n, (long long)x.heads, (long long)x.dim, xn);
+        if (flat_f32(v[i ? 7 : 3], x.dim, "weight", &dev, &weight)) return NULL;
+        t[i].x_dev = x.p, t[i].x_ld = x.ld, t[i].x_head = x.head;
+        t[i].y_dev = y.p, t[i].y_ld = y.ld, t[i].y_head = y.head;
+        t[i].weight_dev = weight;
+        t[i].heads = (int32_t)x.heads;
+        t[i].type = x.type;
+        if (!i && v[4] != Py_None) {
+            if (heads_of(v[4], "gate", &dev, &gate)) return NULL;
+            CHECK(gate.n == x.n && gate.heads == x.heads && gate.dim == x.dim && gate.type == x.type,
+                  "gate is %lld x %lld x %lld, expected %lld x %lld x %lld of x's type", (long long)gate.n,
+                  (long long)gate.heads, (long long)gate.dim, (long long)x.n, (long long)x.heads, (long long)x.dim);
+            t[i].gate_dev = gate.p, t[i].gate_ld = gate.ld, t[i].gate_head = gate.head;
+        }
+    }
+    CHECK(second || v[7] == Py_None, "weight2 goes with x2");
+    if (flat_i32(v[8], tokens, "pos", &dev, &pos) || flat_f32(v[9], c.rot_dim / 2, "inv_freq", &dev, &freq) ||
+        stream_of(v[10], &st))
+        return NULL;
+    STATUS(moe_head_norm(&c, &t[0], second ? &t[1] : NULL, pos, freq, tokens, st));
+}
+
+/* q, k, v, g, beta, state, o, scale, seqs, workspace, stream */
+static PyObject* delta(ARGS) {
+    moe_delta_config c;
+    heads_t q, k, val, o;
+    moe_seqs b;
+    const moe_seqs* bp;
+    void *g, *beta, *state = NULL, *ws, *st;
+    long long slots = 0, bytes = 0;
+    int dev = moe_binding_device();
+    (void)self;
+    if (count(n, 11) || heads_of(v[0], "q", &dev, &q) || heads_of(v[1], "k", &dev, &k) ||
+        heads_of(v[2], "v", &dev, &val) || heads_of(v[6], "o", &dev, &o))
+        return NULL;
+    const double scale = PyFloat_AsDouble(v[7]);
+    if (scale == -1.0 && PyErr_Occurred()) return NULL;
+    CHECK(q.type == MOE_BF16 && k.type == MOE_BF16 && val.type == MOE_BF16 && o.type == MOE_BF16,
+          "q, k, v and o: expected bfloat16");
+    CHECK(q.n == val.n && k.n == val.n && k.heads == q.heads && k.dim == q.dim,
+          "q is %lld x %lld x %lld, k %lld x %lld x %lld, v has %lld tokens", (long long)q.n, (long long)q.heads,
+          (long long)q.dim, (long long)k.n, (long long)k.heads, (long long)k.dim, (long long)val.n);
+    CHECK(o.n >= val.n && o.heads == val.heads && o.dim == val.dim, "o is %lld x %lld x %lld, v %lld x %lld x %lld",
+          (long long)o.n, (long long)o.heads, (long long)o.dim, (long long)val.n, (long long)val.heads, (long long)val.dim);
+    CHECK(q.head == q.dim && k.head == k.dim && val.head == val.dim && o.head == o.dim,
+          "q, k, v and o: the heads of a token have to stand side by side");
+    c.k_heads = (int32_t)q.heads, c.v_heads = (int32_t)val.heads;
+    c.k_dim = (int32_t)q.dim, c.v_dim = (int32_t)val.dim;
+    c.scale = (float)scale;
+    const long long rows = val.n * val.heads;
+    if (flat_f32(v[3], rows, "g", &dev, &g) || flat_f32(v[4], rows, "beta", &dev, &beta) ||
+        batch(v[8], &b, &bp, &dev) || flat(v[9], t_u8, 0, "workspace", "a contiguous uint8 CUDA tensor", &dev, &ws) ||
+        stream_of(v[10], &st))
+        return NULL;
+    CHECK(g && beta, "g and beta are required");
+    if (v[9] != Py_None && (bytes = number(v[9], s_numel)) < 0) return NULL;
+    if (v[5] != Py_None) {
+        if ((slots = first_extent(v[5], "state")) < 0) return NULL;
+        if (flat(v[5], t_f32, slots * val.heads * val.dim * q.dim, "state",
+                 "a contiguous float32 CUDA tensor [slots, v_heads, v_dim, k_dim]", &dev, &state))
+            return NULL;
+        if (!slots) Py_RETURN_NONE;
+    }
+    STATUS(moe_delta(&c, bp, q.p, q.ld, k.p, k.ld, val.p, val.ld, g, beta, state, slots, o.p, o.ld, val.n, ws,
+                     (size_t)bytes, st));
+}
+
 /* the torch dtypes float32, bfloat16, int32, uint8 */
 static PyObject* dtypes(ARGS) {
     (void)self;
@@ -322,7 +504,8 @@ static PyObject* dtypes(ARGS) {
 
 #define FN(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {FN(route),   FN(dispatch), FN(quantise), FN(dequantise),
-                                FN(product), FN(combine),  FN(dtypes),   {NULL, NULL, 0, NULL}};
+                                FN(product), FN(combine),  FN(conv),     FN(head_norm),
+                                FN(delta),   FN(dtypes),   {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__call(void) {

@@ -1,0 +1,95 @@
+// mix.h -- the operators between two expert layers (short convolution, head
+// norms, gated delta rule): launchers, and how a batch's sequences are found.
+#pragma once
+
+#include "mx.h"
+
+namespace moe {
+
+constexpr int kDeltaShort = 16;  // rows up to which a sequence of the delta rule runs token by token
+constexpr int kDeltaChunk = 64;
+
+// A batch's sequences (moe_seqs).  Lists on the device are not trusted: rows
+// are clamped to 0..T and a slot outside 0..slots-1 reads as -1.
+struct Seqs {
+    const int32_t* offsets;  // NULL: sequence s has rows s * per .. s * per + per - 1
+    const int32_t* slot_of;
+    const int32_t* carry_of;
+    int n, per;
+    int64_t T;
+    int64_t slots;  // INT64_MAX without a state
+
+    __device__ __forceinline__ int64_t start(int s) const {
+        if (!offsets) return (int64_t)s * per;
+        const int64_t o = offsets[s];
+        return o < 0 ? 0 : o > T ? T : o;
+    }
+    __device__ __forceinline__ int slot(int s) const {
+        const int v = slot_of ? slot_of[s] : s;
+        return v < 0 || v >= slots ? -1 : v;
+    }
+    __device__ __forceinline__ bool carry(int s) const { return !carry_of || carry_of[s] != 0; }
+
+    // Pieces of `size` rows: sequence s has its pieces at start(s) / size + s and after (consecutive sequences never
+    // overlap, see MxRows); `pieces` is their number at most.  The sequence whose pieces begin at or before `piece`,
+    // found by a whole warp, 32 sequences a step.
+    int64_t pieces(int size) const { return offsets ? T / size + n : (int64_t)n * ((per + size - 1) / size); }
+    template <int SIZE>
+    __device__ __forceinline__ int find(int64_t piece, int& index) const {
+        if (!offsets) {
+            const int each = (per + SIZE - 1) / SIZE;
+            index = (int)(piece % each);
+            return (int)(piece / each);
+        }
+        int lo = 0, left = n;
+        while (left > 1) {
+            const int step = (left + 31) >> 5, at = (threadIdx.x & 31) * step;
+            const bool before = at < left && start(lo + at) / SIZE + lo + at <= piece;
+            const int k = __popc(__ballot_sync(0xffffffffu, before));
+            const int skip = k > 1 ? (k - 1) * step : 0;
+            lo += skip;
+            left = min(step, left - skip);
+        }
+        index = (int)(piece - (start(lo) / SIZE + lo));
+        return lo;
+    }
+    template <int SIZE>
+    __device__ __forceinline__ int64_t piece_of(int s) const {
+        return offsets ? start(s) / SIZE + s : (int64_t)s * ((per + SIZE - 1) / SIZE);
+    }
+};
+
+// v / (1 + exp(-v)).  expf, not one multiplication and ex2: that loses |v| 2^-24 of the value, too much for fp32 results
+// from v = -8 on.
+__device__ __forceinline__ float silu(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-v)));
+    return v * r;
+}
+
+// mix_conv.cu
+cudaError_t launch_conv(const Seqs& q, const void* x, int type, int64_t x_ld, int channels, const void* w, int w_type,
+                        int width, const float* bias, int act, void* state, void* y, int64_t y_ld, cudaStream_t st);
+// mix_norm.cu
+cudaError_t launch_head_norm(const moe_head_norm_config& c, const moe_heads& a, const moe_heads* b, const int32_t* pos,
+                             const float* inv_freq, int64_t T, cudaStream_t st);
+// mix_delta.cu
+struct DeltaArgs {
+    moe_delta_config c;
+    Seqs q;
+    const __nv_bfloat16 *qr, *kr, *vr;
+    int64_t q_ld, k_ld, v_ld, o_ld;
+    const float *g, *beta;
+    float* state;
+    __nv_bfloat16* o;
+    uint8_t* ws;
+    int longer_than;  // the chunked kernels leave out sequences of so many rows or fewer, the stepping one those of more
+    int64_t q_pieces;  // of kDeltaChunk rows
+    bool wide;         // q, k and v rows are aligned for 16-byte loads
+    bool o_pairs;      // o rows for stores of two values
+};
+size_t delta_workspace(const moe_delta_config& c, int64_t T, int n);
+cudaError_t launch_delta_steps(const DeltaArgs& a, cudaStream_t st);
+cudaError_t launch_delta_chunks(const DeltaArgs& a, cudaStream_t st);
+
+}  // namespace moe

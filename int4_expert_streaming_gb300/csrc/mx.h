@@ -5,6 +5,9 @@
 
 #include <cuda_bf16.h>
 
+#include <new>
+#include <utility>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -79,6 +82,26 @@ struct MxRows {
         return true;
     }
 };
+
+// For the C entries.
+inline bool type_ok(int t) { return t == MOE_F32 || t == MOE_BF16; }
+
+// an entry's body: no C++ exception leaves the C interface
+template <typename F>
+int guarded(F&& f) {
+    try {
+        return std::forward<F>(f)();
+    } catch (const std::bad_alloc&) {
+        return MOE_ENOMEM;
+    } catch (...) {
+        return MOE_ESTATE;
+    }
+}
+
+inline int launched(cudaError_t e, const char* what) {
+    if (e == cudaSuccess) return MOE_OK;
+    return fail_global(MOE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
 
 // mx_route.cu
 cudaError_t launch_route(const moe_route_config& c, const void* logits, int type, int64_t ld, const float* bias,

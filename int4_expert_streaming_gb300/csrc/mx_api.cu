@@ -1,33 +1,11 @@
 // mx_api.cu -- C entries of the context-free operators: argument checks, then
 // one launcher each (see include/moe.h).
-#include <new>
-#include <utility>
-
 #include "mx.h"
 
 namespace moe {
 namespace {
 
 thread_local bool g_fault = false;  // moe_mx_set_fault
-
-bool type_ok(int t) { return t == MOE_F32 || t == MOE_BF16; }
-
-// an entry's body: no C++ exception leaves the C interface
-template <typename F>
-int guarded(F&& f) {
-    try {
-        return std::forward<F>(f)();
-    } catch (const std::bad_alloc&) {
-        return MOE_ENOMEM;
-    } catch (...) {
-        return MOE_ESTATE;
-    }
-}
-
-int launched(cudaError_t e, const char* what) {
-    if (e == cudaSuccess) return MOE_OK;
-    return fail_global(MOE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
-}
 
 // the descriptor's shape, not its address
 bool mx_ok(const moe_mx* m) {
