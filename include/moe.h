@@ -565,7 +565,7 @@ typedef struct {
     const void* gate_dev; /* likewise, or NULL: y is multiplied by silu(gate) */
     const float* weight_dev; /* fp32 [dim] or NULL */
     int64_t x_ld, x_head, y_ld, y_head, gate_ld, gate_head;
-    int32_t heads; /* 1..65535 */
+    int32_t heads; /* 1..32768 */
     int32_t type;  /* MOE_F32, MOE_BF16: of x, y and gate */
 } moe_heads;
 

@@ -40,7 +40,7 @@ bool all_short(int64_t T, int32_t max_len) { return T <= kDeltaShort || (max_len
 
 int check_heads(const moe_heads& t, const moe_head_norm_config* c, int64_t T, const char* name) {
     if (!type_ok(t.type)) return fail_global(MOE_EINVAL, "moe_head_norm: unknown type %d of %s", t.type, name);
-    if (t.heads < 1 || t.heads > 65535) return fail_global(MOE_EINVAL, "moe_head_norm: %d heads of %s", t.heads, name);
+    if (t.heads < 1 || t.heads > 32768) return fail_global(MOE_EINVAL, "moe_head_norm: %d heads of %s", t.heads, name);
     const int64_t ld[] = {t.x_ld, t.y_ld, t.gate_dev ? t.gate_ld : t.x_ld},
                   head[] = {t.x_head, t.y_head, t.gate_dev ? t.gate_head : t.x_head};
     for (int i = 0; i < 3; ++i)

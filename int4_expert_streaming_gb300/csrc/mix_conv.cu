@@ -9,7 +9,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 32;   // rows of a CTA's piece of a sequence
-constexpr int kAhead = 8;   // rows whose loads are under way at once
+constexpr int kAhead = 8;   // rows that are summed at a time
 
 struct ConvArgs {
     Seqs q;
@@ -23,7 +23,7 @@ struct ConvArgs {
 
 // V consecutive channels of a row as they are in memory
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Row {
+struct alignas(sizeof(T) * V % 16 == 0 ? 16 : sizeof(T) * V % 8 == 0 ? 8 : sizeof(T)) Row {
     T v[V];
 };
 template <typename T, int V>
@@ -32,113 +32,167 @@ __device__ __forceinline__ void widen(const Row<T, V>& r, float (&f)[V]) {
     for (int i = 0; i < V; ++i) f[i] = (float)r.v[i];
 }
 
-// A thread takes V channels (16 bytes, or one where rows are not aligned) down
+template <typename T, bool SILU>
+__device__ __forceinline__ float activated(float v) {
+    return !SILU ? v : sizeof(T) == 2 ? silu_bf16(v) : silu(v);
+}
+
+// the weights of V channels, which stand one after another
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_weights(float (&w)[W][V], const void* from, int c) {
+    Row<T, V * W> r;
+    constexpr int kPart = V * W * sizeof(T) % 8 ? 1 : 8 / (int)sizeof(T);  // wide where c is a multiple of V: 8 bytes
+    const T* p = static_cast<const T*>(from) + (int64_t)c * W;
+    if (kPart > 1 && reinterpret_cast<uintptr_t>(p) % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < V * W / kPart; ++i)
+            reinterpret_cast<Row<T, kPart>*>(r.v)[i] = reinterpret_cast<const Row<T, kPart>*>(p)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W; ++i) r.v[i] = p[i];
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i][j] = (float)r.v[j * W + i];
+}
+
+// A thread takes V channels (8 bytes, or one where rows are not aligned) down
 // a piece of kTile rows, the last W - 1 inputs in registers; a piece reads the
 // W - 1 rows before it again.  Bound by memory: each input and output once.
-// The first piece's CTAs read the old state and also write the new one, so no
-// two CTAs touch a slot's channel.
-template <typename T, int V, int W>
+// Wide rows are copied to shared memory, all of a piece at once, where each
+// thread finds what it has itself copied: the loads under way are then not
+// limited by registers.  The first piece's CTAs read the old state and also
+// write the new one, so no two CTAs touch a slot's channel.
+template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ ConvArgs a) {
+    using R = Row<T, V>;
+    constexpr bool kCopy = V > 1;
+    __shared__ R ring[kCopy ? kTile : 1][kThreads];
     after_previous();
     let_next_start();
     int piece;
     const int s = a.q.find<kTile>(blockIdx.x, piece);
     const int64_t lo = a.q.start(s), hi = a.q.start(s + 1), first = lo + (int64_t)piece * kTile;
     const int slot = a.q.slot(s);
+    const bool carry = a.state && a.q.carry(s);
     const int c = (blockIdx.y * kThreads + threadIdx.x) * V;
     if (piece < 0 || first >= hi || slot < 0 || c >= a.channels) return;
     const int rows = (int)(hi - first < kTile ? hi - first : kTile);
 
-    using R = Row<T, V>;
-    const T* x = static_cast<const T*>(a.x) + c;
+    const T* x = static_cast<const T*>(a.x) + first * a.x_ld + c;
+    if constexpr (kCopy) {
+        const T* from = x;
+#pragma unroll
+        for (int t = 0; t < kTile; ++t, from += a.x_ld) {
+            if (t < rows)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(&ring[t][threadIdx.x])),
+                             "l"(from) : "memory");
+            if (t % kAhead == kAhead - 1) asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+    float w[W][V], bias[V], past[W - 1][V];
+    if (a.w_bf16)
+        load_weights<__nv_bfloat16, V, W>(w, a.w, c);
+    else
+        load_weights<float, V, W>(w, a.w, c);
+#pragma unroll
+    for (int j = 0; j < V; ++j) bias[j] = a.bias ? a.bias[c + j] : 0.0f;
+
     T* y = static_cast<T*>(a.y) + first * a.y_ld + c;
     T* state = a.state ? static_cast<T*>(a.state) + (int64_t)slot * (W - 1) * a.channels + c : nullptr;
-    const bool carry = state && a.q.carry(s);
-
-    R old[W - 1];  // the slot's rows, oldest first
+    R old[W - 1];  // the rows before the piece, oldest first
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
         memset(&old[i], 0, sizeof(R));
-        if (piece == 0 && carry) old[i] = *reinterpret_cast<const R*>(state + (int64_t)i * a.channels);
-    }
-    float w[W][V], bias[V], past[W - 1][V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        bias[j] = a.bias ? a.bias[c + j] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const int64_t at = (int64_t)(c + j) * W + i;
-            w[i][j] = a.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[at]) : static_cast<const float*>(a.w)[at];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < W - 1; ++i) {
-        if (piece > 0) old[i] = *reinterpret_cast<const R*>(x + (first - (W - 1) + i) * a.x_ld);
+        if (piece > 0)
+            old[i] = *reinterpret_cast<const R*>(x + (i - (W - 1)) * a.x_ld);
+        else if (carry)
+            old[i] = *reinterpret_cast<const R*>(state + (int64_t)i * a.channels);
         widen(old[i], past[i]);
     }
-    x += first * a.x_ld;
-    for (int t0 = 0; t0 < rows; t0 += kAhead) {
+#pragma unroll
+    for (int group = 0; group < kTile / kAhead; ++group) {
+        const int t0 = group * kAhead;
+        if (t0 >= rows) break;
         R in[kAhead];
+        if constexpr (kCopy) {
+            // all groups but the ones after this
+            static_assert(kTile / kAhead == 4, "four groups");
+            if (group == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
+            if (group == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
+            if (group == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            if (group == 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-        for (int t = 0; t < kAhead; ++t)
-            if (t0 + t < rows) in[t] = *reinterpret_cast<const R*>(x + (t0 + t) * a.x_ld);
+            for (int t = 0; t < kAhead; ++t) in[t] = ring[t0 + t][threadIdx.x];
+        } else {
 #pragma unroll
-        for (int t = 0; t < kAhead; ++t) {
-            if (t0 + t < rows) {
-                float now[V];
-                widen(in[t], now);
-                R out;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float sum = bias[j];
-#pragma unroll
-                    for (int i = 0; i < W - 1; ++i) sum = fmaf(w[i][j], past[i][j], sum);
-                    sum = fmaf(w[W - 1][j], now[j], sum);
-                    out.v[j] = (T)(a.act == MOE_ACT_SILU ? silu(sum) : sum);
-#pragma unroll
-                    for (int i = 0; i + 1 < W - 1; ++i) past[i][j] = past[i + 1][j];
-                    past[W - 2][j] = now[j];
-                }
-                *reinterpret_cast<R*>(y + (t0 + t) * a.y_ld) = out;
-            }
+            for (int t = 0; t < kAhead; ++t)
+                if (t0 + t < rows) in[t] = *reinterpret_cast<const R*>(x + (t0 + t) * a.x_ld);
         }
+        float win[W - 1 + kAhead][V];  // and the rows before
+#pragma unroll
+        for (int t = 0; t < W - 1; ++t)
+#pragma unroll
+            for (int j = 0; j < V; ++j) win[t][j] = past[t][j];
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t, y += a.y_ld) {
+            widen(in[t], win[W - 1 + t]);
+            R out;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float sum = bias[j];
+#pragma unroll
+                for (int i = 0; i < W; ++i) sum = fmaf(w[i][j], win[t + i][j], sum);
+                out.v[j] = (T)activated<T, SILU>(sum);
+            }
+            if (t0 + t < rows) *reinterpret_cast<R*>(y) = out;
+        }
+#pragma unroll
+        for (int t = 0; t < W - 1; ++t)
+#pragma unroll
+            for (int j = 0; j < V; ++j) past[t][j] = win[kAhead + t][j];
     }
     if (piece == 0 && state) {
         // the last W - 1 of the slot's rows and the sequence's
         const int64_t len = hi - lo;
-        R next[W - 1];
+        R last[W - 1];
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
             const int64_t at = len - (W - 1) + i;
             if (at >= 0) {
-                next[i] = *reinterpret_cast<const R*>(x + at * a.x_ld);
+                last[i] = *reinterpret_cast<const R*>(x + at * a.x_ld);
             } else {
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)
-                    if (j == at + W - 1) next[i] = old[j];
+                    if (j == at + W - 1) last[i] = old[j];
             }
         }
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) *reinterpret_cast<R*>(state + (int64_t)i * a.channels) = next[i];
+        for (int i = 0; i < W - 1; ++i) *reinterpret_cast<R*>(state + (int64_t)i * a.channels) = last[i];
     }
+}
+
+template <typename T, int V, int W>
+cudaError_t launch_act(const ConvArgs& a, cudaStream_t st) {
+    const dim3 grid((unsigned)a.q.pieces(kTile), (unsigned)((a.channels + kThreads * V - 1) / (kThreads * V)));
+    if (a.act == MOE_ACT_SILU) return launch(conv_kernel<T, V, W, true>, grid, kThreads, 0, st, 1, a);
+    return launch(conv_kernel<T, V, W, false>, grid, kThreads, 0, st, 1, a);
 }
 
 template <typename T, int V>
 cudaError_t launch_width(const ConvArgs& a, int width, cudaStream_t st) {
-    const dim3 grid((unsigned)a.q.pieces(kTile), (unsigned)((a.channels + kThreads * V - 1) / (kThreads * V)));
-    switch (width) {
-        case 2: return launch(conv_kernel<T, V, 2>, grid, kThreads, 0, st, 1, a);
-        case 3: return launch(conv_kernel<T, V, 3>, grid, kThreads, 0, st, 1, a);
-        default: return launch(conv_kernel<T, V, 4>, grid, kThreads, 0, st, 1, a);
-    }
+    if (width == 2) return launch_act<T, V, 2>(a, st);
+    if (width == 3) return launch_act<T, V, 3>(a, st);
+    return launch_act<T, V, 4>(a, st);
 }
 
 template <typename T>
 cudaError_t launch_type(const ConvArgs& a, int width, cudaStream_t st) {
-    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int V = 8 / (int)sizeof(T);
     const bool wide = a.channels % V == 0 && a.x_ld % V == 0 && a.y_ld % V == 0 &&
                       (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
-                       reinterpret_cast<uintptr_t>(a.state)) % 16 == 0;
+                       reinterpret_cast<uintptr_t>(a.state)) % 8 == 0;
     return wide ? launch_width<T, V>(a, width, st) : launch_width<T, 1>(a, width, st);
 }
 

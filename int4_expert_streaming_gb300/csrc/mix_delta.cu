@@ -16,117 +16,130 @@ constexpr int kC = kDeltaChunk;
 // ------------------------------------------------------------------ //
 // With S' = e^g S:  u = beta (v - S' k),  S <- S' + u k^T,  o = S' q + u (k q):
 // all sums over k_dim of one token (S' k, S' q, k q) are formed together.
-// Eight threads share a row of S and keep it in registers over the tokens of
-// the run; a warp has four rows twice.  Bound by reading and writing S.
-constexpr int kStepRows = 32;  // rows of S of a CTA of four warps
+// kLanes threads share a row of S and keep it in registers over the tokens of
+// the run, kRows rows each.  Bound by reading and writing S: its loads are
+// issued before anything else is waited for, together with the first tokens'.
+constexpr int kLanes = 16, kRows = 2;
+constexpr int kStepRows = 128 / kLanes * kRows;  // rows of S of a CTA of four warps
+
+// KD / kLanes values of a row of K or Q, still packed
+template <int KD>
+struct Token {
+    static constexpr int kE = KD / kLanes;  // values of a thread: 8 or 4
+    uint32_t k[kE / 2], q[kE / 2];
+    __nv_bfloat16 v[kRows];
+    float g, beta;
+};
+__device__ __forceinline__ void packed(uint32_t (&w)[4], const __nv_bfloat16* p, bool wide) {
+    if (wide) {
+        *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = reinterpret_cast<const unsigned short*>(p)[2 * i] | (uint32_t)reinterpret_cast<const unsigned short*>(p)[2 * i + 1] << 16;
+    }
+}
+__device__ __forceinline__ void packed(uint32_t (&w)[2], const __nv_bfloat16* p, bool wide) {
+    if (wide) {
+        *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = reinterpret_cast<const unsigned short*>(p)[2 * i] | (uint32_t)reinterpret_cast<const unsigned short*>(p)[2 * i + 1] << 16;
+    }
+}
 
 template <int KD>
 __global__ void __launch_bounds__(128) steps_kernel(const __grid_constant__ DeltaArgs a) {
     after_previous();
     let_next_start();
-    constexpr int kJ = KD / 32;  // float4 of a thread's part of a row
+    constexpr int kE = KD / kLanes;
     const int dk = a.c.k_dim, dv = a.c.v_dim, Hv = a.c.v_heads;
     const int blocks = (dv + kStepRows - 1) / kStepRows;
     const int s = blockIdx.x / blocks, h = blockIdx.y, kh = h / (Hv / a.c.k_heads);
     const int64_t lo = a.q.start(s), hi = a.q.start(s + 1);
     const int slot = a.q.slot(s);
+    const bool carry = a.state && a.q.carry(s);
     if (lo >= hi || hi - lo > a.longer_than || slot < 0) return;
-    const int lane = threadIdx.x & 31, sub = lane & 7;
-    const int d0 = (blockIdx.x % blocks) * kStepRows + (threadIdx.x >> 5) * 8 + (lane >> 3);  // and d0 + 4
+    const int lane = threadIdx.x % kLanes, at = lane * kE;
+    const int d0 = (blockIdx.x % blocks) * kStepRows + threadIdx.x / kLanes * kRows;
+    const bool in_k = at < dk;
 
-    float* state = a.state ? a.state + ((int64_t)slot * Hv + h) * dv * dk : nullptr;
-    float4 S[2][kJ];
+    auto load = [&](int64_t t, Token<KD>& in) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-            const int at = 4 * (sub + 8 * j), d = d0 + 4 * p;
-            S[p][j] = make_float4(0, 0, 0, 0);
-            if (state && at < dk && d < dv && a.q.carry(s))
-                S[p][j] = *reinterpret_cast<const float4*>(state + (int64_t)d * dk + at);
-        }
-
-    struct In {
-        float4 k[kJ], q[kJ];
-        float v[2], g, beta;
-    };
-    auto four = [](const __nv_bfloat16* p, bool wide) {
-        uint2 w;
-        if (wide) {
-            w = *reinterpret_cast<const uint2*>(p);
-        } else {
-            unsigned short t[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] = reinterpret_cast<const unsigned short*>(p)[i];
-            memcpy(&w, t, 8);
-        }
-        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                           __uint_as_float(w.y & 0xffff0000u));
-    };
-    auto load = [&](int64_t t, In& in) {
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-            const int at = 4 * (sub + 8 * j);
-            in.k[j] = in.q[j] = make_float4(0, 0, 0, 0);
-            if (at < dk) {
-                in.k[j] = four(a.kr + t * a.k_ld + kh * dk + at, a.wide);
-                in.q[j] = four(a.qr + t * a.q_ld + kh * dk + at, a.wide);
-            }
+        for (int i = 0; i < kE / 2; ++i) in.k[i] = in.q[i] = 0;
+        if (in_k) {
+            packed(in.k, a.kr + t * a.k_ld + kh * dk + at, a.wide);
+            packed(in.q, a.qr + t * a.q_ld + kh * dk + at, a.wide);
         }
 #pragma unroll
-        for (int p = 0; p < 2; ++p) in.v[p] = d0 + 4 * p < dv ? __bfloat162float(a.vr[t * a.v_ld + h * dv + d0 + 4 * p]) : 0;
+        for (int p = 0; p < kRows; ++p) in.v[p] = d0 + p < dv ? a.vr[t * a.v_ld + h * dv + d0 + p] : __nv_bfloat16(0.0f);
         in.g = a.g[t * Hv + h];
         in.beta = a.beta[t * Hv + h];
     };
-    In next;
-    load(lo, next);
+    float* state = a.state ? a.state + (((int64_t)slot * Hv + h) * dv + d0) * dk + at : nullptr;
+    float S[kRows][kE];
+#pragma unroll
+    for (int p = 0; p < kRows; ++p)
+#pragma unroll
+        for (int i = 0; i < kE; i += 4) {
+            const bool there = carry && in_k && d0 + p < dv;
+            *reinterpret_cast<float4*>(&S[p][i]) =
+                there ? *reinterpret_cast<const float4*>(state + p * dk + i) : make_float4(0, 0, 0, 0);
+        }
+    Token<KD> next[2];
+    load(lo, next[0]);
+    if (lo + 1 < hi) load(lo + 1, next[1]);
     for (int64_t t = lo; t < hi; ++t) {
-        const In in = next;
-        if (t + 1 < hi) load(t + 1, next);
+        const Token<KD> in = next[0];
+        next[0] = next[1];
+        if (t + 2 < hi) load(t + 2, next[1]);
         const float decay = expf(in.g);
-        float sk[2] = {0, 0}, sq[2] = {0, 0}, kq = 0;
+        float k[kE], q[kE], sk[kRows], sq[kRows], kq = 0;
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-            const float4 k = in.k[j], q = in.q[j];
-            kq = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, kq))));
+        for (int i = 0; i < kE / 2; ++i) {
+            k[2 * i] = __uint_as_float(in.k[i] << 16), k[2 * i + 1] = __uint_as_float(in.k[i] & 0xffff0000u);
+            q[2 * i] = __uint_as_float(in.q[i] << 16), q[2 * i + 1] = __uint_as_float(in.q[i] & 0xffff0000u);
+        }
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                float4& r = S[p][j];
-                r.x *= decay, r.y *= decay, r.z *= decay, r.w *= decay;
-                sk[p] = fmaf(r.x, k.x, fmaf(r.y, k.y, fmaf(r.z, k.z, fmaf(r.w, k.w, sk[p]))));
-                sq[p] = fmaf(r.x, q.x, fmaf(r.y, q.y, fmaf(r.z, q.z, fmaf(r.w, q.w, sq[p]))));
+        for (int i = 0; i < kE; ++i) kq = fmaf(k[i], q[i], kq);
+#pragma unroll
+        for (int p = 0; p < kRows; ++p) {
+            sk[p] = sq[p] = 0;
+#pragma unroll
+            for (int i = 0; i < kE; ++i) {
+                S[p][i] *= decay;
+                sk[p] = fmaf(S[p][i], k[i], sk[p]);
+                sq[p] = fmaf(S[p][i], q[i], sq[p]);
             }
         }
 #pragma unroll
-        for (int d = 1; d < 8; d <<= 1) {
+        for (int d = 1; d < kLanes; d <<= 1) {
             kq += __shfl_xor_sync(kAll, kq, d);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < kRows; ++p) {
                 sk[p] += __shfl_xor_sync(kAll, sk[p], d);
                 sq[p] += __shfl_xor_sync(kAll, sq[p], d);
             }
         }
+        float o[kRows];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const float u = in.beta * (in.v[p] - sk[p]);
+        for (int p = 0; p < kRows; ++p) {
+            const float u = in.beta * (__bfloat162float(in.v[p]) - sk[p]);
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-                S[p][j].x = fmaf(u, in.k[j].x, S[p][j].x);
-                S[p][j].y = fmaf(u, in.k[j].y, S[p][j].y);
-                S[p][j].z = fmaf(u, in.k[j].z, S[p][j].z);
-                S[p][j].w = fmaf(u, in.k[j].w, S[p][j].w);
-            }
-            if (sub == 0 && d0 + 4 * p < dv)
-                a.o[t * a.o_ld + h * dv + d0 + 4 * p] = __float2bfloat16_rn(a.c.scale * fmaf(u, kq, sq[p]));
+            for (int i = 0; i < kE; ++i) S[p][i] = fmaf(u, k[i], S[p][i]);
+            o[p] = a.c.scale * fmaf(u, kq, sq[p]);
         }
+        if (lane < kRows && d0 + lane < dv)
+            a.o[t * a.o_ld + h * dv + d0 + lane] = __float2bfloat16_rn(lane ? o[kRows - 1] : o[0]);
     }
-    if (state) {
+    if (state && in_k) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < kRows; ++p)
+            if (d0 + p < dv) {
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
-                const int at = 4 * (sub + 8 * j), d = d0 + 4 * p;
-                if (at < dk && d < dv) *reinterpret_cast<float4*>(state + (int64_t)d * dk + at) = S[p][j];
+                for (int i = 0; i < kE; i += 4)
+                    *reinterpret_cast<float4*>(state + p * dk + i) = *reinterpret_cast<const float4*>(&S[p][i]);
             }
     }
 }
@@ -160,7 +173,10 @@ struct Factors {
     float p[kC];   // scale of P's row, times the factor on o
     float qs[kC];  // e^G_i times the scale of q's row, times the factor on o
     float left[kC];  // e^(G_63 - G_i) times the scale of k's row
-    float all[4];  // e^G_63
+    float all;       // e^G_63
+    // how large things can get, from what came before: V - e^G K S^T over the largest of S, beside V; U over the
+    // largest of that; and `left` itself
+    float most_ks, most_t, most_left;
 };
 constexpr int kSquare = kC * kC * 2;
 constexpr int kHeadBytes = (3 * kSquare + (int)sizeof(Factors) + 127) / 128 * 128;
@@ -200,6 +216,7 @@ __device__ __forceinline__ float2 unpack(uint32_t w) { return __half22float2(*re
 
 // The power of two that brings a largest magnitude to [2^14, 2^15), and its
 // inverse.  `e`: the magnitude's exponent field, kept within what both allow.
+constexpr int kOne = 141;  // the exponent field of which both are 1
 __device__ __forceinline__ int field(float m) { return max((int)(__float_as_uint(m) >> 23), 16); }
 __device__ __forceinline__ float up(int e) { return __uint_as_float((uint32_t)(268 - e) << 23); }    // 2^(14 - (e - 127))
 __device__ __forceinline__ float down(int e) {                                                        // 2^(e - 127 - 14)
@@ -224,14 +241,20 @@ __device__ __forceinline__ uint32_t right_at(uint32_t base, int r0, int p, int l
     return base + piece_at<N>(r0 + (lane & 7) + ((lane >> 4) << 3), p + ((lane >> 3) & 1));
 }
 
-constexpr int kPitch = kC + 4;  // floats of a row of A
+constexpr int kPitch = kC + 4;  // floats of a row of A and T: rows of 8 lanes are on different banks
+constexpr int kPrepare = 256;   // threads: four warps for each of two v heads
 
 template <int KD>
 struct PrepareShared {
-    uint8_t k[kC * KD * 2], q[kC * KD * 2];
-    float A[2][kC][kPitch];  // two v heads at a time: A, then T
-    float k_scale[kC], q_scale[kC];
+    float A[2][kC][kPitch];
+    union {
+        uint8_t kq[2][kC * KD * 2];  // K and Q, bf16; then
+        float T[2][kC][kPitch];      // the lower blocks; the upper ones hold what their lower ones are made of
+    };
+    float k_scale[kC], q_scale[kC], k_sum[kC], q_top[kC];
     float g_high[2][kC], g_rest[2][kC], beta[2][kC];
+    float before[2][4][kC];  // e^(G_16w - G_j), j < 16 w
+    unsigned most[2];        // bits of the largest row sum of |T|
 };
 
 __device__ __forceinline__ uint4 eight(const __nv_bfloat16* p, bool wide) {
@@ -244,12 +267,60 @@ __device__ __forceinline__ uint4 eight(const __nv_bfloat16* p, bool wide) {
     return w;
 }
 
-// One chunk and k head: K16 and Q16; then for its v heads, two at a time, the
-// factors, P and T.  (1 + A)^-1 by substitution down each of its 64 columns, a
-// thread a column, in fp32.
+// left[16 x 16] right[16 x 16] (rows of kPitch floats), added to acc: columns 0..7 and 8..15 as accumulator blocks.  Each
+// number enters as two of 11 bits; the product of the two rests is left out, which leaves 2^-22.
+__device__ __forceinline__ void halves(float x, uint32_t& high, uint32_t& rest) {
+    high = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // to nearest
+    rest = (__float_as_uint(x - __uint_as_float(high)) + 0x1000u) & 0xffffe000u;
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void block_product(float (&acc)[2][4], const float* left, const float* right, int lane) {
+    const float *l0 = left + (lane >> 2) * kPitch + (lane & 3), *r0 = right + (lane & 3) * kPitch + (lane >> 2);
+#pragma unroll
+    for (int k = 0; k < 16; k += 8) {
+        uint32_t ah[4], ar[4], bh[2][2], br[2][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) halves(l0[(i & 1) * 8 * kPitch + k + (i >> 1) * 4], ah[i], ar[i]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) halves(r0[(k + 4 * i) * kPitch + 8 * n], bh[n][i], br[n][i]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            mma_tf32(acc[n], ar, bh[n]);
+            mma_tf32(acc[n], ah, br[n]);
+            mma_tf32(acc[n], ah, bh[n]);
+        }
+    }
+}
+__device__ __forceinline__ void block_store(float* to, const float (&acc)[2][4], float sign, int lane) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2*>(to + ((lane >> 2) + 8 * i) * kPitch + 8 * n + (lane & 3) * 2) =
+                make_float2(sign * acc[n][2 * i], sign * acc[n][2 * i + 1]);
+}
+// the four warps of one of the two heads
+__device__ __forceinline__ void head_barrier(int b) {
+    if (b)
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+    else
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+// One chunk and two v heads of a k head: K16 and Q16, the factors, P and T.
+// (1 + A)^-1 by blocks of 16: the four on the diagonal by substitution in fp32,
+// a lane a column; then T_10 and T_32, and of those the lower left quarter, by
+//   (T_11 0; T_21 T_22) with T_21 = -T_22 A_21 T_11.
+// Bound by issuing instructions.
 template <int KD>
-__global__ void __launch_bounds__(128) prepare_kernel(const __grid_constant__ DeltaArgs a) {
-    extern __shared__ uint8_t raw[];
+__global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_constant__ DeltaArgs a) {
+    extern __shared__ __align__(128) uint8_t raw[];
     PrepareShared<KD>& m = *reinterpret_cast<PrepareShared<KD>*>(raw);
     after_previous();
     let_next_start();
@@ -259,29 +330,44 @@ __global__ void __launch_bounds__(128) prepare_kernel(const __grid_constant__ De
     if (c < 0 || hi - lo <= a.longer_than || (int64_t)c * kC >= hi - lo || a.q.slot(s) < 0) return;
     const int64_t row0 = lo + (int64_t)c * kC;
     const int rows = (int)(hi - row0 < kC ? hi - row0 : kC);
-    const int kh = blockIdx.y, Hk = a.c.k_heads, Hv = a.c.v_heads, share = Hv / Hk, dk = a.c.k_dim;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int Hk = a.c.k_heads, Hv = a.c.v_heads, share = Hv / Hk, dk = a.c.k_dim;
+    const int twos = (share + 1) / 2, kh = blockIdx.y / twos, h0 = blockIdx.y % twos * 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3, b = tid >> 7;  // b: which of two heads
+    const bool there = h0 + b < share;
+    const int h = kh * share + h0 + (there ? b : 0);
     uint8_t* pair = a.ws + ((int64_t)blockIdx.x * Hk + kh) * pair_bytes(KD);
-    uint8_t* heads = a.ws + a.q_pieces * Hk * pair_bytes(KD) + ((int64_t)blockIdx.x * Hv + kh * share) * kHeadBytes;
+    uint8_t* out = a.ws + a.q_pieces * Hk * pair_bytes(KD) + ((int64_t)blockIdx.x * Hv + h) * kHeadBytes;
+    Factors& f = *reinterpret_cast<Factors*>(out + 3 * kSquare);
 
-    // rows of K and Q: KD / 8 threads a row
-    constexpr int kRow = KD / 8, kPass = 128 / kRow, kN = kC / kPass;
+    float g[2] = {0, 0}, beta2[2] = {0, 0};  // of two neighbouring tokens a lane, in the first warp
+    if (warp == 0) {
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        const __nv_bfloat16* src = (which ? a.qr + row0 * a.q_ld : a.kr + row0 * a.k_ld) + kh * dk;
-        const int64_t ld = which ? a.q_ld : a.k_ld;
-        const int p = tid % kRow;
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            if (r < rows) {
+                g[i] = a.g[(row0 + r) * Hv + h];
+                beta2[i] = a.beta[(row0 + r) * Hv + h];
+            }
+        }
+    }
+    // rows of K (the first four warps) and Q: KD / 8 threads a row
+    constexpr int kRow = KD / 8, kPass = 128 / kRow, kN = kC / kPass;
+    {
+        const __nv_bfloat16* src = (b ? a.qr + row0 * a.q_ld : a.kr + row0 * a.k_ld) + kh * dk;
+        const int64_t ld = b ? a.q_ld : a.k_ld;
+        const int p = tid % kRow, r0 = (tid & 127) / kRow;
         uint4 w[kN];
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int r = tid / kRow + i * kPass;
+            const int r = r0 + i * kPass;
             w[i] = make_uint4(0, 0, 0, 0);
             if (r < rows && p * 8 < dk) w[i] = eight(src + r * ld + p * 8, a.wide);
         }
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int r = tid / kRow + i * kPass;
+            const int r = r0 + i * kPass;
             const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            *reinterpret_cast<uint4*>(m.kq[b] + piece_at<kRow>(r, p)) = w[i];
             uint32_t top = 0;  // of the magnitudes' bits, which order as the magnitudes do
 #pragma unroll
             for (int j = 0; j < 4; ++j) top = __vmaxu2(top, v[j] & 0x7fff7fffu);
@@ -290,169 +376,247 @@ __global__ void __launch_bounds__(128) prepare_kernel(const __grid_constant__ De
             for (int d = 1; d < kRow; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
             const int e = max((int)(top >> 7), 16);
             const float f = up(e);
-            uint4 h;
-            uint32_t* hw = reinterpret_cast<uint32_t*>(&h);
+            uint4 w16;
+            uint32_t* hw = reinterpret_cast<uint32_t*>(&w16);
+            float sum = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                hw[j] = pack(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
-            *reinterpret_cast<uint4*>(pair + which * (kC * KD * 2) + piece_at<kRow>(r, p)) = h;
-            *reinterpret_cast<uint4*>((which ? m.q : m.k) + piece_at<kRow>(r, p)) = w[i];
-            if (p == 0) (which ? m.q_scale : m.k_scale)[r] = down(e);
+            for (int j = 0; j < 4; ++j) {
+                const float x = __uint_as_float(v[j] << 16), y = __uint_as_float(v[j] & 0xffff0000u);
+                hw[j] = pack(x * f, y * f);
+                sum += fabsf(x) + fabsf(y);
+            }
+            if (h0 == 0) *reinterpret_cast<uint4*>(pair + b * (kC * KD * 2) + piece_at<kRow>(r, p)) = w16;
+            if (!b) {
+#pragma unroll
+                for (int d = 1; d < kRow; d <<= 1) sum += __shfl_xor_sync(kAll, sum, d);
+            }
+            if (p == 0) {
+                (b ? m.q_scale : m.k_scale)[r] = down(e);
+                (b ? m.q_top : m.k_sum)[r] = b ? __uint_as_float(top << 16) : sum;
+            }
         }
+    }
+    // sums of g in fp64 (64 additions), kept as two floats: differences of far sums stay exact
+    if (warp == 0) {
+        double G[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            G[i] = g[i] < -120.0f ? -120.0f : g[i];  // e^-120 is 0 in fp32, and -inf has no differences
+            m.beta[b][2 * lane + i] = beta2[i];
+        }
+        G[1] += G[0];
+        double before = G[1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const double o = __shfl_up_sync(kAll, before, d);
+            if (lane >= d) before += o;
+        }
+        before = __shfl_up_sync(kAll, before, 1);
+        if (lane == 0) before = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            G[i] += before;
+            m.g_high[b][2 * lane + i] = (float)G[i];
+            m.g_rest[b][2 * lane + i] = (float)(G[i] - (double)(float)G[i]);
+        }
+        if (lane == 0) m.most[b] = 0;
     }
     __syncthreads();
 
-    // K K^T and Q K^T, rows 16 warp .. +15, columns up to the diagonal block
-    float kk[8][4], qk[8][4];
+    const float *gh = m.g_high[b], *gr = m.g_rest[b];
+    const uint32_t k_at = smem_at(m.kq[0]), q_at = smem_at(m.kq[1]);
+    if (there) {
+        // e^(G_i - G_j) = e^(G_i - G_16w) e^(G_16w - G_j) in the blocks left of the diagonal ones, both 1 or less
+        float most_k = fmaxf(m.k_sum[lane], m.k_sum[lane + 32]);
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+        for (int d = 1; d < 32; d <<= 1) most_k = fmaxf(most_k, __shfl_xor_sync(kAll, most_k, d));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kk[n][i] = qk[n][i] = 0;
-    const uint32_t k_at = smem_at(m.k), q_at = smem_at(m.q);
-#pragma unroll
-    for (int t = 0; t < KD / 16; ++t) {
-        uint32_t ka[4], qa[4];
-        ldmatrix(ka, left_at<kRow>(k_at, 16 * warp, 2 * t, lane));
-        ldmatrix(qa, left_at<kRow>(q_at, 16 * warp, 2 * t, lane));
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            if (n > warp) continue;
-            uint32_t b[4];
-            ldmatrix(b, right_at<kRow>(k_at, 16 * n, 2 * t, lane));
-            mma_bf16(kk[2 * n], ka, b[0], b[1]);
-            mma_bf16(kk[2 * n + 1], ka, b[2], b[3]);
-            mma_bf16(qk[2 * n], qa, b[0], b[1]);
-            mma_bf16(qk[2 * n + 1], qa, b[2], b[3]);
+        for (int i = 0; i < 2; ++i) {
+            const int j = lane + 32 * i;
+            if (j < 16 * warp) m.before[b][warp][j] = expf((gh[16 * warp] - gh[j]) + (gr[16 * warp] - gr[j]));
         }
-    }
-
-    for (int h0 = 0; h0 < share; h0 += 2) {
-        const int count = min(2, share - h0);
-        // sums of g in fp64 (64 additions), kept as two floats: differences of far sums stay exact
-        if (warp < count) {
-            const int h = kh * share + h0 + warp;
-            double G[2];
+        __syncwarp();
+        if (warp == 0) {  // which has the shortest rows below
+            float most_ks = 0, most_left = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = 2 * lane + i;
-                float g = 0, beta = 0;
-                if (r < rows) {
-                    g = a.g[(row0 + r) * Hv + h];
-                    beta = a.beta[(row0 + r) * Hv + h];
-                    if (g < -120.0f) g = -120.0f;  // e^-120 is 0 in fp32, and -inf has no differences
-                }
-                G[i] = g;
-                m.beta[warp][r] = beta;
+                const int r = lane + 32 * i;
+                const float e = expf(gh[r] + gr[r]);
+                const float left = expf((gh[kC - 1] - gh[r]) + (gr[kC - 1] - gr[r])) * m.k_scale[r];
+                f.ks[r] = e * m.k_scale[r];
+                f.qs[r] = e * m.q_scale[r] * a.c.scale;
+                f.left[r] = left;
+                most_ks = fmaxf(most_ks, e * m.k_sum[r]);
+                most_left = fmaxf(most_left, left);
+                if (r == kC - 1) f.all = e;
             }
-            G[1] += G[0];
-            double before = G[1];
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const double o = __shfl_up_sync(kAll, before, d);
-                if (lane >= d) before += o;
+                most_ks = fmaxf(most_ks, __shfl_xor_sync(kAll, most_ks, d));
+                most_left = fmaxf(most_left, __shfl_xor_sync(kAll, most_left, d));
             }
-            before = __shfl_up_sync(kAll, before, 1);
-            if (lane == 0) before = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                G[i] += before;
-                m.g_high[warp][2 * lane + i] = (float)G[i];
-                m.g_rest[warp][2 * lane + i] = (float)(G[i] - (double)(float)G[i]);
-            }
+            if (lane == 0) f.most_ks = most_ks, f.most_left = most_left;
         }
-        __syncthreads();
-        for (int b = 0; b < count; ++b) {
-            uint8_t* out = heads + (int64_t)(h0 + b) * kHeadBytes;
-            Factors& f = *reinterpret_cast<Factors*>(out + 3 * kSquare);
-            const float *gh = m.g_high[b], *gr = m.g_rest[b];
-            if (tid < kC) {
-                const float e = expf(gh[tid] + gr[tid]);
-                const float rest = expf((gh[kC - 1] - gh[tid]) + (gr[kC - 1] - gr[tid]));
-                f.ks[tid] = e * m.k_scale[tid];
-                f.qs[tid] = e * m.q_scale[tid] * a.c.scale;
-                f.left[tid] = rest * m.k_scale[tid];
-                if (tid == kC - 1) f.all[0] = e;
+        // A and P, rows 16 warp .. +15, columns up to the diagonal block
+        float after[2], beta[2], p_up[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 16 * warp + (lane >> 2) + 8 * i;
+            after[i] = expf((gh[r] - gh[16 * warp]) + (gr[r] - gr[16 * warp]));
+            beta[i] = m.beta[b][r];
+            // |q_i k_j| is at most the largest of q_i times the sum of k_j; a bound will do for 11 bits
+            const int e = field(2.0f * m.q_top[r] * most_k);
+            p_up[i] = up(e);
+            if ((lane & 3) == 0) f.p[r] = down(e) * a.c.scale;
+        }
+        auto decay = [&](int n, float (&L)[2][2]) {
+            const int j = 8 * n + 2 * (lane & 3);
+            if (n >= 2 * warp) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 16 * warp + (lane >> 2) + 8 * i;
+                    L[i][0] = j <= r ? expf((gh[r] - gh[j]) + (gr[r] - gr[j])) : 0.0f;
+                    L[i][1] = j + 1 <= r ? expf((gh[r] - gh[j + 1]) + (gr[r] - gr[j + 1])) : 0.0f;
+                }
+            } else {
+                const float2 e = *reinterpret_cast<const float2*>(&m.before[b][warp][j]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) L[i][0] = after[i] * e.x, L[i][1] = after[i] * e.y;
             }
-            float top[2] = {0, 0};
-            float P[8][4];
+        };
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {  // K K^T, then Q K^T
+            float acc[8][4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][i] = 0;
+#pragma unroll
+            for (int t = 0; t < KD / 16; ++t) {
+                uint32_t l[4];
+                ldmatrix(l, left_at<kRow>(which ? q_at : k_at, 16 * warp, 2 * t, lane));
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    if (n > warp) continue;
+                    uint32_t w[4];
+                    ldmatrix(w, right_at<kRow>(k_at, 16 * n, 2 * t, lane));
+                    mma_bf16(acc[2 * n], l, w[0], w[1]);
+                    mma_bf16(acc[2 * n + 1], l, w[2], w[3]);
+                }
+            }
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
                 if (n > 2 * warp + 1) continue;
+                const int j = 8 * n + 2 * (lane & 3);
+                float L[2][2];
+                decay(n, L);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * warp + (lane >> 2) + 8 * (i >> 1), j = 8 * n + 2 * (lane & 3) + (i & 1);
-                    const float L = j <= r ? expf((gh[r] - gh[j]) + (gr[r] - gr[j])) : 0.0f;
-                    m.A[b][r][j] = j < r ? m.beta[b][r] * L * kk[n][i] : 0.0f;
-                    P[n][i] = j <= r ? L * qk[n][i] : 0.0f;
-                    top[i >> 1] = fmaxf(top[i >> 1], fabsf(P[n][i]));
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 16 * warp + (lane >> 2) + 8 * i;
+                    const float by = which ? p_up[i] : beta[i];
+                    float v0 = by * (L[i][0] * acc[n][2 * i]), v1 = by * (L[i][1] * acc[n][2 * i + 1]);
+                    if (n >= 2 * warp) {  // nothing from above the diagonal, also where a product is not a number
+                        if (j + !which > r) v0 = 0;
+                        if (j + 1 + !which > r) v1 = 0;
+                    }
+                    if (which)
+                        *reinterpret_cast<uint32_t*>(out + 2 * kSquare + piece_at<8>(r, n) + 4 * (lane & 3)) = pack(v0, v1);
+                    else
+                        *reinterpret_cast<float2*>(&m.A[b][r][j]) = make_float2(v0, v1);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
-                top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
-                const int r = 16 * warp + (lane >> 2) + 8 * i, e = field(top[i]);
-                const float scale = up(e);
-                if ((lane & 3) == 0) f.p[r] = down(e) * a.c.scale;
-#pragma unroll
-                for (int n = 0; n < 8; ++n)
-                    if (n <= 2 * warp + 1)
-                        *reinterpret_cast<uint32_t*>(out + 2 * kSquare + piece_at<8>(r, n) + 4 * (lane & 3)) =
-                            pack(P[n][2 * i] * scale, P[n][2 * i + 1] * scale);
-            }
         }
-        __syncthreads();
-        const int b = tid >> 6, col = tid & 63;
-        float t[kC];
-        if (b < count) {
+    }
+    __syncthreads();  // all are done with K and Q, where T goes
+    if (there) {
+        // the diagonal block
+        if (lane < 16) {
+            const float* A = &m.A[b][16 * warp][16 * warp];
+            float t[16];
 #pragma unroll
-            for (int i = 0; i < kC; ++i) {
-                float sum[4] = {i == col ? 1.0f : 0.0f, 0, 0, 0};
+            for (int i = 0; i < 16; ++i) {
+                float sum[2] = {i == lane ? 1.0f : 0.0f, 0};
 #pragma unroll
                 for (int j = 0; j < i; j += 4) {
-                    const float4 r = *reinterpret_cast<const float4*>(&m.A[b][i][j]);
+                    const float4 r = *reinterpret_cast<const float4*>(A + i * kPitch + j);
                     sum[0] = fmaf(-r.x, t[j], sum[0]);
                     if (j + 1 < i) sum[1] = fmaf(-r.y, t[j + 1], sum[1]);
-                    if (j + 2 < i) sum[2] = fmaf(-r.z, t[j + 2], sum[2]);
-                    if (j + 3 < i) sum[3] = fmaf(-r.w, t[j + 3], sum[3]);
+                    if (j + 2 < i) sum[0] = fmaf(-r.z, t[j + 2], sum[0]);
+                    if (j + 3 < i) sum[1] = fmaf(-r.w, t[j + 3], sum[1]);
                 }
-                t[i] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                t[i] = sum[0] + sum[1];
+                m.T[b][16 * warp + i][16 * warp + lane] = t[i];
             }
         }
-        __syncthreads();
-        if (b < count) {
-            const float beta = m.beta[b][col];
-#pragma unroll
-            for (int i = 0; i < kC; ++i) m.A[b][i][col] = t[i] * beta;
+        head_barrier(b);
+        auto A = [&](int i, int k) { return &m.A[b][16 * i][16 * k]; };
+        auto T = [&](int i, int k) { return &m.T[b][16 * i][16 * k]; };
+        if ((warp & 1) == 0) {  // T_10, T_32
+            const int i = warp + 1;
+            float acc[2][4] = {}, acc2[2][4] = {};
+            block_product(acc, A(i, warp), T(warp, warp), lane);
+            block_store(T(warp, i), acc, 1.0f, lane);  // above the diagonal, where nothing else stands
+            __syncwarp();
+            block_product(acc2, T(i, i), T(warp, i), lane);
+            block_store(T(i, warp), acc2, -1.0f, lane);
         }
-        __syncthreads();
-        // rows of T out: eight threads a row
-        for (int r = tid >> 3; r < count * kC; r += 16) {
-            const int which = r / kC, row = r % kC, p = tid & 7;
-            uint8_t* out = heads + (int64_t)(h0 + which) * kHeadBytes;
-            const float4 x = *reinterpret_cast<const float4*>(&m.A[which][row][8 * p]);
-            const float4 y = *reinterpret_cast<const float4*>(&m.A[which][row][8 * p + 4]);
-            const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            float top = 0;
+        head_barrier(b);
+        {  // W = A_21 T_11, to the upper right quarter: blocks (0, 2), (0, 3), (1, 2), (1, 3)
+            const int i = 2 + (warp >> 1), j = warp & 1;
+            float acc[2][4] = {};
+            block_product(acc, A(i, 1), T(1, j), lane);
+            if (j == 0) block_product(acc, A(i, 0), T(0, 0), lane);
+            block_store(T(j, i), acc, 1.0f, lane);
+        }
+        head_barrier(b);
+        {  // the lower left quarter: -T_22 W
+            const int i = 2 + (warp >> 1), j = warp & 1;
+            float acc[2][4] = {};
+            block_product(acc, T(i, i), T(j, i), lane);
+            if (i == 3) block_product(acc, T(3, 2), T(j, 2), lane);
+            block_store(T(i, j), acc, -1.0f, lane);
+        }
+        head_barrier(b);
+        {
+            // rows of T diag(beta) out: eight threads a row
+            const int p = tid & 7;
+            float beta[8], most = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+            for (int j = 0; j < 8; ++j) beta[j] = m.beta[b][8 * p + j];
+            for (int row = (tid & 127) >> 3; row < kC; row += 16) {
+                const float4 x = *reinterpret_cast<const float4*>(&m.T[b][row][8 * p]);
+                const float4 y = *reinterpret_cast<const float4*>(&m.T[b][row][8 * p + 4]);
+                float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}, top = 0, sum = 0;
 #pragma unroll
-            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-            const int e = field(top);
-            const float scale = up(e);
-            uint32_t high[4], rest[4];
+                for (int j = 0; j < 8; ++j) {
+                    v[j] = (p >> 1) <= (row >> 4) ? v[j] * beta[j] : 0.0f;  // above the diagonal blocks stand other things
+                    top = fmaxf(top, fabsf(v[j]));
+                    sum += fabsf(v[j]);
+                }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float u0 = v[2 * j] * scale, u1 = v[2 * j + 1] * scale;
-                high[j] = pack(u0, u1);
-                const float2 h = unpack(high[j]);
-                rest[j] = pack(u0 - h.x, u1 - h.y);
+                for (int d = 1; d < 8; d <<= 1) {
+                    top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+                    sum += __shfl_xor_sync(kAll, sum, d);
+                }
+                most = fmaxf(most, sum);
+                const int e = field(top);
+                const float scale = up(e);
+                uint32_t high[4], rest[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float u0 = v[2 * j] * scale, u1 = v[2 * j + 1] * scale;
+                    high[j] = pack(u0, u1);
+                    const float2 h = unpack(high[j]);
+                    rest[j] = pack(u0 - h.x, u1 - h.y);
+                }
+                *reinterpret_cast<uint4*>(out + piece_at<8>(row, p)) = make_uint4(high[0], high[1], high[2], high[3]);
+                *reinterpret_cast<uint4*>(out + kSquare + piece_at<8>(row, p)) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+                if (p == 0) f.t[row] = down(e);
             }
-            *reinterpret_cast<uint4*>(out + piece_at<8>(row, p)) = make_uint4(high[0], high[1], high[2], high[3]);
-            *reinterpret_cast<uint4*>(out + kSquare + piece_at<8>(row, p)) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-            if (p == 0) reinterpret_cast<Factors*>(out + 3 * kSquare)->t[row] = down(e);
+            if (p == 0) atomicMax(&m.most[b], __float_as_uint(most));
         }
-        __syncthreads();
+        head_barrier(b);
+        if ((tid & 127) == 0) f.most_t = __uint_as_float(m.most[b]);
     }
 }
 
@@ -476,23 +640,15 @@ __device__ __forceinline__ void split_high(uint32_t (&high)[2], const float (&c)
 #pragma unroll
     for (int i = 0; i < 2; ++i) high[i] = transposed(pack(c[2 * i] * f0, c[2 * i + 1] * f1));
 }
-// exponent fields of the two columns' largest magnitudes over N accumulator blocks
-template <int N>
-__device__ __forceinline__ void fields(int (&e)[2], const float (&c)[N][4]) {
-    float m0 = 0, m1 = 0;
+// Exponent fields of two columns' largest magnitudes, of which each lane has its rows' as the high halves of floats in one
+// word.  The same word for the 8 lanes of a column pair.
+__device__ __forceinline__ uint32_t columns_max(uint32_t w) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        m0 = fmaxf(m0, fmaxf(fabsf(c[n][0]), fabsf(c[n][2])));
-        m1 = fmaxf(m1, fmaxf(fabsf(c[n][1]), fabsf(c[n][3])));
-    }
-#pragma unroll
-    for (int d = 4; d < 32; d <<= 1) {
-        m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, d));
-        m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, d));
-    }
-    e[0] = field(m0);
-    e[1] = field(m1);
+    for (int d = 4; d < 32; d <<= 1) w = __vmaxu2(w, __shfl_xor_sync(kAll, w, d));
+    return w;
 }
+__device__ __forceinline__ float first_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float second_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 template <int KD, int NT, int NW>
 struct ChunkShape {
@@ -571,6 +727,9 @@ __global__ void __launch_bounds__(NW * 32, 1) chunks_kernel(const __grid_constan
                 S[n][m][i] = carry && d < dv && k < dk ? state[(int64_t)d * dk + k] : 0.0f;
             }
 
+    int unit[NT][2];  // S stands in units of down(unit), by column
+#pragma unroll
+    for (int n = 0; n < NT; ++n) unit[n][0] = unit[n][1] = kOne;
     for (int c = 0; c < chunks; ++c) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();  // chunk c is there for all, and all are done with chunk c - 1
@@ -582,57 +741,93 @@ __global__ void __launch_bounds__(NW * 32, 1) chunks_kernel(const __grid_constan
         const uint8_t* V = stage + pair_bytes(KD) + kHeadBytes;
         const int r0 = lane >> 2;
 
-        // K S^T and Q S^T
-        float x[NT][4][4], qs[NT][4][4];
-        int e_s[NT][2];
-        float s_up[NT][2], s_down[NT][2];
+        // Scales.  S's is from its largest value.  Those of V - e^G K S^T, U and what goes into S are from bounds that
+        // follow from it: fp16 has room for a bound that is 2^10 too large without loss, and reductions over the
+        // columns in mid-chunk would be on the path from one chunk to the next.
+        float s_up[NT][2], s_down[NT][2], x_up[NT][2], x_down[NT][2], u_up[NT][2], u_down[NT][2], l_up[NT][2], grow[NT][2];
+        uint32_t v[NT][4][2];
+        const float most_ks = f.most_ks, most_t = f.most_t, most_left = f.most_left, all = f.all;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            fields(e_s[n], S[n]);
+            float m0 = 0, m1 = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) s_up[n][i] = up(e_s[n][i]), s_down[n][i] = down(e_s[n][i]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[n][m][i] = qs[n][m][i] = 0;
-        }
-#pragma unroll
-        for (int t = 0; t < kM; ++t) {
-            Fragment b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = split(S[n][t], s_up[n][0], s_up[n][1]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                uint32_t w[4];
-                ldmatrix(w, left_at<kRow>(K16, 16 * m, 2 * t, lane));
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(x[n][m], w, b[n].high[0], b[n].high[1]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(x[n][m], w, b[n].rest[0], b[n].rest[1]);
-                ldmatrix(w, left_at<kRow>(Q16, 16 * m, 2 * t, lane));
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(qs[n][m], w, b[n].high[0], b[n].high[1]);
+            for (int m = 0; m < kM; ++m) {
+                m0 = fmaxf(m0, fmaxf(fabsf(S[n][m][0]), fabsf(S[n][m][2])));
+                m1 = fmaxf(m1, fmaxf(fabsf(S[n][m][1]), fabsf(S[n][m][3])));
             }
-        }
-        // X = V - e^G K S^T
-        float x_up[NT][2], x_down[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
+            const uint32_t ms = columns_max(__byte_perm(__float_as_uint(m0), __float_as_uint(m1), 0x7632));
+            uint32_t mv = 0;
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int r = 16 * m + r0 + 8 * i;
-                    const uint32_t v = *reinterpret_cast<const uint32_t*>(V + r * Shape::kVPitch + (d0 - first + 8 * n) * 2);
-                    const float ks = f.ks[r];
-                    x[n][m][2 * i] = fmaf(-ks * s_down[n][0], x[n][m][2 * i], __uint_as_float(v << 16));
-                    x[n][m][2 * i + 1] = fmaf(-ks * s_down[n][1], x[n][m][2 * i + 1], __uint_as_float(v & 0xffff0000u));
+                    v[n][m][i] = *reinterpret_cast<const uint32_t*>(V + (16 * m + r0 + 8 * i) * Shape::kVPitch + (d0 - first + 8 * n) * 2);
+                    mv = __vmaxu2(mv, v[n][m][i] & 0x7fff7fffu);
                 }
-            int e[2];
-            fields(e, x[n]);
+            mv = columns_max(mv);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) x_up[n][i] = up(e[i]), x_down[n][i] = down(e[i]);
+            for (int i = 0; i < 2; ++i) {
+                const float top = i ? second_of(ms) : first_of(ms);  // rounded down, but within its power of two
+                const int e = field(top);
+                s_up[n][i] = up(e);
+                s_down[n][i] = down(e) * down(unit[n][i]);
+                // a power of two above each bound; 2^14 stands for it
+                const float x = (i ? second_of(mv) : first_of(mv)) + most_ks * (2.0f * top * down(unit[n][i]));
+                const float u = x * most_t, l = u * most_left;
+                const int ex = field(2.0f * x), eu = field(2.0f * u);
+                x_up[n][i] = up(ex), x_down[n][i] = down(ex);
+                u_up[n][i] = up(eu), u_down[n][i] = down(eu);
+                // S has to stay finite in the new units, and its change of units a number of fp32; what updates lose by
+                // that is 2^-60 of S, or 2^-100 of what they were made for before
+                const int el = min(max(field(2.0f * l), max(e + unit[n][i] - kOne - 60, unit[n][i] - 120)), 254);
+                l_up[n][i] = up(el);
+                grow[n][i] = all * __uint_as_float((uint32_t)(127 + min(max(unit[n][i] - el, -126), 127)) << 23);
+                unit[n][i] = el;
+            }
         }
+
+        // K S^T and Q S^T
+        float x[NT][4][4], qs[NT][4][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[n][m][i] = qs[n][m][i] = 0;
+#pragma unroll
+        for (int t = 0; t < kM; ++t) {
+            Fragment b[NT];
+            uint32_t kw[4][4], qw[4][4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) ldmatrix(kw[m], left_at<kRow>(K16, 16 * m, 2 * t, lane));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[n] = split(S[n][t], s_up[n][0], s_up[n][1]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) ldmatrix(qw[m], left_at<kRow>(Q16, 16 * m, 2 * t, lane));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) mma_f16(x[n][m], kw[m], b[n].high[0], b[n].high[1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) mma_f16(qs[n][m], qw[m], b[n].high[0], b[n].high[1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) mma_f16(x[n][m], kw[m], b[n].rest[0], b[n].rest[1]);
+        }
+        // X = V - e^G K S^T
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float ks = f.ks[16 * m + r0 + 8 * i];
+                    x[n][m][2 * i] = fmaf(-ks * s_down[n][0], x[n][m][2 * i], first_of(v[n][m][i]));
+                    x[n][m][2 * i + 1] = fmaf(-ks * s_down[n][1], x[n][m][2 * i + 1], second_of(v[n][m][i]));
+                }
         // U = T X
         float u[NT][4][4];
 #pragma unroll
@@ -644,33 +839,66 @@ __global__ void __launch_bounds__(NW * 32, 1) chunks_kernel(const __grid_constan
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             Fragment b[NT];
+            uint32_t high[4][4], rest[4][4];
+#pragma unroll
+            for (int m = t; m < 4; ++m) {
+                ldmatrix(high[m], left_at<8>(T_high, 16 * m, 2 * t, lane));
+                ldmatrix(rest[m], left_at<8>(T_rest, 16 * m, 2 * t, lane));
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) b[n] = split(x[n][t], x_up[n][0], x_up[n][1]);
 #pragma unroll
-            for (int m = t; m < 4; ++m) {
-                uint32_t w[4];
-                ldmatrix(w, left_at<8>(T_high, 16 * m, 2 * t, lane));
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(u[n][m], w, b[n].high[0], b[n].high[1]);
+                for (int m = t; m < 4; ++m) mma_f16(u[n][m], high[m], b[n].high[0], b[n].high[1]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(u[n][m], w, b[n].rest[0], b[n].rest[1]);
-                ldmatrix(w, left_at<8>(T_rest, 16 * m, 2 * t, lane));
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(u[n][m], w, b[n].high[0], b[n].high[1]);
-            }
+                for (int m = t; m < 4; ++m) mma_f16(u[n][m], rest[m], b[n].high[0], b[n].high[1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = t; m < 4; ++m) mma_f16(u[n][m], high[m], b[n].rest[0], b[n].rest[1]);
         }
-        float u_up[NT][2], u_down[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) u[n][m][i] *= f.t[16 * m + r0 + 8 * (i >> 1)] * x_down[n][i & 1];
-            int e[2];
-            fields(e, u[n]);
+
+        // S <- e^G_63 S + U^T (e^(G_63 - G) K)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) u_up[n][i] = up(e[i]), u_down[n][i] = down(e[i]);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[n][m][i] *= grow[n][i & 1];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            Fragment b[NT];
+            const float l0 = f.left[16 * t + r0], l1 = f.left[16 * t + r0 + 8];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float left[4] = {u[n][t][0] * l0, u[n][t][1] * l0, u[n][t][2] * l1, u[n][t][3] * l1};
+                b[n] = split(left, l_up[n][0], l_up[n][1]);
+            }
+#pragma unroll
+            for (int half = 0; half < kM; half += 4) {
+                uint32_t w[4][4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) ldmatrix_trans(w[m], right_at<kRow>(K16, 16 * t, 2 * (half + m), lane));
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) mma_f16(S[n][half + m], w[m], b[n].high[0], b[n].high[1]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) mma_f16(S[n][half + m], w[m], b[n].rest[0], b[n].rest[1]);
+            }
         }
+
         // o
         float pu[NT][4][4];
 #pragma unroll
@@ -681,83 +909,40 @@ __global__ void __launch_bounds__(NW * 32, 1) chunks_kernel(const __grid_constan
                 for (int i = 0; i < 4; ++i) pu[n][m][i] = 0;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            uint32_t b[NT][2];
+            uint32_t b[NT][2], w[4][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n) split_high(b[n], u[n][t], u_up[n][0], u_up[n][1]);
 #pragma unroll
-            for (int m = t; m < 4; ++m) {
-                uint32_t w[4];
-                ldmatrix(w, left_at<8>(P16, 16 * m, 2 * t, lane));
+            for (int m = t; m < 4; ++m) ldmatrix(w[m], left_at<8>(P16, 16 * m, 2 * t, lane));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(pu[n][m], w, b[n][0], b[n][1]);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = t; m < 4; ++m) mma_f16(pu[n][m], w[m], b[n][0], b[n][1]);
         }
         const int64_t row0 = lo + (int64_t)c * kC;
+        const int rows = (int)(hi - row0 < kC ? hi - row0 : kC);
+        __nv_bfloat16* o = a.o + (row0 + r0) * a.o_ld + h * dv + d0;
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = 16 * m + r0 + 8 * i;
-                const float fq = f.qs[r], fp = f.p[r];
+                const int r = 16 * m + 8 * i;
+                const float fq = f.qs[r + r0], fp = f.p[r + r0];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const float y0 = fmaf(fq * s_down[n][0], qs[n][m][2 * i], fp * u_down[n][0] * pu[n][m][2 * i]);
                     const float y1 = fmaf(fq * s_down[n][1], qs[n][m][2 * i + 1], fp * u_down[n][1] * pu[n][m][2 * i + 1]);
-                    const int d = d0 + 8 * n;
-                    if (row0 + r < hi && d < dv) {
-                        __nv_bfloat16* o = a.o + (row0 + r) * a.o_ld + h * dv + d;
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(y0, y1);
+                    if (r + r0 < rows && d0 + 8 * n < dv) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(y0, y1);
                         if (a.o_pairs) {
-                            *reinterpret_cast<__nv_bfloat162*>(o) = v;
+                            *reinterpret_cast<__nv_bfloat162*>(o + r * a.o_ld + 8 * n) = y;
                         } else {
-                            o[0] = v.x;
-                            o[1] = v.y;
+                            o[r * a.o_ld + 8 * n] = y.x;
+                            o[r * a.o_ld + 8 * n + 1] = y.y;
                         }
                     }
                 }
             }
-        // S <- e^G_63 S + U^T (e^(G_63 - G) K), the sum in units of the updates' scale
-        const float all = f.all[0];
-        float l_up[NT][2], l_down[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[n][m][i] *= f.left[16 * m + r0 + 8 * (i >> 1)];
-            int e[2];
-            fields(e, u[n]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                e[i] = max(e[i], e_s[n][i] - 60);  // S stays finite in these units; updates 2^-60 of it do not count
-                l_up[n][i] = up(e[i]), l_down[n][i] = down(e[i]);
-            }
-#pragma unroll
-            for (int m = 0; m < kM; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[n][m][i] *= all * l_up[n][i & 1];
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            Fragment b[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) b[n] = split(u[n][t], l_up[n][0], l_up[n][1]);
-#pragma unroll
-            for (int m = 0; m < kM; ++m) {
-                uint32_t w[4];
-                ldmatrix_trans(w, right_at<kRow>(K16, 16 * t, 2 * m, lane));
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(S[n][m], w, b[n].high[0], b[n].high[1]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(S[n][m], w, b[n].rest[0], b[n].rest[1]);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < kM; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[n][m][i] *= l_down[n][i & 1];
     }
     if (state) {
 #pragma unroll
@@ -767,7 +952,7 @@ __global__ void __launch_bounds__(NW * 32, 1) chunks_kernel(const __grid_constan
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int d = d0 + 8 * n + (i & 1), k = 16 * m + (lane >> 2) + 8 * (i >> 1);
-                    if (d < dv && k < dk) state[(int64_t)d * dk + k] = S[n][m][i];
+                    if (d < dv && k < dk) state[(int64_t)d * dk + k] = S[n][m][i] * down(unit[n][i & 1]);
                 }
     }
 }
@@ -788,7 +973,8 @@ cudaError_t launch_chunked(const DeltaArgs& a, cudaStream_t st) {
     if (cudaError_t e = cudaFuncSetAttribute(prepare_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)sizeof(PrepareShared<KD>)))
         return e;
-    if (cudaError_t e = launch(prepare_kernel<KD>, dim3((unsigned)a.q_pieces, (unsigned)a.c.k_heads), 128,
+    if (cudaError_t e = launch(prepare_kernel<KD>, dim3((unsigned)a.q_pieces, (unsigned)(a.c.k_heads * ((a.c.v_heads / a.c.k_heads + 1) / 2))),
+                               kPrepare,
                                sizeof(PrepareShared<KD>), st, 1, a))
         return e;
     return launch_shape<KD, 1, 4>(a, st);

@@ -8,16 +8,15 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kTable = 4096;  // angles of a CTA at most
 
 struct NormArgs {
     moe_head_norm_config c;
     moe_heads a, b;
     const int32_t* pos;
     const float* inv_freq;
-    int64_t rows;   // T * heads
-    int heads;      // a's and b's
-    int per_block;  // rows of a CTA
+    int64_t T;
+    uint32_t inverse_a, inverse_b;  // 2^32 / heads, rounded up
+    unsigned first_blocks;          // the CTAs with heads of a
 };
 
 // sin and cos of pos * f: the product is reduced to a part of a turn in fp64
@@ -31,87 +30,135 @@ __device__ __forceinline__ float2 turn(int pos, float f) {
     return r;
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// E values of a head for each thread, P for each load: E = P * chunks, and the
-// chunk i of lane l begins at (l + LANES * i) * P.
+// P consecutive values as they are in memory
 template <typename T, int P>
-struct Piece;
-template <typename T>
-struct Piece<T, 8> {
-    static __device__ __forceinline__ void load(const T* p, float (&v)[8]) { load8(p, v); }
-    static __device__ __forceinline__ void store(T* p, const float (&v)[8]) { store8(p, v); }
+struct Raw {
+    uint32_t w[P * sizeof(T) / 4 ? P * sizeof(T) / 4 : 1];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (P == 1) {
+            if constexpr (sizeof(T) == 4)
+                w[0] = __float_as_uint(*reinterpret_cast<const float*>(p));
+            else
+                w[0] = (uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)(P * sizeof(T)) / 16; ++i)
+                reinterpret_cast<uint4*>(w)[i] = reinterpret_cast<const uint4*>(p)[i];
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[P]) const {
+        if constexpr (P == 1) {
+            v[0] = __uint_as_float(w[0]);
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
 };
-template <typename T>
-struct Piece<T, 1> {
-    static __device__ __forceinline__ void load(const T* p, float (&v)[1]) { v[0] = (float)*p; }
-    static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { *p = (T)v[0]; }
-};
+template <typename T, int P>
+__device__ __forceinline__ void store(T* p, const float (&v)[P]) {
+    if constexpr (P == 1) {
+        *p = (T)v[0];
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < P / 4; ++i)
+            reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+        uint32_t w[P / 2];
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+#pragma unroll
+        for (int i = 0; i < P / 8; ++i)
+            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+}
 
-// LANES threads take one head, in CH chunks of P values each: P = 8 where every
-// address allows wide loads, one value otherwise (then also rotations whose
-// halves are not a multiple of 8).  The partner of a rotated value is read
-// again (it is in the first-level cache) rather than passed between threads.
-// All reads of a head come before its first write, so y may be x.  sin and cos
-// are found once for each token of a CTA, for all its heads.  Bound by memory.
-template <typename T, int LANES, int CH, int P>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormArgs g) {
+// LANES threads take one head, in CH chunks of P values each (chunk i of lane l
+// begins at (l + LANES * i) * P): P = 8 where every address allows wide loads,
+// one value otherwise (then also rotations whose halves are not a multiple of
+// 8).  They take U heads at a time, all of whose loads are under way together.
+// A CTA has heads of one tensor only; its lanes keep their part of the weights.
+// The partner of a rotated value comes from its lane (CH = 1), else it is read
+// again.  All reads of a head come before its first write, so y may be x.  sin
+// and cos are found once for each token of a CTA, for all its heads, behind the
+// loads.  Bound by memory.
+template <typename T, int LANES, int CH, int P, int U, bool ROT, bool GATE>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 && !GATE ? 4 : 1) norm_kernel(const __grid_constant__ NormArgs g) {
     extern __shared__ float2 table[];  // [token of the CTA][pair]
     after_previous();
     let_next_start();
-    const int64_t row0 = (int64_t)blockIdx.x * g.per_block;
-    const int64_t end = row0 + g.per_block < g.rows ? row0 + g.per_block : g.rows;
-    const int64_t token0 = row0 / g.heads;
-    const int half = g.c.rot_dim / 2, D = g.c.dim;
-    if (half) {
-        const int tokens = (int)((end - 1) / g.heads - token0) + 1;
+    constexpr int kPass = kThreads / LANES;
+    const bool second = blockIdx.x >= g.first_blocks;
+    const moe_heads& t = second ? g.b : g.a;
+    const uint32_t inverse = second ? g.inverse_b : g.inverse_a;  // of the heads, 32 bits behind the point, rounded up
+    const int64_t row0 = (int64_t)(blockIdx.x - (second ? g.first_blocks : 0)) * (kPass * U), rows = g.T * t.heads;
+    const int here = (int)(rows - row0 < kPass * U ? rows - row0 : kPass * U);
+    const int64_t token0 = row0 / t.heads;
+    const int half = g.c.rot_dim / 2, D = g.c.dim, lane = threadIdx.x % LANES;
+    const int first = (int)(row0 - token0 * t.heads);
+
+    // token (of the CTA's) and head of a thread's u-th row; rows past the last redo the last one's sums: every thread of a
+    // warp takes part in the shuffles.  Found again where needed: it is two instructions, and registers are CTAs
+    auto place = [&](int u, int& token, int& h) {
+        const int r = threadIdx.x / LANES + u * kPass;
+        const uint32_t at = first + (r < here ? r : here - 1);  // below heads + 128, so the product is exact
+        token = t.heads == 1 ? at : __umulhi(at, inverse);
+        h = at - token * t.heads;
+    };
+    Raw<T, P> x[U][CH], gate[U][CH];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        int token, h;
+        place(u, token, h);
+        const T* from = static_cast<const T*>(t.x_dev) + (token0 + token) * t.x_ld + h * t.x_head;
+        const T* gfrom = static_cast<const T*>(t.gate_dev) + (token0 + token) * t.gate_ld + h * t.gate_head;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int e = (lane + LANES * i) * P;
+            memset(&x[u][i], 0, sizeof x[u][i]);
+            if (e < D) {
+                x[u][i].load(from + e);
+                if (GATE && t.gate_dev) gate[u][i].load(gfrom + e);
+            }
+        }
+    }
+    float w[CH][P];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int e = (lane + LANES * i) * P;
+#pragma unroll
+        for (int j = 0; j < P; ++j) w[i][j] = 1;
+        if (t.weight_dev && e < D) {
+            Raw<float, P> r;
+            r.load(t.weight_dev + e);
+            r.get(w[i]);
+#pragma unroll
+            for (int j = 0; j < P; ++j) w[i][j] += g.c.weight_offset;
+        }
+    }
+    if (ROT) {
+        const int tokens = (first + here - 1) / t.heads + 1;
         for (int i = threadIdx.x; i < tokens * half; i += kThreads)
             table[i] = turn(g.pos[token0 + i / half], g.inv_freq[i % half]);
         __syncthreads();
     }
-    const int lane = threadIdx.x % LANES;
-    const int first = (int)(row0 - token0 * g.heads);
-    for (int r = threadIdx.x / LANES; r < g.per_block; r += kThreads / LANES) {
-        const bool there = row0 + r < end;
-        // rows past the last redo the last one's sums: every thread of a warp takes part in the shuffles
-        const int at = first + (there ? r : (int)(end - 1 - row0));
-        const int token = at / g.heads;
-        int h = at - token * g.heads;
-        const moe_heads& t = h < g.a.heads ? g.a : g.b;
-        h -= h < g.a.heads ? 0 : g.a.heads;
-        const T* x = static_cast<const T*>(t.x_dev) + (token0 + token) * t.x_ld + h * t.x_head;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        int token, h;
+        place(u, token, h);
         float v[CH][P], sum = 0;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int e = (lane + LANES * i) * P;
-#pragma unroll
-            for (int j = 0; j < P; ++j) v[i][j] = 0;
-            if (e < D) Piece<T, P>::load(x + e, v[i]);
+            x[u][i].get(v[i]);
 #pragma unroll
             for (int j = 0; j < P; ++j) sum = fmaf(v[i][j], v[i][j], sum);
         }
@@ -119,95 +166,111 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
         if (g.c.norm != MOE_NORM_NONE) {
 #pragma unroll
             for (int d = LANES / 2; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-            factor = 1.0f / sqrtf((g.c.norm == MOE_NORM_RMS ? sum / (float)D : sum) + g.c.eps);
+            factor = rsqrtf((g.c.norm == MOE_NORM_RMS ? sum / (float)D : sum) + g.c.eps);
         }
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int e = (lane + LANES * i) * P;
-            if (e >= D) continue;
-            float w[P];
-            if (t.weight_dev) Piece<float, P>::load(t.weight_dev + e, w);
-            float o[P];
-            auto scaled = [&](float value, float weight) {
-                return value * factor * (t.weight_dev ? g.c.weight_offset + weight : 1.0f);
-            };
-            if (e < g.c.rot_dim && (P == 1 || g.c.pairs == MOE_ROT_HALVES)) {
-                // the other value of each pair
-                int f;
-                bool second;
-                if (g.c.pairs == MOE_ROT_HALVES) {
-                    second = e >= half;
-                    f = second ? e - half : e + half;
-                } else {
-                    second = e & 1;
-                    f = e ^ 1;
-                }
-                float u[P], wu[P];
-                Piece<T, P>::load(x + f, u);
-                if (t.weight_dev) Piece<float, P>::load(t.weight_dev + f, wu);
-                const int pair = g.c.pairs == MOE_ROT_HALVES ? (second ? f : e) : e / 2;
+        for (int i = 0; i < CH; ++i)
 #pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const float2 cs = table[token * half + pair + j];
-                    const float z = scaled(v[i][j], w[j]), other = scaled(u[j], wu[j]);
-                    o[j] = fmaf(z, cs.x, second ? other * cs.y : -(other * cs.y));
-                }
-            } else {
+            for (int j = 0; j < P; ++j) v[i][j] = v[i][j] * factor * w[i][j];
+        if constexpr (ROT) {
+            const float2* cs = table + token * half;
+            if (P > 1 && g.c.pairs == MOE_ROT_ADJACENT) {
 #pragma unroll
-                for (int j = 0; j < P; ++j) o[j] = scaled(v[i][j], w[j]);
-                if (P > 1 && e < g.c.rot_dim) {
+                for (int i = 0; i < CH; ++i) {
+                    const int e = (lane + LANES * i) * P;
 #pragma unroll
                     for (int j = 0; j + 1 < P; j += 2)
                         if (e + j < g.c.rot_dim) {
-                            const float2 cs = table[token * half + (e + j) / 2];
-                            const float z = o[j], y = o[j + 1];
-                            o[j] = fmaf(z, cs.x, -(y * cs.y));
-                            o[j + 1] = fmaf(y, cs.x, z * cs.y);
+                            const float2 r = cs[(e + j) / 2];
+                            const float p = v[i][j], q = v[i][j + 1];
+                            v[i][j] = fmaf(p, r.x, -(q * r.y));
+                            v[i][j + 1] = fmaf(q, r.x, p * r.y);
                         }
                 }
-            }
+            } else if constexpr (CH == 1 && P > 1) {
+                const int e = lane * P;
+                const bool upper = e >= half;
+                const int partner = (upper ? e - half : e + half) / P;
+                float q[P];
 #pragma unroll
-            for (int j = 0; j < P; ++j) v[i][j] = o[j];
+                for (int j = 0; j < P; ++j) q[j] = __shfl_sync(kAll, v[0][j], partner, LANES);
+                if (e < g.c.rot_dim) {
+                    const float4* r = reinterpret_cast<const float4*>(cs + (upper ? e - half : e));
+#pragma unroll
+                    for (int j = 0; j < P; j += 2) {
+                        const float4 f = r[j / 2];
+                        v[0][j] = fmaf(v[0][j], f.x, upper ? q[j] * f.y : -(q[j] * f.y));
+                        v[0][j + 1] = fmaf(v[0][j + 1], f.z, upper ? q[j + 1] * f.w : -(q[j + 1] * f.w));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int e = (lane + LANES * i) * P;
+                    if (e >= g.c.rot_dim) continue;
+                    const bool halves = g.c.pairs == MOE_ROT_HALVES, upper = halves ? e >= half : e & 1;
+                    const int f = halves ? (upper ? e - half : e + half) : e ^ 1;
+                    const int pair = halves ? (upper ? f : e) : e / 2;
+                    Raw<T, P> other;
+                    Raw<float, P> wr;
+                    float q[P], wq[P];
+                    other.load(static_cast<const T*>(t.x_dev) + (token0 + token) * t.x_ld + h * t.x_head + f);
+                    other.get(q);
+                    if (t.weight_dev) wr.load(t.weight_dev + f), wr.get(wq);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        const float2 r = cs[pair + j];
+                        q[j] *= factor * (t.weight_dev ? g.c.weight_offset + wq[j] : 1.0f);
+                        v[i][j] = fmaf(v[i][j], r.x, upper ? q[j] * r.y : -(q[j] * r.y));
+                    }
+                }
+                __syncwarp();  // every lane has read its partners
+            }
         }
-        if (t.gate_dev) {
-            const T* gate = static_cast<const T*>(t.gate_dev) + (token0 + token) * t.gate_ld + h * t.gate_head;
+        if (GATE && t.gate_dev) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const int e = (lane + LANES * i) * P;
-                if (e < D) {
-                    float u[P];
-                    Piece<T, P>::load(gate + e, u);
+                float z[P];
+                gate[u][i].get(z);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) v[i][j] *= silu(u[j]);
-                }
+                for (int j = 0; j < P; ++j) v[i][j] *= sizeof(T) == 2 ? silu_bf16(z[j]) : silu(z[j]);
             }
         }
-        __syncwarp();  // every lane has read its partners
-        if (there) {
+        if (threadIdx.x / LANES + u * kPass < here) {
             T* y = static_cast<T*>(t.y_dev) + (token0 + token) * t.y_ld + h * t.y_head;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int e = (lane + LANES * i) * P;
-                if (e < D) Piece<T, P>::store(y + e, v[i]);
+                if (e < D) store<T, P>(y + e, v[i]);
             }
         }
     }
 }
 
+template <typename T, int LANES, int CH, int P, int U, bool ROT, bool GATE>
+cudaError_t launch_heads(NormArgs& g, cudaStream_t st) {
+    constexpr int kRows = kThreads / LANES * U;  // heads of a CTA
+    auto tokens = [](int heads) { return heads == 0 ? 0 : kRows / heads + 2 < kRows ? kRows / heads + 2 : kRows; };
+    const int most = tokens(g.a.heads) > tokens(g.b.heads) ? tokens(g.a.heads) : tokens(g.b.heads);
+    const size_t table = ROT ? (size_t)most * (g.c.rot_dim / 2) * sizeof(float2) : 0;
+    g.first_blocks = (unsigned)((g.T * g.a.heads + kRows - 1) / kRows);
+    const unsigned grid = g.first_blocks + (unsigned)((g.T * g.b.heads + kRows - 1) / kRows);
+    return launch(norm_kernel<T, LANES, CH, P, U, ROT, GATE>, dim3(grid), kThreads, table, st, 1, g);
+}
+
+// Few heads: one at a time, so that more CTAs start at once.
 template <typename T, int LANES, int CH, int P>
 cudaError_t launch_rows(NormArgs& g, cudaStream_t st) {
-    constexpr int kPass = kThreads / LANES;  // rows a CTA has under way
-    const int half = g.c.rot_dim / 2;
-    // Few rows: one pass a CTA, so that more of them start at once.
-    int passes = g.rows >= (int64_t)kPass * 152 * 8 ? 4 : 1;
-    auto angles = [&](int p) {
-        const int rows = p * kPass, tokens = rows / g.heads + 2;
-        return (tokens < rows ? tokens : rows) * half;
-    };
-    while (passes > 1 && angles(passes) > kTable) passes >>= 1;
-    g.per_block = passes * kPass;
-    const unsigned grid = (unsigned)((g.rows + g.per_block - 1) / g.per_block);
-    return launch(norm_kernel<T, LANES, CH, P>, dim3(grid), kThreads, (size_t)angles(passes) * sizeof(float2), st, 1, g);
+    constexpr int kMany = CH == 1 && P > 1 ? 4 : 1;
+    const bool many = g.T * (g.a.heads + g.b.heads) >= (int64_t)(kThreads / LANES) * 152 * 8;
+    const bool gate = g.a.gate_dev || g.b.gate_dev;
+    if (g.c.rot_dim) {
+        if (gate) return launch_heads<T, LANES, CH, P, 1, true, true>(g, st);
+        return many ? launch_heads<T, LANES, CH, P, kMany, true, false>(g, st) : launch_heads<T, LANES, CH, P, 1, true, false>(g, st);
+    }
+    if (gate)
+        return many ? launch_heads<T, LANES, CH, P, kMany, false, true>(g, st) : launch_heads<T, LANES, CH, P, 1, false, true>(g, st);
+    return many ? launch_heads<T, LANES, CH, P, kMany, false, false>(g, st) : launch_heads<T, LANES, CH, P, 1, false, false>(g, st);
 }
 
 template <typename T>
@@ -236,8 +299,8 @@ cudaError_t launch_type(NormArgs& g, bool second, cudaStream_t st) {
 
 cudaError_t launch_head_norm(const moe_head_norm_config& c, const moe_heads& a, const moe_heads* b, const int32_t* pos,
                              const float* inv_freq, int64_t T, cudaStream_t st) {
-    NormArgs g{c, a, b ? *b : moe_heads{}, pos, inv_freq, T * (a.heads + (b ? b->heads : 0)),
-               a.heads + (b ? b->heads : 0), 0};
+    auto inverse = [](int heads) { return (uint32_t)((UINT64_C(1) << 32) / heads + 1); };
+    NormArgs g{c, a, b ? *b : moe_heads{}, pos, inv_freq, T, inverse(a.heads), b ? inverse(b->heads) : 0, 0};
     return a.type == MOE_BF16 ? launch_type<__nv_bfloat16>(g, b != nullptr, st) : launch_type<float>(g, b != nullptr, st);
 }
 

@@ -82,7 +82,7 @@ def test_head_norm_refuses_bad_arguments(lib):
     refused(call(freq=None), "rotation")
     refused(call(a=heads(kind=2)), "type")
     refused(call(a=heads(n=0)), "heads")
-    refused(call(a=heads(n=65536)), "heads")
+    refused(call(a=heads(n=32769)), "heads")
     refused(call(a=heads(x=None)), "required")
     refused(call(a=heads(y=None)), "required")
     refused(call(a=heads(y=2 * P, y_head=63)), "shorter")
@@ -92,7 +92,7 @@ def test_head_norm_refuses_bad_arguments(lib):
     refused(call(a=heads(y_ld=512)), "other strides")
     refused(call(b=heads(kind=1, y=2 * P, x=2 * P)), "differ in type")
     refused(call(b=heads()), "same y")
-    refused(call(a=heads(n=65535), T=(1 << 31) - 1), "2^33")
+    refused(call(a=heads(n=32768), T=(1 << 31) - 1), "2^33")
     assert call(a=heads(x=None, y=None), T=0, pos=None, freq=None) == moe.MOE_OK
 
 
