@@ -83,12 +83,16 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ 
     const T* x = static_cast<const T*>(a.x) + first * a.x_ld + c;
     if constexpr (kCopy) {
         const T* from = x;
+        uint32_t to = (uint32_t)__cvta_generic_to_shared(&ring[0][threadIdx.x]);
 #pragma unroll
-        for (int t = 0; t < kTile; ++t, from += a.x_ld) {
-            if (t < rows)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(&ring[t][threadIdx.x])),
-                             "l"(from) : "memory");
-            if (t % kAhead == kAhead - 1) asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int group = 0; group < kTile / kAhead; ++group) {
+            if (group * kAhead < rows) {
+#pragma unroll
+                for (int t = 0; t < kAhead; ++t, from += a.x_ld, to += sizeof(ring[0]))
+                    if (group * kAhead + t < rows)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         }
     }
     float w[W][V], bias[V], past[W - 1][V];
@@ -138,6 +142,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ 
 #pragma unroll
         for (int t = 0; t < kAhead; ++t, y += a.y_ld) {
             widen(in[t], win[W - 1 + t]);
+            if (t0 + t >= rows) continue;
             R out;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ 
                 for (int i = 0; i < W; ++i) sum = fmaf(w[i][j], win[t + i][j], sum);
                 out.v[j] = (T)activated<T, SILU>(sum);
             }
-            if (t0 + t < rows) *reinterpret_cast<R*>(y) = out;
+            *reinterpret_cast<R*>(y) = out;
         }
 #pragma unroll
         for (int t = 0; t < W - 1; ++t)

@@ -30,26 +30,30 @@ __device__ __forceinline__ float2 turn(int pos, float f) {
     return r;
 }
 
-// P consecutive values as they are in memory
+// P consecutive values as they are in memory: one, four or eight
 template <typename T, int P>
 struct Raw {
-    uint32_t w[P * sizeof(T) / 4 ? P * sizeof(T) / 4 : 1];
+    static constexpr int kWords = P == 1 ? 1 : P * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
     __device__ __forceinline__ void load(const T* p) {
         if constexpr (P == 1) {
             if constexpr (sizeof(T) == 4)
                 w[0] = __float_as_uint(*reinterpret_cast<const float*>(p));
             else
                 w[0] = (uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16;
+        } else if constexpr (kWords == 2) {
+            const uint2 q = *reinterpret_cast<const uint2*>(p);
+            w[0] = q.x, w[1] = q.y;
         } else {
 #pragma unroll
-            for (int i = 0; i < (int)(P * sizeof(T)) / 16; ++i)
-                reinterpret_cast<uint4*>(w)[i] = reinterpret_cast<const uint4*>(p)[i];
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 q = reinterpret_cast<const uint4*>(p)[i / 4];
+                w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
+            }
         }
     }
-    __device__ __forceinline__ void get(float (&v)[P]) const {
-        if constexpr (P == 1) {
-            v[0] = __uint_as_float(w[0]);
-        } else if constexpr (sizeof(T) == 4) {
+    __device__ __forceinline__ void get(float* v) const {
+        if constexpr (P == 1 || sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < P; ++i) v[i] = __uint_as_float(w[i]);
         } else {
@@ -62,13 +66,12 @@ struct Raw {
     }
 };
 template <typename T, int P>
-__device__ __forceinline__ void store(T* p, const float (&v)[P]) {
+__device__ __forceinline__ void store(T* p, const float* v) {
     if constexpr (P == 1) {
         *p = (T)v[0];
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < P / 4; ++i)
-            reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        for (int i = 0; i < P; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     } else {
         uint32_t w[P / 2];
 #pragma unroll
@@ -76,35 +79,40 @@ __device__ __forceinline__ void store(T* p, const float (&v)[P]) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
-#pragma unroll
-        for (int i = 0; i < P / 8; ++i)
-            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        if constexpr (P == 4)
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
-// LANES threads take one head, in CH chunks of P values each (chunk i of lane l
-// begins at (l + LANES * i) * P): P = 8 where every address allows wide loads,
-// one value otherwise (then also rotations whose halves are not a multiple of
-// 8).  They take U heads at a time, all of whose loads are under way together.
-// A CTA has heads of one tensor only; its lanes keep their part of the weights.
-// The partner of a rotated value comes from its lane (CH = 1), else it is read
-// again.  All reads of a head come before its first write, so y may be x.  sin
-// and cos are found once for each token of a CTA, for all its heads, behind the
-// loads.  Bound by memory.
+// LANES threads take one head, in CH chunks of P values each.  P = 8 where
+// every address allows wide loads: a chunk is eight values in a row, but in the
+// part that turns by halves two pieces of four, the same place of both halves,
+// so that pairs meet in a thread.  P = 1
+// otherwise (then also rotations whose halves are not a multiple of 4), and the
+// partner of a rotated value is read again.  The threads take U heads at a
+// time, all of whose loads are under way together.  A CTA has heads of one
+// tensor only; its lanes keep their part of the weights.  All reads of a head
+// come before its first write, so y may be x.  sin and cos are found once for
+// each token of a CTA, for all its heads, behind the loads.  Bound by memory.
 template <typename T, int LANES, int CH, int P, int U, bool ROT, bool GATE>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 && !GATE ? 4 : 1) norm_kernel(const __grid_constant__ NormArgs g) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 : 4) : 1)
+    norm_kernel(const __grid_constant__ NormArgs g) {
     extern __shared__ float2 table[];  // [token of the CTA][pair]
     after_previous();
     let_next_start();
-    constexpr int kPass = kThreads / LANES;
+    constexpr int kPass = kThreads / LANES, kPiece = P == 8 && ROT ? 4 : P, kPieces = P / kPiece;
     const bool second = blockIdx.x >= g.first_blocks;
     const moe_heads& t = second ? g.b : g.a;
     const uint32_t inverse = second ? g.inverse_b : g.inverse_a;  // of the heads, 32 bits behind the point, rounded up
     const int64_t row0 = (int64_t)(blockIdx.x - (second ? g.first_blocks : 0)) * (kPass * U), rows = g.T * t.heads;
     const int here = (int)(rows - row0 < kPass * U ? rows - row0 : kPass * U);
-    const int64_t token0 = row0 / t.heads;
+    // 64-bit division is a hundred instructions before the first load
+    const int64_t token0 = rows <= UINT32_MAX ? (uint32_t)row0 / (uint32_t)t.heads : row0 / t.heads;
     const int half = g.c.rot_dim / 2, D = g.c.dim, lane = threadIdx.x % LANES;
     const int first = (int)(row0 - token0 * t.heads);
+    const bool halves = ROT && g.c.pairs == MOE_ROT_HALVES;
 
     // token (of the CTA's) and head of a thread's u-th row; rows past the last redo the last one's sums: every thread of a
     // warp takes part in the shuffles.  Found again where needed: it is two instructions, and registers are CTAs
@@ -114,7 +122,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 && !GATE ? 4
         token = t.heads == 1 ? at : __umulhi(at, inverse);
         h = at - token * t.heads;
     };
-    Raw<T, P> x[U][CH], gate[U][CH];
+    // where piece p of chunk i begins
+    auto at = [&](int i, int p) {
+        const int c = lane + LANES * i;
+        if (P == 8 && halves && c < g.c.rot_dim / 8) return 4 * c + p * half;
+        return c * P + p * kPiece;
+    };
+    Raw<T, kPiece> x[U][CH][kPieces], gate[U][CH][kPieces];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         int token, h;
@@ -123,24 +137,28 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 && !GATE ? 4
         const T* gfrom = static_cast<const T*>(t.gate_dev) + (token0 + token) * t.gate_ld + h * t.gate_head;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int e = (lane + LANES * i) * P;
             memset(&x[u][i], 0, sizeof x[u][i]);
-            if (e < D) {
-                x[u][i].load(from + e);
-                if (GATE && t.gate_dev) gate[u][i].load(gfrom + e);
+            if ((lane + LANES * i) * P < D) {
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) {
+                    x[u][i][p].load(from + at(i, p));
+                    if (GATE && t.gate_dev) gate[u][i][p].load(gfrom + at(i, p));
+                }
             }
         }
     }
     float w[CH][P];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int e = (lane + LANES * i) * P;
 #pragma unroll
         for (int j = 0; j < P; ++j) w[i][j] = 1;
-        if (t.weight_dev && e < D) {
-            Raw<float, P> r;
-            r.load(t.weight_dev + e);
-            r.get(w[i]);
+        if (t.weight_dev && (lane + LANES * i) * P < D) {
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                Raw<float, kPiece> r;
+                r.load(t.weight_dev + at(i, p));
+                r.get(&w[i][p * kPiece]);
+            }
 #pragma unroll
             for (int j = 0; j < P; ++j) w[i][j] += g.c.weight_offset;
         }
@@ -158,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 && !GATE ? 4
         float v[CH][P], sum = 0;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            x[u][i].get(v[i]);
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) x[u][i][p].get(&v[i][p * kPiece]);
 #pragma unroll
             for (int j = 0; j < P; ++j) sum = fmaf(v[i][j], v[i][j], sum);
         }
@@ -172,66 +191,56 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 && !GATE ? 4
         for (int i = 0; i < CH; ++i)
 #pragma unroll
             for (int j = 0; j < P; ++j) v[i][j] = v[i][j] * factor * w[i][j];
-        if constexpr (ROT) {
-            const float2* cs = table + token * half;
-            if (P > 1 && g.c.pairs == MOE_ROT_ADJACENT) {
+        if constexpr (ROT && P == 8) {
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int e = (lane + LANES * i) * P;
+            for (int i = 0; i < CH; ++i) {
+                const int c = lane + LANES * i;
+                const float2* cs = table + token * half + 4 * c;  // of the chunk's four pairs, either way
+                if (halves) {
+                    if (c < g.c.rot_dim / 8) {
 #pragma unroll
-                    for (int j = 0; j + 1 < P; j += 2)
-                        if (e + j < g.c.rot_dim) {
-                            const float2 r = cs[(e + j) / 2];
-                            const float p = v[i][j], q = v[i][j + 1];
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 r = cs[j];
+                            const float p = v[i][j], q = v[i][4 + j];
                             v[i][j] = fmaf(p, r.x, -(q * r.y));
-                            v[i][j + 1] = fmaf(q, r.x, p * r.y);
+                            v[i][4 + j] = fmaf(q, r.x, p * r.y);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (8 * c + 2 * j < g.c.rot_dim) {
+                            const float2 r = cs[j];
+                            const float p = v[i][2 * j], q = v[i][2 * j + 1];
+                            v[i][2 * j] = fmaf(p, r.x, -(q * r.y));
+                            v[i][2 * j + 1] = fmaf(q, r.x, p * r.y);
                         }
                 }
-            } else if constexpr (CH == 1 && P > 1) {
-                const int e = lane * P;
-                const bool upper = e >= half;
-                const int partner = (upper ? e - half : e + half) / P;
-                float q[P];
-#pragma unroll
-                for (int j = 0; j < P; ++j) q[j] = __shfl_sync(kAll, v[0][j], partner, LANES);
-                if (e < g.c.rot_dim) {
-                    const float4* r = reinterpret_cast<const float4*>(cs + (upper ? e - half : e));
-#pragma unroll
-                    for (int j = 0; j < P; j += 2) {
-                        const float4 f = r[j / 2];
-                        v[0][j] = fmaf(v[0][j], f.x, upper ? q[j] * f.y : -(q[j] * f.y));
-                        v[0][j + 1] = fmaf(v[0][j + 1], f.z, upper ? q[j + 1] * f.w : -(q[j + 1] * f.w));
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int e = (lane + LANES * i) * P;
-                    if (e >= g.c.rot_dim) continue;
-                    const bool halves = g.c.pairs == MOE_ROT_HALVES, upper = halves ? e >= half : e & 1;
-                    const int f = halves ? (upper ? e - half : e + half) : e ^ 1;
-                    const int pair = halves ? (upper ? f : e) : e / 2;
-                    Raw<T, P> other;
-                    Raw<float, P> wr;
-                    float q[P], wq[P];
-                    other.load(static_cast<const T*>(t.x_dev) + (token0 + token) * t.x_ld + h * t.x_head + f);
-                    other.get(q);
-                    if (t.weight_dev) wr.load(t.weight_dev + f), wr.get(wq);
-#pragma unroll
-                    for (int j = 0; j < P; ++j) {
-                        const float2 r = cs[pair + j];
-                        q[j] *= factor * (t.weight_dev ? g.c.weight_offset + wq[j] : 1.0f);
-                        v[i][j] = fmaf(v[i][j], r.x, upper ? q[j] * r.y : -(q[j] * r.y));
-                    }
-                }
-                __syncwarp();  // every lane has read its partners
             }
+        } else if constexpr (ROT) {
+            const float2* cs = table + token * half;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int e = lane + LANES * i;
+                if (e >= g.c.rot_dim) continue;
+                const bool upper = halves ? e >= half : e & 1;
+                const int f = halves ? (upper ? e - half : e + half) : e ^ 1;
+                Raw<T, 1> other;
+                float q;
+                other.load(static_cast<const T*>(t.x_dev) + (token0 + token) * t.x_ld + h * t.x_head + f);
+                other.get(&q);
+                q *= factor * (t.weight_dev ? g.c.weight_offset + t.weight_dev[f] : 1.0f);
+                const float2 r = cs[halves ? (upper ? f : e) : e / 2];
+                v[i][0] = fmaf(v[i][0], r.x, upper ? q * r.y : -(q * r.y));
+            }
+            __syncwarp();  // every lane has read its partners
         }
         if (GATE && t.gate_dev) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 float z[P];
-                gate[u][i].get(z);
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) gate[u][i][p].get(&z[p * kPiece]);
 #pragma unroll
                 for (int j = 0; j < P; ++j) v[i][j] *= sizeof(T) == 2 ? silu_bf16(z[j]) : silu(z[j]);
             }
@@ -239,10 +248,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 && !GATE ? 4
         if (threadIdx.x / LANES + u * kPass < here) {
             T* y = static_cast<T*>(t.y_dev) + (token0 + token) * t.y_ld + h * t.y_head;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int e = (lane + LANES * i) * P;
-                if (e < D) store<T, P>(y + e, v[i]);
-            }
+            for (int i = 0; i < CH; ++i)
+                if ((lane + LANES * i) * P < D) {
+#pragma unroll
+                    for (int p = 0; p < kPieces; ++p) store<T, kPiece>(y + at(i, p), &v[i][p * kPiece]);
+                }
         }
     }
 }
@@ -258,19 +268,22 @@ cudaError_t launch_heads(NormArgs& g, cudaStream_t st) {
     return launch(norm_kernel<T, LANES, CH, P, U, ROT, GATE>, dim3(grid), kThreads, table, st, 1, g);
 }
 
-// Few heads: one at a time, so that more CTAs start at once.
-template <typename T, int LANES, int CH, int P>
+template <typename T, int LANES, int CH, int P, int U>
 cudaError_t launch_rows(NormArgs& g, cudaStream_t st) {
-    constexpr int kMany = CH == 1 && P > 1 ? 4 : 1;
-    const bool many = g.T * (g.a.heads + g.b.heads) >= (int64_t)(kThreads / LANES) * 152 * 8;
     const bool gate = g.a.gate_dev || g.b.gate_dev;
-    if (g.c.rot_dim) {
-        if (gate) return launch_heads<T, LANES, CH, P, 1, true, true>(g, st);
-        return many ? launch_heads<T, LANES, CH, P, kMany, true, false>(g, st) : launch_heads<T, LANES, CH, P, 1, true, false>(g, st);
-    }
-    if (gate)
-        return many ? launch_heads<T, LANES, CH, P, kMany, false, true>(g, st) : launch_heads<T, LANES, CH, P, 1, false, true>(g, st);
-    return many ? launch_heads<T, LANES, CH, P, kMany, false, false>(g, st) : launch_heads<T, LANES, CH, P, 1, false, false>(g, st);
+    if (g.c.rot_dim)
+        return gate ? launch_heads<T, LANES, CH, P, U, true, true>(g, st) : launch_heads<T, LANES, CH, P, U, true, false>(g, st);
+    return gate ? launch_heads<T, LANES, CH, P, U, false, true>(g, st) : launch_heads<T, LANES, CH, P, U, false, false>(g, st);
+}
+
+// Heads of up to 16 LANES values.  Sixteen values a thread and two heads at a time: what a head costs beside its values
+// (its place, its sum's exchange) is then small, and loads of 64 bytes a thread are under way.  Few heads: eight values
+// and one head, so that more threads start at once.
+template <typename T, int LANES>
+cudaError_t launch_wide(NormArgs& g, cudaStream_t st) {
+    if (LANES < 32 && g.T * (g.a.heads + g.b.heads) < (int64_t)(kThreads / LANES) * 152 * 4)
+        return launch_rows<T, LANES < 32 ? 2 * LANES : 32, LANES < 32 ? 1 : 2, 8, 1>(g, st);
+    return launch_rows<T, LANES, 2, 8, LANES < 32 ? 2 : 1>(g, st);
 }
 
 template <typename T>
@@ -284,15 +297,15 @@ bool wide(const moe_heads& t, int D) {
 template <typename T>
 cudaError_t launch_type(NormArgs& g, bool second, cudaStream_t st) {
     const int D = g.c.dim;
-    const bool halves = g.c.pairs == MOE_ROT_ADJACENT || g.c.rot_dim % 16 == 0;
+    const bool halves = g.c.pairs == MOE_ROT_ADJACENT || g.c.rot_dim % 8 == 0;
     if (halves && wide<T>(g.a, D) && (!second || wide<T>(g.b, D))) {
-        if (D <= 64) return launch_rows<T, 8, 1, 8>(g, st);
-        if (D <= 128) return launch_rows<T, 16, 1, 8>(g, st);
-        if (D <= 256) return launch_rows<T, 32, 1, 8>(g, st);
-        return launch_rows<T, 32, 2, 8>(g, st);
+        if (D <= 64) return launch_wide<T, 4>(g, st);
+        if (D <= 128) return launch_wide<T, 8>(g, st);
+        if (D <= 256) return launch_wide<T, 16>(g, st);
+        return launch_wide<T, 32>(g, st);
     }
-    if (D <= 128) return launch_rows<T, 32, 4, 1>(g, st);
-    return launch_rows<T, 32, 16, 1>(g, st);
+    if (D <= 128) return launch_rows<T, 32, 4, 1, 1>(g, st);
+    return launch_rows<T, 32, 16, 1, 1>(g, st);
 }
 
 }  // namespace
