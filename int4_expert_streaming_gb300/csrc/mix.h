@@ -81,7 +81,7 @@ cudaError_t launch_conv(const Seqs& q, const void* x, int type, int64_t x_ld, in
 // mix_norm.cu
 cudaError_t launch_head_norm(const moe_head_norm_config& c, const moe_heads& a, const moe_heads* b, const int32_t* pos,
                              const float* inv_freq, int64_t T, cudaStream_t st);
-// mix_delta.cu
+// mix_delta.cu, mix_chunks.cu
 struct DeltaArgs {
     moe_delta_config c;
     Seqs q;
@@ -94,7 +94,7 @@ struct DeltaArgs {
     int longer_than;  // the chunked kernels leave out sequences of so many rows or fewer, the stepping one those of more
     int64_t q_pieces;  // of kDeltaChunk rows
     bool wide;         // q, k and v rows are aligned for 16-byte loads
-    bool o_pairs;      // o rows for stores of two values
+    bool o_pairs;      // o's for stores of two values
 };
 size_t delta_workspace(const moe_delta_config& c, int64_t T, int n);
 cudaError_t launch_delta_steps(const DeltaArgs& a, cudaStream_t st);
