@@ -395,6 +395,7 @@ def _binding():
 
         mod = importlib.import_module("._call", __name__)  # built beside libmoe.so
         mod.dtypes(torch.float32, torch.bfloat16, torch.int32, torch.uint8)
+        mod.on_failure(_check)
         _ops = mod
     return _ops
 
@@ -513,40 +514,22 @@ def make_seqs(n: int, offsets=None, slot=None, carry=None, max_len: int = 0) -> 
     return q
 
 
-def moe_conv(x, w, y, bias=None, act: int = MOE_ACT_SILU, seqs: moe_seqs | None = None, state=None, stream=None) -> None:
-    """Causal convolution of each column of x [T, channels] by w [channels, width], into y; state [slots, width - 1,
-    channels], of x's type, is read and replaced."""
-    rc = (_ops or _binding()).conv(x, w, y, bias, act, seqs, state, stream)
-    if rc:
-        _check(rc)
-
-
 def make_head_norm_config(norm: int = MOE_NORM_RMS, eps: float = 1e-6, weight_offset: float = 0.0, rot_dim: int = 0,
                           pairs: int = MOE_ROT_HALVES) -> moe_head_norm_config:
     """Without the heads' dimension, which a call takes from its tensors."""
     return moe_head_norm_config(0, norm, rot_dim, pairs, eps, weight_offset)
 
 
-def moe_head_norm(cfg: moe_head_norm_config, x, y, weight=None, gate=None, x2=None, y2=None, weight2=None, pos=None,
-                  inv_freq=None, stream=None) -> None:
-    """Norm of each head of x [T, heads, dim], then the rotation or the gate, into y (which may be x); x2, y2: a second
-    tensor in the same pass.  pos [T] int32, inv_freq [rot_dim / 2] fp32."""
-    rc = (_ops or _binding()).head_norm(cfg, x, y, weight, gate, x2, y2, weight2, pos, inv_freq, stream)
-    if rc:
-        _check(rc)
-
-
 def moe_delta_workspace(T: int, n: int, k_heads: int, v_heads: int, k_dim: int, v_dim: int, max_len: int = 0) -> int:
     return int(load_library().moe_delta_workspace(moe_delta_config(k_heads, v_heads, k_dim, v_dim, 1.0), T, n, max_len))
 
 
-def moe_delta(q, k, v, g, beta, state, o, scale: float = 1.0, seqs: moe_seqs | None = None, workspace=None,
-              stream=None) -> None:
-    """The gated delta rule: q, k [T, k_heads, k_dim], v, o [T, v_heads, v_dim] bf16, g, beta [T, v_heads] fp32, state
-    [slots, v_heads, v_dim, k_dim] fp32 (read and replaced) or None; workspace: uint8, moe_delta_workspace() bytes."""
-    rc = (_ops or _binding()).delta(q, k, v, g, beta, state, o, scale, seqs, workspace, stream)
-    if rc:
-        _check(rc)
+def __getattr__(name):
+    """moe_conv, moe_head_norm and moe_delta are _call's own functions, found when first asked for."""
+    if name in ("moe_conv", "moe_head_norm", "moe_delta"):
+        globals()[name] = f = getattr(_binding(), name)
+        return f
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 # --------------------------------------------------------------------------

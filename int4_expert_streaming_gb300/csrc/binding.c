@@ -6,8 +6,10 @@
  * launch, here well under one.
  *
  * Tensors are read through their Python attributes only, so this depends on
- * neither PyTorch's headers nor its version.  Every function returns the C
- * call's status; a tensor that does not fit raises ValueError.
+ * neither PyTorch's headers nor its version.  A function returns the C call's
+ * status; those with names raise what it stands for, and are the package's
+ * functions themselves (a Python function around them would cost a tenth of a
+ * small call).  A tensor that does not fit raises ValueError.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -210,6 +212,52 @@ static int descriptor(PyObject* o, moe_mx* out, const char* what, int* dev) {
     return d < 0 ? 0 : same_device(d, what, dev);
 }
 
+/*
+ * Arguments by place and by name into v[0..n-1], in the order of the names; the first `required` have to be given, the
+ * others stay None.  The names are interned, as the ones in a caller's code are.
+ */
+static int arguments(PyObject* const* given, Py_ssize_t n_given, PyObject* kwnames, PyObject* const* names, int n,
+                     int required, const char* what, PyObject** v) {
+    if (n_given > n) {
+        PyErr_Format(PyExc_TypeError, "%s: at most %d arguments, got %zd", what, n, n_given);
+        return -1;
+    }
+    for (int i = 0; i < n; ++i) v[i] = i < n_given ? given[i] : NULL;
+    const Py_ssize_t kw = kwnames ? PyTuple_GET_SIZE(kwnames) : 0;
+    for (Py_ssize_t k = 0; k < kw; ++k) {
+        PyObject* name = PyTuple_GET_ITEM(kwnames, k);
+        int i = 0;
+        while (i < n && names[i] != name) ++i;
+        if (i == n)
+            for (i = 0; i < n && PyUnicode_Compare(names[i], name) != 0; ++i)
+                if (PyErr_Occurred()) return -1;
+        if (i == n || v[i]) {
+            PyErr_Format(PyExc_TypeError, i == n ? "%s: no argument %R" : "%s: %R is given twice", what, name);
+            return -1;
+        }
+        v[i] = given[n_given + k];
+    }
+    for (int i = 0; i < n; ++i) {
+        if (!v[i] && i < required) {
+            PyErr_Format(PyExc_TypeError, "%s: %S is required", what, names[i]);
+            return -1;
+        }
+        if (!v[i]) v[i] = Py_None;
+    }
+    return 0;
+}
+#define KWARGS PyObject *self, PyObject *const *given, Py_ssize_t n_given, PyObject *kwnames
+static PyObject* failed; /* the package's function that raises what a status stands for */
+#define NONE_OR_RAISE(call)                                     \
+    do {                                                        \
+        int rc_;                                                \
+        Py_BEGIN_ALLOW_THREADS                                  \
+        rc_ = (call);                                           \
+        Py_END_ALLOW_THREADS                                    \
+        if (rc_ >= 0) Py_RETURN_NONE;                           \
+        return PyObject_CallFunction(failed, "i", rc_);         \
+    } while (0)
+
 static int count(Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return 0;
     PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
@@ -368,8 +416,13 @@ static long long first_extent(PyObject* t, const char* what) {
     return n;
 }
 
-/* x, w, y, bias, act, seqs, state, stream */
-static PyObject* conv(ARGS) {
+static PyObject* conv_names[8];
+static const char conv_doc[] =
+    "moe_conv(x, w, y, bias=None, act=MOE_ACT_SILU, seqs=None, state=None, stream=None)\n--\n\n"
+    "Causal convolution of each column of x [T, channels] by w [channels, width], into y; state [slots, width - 1,\n"
+    "channels], of x's type, is read and replaced.";
+static PyObject* conv(KWARGS) {
+    PyObject* v[8];
     matrix_t x, w, y;
     moe_seqs q;
     const moe_seqs* qp;
@@ -377,9 +430,10 @@ static PyObject* conv(ARGS) {
     long long slots = 0;
     int dev = moe_binding_device();
     (void)self;
-    if (count(n, 8) || matrix(v[0], "x", &dev, &x) || matrix(v[1], "w", &dev, &w) || matrix(v[2], "y", &dev, &y))
+    if (arguments(given, n_given, kwnames, conv_names, 8, 3, "moe_conv", v) || matrix(v[0], "x", &dev, &x) ||
+        matrix(v[1], "w", &dev, &w) || matrix(v[2], "y", &dev, &y))
         return NULL;
-    const long act = PyLong_AsLong(v[4]);
+    const long act = v[4] == Py_None ? MOE_ACT_SILU : PyLong_AsLong(v[4]);
     if (act == -1 && PyErr_Occurred()) return NULL;
     CHECK(x.cols <= INT32_MAX && w.rows == x.cols && w.cols <= INT32_MAX && w.ld == w.cols,
           "w is %lld x %lld, expected contiguous rows of each of %lld channels", (long long)w.rows, (long long)w.cols,
@@ -395,19 +449,26 @@ static PyObject* conv(ARGS) {
         /* a state of no slots still is one: every sequence is left out */
         if (!slots) Py_RETURN_NONE;
     }
-    STATUS(moe_conv(qp, x.p, x.type, x.ld, x.rows, (int32_t)x.cols, w.p, w.type, (int32_t)w.cols, bias, (int32_t)act,
-                    state, slots, y.p, y.ld, st));
+    NONE_OR_RAISE(moe_conv(qp, x.p, x.type, x.ld, x.rows, (int32_t)x.cols, w.p, w.type, (int32_t)w.cols, bias, (int32_t)act,
+                           state, slots, y.p, y.ld, st));
 }
 
-/* cfg, x, y, weight, gate, x2, y2, weight2, pos, inv_freq, stream; cfg.dim is x's */
-static PyObject* head_norm(ARGS) {
+static PyObject* head_norm_names[11];
+static const char head_norm_doc[] =
+    "moe_head_norm(cfg, x, y, weight=None, gate=None, x2=None, y2=None, weight2=None, pos=None, inv_freq=None, "
+    "stream=None)\n--\n\n"
+    "Norm of each head of x [T, heads, dim], then the rotation or the gate, into y (which may be x); x2, y2: a second\n"
+    "tensor in the same pass.  pos [T] int32, inv_freq [rot_dim / 2] fp32.";
+static PyObject* head_norm(KWARGS) {
+    PyObject* v[11];
     moe_head_norm_config c;
     moe_heads t[2];
     heads_t x, y, gate;
     void *pos, *freq, *weight, *st;
     int dev = moe_binding_device();
     (void)self;
-    if (count(n, 11) || structure(v[0], &c, sizeof c, "cfg")) return NULL;
+    if (arguments(given, n_given, kwnames, head_norm_names, 11, 3, "moe_head_norm", v) || structure(v[0], &c, sizeof c, "cfg"))
+        return NULL;
     const int second = v[5] != Py_None;
     CHECK(second || v[6] == Py_None, "y2 goes with x2");
     memset(t, 0, sizeof t);
@@ -442,23 +503,29 @@ static PyObject* head_norm(ARGS) {
     if (flat_i32(v[8], tokens, "pos", &dev, &pos) || flat_f32(v[9], c.rot_dim / 2, "inv_freq", &dev, &freq) ||
         stream_of(v[10], &st))
         return NULL;
-    STATUS(moe_head_norm(&c, &t[0], second ? &t[1] : NULL, pos, freq, tokens, st));
+    NONE_OR_RAISE(moe_head_norm(&c, &t[0], second ? &t[1] : NULL, pos, freq, tokens, st));
 }
 
-/* q, k, v, g, beta, state, o, scale, seqs, workspace, stream */
-static PyObject* delta(ARGS) {
+static PyObject* delta_names[11];
+static const char delta_doc[] =
+    "moe_delta(q, k, v, g, beta, state, o, scale=1.0, seqs=None, workspace=None, stream=None)\n--\n\n"
+    "The gated delta rule: q, k [T, k_heads, k_dim], v, o [T, v_heads, v_dim] bf16, g, beta [T, v_heads] fp32, state\n"
+    "[slots, v_heads, v_dim, k_dim] fp32 (read and replaced) or None; workspace: uint8, moe_delta_workspace() bytes,\n"
+    "not looked at where that is 0.";
+static PyObject* delta(KWARGS) {
+    PyObject* v[11];
     moe_delta_config c;
     heads_t q, k, val, o;
     moe_seqs b;
     const moe_seqs* bp;
-    void *g, *beta, *state = NULL, *ws, *st;
+    void *g, *beta, *state = NULL, *ws = NULL, *st;
     long long slots = 0, bytes = 0;
     int dev = moe_binding_device();
     (void)self;
-    if (count(n, 11) || heads_of(v[0], "q", &dev, &q) || heads_of(v[1], "k", &dev, &k) ||
+    if (arguments(given, n_given, kwnames, delta_names, 11, 7, "moe_delta", v) || heads_of(v[0], "q", &dev, &q) || heads_of(v[1], "k", &dev, &k) ||
         heads_of(v[2], "v", &dev, &val) || heads_of(v[6], "o", &dev, &o))
         return NULL;
-    const double scale = PyFloat_AsDouble(v[7]);
+    const double scale = v[7] == Py_None ? 1.0 : PyFloat_AsDouble(v[7]);
     if (scale == -1.0 && PyErr_Occurred()) return NULL;
     CHECK(q.type == MOE_BF16 && k.type == MOE_BF16 && val.type == MOE_BF16 && o.type == MOE_BF16,
           "q, k, v and o: expected bfloat16");
@@ -474,11 +541,13 @@ static PyObject* delta(ARGS) {
     c.scale = (float)scale;
     const long long rows = val.n * val.heads;
     if (flat_f32(v[3], rows, "g", &dev, &g) || flat_f32(v[4], rows, "beta", &dev, &beta) ||
-        batch(v[8], &b, &bp, &dev) || flat(v[9], t_u8, 0, "workspace", "a contiguous uint8 CUDA tensor", &dev, &ws) ||
-        stream_of(v[10], &st))
+        batch(v[8], &b, &bp, &dev) || stream_of(v[10], &st))
         return NULL;
     CHECK(g && beta, "g and beta are required");
-    if (v[9] != Py_None && (bytes = number(v[9], s_numel)) < 0) return NULL;
+    if (v[9] != Py_None && moe_delta_workspace(&c, val.n, bp ? bp->n : 1, bp ? bp->offsets_dev ? bp->max_len : 1 : 0)) {
+        if (flat(v[9], t_u8, 0, "workspace", "a contiguous uint8 CUDA tensor", &dev, &ws) || (bytes = number(v[9], s_numel)) < 0)
+            return NULL;
+    }
     if (v[5] != Py_None) {
         if ((slots = first_extent(v[5], "state")) < 0) return NULL;
         if (flat(v[5], t_f32, slots * val.heads * val.dim * q.dim, "state",
@@ -486,8 +555,17 @@ static PyObject* delta(ARGS) {
             return NULL;
         if (!slots) Py_RETURN_NONE;
     }
-    STATUS(moe_delta(&c, bp, q.p, q.ld, k.p, k.ld, val.p, val.ld, g, beta, state, slots, o.p, o.ld, val.n, ws,
-                     (size_t)bytes, st));
+    NONE_OR_RAISE(moe_delta(&c, bp, q.p, q.ld, k.p, k.ld, val.p, val.ld, g, beta, state, slots, o.p, o.ld, val.n, ws,
+                            (size_t)bytes, st));
+}
+
+/* the package's function for a failed call's status */
+static PyObject* on_failure(ARGS) {
+    (void)self;
+    if (count(n, 1)) return NULL;
+    Py_INCREF(v[0]);
+    Py_XSETREF(failed, v[0]);
+    Py_RETURN_NONE;
 }
 
 /* the torch dtypes float32, bfloat16, int32, uint8 */
@@ -503,9 +581,10 @@ static PyObject* dtypes(ARGS) {
 }
 
 #define FN(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
+#define KWFN(name) {"moe_" #name, (PyCFunction)(void (*)(void))name, METH_FASTCALL | METH_KEYWORDS, name##_doc}
 static PyMethodDef methods[] = {FN(route),   FN(dispatch), FN(quantise), FN(dequantise),
-                                FN(product), FN(combine),  FN(conv),     FN(head_norm),
-                                FN(delta),   FN(dtypes),   {NULL, NULL, 0, NULL}};
+                                FN(product), FN(combine),  FN(dtypes),   FN(on_failure),
+                                KWFN(conv),  KWFN(head_norm), KWFN(delta), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__call(void) {
@@ -517,5 +596,14 @@ PyMODINIT_FUNC PyInit__call(void) {
                  {&s_shape, "shape"}, {&s_stride, "stride"}, {&s_cuda_stream, "cuda_stream"}};
     for (size_t i = 0; i < sizeof names / sizeof names[0]; ++i)
         if (!(*names[i].at = PyUnicode_InternFromString(names[i].name))) return NULL;
+    static const char* const conv_args[] = {"x", "w", "y", "bias", "act", "seqs", "state", "stream"};
+    static const char* const head_norm_args[] = {"cfg", "x", "y", "weight", "gate", "x2", "y2", "weight2", "pos", "inv_freq", "stream"};
+    static const char* const delta_args[] = {"q", "k", "v", "g", "beta", "state", "o", "scale", "seqs", "workspace", "stream"};
+    for (int i = 0; i < 8; ++i)
+        if (!(conv_names[i] = PyUnicode_InternFromString(conv_args[i]))) return NULL;
+    for (int i = 0; i < 11; ++i)
+        if (!(head_norm_names[i] = PyUnicode_InternFromString(head_norm_args[i])) ||
+            !(delta_names[i] = PyUnicode_InternFromString(delta_args[i])))
+            return NULL;
     return PyModule_Create(&module);
 }

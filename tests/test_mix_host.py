@@ -211,10 +211,16 @@ def test_python_module_refuses_tensors_that_do_not_fit(lib):
     no(delta(beta=None), "required")
     no(delta(state=Tensor(F, 2, 4, 16, 7)), "state")
     no(delta(state=Tensor(F, 2, 4, 16, 8, device=1)), "GPU 1")
-    no(delta(workspace=Tensor(F, 100)), "workspace")
+    q, v, g = Tensor(B, 50, 2, 8), Tensor(B, 50, 4, 16), Tensor(F, 50, 4)  # long enough for a workspace
+    no(delta(q=q, k=q, v=v, g=g, beta=g, o=v, workspace=Tensor(F, 100)), "workspace")
     with pytest.raises(moe.MoeError, match="workspace"):  # the library's own refusal comes through
-        moe.moe_delta(Tensor(B, 50, 2, 8), Tensor(B, 50, 2, 8), Tensor(B, 50, 4, 16), Tensor(F, 50, 4), Tensor(F, 50, 4), None,
-                      Tensor(B, 50, 4, 16))
+        moe.moe_delta(q, q, v, g, g, None, v)
+    for call in (lambda: moe.moe_delta(q, q, v), lambda: moe.moe_delta(q, q, v, g, g, None, v, q=q),
+                 lambda: moe.moe_delta(q, q, v, g, g, None, v, other=1), lambda: moe.moe_conv(*[x] * 9)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(AttributeError):
+        moe.moe_nothing
     with pytest.raises(ValueError):
         moe.make_seqs(3, offsets=torch.zeros(4, dtype=torch.int32))
 
