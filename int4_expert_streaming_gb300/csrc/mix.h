@@ -75,6 +75,31 @@ __device__ __forceinline__ float silu_bf16(float v) {
     return v * r;
 }
 
+// Two fp32 numbers in a 64-bit register: one instruction multiplies and adds both.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 both(float x, float y) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 apart(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// two bf16 as they are in memory
+__device__ __forceinline__ f32x2 both_of(uint32_t w) { return both(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+
 // mix_conv.cu
 cudaError_t launch_conv(const Seqs& q, const void* x, int type, int64_t x_ld, int channels, const void* w, int w_type,
                         int width, const float* bias, int act, void* state, void* y, int64_t y_ld, cudaStream_t st);

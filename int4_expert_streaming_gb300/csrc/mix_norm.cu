@@ -17,16 +17,28 @@ struct NormArgs {
     int64_t T;
     uint32_t inverse_a, inverse_b;  // 2^32 / heads, rounded up
     unsigned first_blocks;          // the CTAs with heads of a
+    float part;                     // of the sum of squares in the norm: 1 / dim, or 1
 };
 
-// sin and cos of pos * f: the product is reduced to a part of a turn in fp64
-// (a few operations an angle; relative to 2^31 turns that leaves 2^-21), the
-// rest is fp32.
+// sin and cos of pos * f.  The angle in turns is reduced to a part of one
+// before it is rounded: pos f / 2 pi as a sum of two fp32, exact to 2^-26 of a
+// turn up to the 16 millionth position and f of 1; beyond, in fp64, whose few
+// operations cost as much as the rest of the kernel where every angle takes them.
 __device__ __forceinline__ float2 turn(int pos, float f) {
-    double t = (double)pos * ((double)f * 0.15915494309189535);
-    t -= rint(t);
+    constexpr double kTurns = 0.15915494309189535;  // 1 / 2 pi
+    constexpr float kHigh = (float)kTurns, kRest = (float)(kTurns - (double)kHigh);
+    float t;
+    if (abs(pos) <= 1 << 24 && fabsf(f) <= 1.0f) {
+        const float p = (float)pos, high = f * kHigh, rest = fmaf(f, kHigh, -high) + f * kRest;
+        const float whole = p * high;
+        t = (whole - rintf(whole)) + fmaf(p, rest, fmaf(p, high, -whole));
+        t -= rintf(t);
+    } else {
+        double d = (double)pos * ((double)f * kTurns);
+        t = (float)(d - rint(d));
+    }
     float2 r;
-    sincospif(2.0f * (float)t, &r.y, &r.x);
+    sincospif(2.0f * t, &r.y, &r.x);
     return r;
 }
 
@@ -50,6 +62,18 @@ struct Raw {
                 const uint4 q = reinterpret_cast<const uint4*>(p)[i / 4];
                 w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
             }
+        }
+    }
+    // as pairs; one value with a zero
+    __device__ __forceinline__ void get2(f32x2* v) const {
+        if constexpr (P == 1) {
+            v[0] = both(__uint_as_float(w[0]), 0.0f);
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) v[i] = both(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) v[i] = both_of(w[i]);
         }
     }
     __device__ __forceinline__ void get(float* v) const {
@@ -147,21 +171,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 
             }
         }
     }
-    float w[CH][P];
+    // the lane's part of the weights, two values a register pair
+    constexpr int kTwos = P == 1 ? 1 : P / 2;
+    f32x2 w[CH][kTwos];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
+        float f[P];
 #pragma unroll
-        for (int j = 0; j < P; ++j) w[i][j] = 1;
+        for (int j = 0; j < P; ++j) f[j] = 1;
         if (t.weight_dev && (lane + LANES * i) * P < D) {
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
                 Raw<float, kPiece> r;
                 r.load(t.weight_dev + at(i, p));
-                r.get(&w[i][p * kPiece]);
+                r.get(&f[p * kPiece]);
             }
 #pragma unroll
-            for (int j = 0; j < P; ++j) w[i][j] += g.c.weight_offset;
+            for (int j = 0; j < P; ++j) f[j] += g.c.weight_offset;
         }
+#pragma unroll
+        for (int j = 0; j < kTwos; ++j) w[i][j] = both(f[P == 1 ? 0 : 2 * j], P == 1 ? 0.0f : f[2 * j + 1]);
     }
     if (ROT) {
         const int tokens = (first + here - 1) / t.heads + 1;
@@ -173,24 +202,29 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 
     for (int u = 0; u < U; ++u) {
         int token, h;
         place(u, token, h);
-        float v[CH][P], sum = 0;
+        f32x2 v2[CH][kTwos], sum2 = 0;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
 #pragma unroll
-            for (int p = 0; p < kPieces; ++p) x[u][i][p].get(&v[i][p * kPiece]);
+            for (int p = 0; p < kPieces; ++p) x[u][i][p].get2(&v2[i][p * kPiece / 2]);
 #pragma unroll
-            for (int j = 0; j < P; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+            for (int j = 0; j < kTwos; ++j) sum2 = fma2(v2[i][j], v2[i][j], sum2);
         }
-        float factor = 1;
+        float sum = apart(sum2).x + apart(sum2).y, factor = 1;
         if (g.c.norm != MOE_NORM_NONE) {
 #pragma unroll
             for (int d = LANES / 2; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-            factor = rsqrtf((g.c.norm == MOE_NORM_RMS ? sum / (float)D : sum) + g.c.eps);
+            factor = rsqrtf(fmaf(sum, g.part, g.c.eps));
         }
+        float v[CH][P];
 #pragma unroll
         for (int i = 0; i < CH; ++i)
 #pragma unroll
-            for (int j = 0; j < P; ++j) v[i][j] = v[i][j] * factor * w[i][j];
+            for (int j = 0; j < kTwos; ++j) {
+                const float2 f = apart(mul2(mul2(v2[i][j], both(factor, factor)), w[i][j]));
+                v[i][P == 1 ? 0 : 2 * j] = f.x;
+                if (P > 1) v[i][2 * j + 1] = f.y;
+            }
         if constexpr (ROT && P == 8) {
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -313,7 +347,8 @@ cudaError_t launch_type(NormArgs& g, bool second, cudaStream_t st) {
 cudaError_t launch_head_norm(const moe_head_norm_config& c, const moe_heads& a, const moe_heads* b, const int32_t* pos,
                              const float* inv_freq, int64_t T, cudaStream_t st) {
     auto inverse = [](int heads) { return (uint32_t)((UINT64_C(1) << 32) / heads + 1); };
-    NormArgs g{c, a, b ? *b : moe_heads{}, pos, inv_freq, T, inverse(a.heads), b ? inverse(b->heads) : 0, 0};
+    NormArgs g{c, a, b ? *b : moe_heads{}, pos, inv_freq, T, inverse(a.heads), b ? inverse(b->heads) : 0, 0,
+               c.norm == MOE_NORM_RMS ? 1.0f / (float)c.dim : 1.0f};
     return a.type == MOE_BF16 ? launch_type<__nv_bfloat16>(g, b != nullptr, st) : launch_type<float>(g, b != nullptr, st);
 }
 
