@@ -130,6 +130,8 @@ extern "C" int moe_delta(const moe_delta_config* c, const moe_seqs* seqs, const 
         if (T == 0 || a.q.n == 0) return MOE_OK;
         if (!q || !k || !v || !g || !beta || !o)
             return fail_global(MOE_EINVAL, "moe_delta: q, k, v, g, beta and o are required");
+        if ((int64_t)a.q.n * c->v_heads * ((c->v_dim + 31) / 32) > INT32_MAX)
+            return fail_global(MOE_EINVAL, "moe_delta: n=%d sequences are too many for %d heads", a.q.n, c->v_heads);
         const int32_t max_len = !seqs ? 0 : seqs->offsets_dev ? seqs->max_len : 1;
         const bool chunks = !all_short(T, max_len);
         const size_t need = chunks ? delta_workspace(*c, T, a.q.n) : 0;

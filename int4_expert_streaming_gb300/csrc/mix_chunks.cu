@@ -31,7 +31,8 @@ constexpr int kC = kDeltaChunk;
 
 // Workspace, per chunk and k head: K16 and Q16, panels of 64 columns of 128 rows
 // (K's, then Q's).  Per chunk and v head: T high over P T [128 x 64], T rest
-// [64 x 64], and the factors.  Rows are of 128 bytes with their 16-byte pieces
+// [64 x 64], and the factors.  At the end the sequences, longest first (up to
+// kSorted of them).  Rows are of 128 bytes with their 16-byte pieces
 // exchanged (piece p of row r at p ^ (r & 7)): read from shared memory without
 // conflicts.
 struct Factors {
@@ -48,6 +49,8 @@ constexpr int kSquare = kC * 128;
 constexpr int kPanel = 2 * kSquare;
 constexpr int kHeadTiles = 3 * kSquare;
 constexpr int kHeadBytes = (kHeadTiles + (int)sizeof(Factors) + 127) / 128 * 128;
+
+constexpr int kSorted = 1024;
 
 __host__ __device__ constexpr int padded_dim(int k_dim) { return k_dim <= 64 ? 64 : 128; }
 __host__ __device__ constexpr int pair_bytes(int KD) { return KD / 64 * kPanel; }
@@ -186,6 +189,25 @@ __device__ __forceinline__ void head_barrier(int b) {
         asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
+__host__ __device__ __forceinline__ int32_t* sorted_of(const DeltaArgs& a, int pair, int head) {
+    return reinterpret_cast<int32_t*>(a.ws + a.q_pieces * ((int64_t)a.c.k_heads * pair + (int64_t)a.c.v_heads * head));
+}
+// The sequences, longest first: the long ones' CTAs then start first, and the
+// last to start are short (9001 rows in seven runs, 24 heads: 131 us, in their own
+// order 143).  Above kSorted sequences no one of them is long beside the whole.
+__device__ __forceinline__ void sort_sequences(const DeltaArgs& a, int* lens) {
+    const int n = a.q.n;
+    if (n == 1 || n > kSorted) return;
+    for (int i = threadIdx.x; i < n; i += kPrepare) lens[i] = (int)(a.q.start(i + 1) - a.q.start(i));
+    __syncthreads();
+    int32_t* sorted = sorted_of(a, pair_bytes(padded_dim(a.c.k_dim)), kHeadBytes);
+    for (int i = threadIdx.x; i < n; i += kPrepare) {
+        int before = 0;
+        for (int j = 0; j < n; ++j) before += lens[j] > lens[i] || (lens[j] == lens[i] && j < i);
+        sorted[before] = i;
+    }
+}
+
 // One chunk and two v heads of a k head: K16 and Q16, the factors, T and P T.
 // (1 + A)^-1 by blocks of 16: the four on the diagonal by substitution in fp32,
 // a lane a column; then T_10 and T_32, and of those the lower left quarter, by
@@ -197,6 +219,10 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
     PrepareShared<KD>& m = *reinterpret_cast<PrepareShared<KD>*>(raw);
     after_previous();
     let_next_start();
+    if (blockIdx.x == a.q_pieces) {
+        if (blockIdx.y == 0) sort_sequences(a, reinterpret_cast<int*>(raw));
+        return;
+    }
     int c;
     const int s = a.q.find<kC>(blockIdx.x, c);
     const int64_t lo = a.q.start(s), hi = a.q.start(s + 1);
@@ -623,8 +649,10 @@ __global__ void __launch_bounds__(2 * kHalf, 1) chunks_kernel(const __grid_const
     let_next_start();
     constexpr int kT = Shape::kTiles, kN = 2 * kT;
     const int dk = a.c.k_dim, dv = a.c.v_dim, Hk = a.c.k_heads, Hv = a.c.v_heads;
-    const int blocks = (dv + kCols - 1) / kCols;
-    const int s = blockIdx.x / blocks, h = blockIdx.y, kh = h / (Hv / Hk);
+    // blocks of columns, heads, and slowest the sequences, longest first
+    const int blocks = (dv + kCols - 1) / kCols, place = blockIdx.x / (blocks * Hv);
+    const int s = a.q.n > 1 && a.q.n <= kSorted ? sorted_of(a, pair_bytes(KD), kHeadBytes)[place] : place;
+    const int h = blockIdx.x / blocks % Hv, kh = h / (Hv / Hk);
     const int64_t lo = a.q.start(s), hi = a.q.start(s + 1), len = hi - lo;
     const int slot = a.q.slot(s);
     if (len <= 0 || len <= a.longer_than || slot < 0) return;
@@ -976,17 +1004,18 @@ cudaError_t launch_chunked(const DeltaArgs& a, cudaStream_t st) {
     constexpr int kShared = (int)sizeof(PrepareShared<KD>);
     if (cudaError_t e = cudaFuncSetAttribute(prepare_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared)) return e;
     if (cudaError_t e = cudaFuncSetAttribute(chunks_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes)) return e;
-    if (cudaError_t e = launch(prepare_kernel<KD>, dim3((unsigned)a.q_pieces, (unsigned)(a.c.k_heads * twos)), kPrepare, kShared,
+    if (cudaError_t e = launch(prepare_kernel<KD>, dim3((unsigned)a.q_pieces + 1, (unsigned)(a.c.k_heads * twos)), kPrepare, kShared,
                                st, 1, a))
         return e;
-    return launch(chunks_kernel<KD>, dim3((unsigned)(a.q.n * blocks), (unsigned)a.c.v_heads), 2 * kHalf, Shape::kBytes, st, 1, a);
+    return launch(chunks_kernel<KD>, dim3((unsigned)((int64_t)a.q.n * a.c.v_heads * blocks)), 2 * kHalf, Shape::kBytes, st, 1, a);
 }
 
 }  // namespace
 
 size_t delta_workspace(const moe_delta_config& c, int64_t T, int n) {
     return (size_t)(T / kC + n) *
-           ((size_t)c.k_heads * pair_bytes(padded_dim(c.k_dim)) + (size_t)c.v_heads * kHeadBytes);
+               ((size_t)c.k_heads * pair_bytes(padded_dim(c.k_dim)) + (size_t)c.v_heads * kHeadBytes) +
+           kSorted * sizeof(int32_t);
 }
 
 cudaError_t launch_delta_chunks(const DeltaArgs& a, cudaStream_t st) {
