@@ -193,8 +193,8 @@ __host__ __device__ __forceinline__ int32_t* sorted_of(const DeltaArgs& a, int p
     return reinterpret_cast<int32_t*>(a.ws + a.q_pieces * ((int64_t)a.c.k_heads * pair + (int64_t)a.c.v_heads * head));
 }
 // The sequences, longest first: the long ones' CTAs then start first, and the
-// last to start are short (9001 rows in seven runs, 24 heads: 131 us, in their own
-// order 143).  Above kSorted sequences no one of them is long beside the whole.
+// last to start are short (9001 rows in 24 sequences: 131 us, in their own order
+// 143).  Above kSorted sequences no one of them is long beside the whole.
 __device__ __forceinline__ void sort_sequences(const DeltaArgs& a, int* lens) {
     const int n = a.q.n;
     if (n == 1 || n > kSorted) return;

@@ -4,7 +4,7 @@
          -> moe_mx_quantise (SwiGLU) -> moe_mx_product (down) -> moe_combine
 
 ``python -m int4_expert_streaming_gb300.mx_layer`` runs one layer of the 512-expert shapes on random weights and prints
-its time; ``MxLayer`` is the same as a class, and an example of how the calls go together: what is laid out once, what
+its time, and then that of a decoder layer: the delta rule's mixer (delta_layer.py) and these experts; ``MxLayer`` is the same as a class, and an example of how the calls go together: what is laid out once, what
 is sized by the largest batch, and what each call is given.
 
 An e4m3 scale has a narrow range, 2^-9 to 448, so every e4m3 matrix takes a tensor scale beside it: without one, blocks
@@ -135,7 +135,44 @@ class MxLayer:
         return b
 
 
+def time_of(call, iters: int = 50) -> float:
+    """us of one call, in a CUDA graph."""
+    for _ in range(3):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    graph.replay()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    for _ in range(iters):
+        graph.replay()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b) * 1000 / iters
+
+
+class DecoderLayer:
+    """x + mixer(rms norm of x), and on that the same with the experts, whose logits are the normed rows times router
+    [E, hidden] bf16."""
+
+    def __init__(self, mixer, experts: MxLayer, router):
+        self.mixer, self.experts, self.router = mixer, experts, router
+        self.mixed = torch.zeros((mixer.max_tokens, mixer.hidden), dtype=torch.bfloat16, device="cuda")
+        self.expert_out = torch.zeros_like(self.mixed)
+
+    def forward(self, x, seqs: moe.moe_seqs):
+        """x [T, hidden] bf16 -> a new tensor like it, on the current stream."""
+        T, width = x.shape
+        x = x + self.mixer.forward(torch.rms_norm(x, (width,), eps=1e-6), seqs, self.mixed[:T])
+        normed = torch.rms_norm(x, (width,), eps=1e-6)
+        return x + self.experts.forward(normed, normed @ self.router.T, self.expert_out[:T])
+
+
 def main() -> None:
+    from .delta_layer import DeltaMixer
+
     E, k, hidden, inter = 512, 10, 2048, 512
     g = torch.Generator(device="cuda").manual_seed(0)
 
@@ -147,21 +184,23 @@ def main() -> None:
         layer = MxLayer(gate_up, down, moe.make_route_config(E, k), max_tokens=T, **scales)
         x, logits = normal(T, hidden), normal(T, E).float()
         y = torch.empty((T, hidden), device="cuda")
-        for _ in range(3):
-            layer.forward(x, logits, y)
-        torch.cuda.synchronize()
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
-            layer.forward(x, logits, y)
-        graph.replay()
-        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        a.record()
-        for _ in range(50):
-            graph.replay()
-        b.record()
-        torch.cuda.synchronize()
+        us = time_of(lambda: layer.forward(x, logits, y))
         how = "given" if scales else "measured from the batch"
-        print(f"{T} tokens, activation scales {how}: {a.elapsed_time(b) * 20:.1f} us a layer")
+        print(f"{T} tokens, activation scales {how}: {us:.1f} us a layer")
+
+    Hk, Hv, d = 16, 32, 128
+    C, inner = (2 * Hk + Hv) * d, Hv * d
+    weights = (normal(C + inner, hidden, sigma=0.02), normal(2 * Hv, hidden, sigma=0.02), normal(C, 4, sigma=0.5),
+               torch.zeros(Hv, device="cuda"), torch.zeros(Hv, device="cuda"), torch.ones(d, device="cuda"),
+               normal(hidden, inner, sigma=0.02))
+    router = normal(E, hidden, sigma=0.02)
+    for T, n in ((1, 1), (8, 8), (64, 64), (4096, 1)):
+        mixer = DeltaMixer(*weights, (Hk, Hv, d, d), n, T, n)
+        layer = DecoderLayer(mixer, MxLayer(gate_up, down, moe.make_route_config(E, k), max_tokens=T, **given), router)
+        offsets = None if n == T else torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        x, y, seqs = normal(T, hidden), torch.empty((T, hidden), dtype=torch.bfloat16, device="cuda"), moe.make_seqs(n, offsets)
+        print(f"{T} tokens of {n} sequences: mixer {time_of(lambda: mixer.forward(x, seqs, y)):.1f} us, decoder layer "
+              f"{time_of(lambda: layer.forward(x, seqs)):.1f} us")
 
 
 if __name__ == "__main__":
