@@ -514,7 +514,7 @@ int moe_combine_rows(const void* rows_dev, int64_t n_rows, int32_t rows_type, in
  *                may not share a slot: what they read and leave there is then not defined
  *   carry_dev    int32 [n]: 0 = the sequence starts now, from a state of zeros, and what its slot holds is not read;
  *                NULL: all go on from their slots
- *   max_len      no sequence has more rows (0: not known); from 1 to 16 moe_delta needs neither its workspace nor its
+ *   max_len      no sequence has more rows (0: not known); from 1 to 24 moe_delta needs neither its workspace nor its
  *                kernels for long runs.  Calls stay right, if slow, where it is too small
  * A sequence without rows leaves its slot as it is.  seqs = NULL: all T rows are one sequence, with slot 0.
  */
@@ -576,8 +576,8 @@ typedef struct {
  *   (z_i, z_j) = (z_i cos - z_j sin, z_j cos + z_i sin)  for each pair, angle = pos[t] * inv_freq[pair]
  *   y = z * silu(gate)
  * a head of zeros with eps 0 gives NaN, as the formula does.
- *   pos_dev int32 [T], inv_freq_dev fp32 [rot_dim / 2]: with rot_dim > 0 only.  The angle is reduced in fp64, so
- *   positions far from 0 lose nothing.
+ *   pos_dev int32 [T], inv_freq_dev fp32 [rot_dim / 2]: with rot_dim > 0 only.  The angle loses nothing for
+ *   positions far from 0: it is reduced to turns in two fp32 numbers, or in fp64 where those would not do.
  */
 int moe_head_norm(const moe_head_norm_config* cfg, const moe_heads* a, const moe_heads* b, const int32_t* pos_dev,
                   const float* inv_freq_dev, int64_t T, void* stream);
@@ -602,12 +602,12 @@ typedef struct {
  *                 cleared), and above 0 the result is defined only as far as fp32 holds exp of its sums
  *   state_dev     fp32 [slots x v_heads x v_dim x k_dim], contiguous, 16-byte aligned; NULL: every sequence starts from
  *                 zeros and leaves nothing behind
- * Sequences of up to 16 rows run token by token, with the state in registers
+ * Sequences of up to 24 rows run token by token, with the state in registers
  * and fp32 throughout.  Longer ones run in chunks of 64 tokens on the tensor
  * cores: within a chunk the updates come from one triangular system; the
  * state, the chunk's inverse and the updates enter the products as pairs of
- * fp16 numbers (each row or column scaled by a power of two; about 2^-22) and
- * are summed in fp32.  Which of the two a sequence takes depends on its own
+ * fp16 numbers in units of powers of two (together about 2^-22 of the largest)
+ * and are summed in fp32; what goes only into o enters as one fp16 number.  Which of the two a sequence takes depends on its own
  * length alone (max_len being right), so its results do not depend on its batch.
  * workspace_dev: moe_delta_workspace() bytes (0: may be NULL), 128-byte aligned, contents irrelevant; two calls that may
  * run at the same time (or two graphs) need one each.

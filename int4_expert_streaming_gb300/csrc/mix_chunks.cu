@@ -603,24 +603,28 @@ __device__ __forceinline__ void get4(float (&w)[4], uint32_t at) {
     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]) : "r"(at) : "memory");
 }
 
-constexpr int kPairs = 2;                // of warps with S
-constexpr int kCols = 16 * kPairs;       // columns of V of a CTA
-constexpr int kVPitch = kCols * 2 + 16;  // bytes of a row; the 16 keep 8 rows on different banks
-constexpr int kHalf = kPairs * 2 * 32;   // threads with S, and as many for o
-constexpr int kStages = 3;
-constexpr int kVector = 32 * 16;         // bytes: 16 of each thread of a warp
+constexpr int kVector = 32 * 16;  // bytes: 16 of each thread of a warp
 
-template <int KD>
+template <int KD, int PAIRS>  // pairs of warps with S
 struct ChunkShape {
-    static constexpr int kTiles = KD / 32;                // 16 x 16 blocks of a warp's half of S^T
-    static constexpr int kV = pair_bytes(KD) + kHeadBytes;  // of a stage
+    static constexpr int kCols = 16 * PAIRS;       // columns of V of a CTA
+    static constexpr int kVPitch = kCols * 2 + 16;  // bytes of a row; the 16 keep 8 rows on different banks
+    static constexpr int kHalf = PAIRS * 2 * 32;   // threads with S, and as many for o
+    static constexpr int kTiles = KD / 32;         // 16 x 16 blocks of a warp's half of S^T
+    // a stage: K and Q, T high, P T and T rest, V; two of them, and of the factors three
+    static constexpr int kV = pair_bytes(KD) + kHeadTiles;
     static constexpr int kStage = kV + kC * kVPitch;
+    static constexpr int kFactors = kHeadBytes - kHeadTiles;
     // handed to the warps for o, by each warp with S, twice: the high numbers of its half of S and of its tokens' X
     static constexpr int kHand = (kTiles + 2) * kVector;
     // exchanged in a pair, by each warp: sums for the other's tokens, then what goes into S (high, rest); rests of X
     static constexpr int kSwap = 4 * kVector, kRests = 2 * kVector;
-    static constexpr int kOffSwap = kStages * kStage + 2 * 2 * kPairs * kHand, kOffRests = kOffSwap + 2 * kPairs * kSwap;
-    static constexpr int kBytes = kOffRests + 2 * kPairs * kRests;
+    static constexpr int kOffFactors = 2 * kStage, kOffHands = kOffFactors + 3 * kFactors;
+    static constexpr int kOffSwap = kOffHands + 2 * 2 * PAIRS * kHand, kOffRests = kOffSwap + 2 * PAIRS * kSwap;
+    static constexpr int kBytes = kOffRests + 2 * PAIRS * kRests;
+    // registers of a thread with S and of one for o, where the same number for both would be too few for S
+    static constexpr int kMost = 168, kLeast = 88;
+    static_assert(PAIRS == 2 || 2 * kHalf * 128 == kHalf * (kMost + kLeast), "registers of the launch");
 };
 
 // The 16 tokens numbered g = 0, 1 of a warp's half q of a pair: 0..15 and 48..63, or 16..31 and 32..47; T is triangular,
@@ -639,9 +643,10 @@ __device__ __forceinline__ int group_of(int q, int g) { return q ? 1 + g : 3 * g
 //
 // The way from chunk to chunk bounds this where there are few sequences and
 // heads: 4096 tokens with 32 heads are 64 chunks one after another on 128 CTAs.
-template <int KD>
-__global__ void __launch_bounds__(2 * kHalf, 1) chunks_kernel(const __grid_constant__ DeltaArgs a) {
-    using Shape = ChunkShape<KD>;
+template <int KD, int PAIRS>
+__global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_kernel(const __grid_constant__ DeltaArgs a) {
+    using Shape = ChunkShape<KD, PAIRS>;
+    constexpr int kPairs = PAIRS, kCols = Shape::kCols, kHalf = Shape::kHalf, kVPitch = Shape::kVPitch;
     extern __shared__ __align__(128) uint8_t raw[];
     __shared__ float2 units[2][2 * kPairs];                  // of S and of X
     __shared__ float2 found[2 * kPairs];                     // by a warp for the other of its pair: largest of S and of V
@@ -662,23 +667,32 @@ __global__ void __launch_bounds__(2 * kHalf, 1) chunks_kernel(const __grid_const
     const int64_t piece = a.q.piece_of<kC>(s);
     const uint32_t base = smem_at(raw);
     constexpr int kHands = 2 * kPairs * Shape::kHand;  // from one time's to the next
-    const uint32_t hands = base + kStages * Shape::kStage + lane * 16;
+    const uint32_t hands = base + Shape::kOffHands + lane * 16;
     const int r0 = lane >> 2, c0 = 2 * (lane & 3);
 
     if (tid >= kHalf) {
+        if (PAIRS > 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Shape::kLeast));
         auto copy16 = [](uint32_t to, const void* from, bool there) {
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
         };
         const int t = tid - kHalf;
-        auto fetch = [&](int c) {
+        // K, T, V and the factors of a chunk: what the warps with S read
+        auto fetch_s = [&](int c) {
             if (c < chunks) {
-                const uint32_t to = base + (c % kStages) * Shape::kStage;
+                const uint32_t to = base + (c & 1) * Shape::kStage;
                 const uint8_t* pair = a.ws + ((piece + c) * Hk + kh) * pair_bytes(KD);
                 const uint8_t* head = a.ws + a.q_pieces * Hk * pair_bytes(KD) + ((piece + c) * Hv + h) * kHeadBytes;
-#pragma unroll 8
-                for (int i = t * 16; i < pair_bytes(KD); i += kHalf * 16) copy16(to + i, pair + i, true);
-#pragma unroll 8
-                for (int i = t * 16; i < kHeadBytes; i += kHalf * 16) copy16(to + pair_bytes(KD) + i, head + i, true);
+#pragma unroll
+                for (int n = 0; n < KD / 64; ++n)
+#pragma unroll
+                    for (int i = t * 16; i < kSquare; i += kHalf * 16) copy16(to + n * kPanel + i, pair + n * kPanel + i, true);
+#pragma unroll
+                for (int i = t * 16; i < kSquare; i += kHalf * 16) {
+                    copy16(to + pair_bytes(KD) + i, head + i, true);
+                    copy16(to + pair_bytes(KD) + 2 * kSquare + i, head + 2 * kSquare + i, true);
+                }
+                for (int i = t * 16; i < Shape::kFactors; i += kHalf * 16)
+                    copy16(base + Shape::kOffFactors + c % 3 * Shape::kFactors + i, head + kHeadTiles + i, true);
                 const int64_t row0 = lo + (int64_t)c * kC;
 #pragma unroll
                 for (int i = t; i < kC * (kCols / 8); i += kHalf) {
@@ -689,22 +703,40 @@ __global__ void __launch_bounds__(2 * kHalf, 1) chunks_kernel(const __grid_const
                     if (a.wide) {
                         copy16(to + at, from, there);
                     } else {
-                        *reinterpret_cast<uint4*>(raw + (c % kStages) * Shape::kStage + at) =
+                        *reinterpret_cast<uint4*>(raw + (c & 1) * Shape::kStage + at) =
                             there ? eight(from, false) : make_uint4(0, 0, 0, 0);
                     }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        fetch(0);
+        auto fetch_o = [&](int c) {  // Q and P T
+            if (c < chunks) {
+                const uint32_t to = base + (c & 1) * Shape::kStage + kSquare;
+                const uint8_t* pair = a.ws + ((piece + c) * Hk + kh) * pair_bytes(KD) + kSquare;
+                const uint8_t* head = a.ws + a.q_pieces * Hk * pair_bytes(KD) + ((piece + c) * Hv + h) * kHeadBytes + kSquare;
+#pragma unroll
+                for (int i = t * 16; i < kSquare; i += kHalf * 16) {
+#pragma unroll
+                    for (int n = 0; n < KD / 64; ++n) copy16(to + n * kPanel + i, pair + n * kPanel + i, true);
+                    copy16(to + pair_bytes(KD) + i, head + i, true);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        fetch_s(0);
+        fetch_o(0);
         for (int c = 0; c <= chunks; ++c) {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            __syncthreads();  // chunk c is there; what goes into o of chunk c - 1 too; nobody reads chunk c - 2 any more
-            fetch(c + 1);
-            if (c == 0) continue;
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but Q and P T of chunk c
+            __syncthreads();  // K, T and V of chunk c are there, and what goes into o of c - 1; nobody reads K, T, V of c - 1
+            fetch_s(c + 1);
+            if (c == 0) {
+                fetch_o(1);
+                continue;
+            }
             const int o_c = c - 1;
-            const uint32_t stage = base + (o_c % kStages) * Shape::kStage, hand = hands + (o_c & 1) * kHands + 2 * p * Shape::kHand;
-            const Factors& f = *reinterpret_cast<const Factors*>(raw + (o_c % kStages) * Shape::kStage + pair_bytes(KD) + kHeadTiles);
+            const uint32_t stage = base + (o_c & 1) * Shape::kStage, hand = hands + (o_c & 1) * kHands + 2 * p * Shape::kHand;
+            const Factors& f = *reinterpret_cast<const Factors*>(raw + Shape::kOffFactors + o_c % 3 * Shape::kFactors);
             float o[4][4];  // of this warp's two groups of 16 tokens
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -756,6 +788,8 @@ __global__ void __launch_bounds__(2 * kHalf, 1) chunks_kernel(const __grid_const
                     for (int i = 0; i < 4; ++i) o[n][i] = fmaf(i & 1 ? b1 : b0, acc[n][i], o[n][i]);
                 }
             }
+            asm volatile("bar.sync %0, %1;" ::"r"(kPairs + 1), "r"(kHalf) : "memory");  // nobody reads Q and P T of c - 1 any more
+            fetch_o(c + 1);
             const int64_t row0 = lo + (int64_t)o_c * kC;
             const int rows = (int)(hi - row0 < kC ? hi - row0 : kC), d = first + 16 * p + c0;
             __nv_bfloat16* to = a.o + row0 * a.o_ld + h * dv + d;
@@ -781,15 +815,11 @@ __global__ void __launch_bounds__(2 * kHalf, 1) chunks_kernel(const __grid_const
         return;
     }
 
+    if (PAIRS > 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kMost));
     const uint32_t swap = base + Shape::kOffSwap + lane * 16, rests = base + Shape::kOffRests + lane * 16;
     const uint32_t my_swap = swap + warp * Shape::kSwap, its_swap = swap + (warp ^ 1) * Shape::kSwap;
     const uint32_t my_rests = rests + warp * Shape::kRests, its_rests = rests + (warp ^ 1) * Shape::kRests;
-    auto pair_barrier = [&]() {
-        if (p)
-            asm volatile("bar.sync 2, 64;" ::: "memory");
-        else
-            asm volatile("bar.sync 1, 64;" ::: "memory");
-    };
+    auto pair_barrier = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + p) : "memory"); };
     // S: rows d0, d0 + 8 of v_dim, columns k0 + 8 n (+ 1) of k_dim, in units of down(unit)
     const int d0 = first + 16 * p + r0, k0 = q * (KD / 2) + c0;
     float S[kN][4];
@@ -820,9 +850,8 @@ __global__ void __launch_bounds__(2 * kHalf, 1) chunks_kernel(const __grid_const
 
     for (int c = 0; c < chunks; ++c) {
         __syncthreads();
-        const uint32_t stage = base + (c % kStages) * Shape::kStage, T_high = stage + pair_bytes(KD), T_rest = T_high + 2 * kSquare;
-        const uint8_t* at = raw + (c % kStages) * Shape::kStage;
-        const Factors& f = *reinterpret_cast<const Factors*>(at + pair_bytes(KD) + kHeadTiles);
+        const uint32_t stage = base + (c & 1) * Shape::kStage, T_high = stage + pair_bytes(KD), T_rest = T_high + 2 * kSquare;
+        const Factors& f = *reinterpret_cast<const Factors*>(raw + Shape::kOffFactors + c % 3 * Shape::kFactors);
         const uint32_t hand = hands + (c & 1) * kHands + warp * Shape::kHand, its_hand = hands + (c & 1) * kHands + (warp ^ 1) * Shape::kHand;
 
         // This half's part of K S^T, for the other's tokens first.  S's unit is from a bound: its largest value is found
@@ -997,17 +1026,32 @@ __global__ void __launch_bounds__(2 * kHalf, 1) chunks_kernel(const __grid_const
     }
 }
 
+template <int KD, int PAIRS>
+cudaError_t launch_chunks(const DeltaArgs& a, cudaStream_t st) {
+    using Shape = ChunkShape<KD, PAIRS>;
+    const auto kernel = chunks_kernel<KD, PAIRS>;
+    if (PAIRS > 2) {  // the warps with S wait for registers that the others give back: the launch must have them
+        cudaFuncAttributes f;
+        if (cudaError_t e = cudaFuncGetAttributes(&f, kernel)) return e;
+        if (f.numRegs * 2 < Shape::kMost + Shape::kLeast) return cudaErrorLaunchOutOfResources;
+    }
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes)) return e;
+    const int64_t blocks = (a.c.v_dim + Shape::kCols - 1) / Shape::kCols;
+    return launch(kernel, dim3((unsigned)(a.q.n * a.c.v_heads * blocks)), 2 * Shape::kHalf, Shape::kBytes, st, 1, a);
+}
 template <int KD>
 cudaError_t launch_chunked(const DeltaArgs& a, cudaStream_t st) {
-    using Shape = ChunkShape<KD>;
-    const int twos = (a.c.v_heads / a.c.k_heads + 1) / 2, blocks = (a.c.v_dim + kCols - 1) / kCols;
+    const int twos = (a.c.v_heads / a.c.k_heads + 1) / 2;
     constexpr int kShared = (int)sizeof(PrepareShared<KD>);
     if (cudaError_t e = cudaFuncSetAttribute(prepare_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared)) return e;
-    if (cudaError_t e = cudaFuncSetAttribute(chunks_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes)) return e;
     if (cudaError_t e = launch(prepare_kernel<KD>, dim3((unsigned)a.q_pieces + 1, (unsigned)(a.c.k_heads * twos)), kPrepare, kShared,
                                st, 1, a))
         return e;
-    return launch(chunks_kernel<KD>, dim3((unsigned)((int64_t)a.q.n * a.c.v_heads * blocks)), 2 * kHalf, Shape::kBytes, st, 1, a);
+    // Four pairs take 1.8 times as long for a chunk as two, so they pay where the CTAs of two would be more than the SMs
+    // (and are twos): 64 prompts of 64 tokens, 32 heads of 128: 277 us, two pairs 318; 16 of 256: 178 and 196; 2 of 2048:
+    // 164 and 175; one of 4096, 128 CTAs of two pairs: 267 and 177.
+    const int64_t columns = (a.c.v_dim + 31) / 32, ctas = a.q.n * a.c.v_heads * columns;
+    return ctas > 152 && columns % 2 == 0 ? launch_chunks<KD, 4>(a, st) : launch_chunks<KD, 2>(a, st);
 }
 
 }  // namespace

@@ -312,10 +312,13 @@ cudaError_t launch_rows(NormArgs& g, cudaStream_t st) {
 
 // Heads of up to 16 LANES values.  Sixteen values a thread and two heads at a time: what a head costs beside its values
 // (its place, its sum's exchange) is then small, and loads of 64 bytes a thread are under way.  Few heads: eight values
-// and one head, so that more threads start at once.
+// and one head, so that more threads start at once.  bf16 heads of 128, in us, 8 and 2 x 16 values a thread: 64 heads
+// 1.35 and 1.57, 4096 heads 1.64 and 1.73, 8192 heads 2.30 and 1.75, 65536 heads 7.1 and 4.4; gated, 4096 heads 1.8 and
+// 2.4, 8192 heads 2.9 and 2.5; of 256, rotated, 1024 heads 2.1 and 2.9, 8192 heads 4.4 and 3.5; of 64, 8192 heads 1.60
+// and 1.73, 16384 heads 2.3 and 1.7.
 template <typename T, int LANES>
 cudaError_t launch_wide(NormArgs& g, cudaStream_t st) {
-    if (LANES < 32 && g.T * (g.a.heads + g.b.heads) < (int64_t)(kThreads / LANES) * 152 * 4)
+    if (LANES < 32 && g.T * (g.a.heads + g.b.heads) < (int64_t)(kThreads / LANES) * 380)
         return launch_rows<T, LANES < 32 ? 2 * LANES : 32, LANES < 32 ? 1 : 2, 8, 1>(g, st);
     return launch_rows<T, LANES, 2, 8, LANES < 32 ? 2 : 1>(g, st);
 }

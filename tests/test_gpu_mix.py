@@ -304,13 +304,13 @@ def check_delta(rng, lens, Hk=2, Hv=4, dk=64, dv=64, layout="side by side", padd
 
 @pytest.mark.parametrize("dk,dv", [(8, 8), (64, 64), (64, 128), (128, 64), (128, 128), (96, 40), (72, 104)])
 def test_delta_token_by_token(dk, dv):
-    check_delta(rng_of(dk, dv), [1, 0, 2, 16, 5, 1], dk=dk, dv=dv, padded=(2,))
-    check_delta(rng_of(dv, dk), [1, 3, 7], Hk=1, Hv=3, dk=dk, dv=dv, max_len=16)
+    check_delta(rng_of(dk, dv), [1, 0, 2, 24, 5, 1], dk=dk, dv=dv, padded=(2,))
+    check_delta(rng_of(dv, dk), [1, 3, 7], Hk=1, Hv=3, dk=dk, dv=dv, max_len=24)
 
 
 @pytest.mark.parametrize("dk,dv", [(8, 8), (64, 64), (64, 128), (128, 64), (128, 128), (96, 40), (72, 104)])
 def test_delta_in_chunks(dk, dv):
-    check_delta(rng_of(dk, dv, 1), [17, 63, 0, 64, 3, 65, 200], dk=dk, dv=dv, padded=(4,))
+    check_delta(rng_of(dk, dv, 1), [25, 63, 0, 64, 3, 65, 200], dk=dk, dv=dv, padded=(4,))
 
 
 @pytest.mark.parametrize("Hk,Hv", [(1, 1), (1, 4), (2, 2), (3, 9), (16, 32)])
@@ -321,6 +321,13 @@ def test_delta_shared_heads(Hk, Hv):
 @pytest.mark.parametrize("layout", ["plain", "odd"])
 def test_delta_layouts(layout):
     check_delta(rng_of(4), [70, 2, 130, 1], dk=128, dv=72, layout=layout)
+
+
+@pytest.mark.parametrize("dk,dv,Hk,Hv,layout", [(128, 128, 8, 16, "plain"), (72, 104, 8, 16, "odd"), (64, 40, 16, 32, "plain"),
+                                                (64, 64, 16, 32, "odd")])
+def test_delta_many_sequences_and_heads(dk, dv, Hk, Hv, layout):
+    """More of both than there are SMs for blocks of 32 columns."""
+    check_delta(rng_of(dk, Hv), [70, 2, 130, 64, 0, 29], Hk=Hk, Hv=Hv, dk=dk, dv=dv, layout=layout, padded=(3,))
 
 
 def test_delta_without_state():
@@ -367,7 +374,7 @@ def test_delta_gates_and_sizes(name):
 
 def test_delta_does_not_depend_on_its_batch():
     rng = rng_of(11)
-    lens = [150, 16, 1, 17, 700]
+    lens = [150, 24, 1, 25, 700, 30, 64, 65, 2, 128, 40, 90]
     T, n = sum(lens), len(lens)
     q, k, v, g, beta = delta_inputs(rng, T, 2, 4, 128, 128)
     off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)

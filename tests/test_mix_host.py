@@ -120,18 +120,18 @@ def test_delta_refuses_bad_arguments(lib):
     refused(call(size=need - 1), "workspace")
     refused(call(ws=None), "workspace")
     refused(call(ws=P + 64), "workspace")
-    refused(call(q=seqs(2, max_len=17), size=0), "workspace")
+    refused(call(q=seqs(2, max_len=25), size=0), "workspace")
     assert call(T=0, ptr=(None,) * 5, o=None, ws=None, size=0) == moe.MOE_OK
     assert call(q=seqs(0), ws=None, size=0) == moe.MOE_OK
 
 
 def test_delta_workspace():
     w = moe.moe_delta_workspace
-    assert w(16, 1, 16, 32, 128, 128) == 0 and w(4096, 4096, 16, 32, 128, 128, 1) == 0 and w(4096, 300, 16, 32, 128, 128, 16) == 0
+    assert w(24, 1, 16, 32, 128, 128) == 0 and w(4096, 4096, 16, 32, 128, 128, 1) == 0 and w(4096, 300, 16, 32, 128, 128, 24) == 0
     one = w(128, 1, 1, 1, 64, 64) - w(64, 1, 1, 1, 64, 64)
     assert 0 < one and one % 128 == 0
-    assert w(17, 3, 1, 1, 64, 64) - w(17, 1, 1, 1, 64, 64) == 2 * one  # a chunk for each 64 rows, and one for each sequence
-    assert one <= w(17, 1, 1, 1, 64, 64) <= one + 4096
+    assert w(25, 3, 1, 1, 64, 64) - w(25, 1, 1, 1, 64, 64) == 2 * one  # a chunk for each 64 rows, and one for each sequence
+    assert one <= w(25, 1, 1, 1, 64, 64) <= one + 4096
     assert w((1 << 31) - 1, 1, 16, 32, 128, 128) > 1 << 32
     for bad in ((-1, 1, 1, 1, 64, 64), (64, -1, 1, 1, 64, 64), (64, 1, 2, 3, 64, 64), (64, 1, 1, 1, 65, 64), (1 << 31, 1, 1, 1, 64, 64)):
         assert w(*bad) == 0
