@@ -318,7 +318,7 @@ cudaError_t launch_rows(NormArgs& g, cudaStream_t st) {
 // and 1.73, 16384 heads 2.3 and 1.7.
 template <typename T, int LANES>
 cudaError_t launch_wide(NormArgs& g, cudaStream_t st) {
-    if (LANES < 32 && g.T * (g.a.heads + g.b.heads) < (int64_t)(kThreads / LANES) * 380)
+    if (LANES < 32 && g.T * (g.a.heads + g.b.heads) < (int64_t)(kThreads / LANES) * 190)
         return launch_rows<T, LANES < 32 ? 2 * LANES : 32, LANES < 32 ? 1 : 2, 8, 1>(g, st);
     return launch_rows<T, LANES, 2, 8, LANES < 32 ? 2 : 1>(g, st);
 }
