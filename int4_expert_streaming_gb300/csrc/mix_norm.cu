@@ -8,6 +8,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 256;
+constexpr int kHalves = 1, kAdjacent = 2;  // rotations
 
 struct NormArgs {
     moe_head_norm_config c;
@@ -120,13 +121,13 @@ __device__ __forceinline__ void store(T* p, const float* v) {
 // tensor only; its lanes keep their part of the weights.  All reads of a head
 // come before its first write, so y may be x.  sin and cos are found once for
 // each token of a CTA, for all its heads, behind the loads.  Bound by memory.
-template <typename T, int LANES, int CH, int P, int U, bool ROT, bool GATE>
+template <typename T, int LANES, int CH, int P, int U, int ROT, bool GATE>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 : 4) : 1)
     norm_kernel(const __grid_constant__ NormArgs g) {
     extern __shared__ float2 table[];  // [token of the CTA][pair]
     after_previous();
     let_next_start();
-    constexpr int kPass = kThreads / LANES, kPiece = P == 8 && ROT ? 4 : P, kPieces = P / kPiece;
+    constexpr int kPass = kThreads / LANES, kPiece = P == 8 && ROT == kHalves ? 4 : P, kPieces = P / kPiece;
     const bool second = blockIdx.x >= g.first_blocks;
     const moe_heads& t = second ? g.b : g.a;
     const uint32_t inverse = second ? g.inverse_b : g.inverse_a;  // of the heads, 32 bits behind the point, rounded up
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 
     const int64_t token0 = rows <= UINT32_MAX ? (uint32_t)row0 / (uint32_t)t.heads : row0 / t.heads;
     const int half = g.c.rot_dim / 2, D = g.c.dim, lane = threadIdx.x % LANES;
     const int first = (int)(row0 - token0 * t.heads);
-    const bool halves = ROT && g.c.pairs == MOE_ROT_HALVES;
+    constexpr bool halves = ROT == kHalves;
 
     // token (of the CTA's) and head of a thread's u-th row; rows past the last redo the last one's sums: every thread of a
     // warp takes part in the shuffles.  Found again where needed: it is two instructions, and registers are CTAs
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 
     }
 }
 
-template <typename T, int LANES, int CH, int P, int U, bool ROT, bool GATE>
+template <typename T, int LANES, int CH, int P, int U, int ROT, bool GATE>
 cudaError_t launch_heads(NormArgs& g, cudaStream_t st) {
     constexpr int kRows = kThreads / LANES * U;  // heads of a CTA
     auto tokens = [](int heads) { return heads == 0 ? 0 : kRows / heads + 2 < kRows ? kRows / heads + 2 : kRows; };
@@ -305,9 +306,11 @@ cudaError_t launch_heads(NormArgs& g, cudaStream_t st) {
 template <typename T, int LANES, int CH, int P, int U>
 cudaError_t launch_rows(NormArgs& g, cudaStream_t st) {
     const bool gate = g.a.gate_dev || g.b.gate_dev;
+    if (g.c.rot_dim && g.c.pairs == MOE_ROT_HALVES)
+        return gate ? launch_heads<T, LANES, CH, P, U, kHalves, true>(g, st) : launch_heads<T, LANES, CH, P, U, kHalves, false>(g, st);
     if (g.c.rot_dim)
-        return gate ? launch_heads<T, LANES, CH, P, U, true, true>(g, st) : launch_heads<T, LANES, CH, P, U, true, false>(g, st);
-    return gate ? launch_heads<T, LANES, CH, P, U, false, true>(g, st) : launch_heads<T, LANES, CH, P, U, false, false>(g, st);
+        return gate ? launch_heads<T, LANES, CH, P, U, kAdjacent, true>(g, st) : launch_heads<T, LANES, CH, P, U, kAdjacent, false>(g, st);
+    return gate ? launch_heads<T, LANES, CH, P, U, 0, true>(g, st) : launch_heads<T, LANES, CH, P, U, 0, false>(g, st);
 }
 
 // Heads of up to 16 LANES values.  Sixteen values a thread and two heads at a time: what a head costs beside its values
