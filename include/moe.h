@@ -576,8 +576,9 @@ typedef struct {
  *   (z_i, z_j) = (z_i cos - z_j sin, z_j cos + z_i sin)  for each pair, angle = pos[t] * inv_freq[pair]
  *   y = z * silu(gate)
  * a head of zeros with eps 0 gives NaN, as the formula does.
- *   pos_dev int32 [T], inv_freq_dev fp32 [rot_dim / 2]: with rot_dim > 0 only.  The angle loses nothing for
- *   positions far from 0: it is reduced to turns in two fp32 numbers, or in fp64 where those would not do.
+ *   pos_dev int32 [T], inv_freq_dev fp32 [rot_dim / 2]: with rot_dim > 0 only.  The angle is reduced to a
+ *   part of a turn before it is rounded (in two fp32 numbers, or in fp64 where those would not do): it is good to 2^-22 of
+ *   a turn at every position while |inv_freq| is up to 1, and while the angle is below 2^30 otherwise.
  */
 int moe_head_norm(const moe_head_norm_config* cfg, const moe_heads* a, const moe_heads* b, const int32_t* pos_dev,
                   const float* inv_freq_dev, int64_t T, void* stream);
@@ -606,9 +607,13 @@ typedef struct {
  * and fp32 throughout.  Longer ones run in chunks of 64 tokens on the tensor
  * cores: within a chunk the updates come from one triangular system; the
  * state, the chunk's inverse and the updates enter the products as pairs of
- * fp16 numbers in units of powers of two (together about 2^-22 of the largest)
+ * fp16 numbers in units of powers of two (together about 2^-22 of the largest
+ * within 16 columns of v_dim and 64 tokens)
  * and are summed in fp32; what goes only into o enters as one fp16 number.  Which of the two a sequence takes depends on its own
  * length alone (max_len being right), so its results do not depend on its batch.
+ * A value of q, k, v, g or beta that is not finite (but for g = -inf) leaves
+ * that head's o undefined from 63 tokens before it on, and its state; other heads
+ * and sequences are not touched.
  * workspace_dev: moe_delta_workspace() bytes (0: may be NULL), 128-byte aligned, contents irrelevant; two calls that may
  * run at the same time (or two graphs) need one each.
  */

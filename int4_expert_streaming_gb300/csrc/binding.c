@@ -416,6 +416,9 @@ static long long first_extent(PyObject* t, const char* what) {
     return n;
 }
 
+/* the address of a state without slots, which is never read or written */
+static _Alignas(16) char no_slots[16];
+
 static PyObject* conv_names[8];
 static const char conv_doc[] =
     "moe_conv(x, w, y, bias=None, act=MOE_ACT_SILU, seqs=None, state=None, stream=None)\n--\n\n"
@@ -446,8 +449,7 @@ static PyObject* conv(KWARGS) {
         if ((slots = first_extent(v[6], "state")) < 0) return NULL;
         if (flat(v[6], x.type == MOE_F32 ? t_f32 : t_bf16, slots * (w.cols - 1) * x.cols, "state", expected, &dev, &state))
             return NULL;
-        /* a state of no slots still is one: every sequence is left out */
-        if (!slots) Py_RETURN_NONE;
+        if (!slots) state = no_slots; /* which torch gives no address: every sequence is left out */
     }
     NONE_OR_RAISE(moe_conv(qp, x.p, x.type, x.ld, x.rows, (int32_t)x.cols, w.p, w.type, (int32_t)w.cols, bias, (int32_t)act,
                            state, slots, y.p, y.ld, st));
@@ -553,7 +555,7 @@ static PyObject* delta(KWARGS) {
         if (flat(v[5], t_f32, slots * val.heads * val.dim * q.dim, "state",
                  "a contiguous float32 CUDA tensor [slots, v_heads, v_dim, k_dim]", &dev, &state))
             return NULL;
-        if (!slots) Py_RETURN_NONE;
+        if (!slots) state = no_slots;
     }
     NONE_OR_RAISE(moe_delta(&c, bp, q.p, q.ld, k.p, k.ld, val.p, val.ld, g, beta, state, slots, o.p, o.ld, val.n, ws,
                             (size_t)bytes, st));

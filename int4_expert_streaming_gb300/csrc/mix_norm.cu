@@ -29,7 +29,7 @@ __device__ __forceinline__ float2 turn(int pos, float f) {
     constexpr double kTurns = 0.15915494309189535;  // 1 / 2 pi
     constexpr float kHigh = (float)kTurns, kRest = (float)(kTurns - (double)kHigh);
     float t;
-    if (abs(pos) <= 1 << 24 && fabsf(f) <= 1.0f) {
+    if ((uint32_t)pos + (1u << 24) <= 1u << 25 && fabsf(f) <= 1.0f) {
         const float p = (float)pos, high = f * kHigh, rest = fmaf(f, kHigh, -high) + f * kRest;
         const float whole = p * high;
         t = (whole - rintf(whole)) + fmaf(p, rest, fmaf(p, high, -whole));

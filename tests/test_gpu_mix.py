@@ -231,6 +231,26 @@ def test_norm_of_zeros_and_negative_positions():
     assert torch.equal(out[1], v[1])
 
 
+def test_norm_positions_at_the_ends():
+    """Both ways of reducing an angle, and the ends of int32.  Good to 2^-22 of a turn, 2 pi 2^-22 = 2^-19.3 in what turns,
+    and ten roundings."""
+    at = [-1 << 31, (1 << 31) - 1, -(1 << 24), 1 << 24, (1 << 24) + 1, -(1 << 24) - 1, 0, -1]
+    freq = np.array([1.0, 0.73, 1e-3, 1e-9], np.float32)
+    rng = rng_of(31)
+    x = cuda(rng.standard_normal((len(at), 2, 8)))
+    y = torch.empty_like(x)
+    moe.moe_head_norm(moe.make_head_norm_config(moe.MOE_NORM_NONE, rot_dim=8), x, y, pos=ints(at), inv_freq=cuda(freq),
+                      stream=torch.cuda.current_stream())
+    want, size = ora.head_norm(f64(x), "none", 0, None, 0, np.array(at), freq, 8, True, None)
+    assert (np.abs(f64(y) - want) <= 2.0 ** -19 * size).all()
+    wild = np.array([1.5, 40.0, -3.0, 1000.0], np.float32)  # angles up to 2^30
+    at = [1000, -70000, 1 << 20, 5]
+    moe.moe_head_norm(moe.make_head_norm_config(moe.MOE_NORM_NONE, rot_dim=8), x[:4], y[:4], pos=ints(at), inv_freq=cuda(wild),
+                      stream=torch.cuda.current_stream())
+    want, size = ora.head_norm(f64(x[:4]), "none", 0, None, 0, np.array(at), wild, 8, True, None)
+    assert (np.abs(f64(y[:4]) - want) <= 2.0 ** -19 * size).all()
+
+
 # ---------------------------------------------------------------------------
 # gated delta rule
 # ---------------------------------------------------------------------------
@@ -390,6 +410,31 @@ def test_delta_does_not_depend_on_its_batch():
         assert torch.equal(o1, o[lo:hi]) and torch.equal(st1[s], st[s])
 
 
+def test_delta_values_that_are_not_finite_stay_in_their_head():
+    """NaN in v of one head, infinity in a key that two heads share: the other heads and sequences keep every bit."""
+    rng = rng_of(15)
+    lens = [100, 70, 10, 40]
+    T, n = sum(lens), len(lens)
+    q, k, v, g, beta = (t.contiguous() for t in delta_inputs(rng, T, 2, 4, 64, 64))
+    seqs = moe.make_seqs(n, ints(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)))
+    start = cuda(rng.standard_normal((n, 4, 64, 64)))
+    results = []
+    for spoilt in (False, True):
+        if spoilt:
+            v[50, 1, 3] = float("nan")
+            k[120, 0, 5] = float("inf")
+            g[185, 3] = float("nan")  # of the last sequence
+        st, o = start.clone(), torch.zeros((T, 4, 64), dtype=BF, device="cuda")
+        run_delta(q, k, v, g, beta, st, o, 0.1, seqs, T, n)
+        torch.cuda.synchronize()
+        results.append((o, st))
+    (o, st), (o1, st1) = results
+    for s, (lo, hi, heads) in enumerate([(0, 100, [0, 2, 3]), (100, 170, [2, 3]), (170, 180, [0, 1, 2, 3]), (180, 220, [0, 1, 2])]):
+        assert torch.equal(o[lo:hi, heads], o1[lo:hi, heads]) and torch.equal(st[s, heads], st1[s, heads])
+    assert o1[50:100, 1, 3].isnan().all() and st1[0, 1, 3].isnan().all()
+    assert not o1[121:170, :2].isfinite().any() and not o1[185:220, 3].isfinite().any()
+
+
 def test_delta_prefill_then_decode_is_the_whole():
     rng = rng_of(12)
     T = 200
@@ -503,3 +548,101 @@ def test_a_run_of_all_against_the_definitions():
         assert np.abs(f64(st) - st64).max() <= 2.0 ** -15 * top.max()
         want, size = ora.head_norm(f64(o), "rms", 1e-6, f64(weight), 0, None, None, 0, True, f64(z))
         assert (np.abs(f64(out) - want) <= 2.0 ** -8 * 1.01 * np.abs(want) + 2.0 ** -18 * size).all()
+
+
+# ---------------------------------------------------------------------------
+# places beyond 2^31 elements; calls side by side
+# ---------------------------------------------------------------------------
+
+def test_states_and_rows_far_behind():
+    """Slots and rows more than 2^31 elements from their tensor's start give what near ones give."""
+    rng = rng_of(16)
+    stream = torch.cuda.current_stream()
+    q, k, v, g, beta = delta_inputs(rng, 72, 1, 1, 128, 128)
+    big = torch.empty((132000, 1, 128, 128), device="cuda")  # 8.7 GB, of which two slots are touched
+    small = cuda(rng.standard_normal((2, 1, 128, 128)))
+    big[[131999, 131072]] = small
+    off = ints([0, 70, 72])
+    o, o1 = (torch.empty((72, 1, 128), dtype=BF, device="cuda") for _ in range(2))
+    run_delta(q, k, v, g, beta, small, o, 0.1, moe.make_seqs(2, off), 72, 2)
+    run_delta(q, k, v, g, beta, big, o1, 0.1, moe.make_seqs(2, off, ints([131999, 131072])), 72, 2)
+    assert torch.equal(o, o1) and torch.equal(small, big[[131999, 131072]])
+    del big
+
+    w = cuda(rng.standard_normal((64, 4)), BF)
+    room = torch.empty(2 * (1 << 31) + 4096, dtype=BF, device="cuda")  # two rows 2^31 elements from one another, and slots
+    far = room.as_strided((3, 64), ((1 << 31), 1))
+    x = cuda(rng.standard_normal((3, 64)), BF)
+    far.copy_(x)
+    slots = torch.empty((11200000, 3, 64), dtype=BF, device="cuda")  # 2^31 elements and more
+    near = cuda(rng.standard_normal((1, 3, 64)), BF)
+    slots[11199999:] = near
+    y, y1 = torch.empty_like(x), torch.empty_like(x)
+    moe.moe_conv(x, w, y, seqs=moe.make_seqs(1, ints([0, 3])), state=near, stream=stream)
+    moe.moe_conv(far, w, y1, seqs=moe.make_seqs(1, ints([0, 3]), ints([11199999])), state=slots, stream=stream)
+    assert torch.equal(y, y1) and torch.equal(near[0], slots[11199999])
+    step, step1 = torch.empty_like(x), torch.empty_like(x)  # each row a sequence
+    moe.moe_conv(x, w, step, seqs=moe.make_seqs(3), stream=stream)
+    moe.moe_conv(far, w, step1, seqs=moe.make_seqs(3), stream=stream)
+    assert torch.equal(step, step1)
+    cfg = moe.make_head_norm_config(moe.MOE_NORM_RMS)
+    n, n1 = (torch.empty((3, 1, 64), dtype=BF, device="cuda") for _ in range(2))
+    moe.moe_head_norm(cfg, x[:, None], n, stream=stream)
+    moe.moe_head_norm(cfg, far[:, None], n1, stream=stream)
+    assert torch.equal(n, n1)
+    moe.moe_head_norm(cfg, far[:, None], far[:, None], stream=stream)  # and written there
+    assert torch.equal(far, n[:, 0])
+
+
+def test_calls_side_by_side_on_two_streams():
+    """Calls of two batches at once, each with its workspace, and two captured graphs at once: every bit as alone."""
+    rng = rng_of(17)
+    jobs = []
+    for T, Hk, Hv, dk, dv in ((900, 4, 8, 128, 128), (700, 2, 8, 64, 96)):
+        q, k, v, g, beta = delta_inputs(rng, T, Hk, Hv, dk, dv)
+        ws = torch.empty(moe.moe_delta_workspace(T, 2, Hk, Hv, dk, dv), dtype=torch.uint8, device="cuda")
+        st, o = torch.zeros((2, Hv, dv, dk), device="cuda"), torch.empty((T, Hv, dv), dtype=BF, device="cuda")
+        seqs = moe.make_seqs(2, ints([0, T // 3, T]), carry=ints([0, 0]))
+
+        def call(stream, a=(q, k, v, g, beta, st, o), kw={"scale": 0.1, "seqs": seqs, "workspace": ws}):
+            moe.moe_delta(*a, **kw, stream=stream)
+        call(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        jobs.append((call, torch.cuda.Stream(), o, st, o.clone(), st.clone()))
+    graphs = []
+    for call, stream, *_ in jobs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            call(torch.cuda.current_stream())
+    for replay in (False, True):
+        for _, _, o, st, _, _ in jobs:
+            o.zero_()
+            st.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for (call, stream, *_), graph in zip(jobs, graphs):
+                with torch.cuda.stream(stream):
+                    graph.replay() if replay else call(stream)
+        torch.cuda.synchronize()
+        for _, _, o, st, o0, st0 in jobs:
+            assert torch.equal(o, o0) and torch.equal(st, st0)
+
+
+def test_a_state_without_slots():
+    """Every sequence is left out, and a batch without a slot list is refused as by the C call."""
+    x, w = torch.ones((3, 8), dtype=BF, device="cuda"), torch.ones((8, 2), dtype=BF, device="cuda")
+    y, none = torch.full_like(x, 5), torch.empty((0, 1, 8), dtype=BF, device="cuda")
+    moe.moe_conv(x, w, y, seqs=moe.make_seqs(3, slot=ints([0, 1, -1])), state=none)
+    moe.moe_conv(x, w, y, seqs=moe.make_seqs(1, ints([0, 3]), slot=ints([0])), state=none)
+    torch.cuda.synchronize()
+    assert (y == 5).all()
+    with pytest.raises(moe.MoeError, match="0 slots"):
+        moe.moe_conv(x, w, y, seqs=moe.make_seqs(3), state=none)
+    q, g = torch.ones((30, 1, 8), dtype=BF, device="cuda"), torch.zeros((30, 1), device="cuda")
+    o, none = torch.full_like(q, 5), torch.empty((0, 1, 8, 8), device="cuda")
+    ws = torch.empty(moe.moe_delta_workspace(30, 1, 1, 1, 8, 8), dtype=torch.uint8, device="cuda")
+    moe.moe_delta(q, q, q, g, g, none, o, seqs=moe.make_seqs(1, ints([0, 30]), slot=ints([0])), workspace=ws)
+    torch.cuda.synchronize()
+    assert (o == 5).all()
+    with pytest.raises(moe.MoeError, match="0 slots"):
+        moe.moe_delta(q, q, q, g, g, none, o, workspace=ws)
