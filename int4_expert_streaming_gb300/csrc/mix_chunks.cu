@@ -262,37 +262,66 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
             w[i] = make_uint4(0, 0, 0, 0);
             if (r < rows && p * 8 < dk) w[i] = eight(src + r * ld + p * 8, a.wide);
         }
+        // the rows' largest magnitudes, whose bits order as they do: two rows a word
+        uint32_t tops[kN / 2];
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const int r = r0 + i * kPass;
             const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            *reinterpret_cast<uint4*>(m.kq[b] + piece_at<kRow>(r, p)) = w[i];
-            uint32_t top = 0;  // of the magnitudes' bits, which order as the magnitudes do
+            *reinterpret_cast<uint4*>(m.kq[b] + piece_at<kRow>(r0 + i * kPass, p)) = w[i];
+            uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) top = __vmaxu2(top, v[j] & 0x7fff7fffu);
             top = max(top >> 16, top & 0xffffu);
+            if (i & 1)
+                tops[i / 2] |= top << 16;
+            else
+                tops[i / 2] = top;
+        }
 #pragma unroll
-            for (int d = 1; d < kRow; d <<= 1) top = max(top, __shfl_xor_sync(kAll, top, d));
+        for (int i = 0; i < kN / 2; ++i)
+#pragma unroll
+            for (int d = 1; d < kRow; d <<= 1) tops[i] = __vmaxu2(tops[i], __shfl_xor_sync(kAll, tops[i], d));
+        float sums[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int r = r0 + i * kPass;
+            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, top = i & 1 ? tops[i / 2] >> 16 : tops[i / 2] & 0xffffu;
             const int e = max((int)(top >> 7), 16);
             const float f = up(e);
             uint4 w16;
             uint32_t* hw = reinterpret_cast<uint32_t*>(&w16);
-            float sum = 0;
+            sums[i] = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float x = __uint_as_float(v[j] << 16), y = __uint_as_float(v[j] & 0xffff0000u);
                 hw[j] = pack(x * f, y * f);
-                sum += fabsf(x) + fabsf(y);
+                sums[i] += fabsf(x) + fabsf(y);
             }
             if (h0 == 0) *reinterpret_cast<uint4*>(pair + (p >> 3) * kPanel + piece_at<8>(b * kC + r, p & 7)) = w16;
-            if (!b) {
-#pragma unroll
-                for (int d = 1; d < kRow; d <<= 1) sum += __shfl_xor_sync(kAll, sum, d);
-            }
             if (p == 0) {
                 (b ? m.q_scale : m.k_scale)[r] = down(e);
-                (b ? m.q_top : m.k_sum)[r] = b ? __uint_as_float(top << 16) : sum;
+                if (b) m.q_top[r] = __uint_as_float(top << 16);
             }
+        }
+        if (!b) {  // sums of the rows of K: half of the rows stay with a lane at each step, until it has one
+            int rest = kN, mine = 0;
+#pragma unroll
+            for (int d = 1; d < kRow; d <<= 1) {
+                if (rest > 1) {
+                    rest /= 2;
+                    const bool high = p & d;
+#pragma unroll
+                    for (int i = 0; i < kN / 2; ++i)
+                        if (i < rest) {
+                            const float other = __shfl_xor_sync(kAll, high ? sums[i] : sums[i + rest], d);
+                            sums[i] = (high ? sums[i + rest] : sums[i]) + other;
+                        }
+                    mine += high ? rest : 0;
+                } else {
+                    sums[0] += __shfl_xor_sync(kAll, sums[0], d);
+                }
+            }
+            m.k_sum[r0 + mine * kPass] = sums[0];
         }
     }
     // sums of g in fp64 (64 additions), kept as two floats: differences of far sums stay exact
@@ -370,15 +399,20 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
             p_up[i] = up(e);
             p_down[i] = down(e);
         }
+        float diagonal[2][2][2];  // of the diagonal block's halves
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 16 * warp + (lane >> 2) + 8 * i, j = 16 * warp + 8 * n + 2 * (lane & 3);
+                diagonal[n][i][0] = j <= r ? expf((gh[r] - gh[j]) + (gr[r] - gr[j])) : 0.0f;
+                diagonal[n][i][1] = j + 1 <= r ? expf((gh[r] - gh[j + 1]) + (gr[r] - gr[j + 1])) : 0.0f;
+            }
         auto decay = [&](int n, float (&L)[2][2]) {
             const int j = 8 * n + 2 * (lane & 3);
             if (n >= 2 * warp) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = 16 * warp + (lane >> 2) + 8 * i;
-                    L[i][0] = j <= r ? expf((gh[r] - gh[j]) + (gr[r] - gr[j])) : 0.0f;
-                    L[i][1] = j + 1 <= r ? expf((gh[r] - gh[j + 1]) + (gr[r] - gr[j + 1])) : 0.0f;
-                }
+                for (int i = 0; i < 2; ++i) L[i][0] = diagonal[n & 1][i][0], L[i][1] = diagonal[n & 1][i][1];
             } else {
                 const float2 e = *reinterpret_cast<const float2*>(&m.before[b][warp][j]);
 #pragma unroll
@@ -854,6 +888,15 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
         const Factors& f = *reinterpret_cast<const Factors*>(raw + Shape::kOffFactors + c % 3 * Shape::kFactors);
         const uint32_t hand = hands + (c & 1) * kHands + warp * Shape::kHand, its_hand = hands + (c & 1) * kHands + (warp ^ 1) * Shape::kHand;
 
+        // V of this warp's tokens, turned: two groups of 16 tokens by 16 columns
+        uint32_t v[2][4], bits = 0;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            ldmatrix_trans(v[g], stage + Shape::kV + (16 * group[g] + (lane & 15)) * kVPitch + 32 * p + (lane >> 4) * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bits = __vmaxu2(bits, v[g][i] & 0x7fff7fffu);
+        }
+        bits = __reduce_max_sync(kAll, max(bits & 0xffff0000u, bits << 16));
         // This half's part of K S^T, for the other's tokens first.  S's unit is from a bound: its largest value is found
         // beside the products.
         const int e_s = field(2.0f * s_bound);
@@ -880,15 +923,6 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
             times_k(t, 2);
         }
         const float most = largest_of_s();
-        // V of this warp's tokens, turned: two groups of 16 tokens by 16 columns
-        uint32_t v[2][4], bits = 0;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            ldmatrix_trans(v[g], stage + Shape::kV + (16 * group[g] + (lane & 15)) * kVPitch + 32 * p + (lane >> 4) * 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) bits = __vmaxu2(bits, v[g][i] & 0x7fff7fffu);
-        }
-        bits = __reduce_max_sync(kAll, max(bits & 0xffff0000u, bits << 16));
         if (lane == 0) found[warp] = make_float2(most, __uint_as_float(bits)), units[c & 1][warp].x = s_down;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
