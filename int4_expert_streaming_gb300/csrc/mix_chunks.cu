@@ -181,6 +181,12 @@ __device__ __forceinline__ void block_store(float* to, const float (&acc)[2][4],
             *reinterpret_cast<float2*>(to + ((lane >> 2) + 8 * i) * kPitch + 8 * n + (lane & 3) * 2) =
                 make_float2(sign * acc[n][2 * i], sign * acc[n][2 * i + 1]);
 }
+// to 2^-22 of the value, and 0 below 2^-126
+__device__ __forceinline__ float exp2_of(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // the four warps of one of the two heads
 __device__ __forceinline__ void head_barrier(int b) {
     if (b)
@@ -324,12 +330,12 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
             m.k_sum[r0 + mine * kPass] = sums[0];
         }
     }
-    // sums of g in fp64 (64 additions), kept as two floats: differences of far sums stay exact
+    // sums of g in fp64 (64 additions), in powers of two, kept as two floats: differences of far sums stay exact
     if (warp == 0) {
         double G[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            G[i] = g[i] < -120.0f ? -120.0f : g[i];  // e^-120 is 0 in fp32, and -inf has no differences
+            G[i] = (g[i] < -120.0f ? -120.0f : g[i]) * 1.4426950408889634;  // e^-120 is 0 in fp32, and -inf has no differences
             m.beta[b][2 * lane + i] = beta2[i];
         }
         G[1] += G[0];
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int j = lane + 32 * i;
-            if (j < 16 * warp) m.before[b][warp][j] = expf((gh[16 * warp] - gh[j]) + (gr[16 * warp] - gr[j]));
+            if (j < 16 * warp) m.before[b][warp][j] = exp2_of((gh[16 * warp] - gh[j]) + (gr[16 * warp] - gr[j]));
         }
         __syncwarp();
         if (warp == 0) {  // which has the shortest rows below
@@ -371,8 +377,8 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = lane + 32 * i;
-                const float e = expf(gh[r] + gr[r]);
-                const float left = expf((gh[kC - 1] - gh[r]) + (gr[kC - 1] - gr[r])) * m.k_scale[r];
+                const float e = exp2_of(gh[r] + gr[r]);
+                const float left = exp2_of((gh[kC - 1] - gh[r]) + (gr[kC - 1] - gr[r])) * m.k_scale[r];
                 f.ks[r] = e * m.k_scale[r];
                 f.qs[r] = e * m.q_scale[r] * a.c.scale;
                 f.left[r] = left;
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = 16 * warp + (lane >> 2) + 8 * i;
-            after[i] = expf((gh[r] - gh[16 * warp]) + (gr[r] - gr[16 * warp]));
+            after[i] = exp2_of((gh[r] - gh[16 * warp]) + (gr[r] - gr[16 * warp]));
             beta[i] = m.beta[b][r];
             // |q_i k_j| is at most the largest of q_i times the sum of k_j; a bound will do for 11 bits
             const int e = field(2.0f * m.q_top[r] * most_k);
@@ -405,8 +411,8 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = 16 * warp + (lane >> 2) + 8 * i, j = 16 * warp + 8 * n + 2 * (lane & 3);
-                diagonal[n][i][0] = j <= r ? expf((gh[r] - gh[j]) + (gr[r] - gr[j])) : 0.0f;
-                diagonal[n][i][1] = j + 1 <= r ? expf((gh[r] - gh[j + 1]) + (gr[r] - gr[j + 1])) : 0.0f;
+                diagonal[n][i][0] = j <= r ? exp2_of((gh[r] - gh[j]) + (gr[r] - gr[j])) : 0.0f;
+                diagonal[n][i][1] = j + 1 <= r ? exp2_of((gh[r] - gh[j + 1]) + (gr[r] - gr[j + 1])) : 0.0f;
             }
         auto decay = [&](int n, float (&L)[2][2]) {
             const int j = 8 * n + 2 * (lane & 3);
