@@ -237,7 +237,9 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
     const int rows = (int)(hi - row0 < kC ? hi - row0 : kC);
     const int Hk = a.c.k_heads, Hv = a.c.v_heads, share = Hv / Hk, dk = a.c.k_dim;
     const int twos = (share + 1) / 2, kh = blockIdx.y / twos, h0 = blockIdx.y % twos * 2;
-    const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) & 3, b = tid >> 7;  // b: which of two heads
+    // b: which of two heads.  A head's later warps have more to do (T is triangular); the second head's are numbered from
+    // the back, so that each scheduler has one of many blocks and one of few
+    const int tid = threadIdx.x, lane = tid & 31, b = tid >> 7, warp = b ? 7 - (tid >> 5) : tid >> 5;
     const bool there = h0 + b < share;
     const int h = kh * share + h0 + (there ? b : 0);
     uint8_t* pair = a.ws + ((int64_t)blockIdx.x * Hk + kh) * pair_bytes(KD);
