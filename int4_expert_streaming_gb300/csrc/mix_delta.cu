@@ -103,6 +103,17 @@ __global__ void __launch_bounds__(128) steps_kernel(const __grid_constant__ Delt
         }
     Token<KD> next;
     load(next);
+    // the next 16 tokens' rows to L1, eight threads a token: four tokens for each of 16 sequences 19.0 us, without this 19.9
+    const int ahead = 1 + threadIdx.x / 8, part = threadIdx.x % 8;
+    if (ahead < hi - lo) {
+        const void* line = nullptr;
+        if (part < 2 && part * 64 < dk) line = a.kr + (lo + ahead) * a.k_ld + kh * dk + part * 64;
+        if (part / 2 == 1 && part % 2 * 64 < dk) line = a.qr + (lo + ahead) * a.q_ld + kh * dk + part % 2 * 64;
+        if (part == 4) line = a.vr + (lo + ahead) * a.v_ld + h * dv + (blockIdx.x % blocks) * kStepRows;
+        if (part == 5) line = a.g + (lo + ahead) * Hv + h;
+        if (part == 6) line = a.beta + (lo + ahead) * Hv + h;
+        if (line) asm volatile("prefetch.global.L1 [%0];" ::"l"(line));
+    }
     __nv_bfloat16* o = a.o + lo * a.o_ld + h * dv + d0 + lane;
     for (int tokens = (int)(hi - lo); tokens > 0; --tokens) {
         const Token<KD> in = next;
