@@ -16,7 +16,7 @@ constexpr unsigned kAll = 0xffffffffu;
 // and four rows share what is unpacked of k and q.  64 sequences, 32 heads,
 // 128 x 128: one token each (256 MB of states) 42.7 us, 89% of the measured
 // copy's rate; with two rows a thread 43.7, with sixteen threads a row 50.7;
-// four tokens for each of 16 sequences 20.1, 21.7 and 24.5 us.
+// four tokens for each of 16 sequences 19.0, 21.7 and 24.5 us.
 constexpr int kLanes = 8, kRows = 4;
 constexpr int kStepRows = 128 / kLanes * kRows;  // rows of S of a CTA
 

@@ -120,7 +120,10 @@ __device__ __forceinline__ void store(T* p, const float* v) {
 // time, all of whose loads are under way together.  A CTA has heads of one
 // tensor only; its lanes keep their part of the weights.  All reads of a head
 // come before its first write, so y may be x.  sin and cos are found once for
-// each token of a CTA, for all its heads, behind the loads.  Bound by memory.
+// each token of a CTA, for all its heads, behind the loads.  bf16: 4096 tokens of
+// 32 gated heads of 128 17.8 us, 83% of the measured copy's rate; of 16 and 2 heads
+// of 256, 64 values of them rotated, 18.2 us, 61%: bound by issuing, 68% of the
+// slots.  Two or more pieces of work a CTA one after another cost 2 to 11% more.
 template <typename T, int LANES, int CH, int P, int U, int ROT, bool GATE>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 : 4) : 1)
     norm_kernel(const __grid_constant__ NormArgs g) {
