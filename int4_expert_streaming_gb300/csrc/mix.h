@@ -7,8 +7,8 @@
 namespace moe {
 
 // Rows up to which a sequence of the delta rule runs token by token.  32 heads of 128 x 128, token by token and in a
-// chunk: one run of 16 rows 11 and 20 us, of 32 rows 19 and 20; 16 runs of 16 rows 40 and 70 us, of 32 rows 73 and 70; 64
-// runs of 16 rows 168 and 275 us, of 32 rows 298 and 276.
+// chunk: one run of 24 rows 15.3 and 16.6 us, of 32 rows 19.3 and 16.7; 16 runs of 24 rows 58 and 63 us, of 32 rows 75 and 64;
+// 64 runs of 24 rows 223 and 234 us, of 32 rows 291 and 237.
 constexpr int kDeltaShort = 24;
 constexpr int kDeltaChunk = 64;
 

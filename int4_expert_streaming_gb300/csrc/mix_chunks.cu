@@ -31,8 +31,7 @@ constexpr int kC = kDeltaChunk;
 
 // Workspace, per chunk and k head: K16 and Q16, panels of 64 columns of 128 rows
 // (K's, then Q's).  Per chunk and v head: T high over P T [128 x 64], T rest
-// [64 x 64], and the factors.  At the end the sequences, longest first (up to
-// kSorted of them).  Rows are of 128 bytes with their 16-byte pieces
+// [64 x 64], and the factors.  At the end the sequences (Taken).  Rows are of 128 bytes with their 16-byte pieces
 // exchanged (piece p of row r at p ^ (r & 7)): read from shared memory without
 // conflicts.
 struct Factors {
@@ -50,7 +49,13 @@ constexpr int kPanel = 2 * kSquare;
 constexpr int kHeadTiles = 3 * kSquare;
 constexpr int kHeadBytes = (kHeadTiles + (int)sizeof(Factors) + 127) / 128 * 128;
 
-constexpr int kSorted = 1024;
+constexpr int kSorted = 512;
+// A sequence as chunks_kernel takes it, in one load: lists, slot and offsets one after another cost a CTA 1 us (64 prompts of
+// 64 tokens, 32 heads: 268 us instead of 252)
+struct alignas(16) Taken {
+    int lo, hi, slot;  // rows; slot -1: not taken
+    uint32_t piece;    // its first chunk's place; bit 31: it goes on from its slot
+};
 
 __host__ __device__ constexpr int padded_dim(int k_dim) { return k_dim <= 64 ? 64 : 128; }
 __host__ __device__ constexpr int pair_bytes(int KD) { return KD / 64 * kPanel; }
@@ -195,23 +200,31 @@ __device__ __forceinline__ void head_barrier(int b) {
         asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
-__host__ __device__ __forceinline__ int32_t* sorted_of(const DeltaArgs& a, int pair, int head) {
-    return reinterpret_cast<int32_t*>(a.ws + a.q_pieces * ((int64_t)a.c.k_heads * pair + (int64_t)a.c.v_heads * head));
+__device__ __forceinline__ Taken* taken_of(const DeltaArgs& a, int pair, int head) {
+    return reinterpret_cast<Taken*>(a.ws + a.q_pieces * ((int64_t)a.c.k_heads * pair + (int64_t)a.c.v_heads * head));
 }
-// The sequences, longest first: the long ones' CTAs then start first, and the
-// last to start are short (9001 rows in 24 sequences: 131 us, in their own order
-// 143).  Above kSorted sequences no one of them is long beside the whole.
-__device__ __forceinline__ void sort_sequences(const DeltaArgs& a, int* lens) {
-    const int n = a.q.n;
-    if (n == 1 || n > kSorted) return;
-    for (int i = threadIdx.x; i < n; i += kPrepare) lens[i] = (int)(a.q.start(i + 1) - a.q.start(i));
-    __syncthreads();
-    int32_t* sorted = sorted_of(a, pair_bytes(padded_dim(a.c.k_dim)), kHeadBytes);
-    for (int i = threadIdx.x; i < n; i += kPrepare) {
-        int before = 0;
-        for (int j = 0; j < n; ++j) before += lens[j] > lens[i] || (lens[j] == lens[i] && j < i);
-        sorted[before] = i;
+// The sequences first .. first + kPrepare - 1 to their places.  Longest first,
+// so that their CTAs start first and the last to start are short (9001 rows in 24
+// sequences: 120 us, in their own order 129).  Above kSorted sequences, where the
+// comparisons would take longer than a chunk, they stand in their own order: no one
+// of so many is long beside the whole.
+__device__ __forceinline__ void list_sequences(const DeltaArgs& a, int first, int* lens) {
+    const int n = a.q.n, s = first + threadIdx.x;
+    const bool sorted = n <= kSorted;
+    if (sorted) {
+        for (int i = threadIdx.x; i < n; i += kPrepare) lens[i] = (int)(a.q.start(i + 1) - a.q.start(i));
+        __syncthreads();
     }
+    if (s >= n) return;
+    const int64_t lo = a.q.start(s), len = a.q.start(s + 1) - lo;
+    int place = s;
+    if (sorted) {
+        place = 0;
+        for (int j = 0; j < n; ++j) place += lens[j] > lens[s] || (lens[j] == lens[s] && j < s);
+    }
+    const int slot = len > a.longer_than ? a.q.slot(s) : -1;
+    taken_of(a, pair_bytes(padded_dim(a.c.k_dim)), kHeadBytes)[place] =
+        {(int)lo, (int)(lo + len), slot, (uint32_t)a.q.piece_of<kC>(s) | (a.state && a.q.carry(s) ? 1u << 31 : 0u)};
 }
 
 // One chunk and two v heads of a k head: K16 and Q16, the factors, T and P T.
@@ -227,8 +240,8 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
     PrepareShared<KD>& m = *reinterpret_cast<PrepareShared<KD>*>(raw);
     after_previous();
     let_next_start();
-    if (blockIdx.x == a.q_pieces) {
-        if (blockIdx.y == 0) sort_sequences(a, reinterpret_cast<int*>(raw));
+    if (blockIdx.x >= a.q_pieces) {
+        if (blockIdx.y == 0) list_sequences(a, (int)(blockIdx.x - a.q_pieces) * kPrepare, reinterpret_cast<int*>(raw));
         return;
     }
     int c;
@@ -704,17 +717,19 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
     let_next_start();
     constexpr int kT = Shape::kTiles, kN = 2 * kT;
     const int dk = a.c.k_dim, dv = a.c.v_dim, Hk = a.c.k_heads, Hv = a.c.v_heads;
-    // blocks of columns, heads, and slowest the sequences, longest first
-    const int blocks = (dv + kCols - 1) / kCols, place = blockIdx.x / (blocks * Hv);
-    const int s = a.q.n > 1 && a.q.n <= kSorted ? sorted_of(a, pair_bytes(KD), kHeadBytes)[place] : place;
-    const int h = blockIdx.x / blocks % Hv, kh = h / (Hv / Hk);
-    const int64_t lo = a.q.start(s), hi = a.q.start(s + 1), len = hi - lo;
-    const int slot = a.q.slot(s);
-    if (len <= 0 || len <= a.longer_than || slot < 0) return;
+    // blocks of columns, heads, and slowest the sequences
+    const int blocks = (dv + kCols - 1) / kCols;
+    Taken taken;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(taken.lo), "=r"(taken.hi), "=r"(taken.slot), "=r"(taken.piece)
+                 : "l"(taken_of(a, pair_bytes(KD), kHeadBytes) + blockIdx.x / (blocks * Hv)) : "memory");
+    const int h = blockIdx.x / blocks % Hv, kh = h / (Hv / Hk), slot = taken.slot;
+    if (slot < 0) return;
+    const int64_t lo = taken.lo, hi = taken.hi, len = hi - lo;
     const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) % (2 * kPairs), p = warp >> 1, q = warp & 1;
     const int first = (blockIdx.x % blocks) * kCols;  // column of V
     const int chunks = (int)((len + kC - 1) / kC);
-    const int64_t piece = a.q.piece_of<kC>(s);
+    const int64_t piece = taken.piece & 0x7fffffffu;
     const uint32_t base = smem_at(raw);
     constexpr int kHands = 2 * kPairs * Shape::kHand;  // from one time's to the next
     const uint32_t hands = base + Shape::kOffHands + lane * 16;
@@ -874,8 +889,8 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
     const int d0 = first + 16 * p + r0, k0 = q * (KD / 2) + c0;
     float S[kN][4];
     int unit = kOne;
+    const bool carry = taken.piece >> 31;
     float* state = a.state ? a.state + ((int64_t)slot * Hv + h) * dv * dk : nullptr;
-    const bool carry = state && a.q.carry(s);
 #pragma unroll
     for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -1094,12 +1109,12 @@ cudaError_t launch_chunked(const DeltaArgs& a, cudaStream_t st) {
     const int twos = (a.c.v_heads / a.c.k_heads + 1) / 2;
     constexpr int kShared = (int)sizeof(PrepareShared<KD>);
     if (cudaError_t e = cudaFuncSetAttribute(prepare_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared)) return e;
-    if (cudaError_t e = launch(prepare_kernel<KD>, dim3((unsigned)a.q_pieces + 1, (unsigned)(a.c.k_heads * twos)), kPrepare, kShared,
+    if (cudaError_t e = launch(prepare_kernel<KD>, dim3((unsigned)(a.q_pieces + (a.q.n + kPrepare - 1) / kPrepare), (unsigned)(a.c.k_heads * twos)), kPrepare, kShared,
                                st, 1, a))
         return e;
     // Four pairs take 1.8 times as long for a chunk as two, so they pay where the CTAs of two would be more than the SMs
-    // (and are twos): 64 prompts of 64 tokens, 32 heads of 128: 277 us, two pairs 318; 16 of 256: 178 and 196; 2 of 2048:
-    // 164 and 175; one of 4096, 128 CTAs of two pairs: 267 and 177.
+    // (and are twos): 64 prompts of 64 tokens, 32 heads of 128: 252 us, two pairs 291; 16 of 256: 166 and 182; 2 of 2048:
+    // 154 and 167; one of 4096, 128 CTAs of two pairs: 252 and 166.
     const int64_t columns = (a.c.v_dim + 31) / 32, ctas = a.q.n * a.c.v_heads * columns;
     return ctas > 152 && columns % 2 == 0 ? launch_chunks<KD, 4>(a, st) : launch_chunks<KD, 2>(a, st);
 }
@@ -1109,7 +1124,7 @@ cudaError_t launch_chunked(const DeltaArgs& a, cudaStream_t st) {
 size_t delta_workspace(const moe_delta_config& c, int64_t T, int n) {
     return (size_t)(T / kC + n) *
                ((size_t)c.k_heads * pair_bytes(padded_dim(c.k_dim)) + (size_t)c.v_heads * kHeadBytes) +
-           kSorted * sizeof(int32_t);
+           (size_t)n * sizeof(Taken);
 }
 
 cudaError_t launch_delta_chunks(const DeltaArgs& a, cudaStream_t st) {
