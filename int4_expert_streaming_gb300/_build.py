@@ -3,12 +3,14 @@
 Each translation unit compiles in parallel into _build/, then one nvcc link
 produces int4_expert_streaming_gb300/libmoe.so (static CUDA runtime).  gcc
 builds _call.so beside it, the Python module that marshals the arguments of
-the operators without a context (csrc/binding.c, linked against libmoe.so).
+the operators without a context (csrc/binding.c, linked against libmoe.so, and
+csrc/tensor.cc, which reads torch's tensors and is compiled with its headers).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -21,6 +23,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 CALL = os.path.join(PKG, "_call.so")
 BINDING = os.path.join(CSRC, "binding.c")
+TENSOR = os.path.join(CSRC, "tensor.cc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,8 +38,15 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
+def _torch() -> str:
+    spec = importlib.util.find_spec("torch")  # without importing it
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch not found: its headers are required to build _call.so")
+    return os.path.dirname(spec.origin)
+
+
 def _deps():
-    return sources() + [BINDING] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "moe.h"),
+    return sources() + [BINDING, TENSOR, os.path.join(_torch(), "version.py")] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "moe.h"),
                                                                os.path.abspath(__file__)]
 
 
@@ -66,6 +76,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj, (r.stdout + r.stderr)
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        tensor = ex.submit(_compile_tensor)
         results = list(ex.map(compile_one, sources()))
     if verbose:
         for _, log in results:
@@ -77,15 +88,27 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_binding()
+    _build_binding(tensor.result())
     return LIB
 
 
-def _build_binding() -> None:
+def _compile_tensor() -> str:
+    obj = os.path.join(BUILD, "tensor.cc.o")
+    inc = os.path.join(_torch(), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", TENSOR, "-o", obj, "-I" + sysconfig.get_paths()["include"], "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on tensor.cc:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _build_binding(tensor: str) -> None:
     tmp = CALL + f".tmp{os.getpid()}"
     cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
-           "-I" + os.path.join(ROOT, "include"), BINDING, "-o", tmp, "-L" + PKG, "-l:" + os.path.basename(LIB),
-           "-Wl,-rpath,$ORIGIN"]
+           "-I" + os.path.join(ROOT, "include"), BINDING, tensor, "-o", tmp, "-L" + PKG, "-l:" + os.path.basename(LIB),
+           "-L" + os.path.join(_torch(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lstdc++",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + os.path.join(_torch(), "lib")]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}")

@@ -5,8 +5,8 @@
  * the same checks in Python with ctypes took 2.5 to 4 us a call beside the
  * launch, here well under one.
  *
- * Tensors are read through their Python attributes only, so this depends on
- * neither PyTorch's headers nor its version.  A function returns the C call's
+ * A torch tensor is read by tensor.cc; any other object that has a tensor's
+ * attributes through those.  A function returns the C call's
  * status; those with names raise what it stands for, and are the package's
  * functions themselves (a Python function around them would cost a tenth of a
  * small call).  A tensor that does not fit raises ValueError.
@@ -15,6 +15,7 @@
 #include <Python.h>
 
 #include "moe.h"
+#include "tensor.h"
 
 int moe_binding_device(void); /* the current device, -1 where there is none; not part of the C interface */
 
@@ -39,12 +40,6 @@ static int bad(PyObject* t, const char* what, const char* expected) {
     return -1;
 }
 
-static int has_type(PyObject* t, PyObject* type) {
-    PyObject* d = PyObject_GetAttr(t, s_dtype);
-    const int yes = d == type;
-    Py_XDECREF(d);
-    return yes;
-}
 /* the method's result as a whole number; -1 and an exception set if there is none */
 static long long number(PyObject* t, PyObject* method) {
     PyObject* v = PyObject_CallMethodNoArgs(t, method);
@@ -53,11 +48,31 @@ static long long number(PyObject* t, PyObject* method) {
     Py_DECREF(v);
     return n;
 }
-static int address(PyObject* t, void** out) {
-    PyObject* v = PyObject_CallMethodNoArgs(t, s_data_ptr);
-    if (!v) return -1;
-    *out = PyLong_AsVoidPtr(v);
-    Py_DECREF(v);
+/* a tuple's first MOE_TENSOR_DIMS numbers; its length, or -1 */
+static int numbers(PyObject* tuple, int64_t* out) {
+    const int n = tuple && PyTuple_Check(tuple) ? (int)PyTuple_GET_SIZE(tuple) : -1;
+    for (int i = 0; i < n && i < MOE_TENSOR_DIMS; ++i) out[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(tuple, i));
+    Py_XDECREF(tuple);
+    return PyErr_Occurred() ? -1 : n;
+}
+/* a tensor, or what has its attributes; -1 (an exception may be set) if that lacks one */
+static int look(PyObject* t, moe_tensor* v) {
+    if (moe_tensor_of(t, v)) return 0;
+    PyObject* d = PyObject_GetAttr(t, s_dtype);
+    Py_XDECREF(d);
+    if (!d) return -1;
+    v->type = d == t_f32 ? MOE_TENSOR_F32 : d == t_bf16 ? MOE_TENSOR_BF16 : d == t_i32 ? MOE_TENSOR_I32 : d == t_u8 ? MOE_TENSOR_U8 : MOE_TENSOR_OTHER;
+    v->device = (int)number(t, s_get_device);
+    if (PyErr_Occurred()) return -1;
+    v->dims = numbers(PyObject_GetAttr(t, s_shape), v->shape);
+    if (PyErr_Occurred() || v->dims != numbers(PyObject_CallMethodNoArgs(t, s_stride), v->stride)) return -1;
+    PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+    v->contiguous = c == Py_True;
+    Py_XDECREF(c);
+    v->numel = c ? number(t, s_numel) : -1;
+    PyObject* p = PyErr_Occurred() ? NULL : PyObject_CallMethodNoArgs(t, s_data_ptr);
+    v->p = p ? PyLong_AsVoidPtr(p) : NULL;
+    Py_XDECREF(p);
     return PyErr_Occurred() ? -1 : 0;
 }
 
@@ -73,27 +88,34 @@ static int same_device(long long d, const char* what, int* dev) {
     return -1;
 }
 /* 0: a CUDA tensor of that device; -1 and an exception if not */
-static int on_device(PyObject* t, const char* what, const char* expected, int* dev) {
-    const long long d = number(t, s_get_device); /* -1 for a tensor of the host */
-    return d < 0 ? bad(t, what, expected) : same_device(d, what, dev);
+static int on_device(PyObject* t, const moe_tensor* v, const char* what, const char* expected, int* dev) {
+    return v->device < 0 ? bad(t, what, expected) : same_device(v->device, what, dev);
 }
 
 /* contiguous CUDA tensor of at least n elements of the type; None gives NULL */
-static int flat(PyObject* t, PyObject* type, long long n, const char* what, const char* expected, int* dev, void** out) {
+static int flat(PyObject* t, int type, long long n, const char* what, const char* expected, int* dev, void** out) {
+    moe_tensor v;
     *out = NULL;
     if (t == Py_None) return 0;
-    if (on_device(t, what, expected, dev)) return -1;
-    PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
-    const int contiguous = c == Py_True;
-    Py_XDECREF(c);
-    if (!contiguous || !has_type(t, type) || number(t, s_numel) < n) return bad(t, what, expected);
-    return address(t, out);
+    if (look(t, &v)) return bad(t, what, expected);
+    if (on_device(t, &v, what, expected, dev)) return -1;
+    if (!v.contiguous || v.type != type || v.numel < n) return bad(t, what, expected);
+    *out = v.p;
+    return 0;
 }
 static int flat_i32(PyObject* t, long long n, const char* what, int* dev, void** out) {
-    return flat(t, t_i32, n, what, "a contiguous int32 CUDA tensor that is long enough", dev, out);
+    return flat(t, MOE_TENSOR_I32, n, what, "a contiguous int32 CUDA tensor that is long enough", dev, out);
 }
 static int flat_f32(PyObject* t, long long n, const char* what, int* dev, void** out) {
-    return flat(t, t_f32, n, what, "a contiguous float32 CUDA tensor that is long enough", dev, out);
+    return flat(t, MOE_TENSOR_F32, n, what, "a contiguous float32 CUDA tensor that is long enough", dev, out);
+}
+
+/* a uint8 tensor's bytes; None has none */
+static int room(PyObject* t, int* dev, void** p, long long* bytes) {
+    moe_tensor v;
+    if (flat(t, MOE_TENSOR_U8, 0, "workspace", "a contiguous uint8 CUDA tensor", dev, p)) return -1;
+    *bytes = t == Py_None || look(t, &v) ? 0 : v.numel;
+    return PyErr_Occurred() ? -1 : 0;
 }
 
 typedef struct {
@@ -105,26 +127,15 @@ typedef struct {
 /* 2D CUDA tensor of fp32 or bf16 with contiguous rows */
 static int matrix(PyObject* t, const char* what, int* dev, matrix_t* m) {
     static const char* expected = "a 2D CUDA tensor of float32 or bfloat16 with contiguous rows";
-    PyObject *d = PyObject_GetAttr(t, s_dtype), *shape = NULL, *stride = NULL;
-    int rc = -1;
-    const int ok = d == t_f32 || d == t_bf16;
-    m->type = d == t_f32 ? MOE_F32 : MOE_BF16;
-    Py_XDECREF(d);
-    if (!ok) return bad(t, what, expected);
-    if (on_device(t, what, expected, dev)) return -1;
-    shape = PyObject_GetAttr(t, s_shape);
-    if (shape) stride = PyObject_CallMethodNoArgs(t, s_stride);
-    if (shape && stride && PyTuple_Check(shape) && PyTuple_Check(stride) && PyTuple_GET_SIZE(shape) == 2 &&
-        PyTuple_GET_SIZE(stride) == 2) {
-        m->rows = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
-        m->cols = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 1));
-        m->ld = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 0));
-        if (m->rows <= 1) m->ld = m->cols; /* one row's stride means nothing */
-        if (m->cols <= 1 || PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 1)) == 1) rc = address(t, &m->p);
-    }
-    Py_XDECREF(shape);
-    Py_XDECREF(stride);
-    return rc ? bad(t, what, expected) : 0;
+    moe_tensor v;
+    if (look(t, &v) || (v.type != MOE_TENSOR_F32 && v.type != MOE_TENSOR_BF16)) return bad(t, what, expected);
+    if (on_device(t, &v, what, expected, dev)) return -1;
+    if (v.dims != 2 || (v.shape[1] > 1 && v.stride[1] != 1)) return bad(t, what, expected);
+    m->p = v.p;
+    m->type = v.type == MOE_TENSOR_F32 ? MOE_F32 : MOE_BF16;
+    m->rows = v.shape[0], m->cols = v.shape[1];
+    m->ld = m->rows <= 1 ? m->cols : v.stride[0]; /* one row's stride means nothing */
+    return 0;
 }
 
 typedef struct {
@@ -136,44 +147,25 @@ typedef struct {
 /* 3D CUDA tensor [tokens, heads, values] of fp32 or bf16, its values contiguous */
 static int heads_of(PyObject* t, const char* what, int* dev, heads_t* m) {
     static const char* expected = "a 3D CUDA tensor of float32 or bfloat16 with contiguous heads";
-    PyObject *d = PyObject_GetAttr(t, s_dtype), *shape = NULL, *stride = NULL;
-    int rc = -1;
-    const int ok = d == t_f32 || d == t_bf16;
-    m->type = d == t_f32 ? MOE_F32 : MOE_BF16;
-    Py_XDECREF(d);
-    if (!ok) return bad(t, what, expected);
-    if (on_device(t, what, expected, dev)) return -1;
-    shape = PyObject_GetAttr(t, s_shape);
-    if (shape) stride = PyObject_CallMethodNoArgs(t, s_stride);
-    if (shape && stride && PyTuple_Check(shape) && PyTuple_Check(stride) && PyTuple_GET_SIZE(shape) == 3 &&
-        PyTuple_GET_SIZE(stride) == 3) {
-        m->n = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
-        m->heads = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 1));
-        m->dim = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 2));
-        m->ld = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 0));
-        m->head = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 1));
-        if (m->heads <= 1) m->head = m->dim; /* one head's or token's stride means nothing */
-        if (m->n <= 1) m->ld = m->heads * m->dim;
-        if (m->heads <= INT32_MAX && m->dim <= INT32_MAX &&
-            (m->dim <= 1 || PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 2)) == 1))
-            rc = address(t, &m->p);
-    }
-    Py_XDECREF(shape);
-    Py_XDECREF(stride);
-    return rc ? bad(t, what, expected) : 0;
+    moe_tensor v;
+    if (look(t, &v) || (v.type != MOE_TENSOR_F32 && v.type != MOE_TENSOR_BF16)) return bad(t, what, expected);
+    if (on_device(t, &v, what, expected, dev)) return -1;
+    if (v.dims != 3 || v.shape[1] > INT32_MAX || v.shape[2] > INT32_MAX || (v.shape[2] > 1 && v.stride[2] != 1))
+        return bad(t, what, expected);
+    m->p = v.p;
+    m->type = v.type == MOE_TENSOR_F32 ? MOE_F32 : MOE_BF16;
+    m->n = v.shape[0], m->heads = v.shape[1], m->dim = v.shape[2];
+    m->head = m->heads <= 1 ? m->dim : v.stride[1]; /* one head's or token's stride means nothing */
+    m->ld = m->n <= 1 ? m->heads * m->dim : v.stride[0];
+    return 0;
 }
 
 /* rows and columns of a 2D tensor */
 static int sides(PyObject* t, const char* what, int64_t* rows, int64_t* cols) {
-    PyObject* shape = PyObject_GetAttr(t, s_shape);
-    int rc = -1;
-    if (shape && PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == 2) {
-        *rows = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
-        *cols = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 1));
-        rc = 0;
-    }
-    Py_XDECREF(shape);
-    return rc ? bad(t, what, "a 2D tensor") : 0;
+    moe_tensor v;
+    if (look(t, &v) || v.dims != 2) return bad(t, what, "a 2D tensor");
+    *rows = v.shape[0], *cols = v.shape[1];
+    return 0;
 }
 
 /* None, a raw cudaStream_t, or an object with one as cuda_stream */
@@ -310,9 +302,8 @@ static PyObject* dispatch(ARGS) {
     if (flat_i32(v[0], T * k, "idx", &dev, &idx) || flat_i32(v[2], E + 1, "offsets", &dev, &off) ||
         flat_i32(v[3], T * k, "row_of_pair", &dev, &rop) || flat_i32(v[4], T * k, "token_of_row", &dev, &tor) ||
         flat_i32(v[5], T * k, "group_of_row", &dev, &gor) ||
-        flat(v[6], t_u8, 0, "workspace", "a contiguous uint8 CUDA tensor", &dev, &ws) || stream_of(v[7], &st))
+        room(v[6], &dev, &ws, &bytes) || stream_of(v[7], &st))
         return NULL;
-    if (v[6] != Py_None && (bytes = number(v[6], s_numel)) < 0) return NULL;
     STATUS(moe_dispatch(idx, T, (int32_t)k, (int32_t)E, off, rop, tor, gor, ws, (size_t)bytes, st));
 }
 
@@ -407,15 +398,10 @@ static int batch(PyObject* o, moe_seqs* out, const moe_seqs** p, int* dev) {
 
 /* the tensor's extent along its first dimension; -1 and an exception if it has none */
 static long long first_extent(PyObject* t, const char* what) {
-    long long n = -1;
-    PyObject* shape = PyObject_GetAttr(t, s_shape);
-    if (shape && PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) >= 1)
-        n = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
-    Py_XDECREF(shape);
-    if (n < 0) bad(t, what, "a tensor with slots along its first dimension");
-    return n;
+    moe_tensor v;
+    if (!look(t, &v) && v.dims >= 1) return v.shape[0];
+    return bad(t, what, "a tensor with slots along its first dimension");
 }
-
 /* the address of a state without slots, which is never read or written */
 static _Alignas(16) char no_slots[16];
 
@@ -447,7 +433,7 @@ static PyObject* conv(KWARGS) {
     if (v[6] != Py_None) {
         static const char* expected = "a contiguous CUDA tensor [slots, width - 1, channels] of x's type";
         if ((slots = first_extent(v[6], "state")) < 0) return NULL;
-        if (flat(v[6], x.type == MOE_F32 ? t_f32 : t_bf16, slots * (w.cols - 1) * x.cols, "state", expected, &dev, &state))
+        if (flat(v[6], x.type == MOE_F32 ? MOE_TENSOR_F32 : MOE_TENSOR_BF16, slots * (w.cols - 1) * x.cols, "state", expected, &dev, &state))
             return NULL;
         if (!slots) state = no_slots; /* which torch gives no address: every sequence is left out */
     }
@@ -546,13 +532,12 @@ static PyObject* delta(KWARGS) {
         batch(v[8], &b, &bp, &dev) || stream_of(v[10], &st))
         return NULL;
     CHECK(g && beta, "g and beta are required");
-    if (v[9] != Py_None && moe_delta_workspace(&c, val.n, bp ? bp->n : 1, bp ? bp->offsets_dev ? bp->max_len : 1 : 0)) {
-        if (flat(v[9], t_u8, 0, "workspace", "a contiguous uint8 CUDA tensor", &dev, &ws) || (bytes = number(v[9], s_numel)) < 0)
-            return NULL;
-    }
+    if (v[9] != Py_None && moe_delta_workspace(&c, val.n, bp ? bp->n : 1, bp ? bp->offsets_dev ? bp->max_len : 1 : 0) &&
+        room(v[9], &dev, &ws, &bytes))
+        return NULL;
     if (v[5] != Py_None) {
         if ((slots = first_extent(v[5], "state")) < 0) return NULL;
-        if (flat(v[5], t_f32, slots * val.heads * val.dim * q.dim, "state",
+        if (flat(v[5], MOE_TENSOR_F32, slots * val.heads * val.dim * q.dim, "state",
                  "a contiguous float32 CUDA tensor [slots, v_heads, v_dim, k_dim]", &dev, &state))
             return NULL;
         if (!slots) state = no_slots;
