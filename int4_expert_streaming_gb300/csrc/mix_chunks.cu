@@ -239,7 +239,6 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
     extern __shared__ __align__(128) uint8_t raw[];
     PrepareShared<KD>& m = *reinterpret_cast<PrepareShared<KD>*>(raw);
     after_previous();
-    let_next_start();
     if (blockIdx.x >= a.q_pieces) {
         if (blockIdx.y == 0) list_sequences(a, (int)(blockIdx.x - a.q_pieces) * kPrepare, reinterpret_cast<int*>(raw));
         return;
@@ -584,6 +583,7 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
         }
         if ((tid & 127) == 0) f.t = down(e), f.most_l = __uint_as_float(m.most[b]) * m.left[b];
         head_barrier(b);
+        let_next_start();  // not earlier: one prompt of 4096 164 us, at the kernel's start 166
         // P T, rows 16 warp .. +15; it goes into o only, so one fp16 of each will do
         const uint32_t t_at = smem_at(T16);
         float acc[8][4];
@@ -714,7 +714,6 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
     __shared__ float2 units[2][2 * kPairs];                  // of S and of X
     __shared__ float2 found[2 * kPairs];                     // by a warp for the other of its pair: largest of S and of V
     after_previous();
-    let_next_start();
     constexpr int kT = Shape::kTiles, kN = 2 * kT;
     const int dk = a.c.k_dim, dv = a.c.v_dim, Hk = a.c.k_heads, Hv = a.c.v_heads;
     // blocks of columns, heads, and slowest the sequences
@@ -1079,6 +1078,7 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
         times_k_turned(L[1], group[3]);
     }
     __syncthreads();  // for the last chunk's o
+    let_next_start();  // not earlier: 8 prompts of 512 with 8 heads 45 us, at the kernel's start 49 (64 of 64 with 32: 256 and 252)
     if (state) {
 #pragma unroll
         for (int n = 0; n < kN; ++n)

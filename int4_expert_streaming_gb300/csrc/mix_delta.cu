@@ -16,7 +16,7 @@ constexpr unsigned kAll = 0xffffffffu;
 // and four rows share what is unpacked of k and q.  64 sequences, 32 heads,
 // 128 x 128: one token each (256 MB of states) 42.7 us, 89% of the measured
 // copy's rate; with two rows a thread 43.7, with sixteen threads a row 50.7;
-// four tokens for each of 16 sequences 19.0, 21.7 and 24.5 us.
+// four tokens for each of 16 sequences 18.6, 21.7 and 24.5 us.
 constexpr int kLanes = 8, kRows = 4;
 constexpr int kStepRows = 128 / kLanes * kRows;  // rows of S of a CTA
 
@@ -47,7 +47,6 @@ __device__ __forceinline__ void packed(uint32_t (&w)[N], const __nv_bfloat16* p,
 template <int KD>
 __global__ void __launch_bounds__(128) steps_kernel(const __grid_constant__ DeltaArgs a) {
     after_previous();
-    let_next_start();
     constexpr int kE = KD / kLanes;
     const int dk = a.c.k_dim, dv = a.c.v_dim, Hv = a.c.v_heads;
     const int blocks = (dv + kStepRows - 1) / kStepRows;
@@ -163,6 +162,7 @@ __global__ void __launch_bounds__(128) steps_kernel(const __grid_constant__ Delt
         if (lane < kRows && in_v) *o = __float2bfloat16_rn(mine);
         o += a.o_ld;
     }
+    let_next_start();  // not earlier: 16 runs of 4 18.6 us, at the kernel's start 19.2; one token 3.3 and 3.5
     if (state && in_v) {
 #pragma unroll
         for (int p = 0; p < kRows; ++p)
