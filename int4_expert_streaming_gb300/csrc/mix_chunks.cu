@@ -232,7 +232,7 @@ __device__ __forceinline__ void list_sequences(const DeltaArgs& a, int first, in
 // a lane a column; then T_10 and T_32, and of those the lower left quarter, by
 //   (T_11 0; T_21 T_22) with T_21 = -T_22 A_21 T_11.
 // Two heads a CTA, since they share K and Q; three CTAs an SM.  4096 tokens, 16
-// and 32 heads of 128: 49 us of the call's 167, with 51% of the issue slots and
+// and 32 heads of 128: 48 us of the call's 164, with 51% of the issue slots and
 // 66% of shared memory's rate in use and a tenth of the time in barriers.
 template <int KD>
 __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_constant__ DeltaArgs a) {
