@@ -259,3 +259,27 @@ def test_definition_of_the_delta_rule():
     ora.delta(k, k, v, np.zeros((4, 1)), np.ones((4, 1)), state, o, 1.0, ora.sequences(4, [0, 4], None, [0]))
     assert np.allclose(o, v)
     assert np.allclose(state[0, 0], np.stack([v[3, 0], v[1, 0], v[2, 0], np.zeros(3)], 1))
+
+
+def test_torch_tensors_that_do_not_fit_are_refused():
+    """Real tensors (the stand-ins above go another way): of the host, without memory, without strides, of other types."""
+    torch = pytest.importorskip("torch")
+    w, y = torch.zeros(8, 4), torch.zeros(2, 8)
+    host = torch.zeros(2, 8)
+    for x in (host, torch.nn.Parameter(host), host.bfloat16(), host.to("meta"), host.double(), host[0], host.reshape(2, 2, 2, 2)):
+        with pytest.raises(ValueError, match="x: expected a 2D CUDA tensor"):
+            moe.moe_conv(x, w, y)
+    with pytest.raises((ValueError, RuntimeError)):
+        moe.moe_conv(host.to_sparse(), w, y)
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode() as mode:
+        fake = mode.from_tensor(host)
+    with pytest.raises((ValueError, RuntimeError)):
+        moe.moe_conv(fake, w, y)
+    for junk in (None, 3, "x", [[1.0]], np.zeros((2, 8), np.float32)):
+        with pytest.raises(ValueError, match="x: expected a 2D CUDA tensor"):
+            moe.moe_conv(junk, w, y)
+    with pytest.raises(ValueError, match="q: expected a 3D CUDA tensor"):
+        moe.moe_delta(host, host, host, host, host, None, host)
+    with pytest.raises(ValueError, match="x: expected a 3D CUDA tensor"):
+        moe.moe_head_norm(moe.make_head_norm_config(), host[None], host[None])
