@@ -5,6 +5,7 @@ produces int4_expert_streaming_gb300/libmoe.so (static CUDA runtime).  gcc
 builds _call.so beside it, the Python module that marshals the arguments of
 the operators without a context (csrc/binding.c, linked against libmoe.so, and
 csrc/tensor.cc, which reads torch's tensors and is compiled with its headers).
+Where torch is not installed that module is left out; libmoe.so needs none.
 """
 from __future__ import annotations
 
@@ -38,30 +39,45 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
-def _torch() -> str:
-    spec = importlib.util.find_spec("torch")  # without importing it
-    if spec is None or not spec.origin:
-        raise RuntimeError("torch not found: its headers are required to build _call.so")
-    return os.path.dirname(spec.origin)
+def _torch() -> str | None:
+    """torch's folder, found without importing it; None where it is not installed."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
-def _deps():
-    return sources() + [BINDING, TENSOR, os.path.join(_torch(), "version.py")] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(ROOT, "include", "moe.h"),
-                                                               os.path.abspath(__file__)]
+def _current(made, *deps) -> bool:
+    deps += (os.path.join(ROOT, "include", "moe.h"), os.path.abspath(__file__))
+    return os.path.exists(made) and all(os.path.getmtime(p) <= os.path.getmtime(made) for p in deps)
+
+
+def _lib_current() -> bool:
+    return _current(LIB, *sources(), *glob.glob(os.path.join(CSRC, "*.h")), *glob.glob(os.path.join(CSRC, "*.cuh")))
+
+
+def _binding_current(torch: str) -> bool:
+    return _current(CALL, BINDING, TENSOR, os.path.join(CSRC, "tensor.h"), os.path.join(torch, "version.py"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    torch = _torch()
+    return _lib_current() and (torch is None or _binding_current(torch))
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
-        return LIB
-    nvcc = _nvcc()
+    torch = _torch()
+    lib, binding = force or not _lib_current(), torch is not None and (force or not _binding_current(torch))
     os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        tensor = ex.submit(_compile_tensor, torch) if binding else None
+        if lib:
+            _build_lib(ex, verbose, extra_flags)
+        if binding:
+            _build_binding(tensor.result(), torch)
+    return LIB
+
+
+def _build_lib(ex, verbose: bool, extra_flags) -> None:
+    nvcc = _nvcc()
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-Wall",
                      "-I" + os.path.join(ROOT, "include")] + list(extra_flags)
 
@@ -75,9 +91,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
         return obj, (r.stdout + r.stderr)
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        tensor = ex.submit(_compile_tensor)
-        results = list(ex.map(compile_one, sources()))
+    results = list(ex.map(compile_one, sources()))
     if verbose:
         for _, log in results:
             if log.strip():
@@ -88,13 +102,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_binding(tensor.result())
-    return LIB
 
 
-def _compile_tensor() -> str:
+def _compile_tensor(torch: str) -> str:
     obj = os.path.join(BUILD, "tensor.cc.o")
-    inc = os.path.join(_torch(), "include")
+    inc = os.path.join(torch, "include")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", TENSOR, "-o", obj, "-I" + sysconfig.get_paths()["include"], "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include")]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -103,12 +115,11 @@ def _compile_tensor() -> str:
     return obj
 
 
-def _build_binding(tensor: str) -> None:
-    tmp = CALL + f".tmp{os.getpid()}"
+def _build_binding(tensor: str, torch: str) -> None:
+    tmp, libs = CALL + f".tmp{os.getpid()}", os.path.join(torch, "lib")
     cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
            "-I" + os.path.join(ROOT, "include"), BINDING, tensor, "-o", tmp, "-L" + PKG, "-l:" + os.path.basename(LIB),
-           "-L" + os.path.join(_torch(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lstdc++",
-           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + os.path.join(_torch(), "lib")]
+           "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lstdc++", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}")
