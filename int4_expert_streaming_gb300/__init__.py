@@ -393,7 +393,12 @@ def _binding():
         load_library()
         import torch
 
+        from . import _build
+
         mod = importlib.import_module("._call", __name__)  # built beside libmoe.so
+        if mod.built_for() != _build.built_for(torch.__version__):
+            raise RuntimeError(f"_call.so was built for {mod.built_for()}, not for {_build.built_for(torch.__version__)}: "
+                               "build it again with int4_expert_streaming_gb300.build()")
         mod.dtypes(torch.float32, torch.bfloat16, torch.int32, torch.uint8)
         mod.on_failure(_check)
         _ops = mod

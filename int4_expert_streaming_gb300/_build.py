@@ -13,6 +13,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -25,6 +26,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 CALL = os.path.join(PKG, "_call.so")
 BINDING = os.path.join(CSRC, "binding.c")
 TENSOR = os.path.join(CSRC, "tensor.cc")
+STAMP = os.path.join(BUILD, "binding.txt")  # what _call.so was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,6 +47,23 @@ def _torch() -> str | None:
     return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
+def built_for(torch_version: str) -> str:
+    """What _call.so is tied to: it reads torch's tensors and Python's objects where these versions have their parts."""
+    return f"torch {torch_version}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _built_for(torch: str) -> str:
+    with open(os.path.join(torch, "version.py")) as f:
+        version = re.search(r"^__version__ = ['\"](.*)['\"]", f.read(), re.M)
+    if version is None:
+        raise RuntimeError(f"{f.name} does not say torch's version")
+    return built_for(version[1])
+
+
+def _stamp(torch: str) -> str:
+    return f"{_built_for(torch)}, {torch}\n"  # and where it looks for torch's libraries
+
+
 def _current(made, *deps) -> bool:
     deps += (os.path.join(ROOT, "include", "moe.h"), os.path.abspath(__file__))
     return os.path.exists(made) and all(os.path.getmtime(p) <= os.path.getmtime(made) for p in deps)
@@ -55,7 +74,10 @@ def _lib_current() -> bool:
 
 
 def _binding_current(torch: str) -> bool:
-    return _current(CALL, BINDING, TENSOR, os.path.join(CSRC, "tensor.h"), os.path.join(torch, "version.py"))
+    if not os.path.exists(STAMP) or not _current(CALL, BINDING, TENSOR, os.path.join(CSRC, "tensor.h")):
+        return False
+    with open(STAMP) as f:
+        return f.read() == _stamp(torch)
 
 
 def up_to_date() -> bool:
@@ -107,8 +129,8 @@ def _build_lib(ex, verbose: bool, extra_flags) -> None:
 def _compile_tensor(torch: str) -> str:
     obj = os.path.join(BUILD, "tensor.cc.o")
     inc = os.path.join(torch, "include")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", TENSOR, "-o", obj, "-I" + sysconfig.get_paths()["include"], "-isystem", inc,
-           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", TENSOR, "-o", obj, "-I" + sysconfig.get_paths()["include"],
+           f'-DMOE_BUILT_FOR="{_built_for(torch)}"', "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include")]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on tensor.cc:\n{r.stdout}\n{r.stderr}")
@@ -124,6 +146,9 @@ def _build_binding(tensor: str, torch: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALL)
+    with open(tmp, "w") as f:
+        f.write(_stamp(torch))
+    os.replace(tmp, STAMP)
 
 
 if __name__ == "__main__":

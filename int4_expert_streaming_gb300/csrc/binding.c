@@ -555,6 +555,12 @@ static PyObject* on_failure(ARGS) {
     Py_RETURN_NONE;
 }
 
+/* the torch and Python that the module was compiled for */
+static PyObject* built_for(PyObject* self, PyObject* none) {
+    (void)self, (void)none;
+    return PyUnicode_FromString(moe_tensor_built_for());
+}
+
 /* the torch dtypes float32, bfloat16, int32, uint8 */
 static PyObject* dtypes(ARGS) {
     (void)self;
@@ -571,7 +577,7 @@ static PyObject* dtypes(ARGS) {
 #define KWFN(name) {"moe_" #name, (PyCFunction)(void (*)(void))name, METH_FASTCALL | METH_KEYWORDS, name##_doc}
 static PyMethodDef methods[] = {FN(route),   FN(dispatch), FN(quantise), FN(dequantise),
                                 FN(product), FN(combine),  FN(dtypes),   FN(on_failure),
-                                KWFN(conv),  KWFN(head_norm), KWFN(delta), {NULL, NULL, 0, NULL}};
+                                KWFN(conv),  KWFN(head_norm), KWFN(delta), {"built_for", built_for, METH_NOARGS, NULL}, {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__call(void) {

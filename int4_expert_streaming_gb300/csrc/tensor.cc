@@ -6,6 +6,9 @@
 
 #include "tensor.h"
 
+// The torch and Python whose headers this was compiled with: the parts of a tensor stand where these say.
+extern "C" const char* moe_tensor_built_for(void) { return MOE_BUILT_FOR; }
+
 // 1: filled.  0: not a torch tensor, or one without plain strides or memory of its own.
 extern "C" int moe_tensor_of(PyObject* o, moe_tensor* v) {
     try {

@@ -16,8 +16,12 @@ typedef struct {
 } moe_tensor;
 
 #ifdef __cplusplus
-extern "C"
+extern "C" {
 #endif
 int moe_tensor_of(PyObject* o, moe_tensor* v);
+const char* moe_tensor_built_for(void);
+#ifdef __cplusplus
+}
+#endif
 
 #endif
