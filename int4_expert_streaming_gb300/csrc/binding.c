@@ -396,11 +396,19 @@ static int batch(PyObject* o, moe_seqs* out, const moe_seqs** p, int* dev) {
     return d < 0 ? 0 : same_device(d, "seqs", dev);
 }
 
-/* the tensor's extent along its first dimension; -1 and an exception if it has none */
-static long long first_extent(PyObject* t, const char* what) {
+/*
+ * A state [slots, d[0], .., d[n - 1]] of the type, contiguous: its slots, and -1 and an exception if it is another tensor.
+ * Every extent is looked at: one with its dimensions exchanged has as many values.
+ */
+static long long state_of(PyObject* t, int type, int n, const int64_t* d, const char* expected, int* dev, void** out) {
     moe_tensor v;
-    if (!look(t, &v) && v.dims >= 1) return v.shape[0];
-    return bad(t, what, "a tensor with slots along its first dimension");
+    if (look(t, &v)) return bad(t, "state", expected);
+    if (on_device(t, &v, "state", expected, dev)) return -1;
+    if (v.dims != n + 1 || v.type != type || !v.contiguous) return bad(t, "state", expected);
+    for (int i = 0; i < n; ++i)
+        if (v.shape[1 + i] != d[i]) return bad(t, "state", expected);
+    *out = v.p;
+    return v.shape[0];
 }
 /* the address of a state without slots, which is never read or written */
 static _Alignas(16) char no_slots[16];
@@ -431,10 +439,10 @@ static PyObject* conv(KWARGS) {
           (long long)y.rows, (long long)y.cols, (long long)x.rows, (long long)x.cols);
     if (flat_f32(v[3], x.cols, "bias", &dev, &bias) || batch(v[5], &q, &qp, &dev) || stream_of(v[7], &st)) return NULL;
     if (v[6] != Py_None) {
-        static const char* expected = "a contiguous CUDA tensor [slots, width - 1, channels] of x's type";
-        if ((slots = first_extent(v[6], "state")) < 0) return NULL;
-        if (flat(v[6], x.type == MOE_F32 ? MOE_TENSOR_F32 : MOE_TENSOR_BF16, slots * (w.cols - 1) * x.cols, "state", expected, &dev, &state))
-            return NULL;
+        const int64_t rest[] = {w.cols - 1, x.cols};
+        slots = state_of(v[6], x.type == MOE_F32 ? MOE_TENSOR_F32 : MOE_TENSOR_BF16, 2, rest,
+                         "a contiguous CUDA tensor [slots, width - 1, channels] of x's type", &dev, &state);
+        if (slots < 0) return NULL;
         if (!slots) state = no_slots; /* which torch gives no address: every sequence is left out */
     }
     NONE_OR_RAISE(moe_conv(qp, x.p, x.type, x.ld, x.rows, (int32_t)x.cols, w.p, w.type, (int32_t)w.cols, bias, (int32_t)act,
@@ -536,10 +544,10 @@ static PyObject* delta(KWARGS) {
         room(v[9], &dev, &ws, &bytes))
         return NULL;
     if (v[5] != Py_None) {
-        if ((slots = first_extent(v[5], "state")) < 0) return NULL;
-        if (flat(v[5], MOE_TENSOR_F32, slots * val.heads * val.dim * q.dim, "state",
-                 "a contiguous float32 CUDA tensor [slots, v_heads, v_dim, k_dim]", &dev, &state))
-            return NULL;
+        const int64_t rest[] = {val.heads, val.dim, q.dim};
+        slots = state_of(v[5], MOE_TENSOR_F32, 3, rest, "a contiguous float32 CUDA tensor [slots, v_heads, v_dim, k_dim]", &dev,
+                         &state);
+        if (slots < 0) return NULL;
         if (!slots) state = no_slots;
     }
     NONE_OR_RAISE(moe_delta(&c, bp, q.p, q.ld, k.p, k.ld, val.p, val.ld, g, beta, state, slots, o.p, o.ld, val.n, ws,

@@ -6,7 +6,7 @@
 #include <stdint.h>
 
 enum { MOE_TENSOR_OTHER = -1, MOE_TENSOR_F32, MOE_TENSOR_BF16, MOE_TENSOR_I32, MOE_TENSOR_U8 };
-#define MOE_TENSOR_DIMS 3 /* of which shape and stride are kept */
+#define MOE_TENSOR_DIMS 4 /* of which shape and stride are kept */
 
 typedef struct {
     void* p;
