@@ -1031,24 +1031,26 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
             else
                 times_t(1, theirs[1], group[3]);  // 2 for 3
         }
+        // U^T (e^(G_63 - G) K) in the new units, with this warp's tokens first: a sum of its own.  The tensor core's additions
+        // round towards zero, and eight a chunk into S itself took 2^-22 of it a chunk
+        float grown[kN][4];
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[n][i] *= grow;
-        // S <- e^G_63 S + U^T (e^(G_63 - G) K) in the new units, with this warp's tokens first
+            for (int i = 0; i < 4; ++i) grown[n][i] = 0;
         auto times_k_turned = [&](const Fragment& l, int t) {
             uint32_t w[kT][4];
 #pragma unroll
             for (int n = 0; n < kT; ++n) ldmatrix_trans(w[n], rows_at(stage, 16 * t, 2 * (q * kT + n), lane));
 #pragma unroll
             for (int n = 0; n < kT; ++n) {
-                mma_f16(S[2 * n], l.high, w[n][0], w[n][1]);
-                mma_f16(S[2 * n + 1], l.high, w[n][2], w[n][3]);
+                mma_f16(grown[2 * n], l.high, w[n][0], w[n][1]);
+                mma_f16(grown[2 * n + 1], l.high, w[n][2], w[n][3]);
             }
 #pragma unroll
             for (int n = 0; n < kT; ++n) {
-                mma_f16(S[2 * n], l.rest, w[n][0], w[n][1]);
-                mma_f16(S[2 * n + 1], l.rest, w[n][2], w[n][3]);
+                mma_f16(grown[2 * n], l.rest, w[n][0], w[n][1]);
+                mma_f16(grown[2 * n + 1], l.rest, w[n][2], w[n][3]);
             }
         };
         Fragment L[2];
@@ -1076,6 +1078,11 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
         }
         times_k_turned(L[0], group[2]);
         times_k_turned(L[1], group[3]);
+        // S <- e^G_63 S + that
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[n][i] = fmaf(S[n][i], grow, grown[n][i]);
     }
     __syncthreads();  // for the last chunk's o
     let_next_start();  // not earlier: 8 prompts of 512 with 8 heads 45 us, at the kernel's start 49 (64 of 64 with 32: 256 and 252)

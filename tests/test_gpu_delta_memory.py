@@ -1,0 +1,74 @@
+"""The gated delta rule over long runs and changes of size, against its definition in 64 bits.
+
+`size` is what tolerances go by: the largest magnitude of a head's state, an earlier one shrunk by the decays since."""
+import pytest
+
+import int4_expert_streaming_gb300 as moe
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    moe.build()
+    moe.load_library()
+
+
+def definition(q, k, v, g, beta, S, scale):
+    """Token by token; o [T, Hv, dv], the state after the last token, size [T, Hv] and o's state sums' magnitude."""
+    share = v.shape[1] // k.shape[1]
+    q, k = (t.double().repeat_interleave(share, 1)[..., None] for t in (q, k))
+    v, g, beta, S = v.double()[..., None], g.double(), beta.double()[..., None, None], S[0].double()
+    o, size, top = torch.empty(v.shape[:3], dtype=torch.float64, device="cuda"), [], S.abs().amax((1, 2))
+    for t in range(len(v)):
+        S = torch.where(torch.isneginf(g[t])[:, None, None], 0, S * torch.exp(g[t])[:, None, None])
+        S = S + beta[t] * (v[t] - S @ k[t]) * k[t].transpose(1, 2)
+        o[t] = scale * (S @ q[t])[..., 0]
+        top = torch.maximum(torch.where(torch.isneginf(g[t]), 0, top * torch.exp(g[t])), S.abs().amax((1, 2)))
+        size.append(top)
+    return o, S[None], torch.stack(size)
+
+
+def inputs(T, Hk, Hv, dk, dv, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device="cuda")
+    q, k = (t / t.norm(dim=2, keepdim=True) for t in (normal(T, Hk, dk), normal(T, Hk, dk)))
+    return q.to(BF), k.to(BF), normal(T, Hv, dv).to(BF), torch.rand((T, Hv), generator=gen, device="cuda"), normal(1, Hv, dv, dk)
+
+
+def run(q, k, v, g, beta, state, scale, piece=None):
+    """One call, or one for each `piece` rows; o and the state after."""
+    T, Hk, dk = q.shape
+    Hv, dv = v.shape[1:]
+    ws = torch.empty(max(1, moe.moe_delta_workspace(T, 1, Hk, Hv, dk, dv)), dtype=torch.uint8, device="cuda")
+    o, state = torch.empty_like(v), state.clone()
+    for lo in range(0, T, piece or T):
+        at = slice(lo, lo + (piece or T))
+        moe.moe_delta(q[at], k[at], v[at], g[at], beta[at], state, o[at], scale, workspace=ws, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    return o.double(), state.double()
+
+
+def check_state(got, want, size, bound, more=0.0):
+    """Every value within bound of the size at the end."""
+    off = (got - want).abs().amax((0, 2, 3)) / (bound * size[-1] + more)
+    assert (off <= 1).all(), off
+
+
+@pytest.mark.parametrize("g,beta", [(-1e-3, 0.5), (0.0, 0.5), (0.0, 0.01), (-1e-5, 0.001)])
+def test_a_long_memory_in_chunks(g, beta):
+    """16384 tokens, in whose 256 chunks little or nothing of the state is forgotten.  A chunk's sums of up to 16 steps of the
+    tensor core lose up to 2^-24 of their size at each in the mean, if those round towards zero: 2^-20, of what the chunk adds
+    to the state and not of the state, so it does not grow with the chunks; three sums follow each other, 2^-18.4.  One
+    rounding a chunk of the state itself, without a bias: 5 sqrt(256) 2^-25.  Together below 2^-17."""
+    q, k, v, r, start = inputs(16384, 1, 2, 128, 128, 1)
+    decay, beta = torch.full_like(r, g), beta * (0.5 + 0.5 * r)
+    o, state, size = definition(q, k, v, decay, beta, start, 0.1)
+    got_o, got = run(q, k, v, decay, beta, start, 0.1)
+    check_state(got, state, size, 2.0 ** -17)
+    near = 2.0 ** -8 * 1.01 * o.abs() + 2.0 ** -9 * 0.1 * size[..., None]  # |q| is 1
+    assert ((got_o - o).abs() <= near).all()
