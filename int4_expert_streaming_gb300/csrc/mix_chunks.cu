@@ -39,7 +39,7 @@ struct Factors {
     float left[kC];  // e^(G_63 - G_i) times the unit of k's row
     float qs[kC];    // e^G_i times the unit of q's row, times the factor on o
     float pt[kC];    // units of P T's row and of T, times the factor on o
-    float all;       // e^G_63
+    float all, rest; // e^G_63: their sum
     float t;         // unit of T
     // how large things can get: X over the largest of S, beside V; what goes into S over the largest of X
     float most_ks, most_l;
@@ -400,7 +400,13 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
                 f.left[r] = left;
                 most_ks = fmaxf(most_ks, e * m.k_sum[r]);
                 most_left = fmaxf(most_left, left);
-                if (r == kC - 1) f.all = e;
+                if (r == kC - 1) {
+                    // Every chunk takes S times this: what one fp32 of e^-0.001 is off by, the same for each, would be 2^-13 of S
+                    // after 4096 of them.  For decays that leave a state in place so long, 1 + (e^G - 1) as two fp32.
+                    const float less = expm1f((gh[r] + gr[r]) * 0.69314718f);
+                    f.all = fabsf(less) < 0.25f ? 1.0f + less : e;
+                    f.rest = fabsf(less) < 0.25f ? less - (f.all - 1.0f) : 0.0f;
+                }
             }
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -970,7 +976,8 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
         // S has to stay finite in the new units, and its change of units a number of fp32; what updates lose by that is 2^-60
         // of S, or 2^-100 of what they were made for before
         const int next = min(max(field(2.0f * l_bound), max(field(s_most) + unit - kOne - 60, unit - 120)), 254);
-        const float grow = f.all * __uint_as_float((uint32_t)(127 + min(max(unit - next, -126), 127)) << 23);
+        const float units_by = __uint_as_float((uint32_t)(127 + min(max(unit - next, -126), 127)) << 23);
+        const float grow = f.all * units_by, grow_rest = f.rest * units_by;
         const float to_l = f.t * x_down * up(next);
         // 64 updates times numbers of K16, below 2^15
         s_bound = fmaf(s_most, grow, l_bound * up(next) * 2097152.0f);
@@ -1037,7 +1044,7 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) grown[n][i] = 0;
+            for (int i = 0; i < 4; ++i) grown[n][i] = S[n][i] * grow_rest;
         auto times_k_turned = [&](const Fragment& l, int t) {
             uint32_t w[kT][4];
 #pragma unroll

@@ -72,3 +72,16 @@ def test_a_long_memory_in_chunks(g, beta):
     check_state(got, state, size, 2.0 ** -17)
     near = 2.0 ** -8 * 1.01 * o.abs() + 2.0 ** -9 * 0.1 * size[..., None]  # |q| is 1
     assert ((got_o - o).abs() <= near).all()
+
+
+def test_constant_decays_in_chunks():
+    """16384 tokens that only decay: what every chunk multiplies the state by must not be off by the same each time.  A
+    chunk's rounding of a value goes one way while its decay does, up to 2^-24; what a head's 1024 values lose together spreads
+    by 256 2^-24.8 sqrt(3 / 1024) = 2^-21, and 5 of that are 2^-18.7."""
+    heads, T = 24, 16384
+    q, k, v, r, start = inputs(T, 1, heads, 32, 32, 4)
+    g = torch.logspace(-6, -3.4, heads, device="cuda").neg().expand(T, heads).contiguous()
+    _, got = run(q, k, v, g, torch.zeros_like(g), start, 0.1)
+    want = start.double() * torch.exp(g.double().sum(0))[None, :, None, None]
+    lost = (got * want).sum((0, 2, 3)) / want.square().sum((0, 2, 3)) - 1
+    assert (lost.abs() <= 2.0 ** -18.7).all(), lost
