@@ -117,8 +117,22 @@ __global__ void __launch_bounds__(128) steps_kernel(const __grid_constant__ Delt
     for (int tokens = (int)(hi - lo); tokens > 0; --tokens) {
         const Token<KD> in = next;
         if (tokens > 1) load(next);
-        const float decay = expf(in.g);
-        const f32x2 decays = both(decay, decay);
+        // S <- e^g S.  Decays near 1 as S + (e^g - 1) S: one fp32 of e^-0.00001, off by the same at every token, would leave
+        // 2^-10 of S after 16384 of them
+        const bool near = fabsf(in.g) < 0.25f;
+        const float by = near ? expm1f(in.g) : expf(in.g);
+        const f32x2 bys = both(by, by);
+        if (near) {
+#pragma unroll
+            for (int p = 0; p < kRows; ++p)
+#pragma unroll
+                for (int i = 0; i < kE / 2; ++i) S[p][i] = fma2(S[p][i], bys, S[p][i]);
+        } else {
+#pragma unroll
+            for (int p = 0; p < kRows; ++p)
+#pragma unroll
+                for (int i = 0; i < kE / 2; ++i) S[p][i] = mul2(S[p][i], bys);
+        }
         f32x2 k[kE / 2], q[kE / 2], kq2 = 0, sk2[kRows], sq2[kRows];
 #pragma unroll
         for (int i = 0; i < kE / 2; ++i) {
@@ -130,7 +144,6 @@ __global__ void __launch_bounds__(128) steps_kernel(const __grid_constant__ Delt
             sk2[p] = sq2[p] = 0;
 #pragma unroll
             for (int i = 0; i < kE / 2; ++i) {
-                S[p][i] = mul2(S[p][i], decays);
                 sk2[p] = fma2(S[p][i], k[i], sk2[p]);
                 sq2[p] = fma2(S[p][i], q[i], sq2[p]);
             }

@@ -1,6 +1,8 @@
 """The gated delta rule over long runs and changes of size, against its definition in 64 bits.
 
 `size` is what tolerances go by: the largest magnitude of a head's state, an earlier one shrunk by the decays since."""
+import math
+
 import pytest
 
 import int4_expert_streaming_gb300 as moe
@@ -85,3 +87,20 @@ def test_constant_decays_in_chunks():
     want = start.double() * torch.exp(g.double().sum(0))[None, :, None, None]
     lost = (got * want).sum((0, 2, 3)) / want.square().sum((0, 2, 3)) - 1
     assert (lost.abs() <= 2.0 ** -18.7).all(), lost
+
+
+@pytest.mark.parametrize("piece", [24, 1])
+@pytest.mark.parametrize("g", [-1e-5, -3e-4])
+def test_a_long_memory_token_by_token(g, piece):
+    """A state in fp32, rounded at each token by up to 2^-24 of a value.  Under a constant decay a value's roundings mostly go
+    the same way, because what is taken from it hardly changes: T 2^-24.  But another value's go another way: what all N
+    values have lost together, sum(got want) / sum(want^2) - 1, spreads by T 2^-24.8 sqrt(3 / N) where their magnitudes
+    are normal, and 5 of that are T 2^-29.  A decay that is itself off by 2^-25 is T 2^-25 there."""
+    T = 16384 if piece > 1 else 1024
+    q, k, v, r, start = inputs(T, 1, 2, 128, 128, 2)
+    decay, beta = torch.full_like(r, g), 0.001 + 0.0 * r
+    o, state, size = definition(q, k, v, decay, beta, start, 0.1)
+    got_o, got = run(q, k, v, decay, beta, start, 0.1, piece)
+    check_state(got, state, size, T * 2.0 ** -24)
+    assert abs((got * state).sum() / state.square().sum() - 1) <= T * 2.0 ** -29
+    assert ((got_o - o).abs() <= 2.0 ** -8 * 1.01 * o.abs() + T * 2.0 ** -24 * 0.1 * size[..., None] * math.sqrt(128)).all()
