@@ -913,10 +913,6 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
     };
     // groups of 16 tokens: this warp's, then the other's
     const int group[4] = {group_of(q, 0), group_of(q, 1), group_of(q ^ 1, 0), group_of(q ^ 1, 1)};
-    float s_bound = largest_of_s();  // of both halves, in their units
-    if (lane == 0) found[warp] = make_float2(s_bound, 0);
-    pair_barrier();
-    s_bound = fmaxf(s_bound, found[warp ^ 1].x);
 
     for (int c = 0; c < chunks; ++c) {
         __syncthreads();
@@ -933,9 +929,10 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
             for (int i = 0; i < 4; ++i) bits = __vmaxu2(bits, v[g][i] & 0x7fff7fffu);
         }
         bits = __reduce_max_sync(kAll, max(bits & 0xffff0000u, bits << 16));
-        // This half's part of K S^T, for the other's tokens first.  S's unit is from a bound: its largest value is found
-        // beside the products.
-        const int e_s = field(2.0f * s_bound);
+        // This half's part of K S^T, for the other's tokens first.  S's unit is from its largest value: a bound from the chunk
+        // before leaves few bits of a state that was cleared there.
+        const float most = largest_of_s();
+        const int e_s = field(most);
         const float s_up = up(e_s), s_down = down(e_s) * down(unit);
         float x[8][4];
         Fragment b[kT];
@@ -958,7 +955,6 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
             put4(hand + t * kVector, b[t].high);
             times_k(t, 2);
         }
-        const float most = largest_of_s();
         if (lane == 0) found[warp] = make_float2(most, __uint_as_float(bits)), units[c & 1][warp].x = s_down;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -979,8 +975,6 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
         const float units_by = __uint_as_float((uint32_t)(127 + min(max(unit - next, -126), 127)) << 23);
         const float grow = f.all * units_by, grow_rest = f.rest * units_by;
         const float to_l = f.t * x_down * up(next);
-        // 64 updates times numbers of K16, below 2^15
-        s_bound = fmaf(s_most, grow, l_bound * up(next) * 2097152.0f);
         if (lane == 0) units[c & 1][warp].y = x_down;
         unit = next;
 

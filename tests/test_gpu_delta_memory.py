@@ -104,3 +104,28 @@ def test_a_long_memory_token_by_token(g, piece):
     check_state(got, state, size, T * 2.0 ** -24)
     assert abs((got * state).sum() / state.square().sum() - 1) <= T * 2.0 ** -29
     assert ((got_o - o).abs() <= 2.0 ** -8 * 1.01 * o.abs() + T * 2.0 ** -24 * 0.1 * size[..., None] * math.sqrt(128)).all()
+
+
+@pytest.mark.parametrize("at", [20, 61, 64, 150])
+@pytest.mark.parametrize("how", ["cleared", "shrunk"])
+@pytest.mark.parametrize("times", [2.0 ** 10, 2.0 ** 20])
+def test_a_large_state_is_cleared(times, how, at):
+    """A state far above what is written later, cleared (or shrunk by e^-27 in three tokens) in the midst of a chunk, at its
+    end, at its beginning, or in a later one.  The chunk with the clear has both sizes in its products, whose numbers are held
+    in steps of 2^-37 of a bound: |k|_1 = 2^3.3 times the largest state, and for what goes into the state that times a row of
+    T, of sums about 4.  Such a step's rounding has a spread of 2^-38.8 of the bound: 2^-33.5 of the largest state, and by
+    up to 43 keys of values of 2^-3.5 into the state 2^-34.3; 5 spreads are below 2^-32.  Later chunks know the new size alone."""
+    q, k, v, beta, start = inputs(266, 1, 2, 128, 128, 3)
+    start = start * times
+    g = -0.05 * beta.flip(0)
+    g[at:at + 3] = -float("inf") if how == "cleared" else -9.0
+    o, state, size = definition(q, k, v, g, beta, start, 0.1)
+    got_o, got = run(q, k, v, g, beta, start, 0.1)
+    left = 2.0 ** -32 * start.double().abs().amax((0, 2, 3))
+    assert torch.isfinite(got).all()
+    check_state(got, state, size, 2.0 ** -16, left)
+    far = size.clone()
+    far[at // 64 * 64:(at + 2) // 64 * 64 + 64] += 2.0 ** -9 * size[at // 64 * 64]  # beside the large ones in its chunk: 2^-20 of those
+    near = 2.0 ** -8 * 1.01 * o.abs() + 0.1 * (2.0 ** -9 * far + left)[..., None]
+    off = ((got_o - o).abs() / near).amax((1, 2))
+    assert (off <= 1).all(), (off.argmax(), off.max())
