@@ -410,6 +410,17 @@ static long long state_of(PyObject* t, int type, int n, const int64_t* d, const 
     *out = v.p;
     return v.shape[0];
 }
+/* contiguous fp32 [at least n, heads]; one of [heads, n] has as many values */
+static int gates_of(PyObject* t, int64_t n, int64_t heads, const char* what, int* dev, void** out) {
+    static const char* expected = "a contiguous float32 CUDA tensor [T, v_heads]";
+    moe_tensor v;
+    if (look(t, &v)) return bad(t, what, expected);
+    if (on_device(t, &v, what, expected, dev)) return -1;
+    if (v.dims != 2 || v.type != MOE_TENSOR_F32 || !v.contiguous || v.shape[0] < n || v.shape[1] != heads)
+        return bad(t, what, expected);
+    *out = v.p;
+    return 0;
+}
 /* the address of a state without slots, which is never read or written */
 static _Alignas(16) char no_slots[16];
 
@@ -535,11 +546,10 @@ static PyObject* delta(KWARGS) {
     c.k_heads = (int32_t)q.heads, c.v_heads = (int32_t)val.heads;
     c.k_dim = (int32_t)q.dim, c.v_dim = (int32_t)val.dim;
     c.scale = (float)scale;
-    const long long rows = val.n * val.heads;
-    if (flat_f32(v[3], rows, "g", &dev, &g) || flat_f32(v[4], rows, "beta", &dev, &beta) ||
+    CHECK(v[3] != Py_None && v[4] != Py_None, "g and beta are required");
+    if (gates_of(v[3], val.n, val.heads, "g", &dev, &g) || gates_of(v[4], val.n, val.heads, "beta", &dev, &beta) ||
         batch(v[8], &b, &bp, &dev) || stream_of(v[10], &st))
         return NULL;
-    CHECK(g && beta, "g and beta are required");
     if (v[9] != Py_None && moe_delta_workspace(&c, val.n, bp ? bp->n : 1, bp ? bp->offsets_dev ? bp->max_len : 1 : 0) &&
         room(v[9], &dev, &ws, &bytes))
         return NULL;

@@ -40,3 +40,21 @@ def test_states_that_are_not_contiguous():
     refused("state", lambda: moe.moe_delta(q, q, v, g, g, Tensor(F, 2, 4, 16, 8, stride=(512, 128, 1, 16)), v))
     refused("state", lambda: moe.moe_conv(Tensor(B, 5, 64), Tensor(B, 64, 4), Tensor(B, 5, 64),
                                           state=Tensor(B, 2, 3, 64, stride=(192, 1, 3))))
+
+
+@pytest.mark.parametrize("shape", [(4, 5), (20,), (5, 4, 1), (10, 2), (4, 4), (5, 5), (1, 5, 4)])
+def test_delta_gates_of_another_shape(shape):
+    q, v, g, other = Tensor(B, 5, 2, 8), Tensor(B, 5, 4, 16), Tensor(F, 5, 4), Tensor(F, *shape)
+    refused("g: expected .*T, v_heads", lambda: moe.moe_delta(q, q, v, other, g, None, v))
+    refused("beta: expected .*T, v_heads", lambda: moe.moe_delta(q, q, v, g, other, None, v))
+    refused("g: expected", lambda: moe.moe_delta(q, q, v, Tensor(F, 5, 4, stride=(1, 5)), g, None, v))
+
+
+def test_shapes_that_fit_reach_the_library():
+    """Its own refusal comes through, so nothing is launched: no workspace, and a stride shorter than a row."""
+    q, v, g = Tensor(B, 50, 2, 8), Tensor(B, 50, 4, 16), Tensor(F, 60, 4)
+    with pytest.raises(moe.MoeError, match="workspace"):
+        moe.moe_delta(q, q, v, g, g, Tensor(F, 2, 4, 16, 8), v)
+    x = Tensor(B, 5, 64, stride=(63, 1))
+    with pytest.raises(moe.MoeError, match="stride"):
+        moe.moe_conv(x, Tensor(B, 64, 4), Tensor(B, 5, 64), state=Tensor(B, 2, 3, 64))
