@@ -526,7 +526,7 @@ typedef struct {
     int32_t max_len;
 } moe_seqs;
 
-#define MOE_ACT_SILU 2 /* x / (1 + exp(-x)), to about 2^-21 */
+#define MOE_ACT_SILU 2 /* x / (1 + exp(-x)), to about 2^-21; in bf16 to 2^-21 + |x| 2^-24; below 2^-126 it may be 0 */
 
 /*
  * Short causal convolution, each channel by itself:

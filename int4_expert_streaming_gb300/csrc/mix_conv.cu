@@ -34,14 +34,18 @@ __device__ __forceinline__ void widen(const Row<T, V>& r, float (&f)[V]) {
     for (int i = 0; i < V; ++i) f[i] = (float)r.v[i];
 }
 
+// What weights and bias, and so the sums, are taken times: bf16 sums that silu follows are 2^-8 of what they stand for, as
+// sigmoid_256 wants them.
+template <typename T, bool SILU>
+constexpr float kPart = SILU && sizeof(T) == 2 ? 1.0f / 256 : 1.0f;
 template <typename T, bool SILU>
 __device__ __forceinline__ float activated(float v) {
-    return !SILU ? v : sizeof(T) == 2 ? silu_bf16(v) : silu(v);
+    return !SILU ? v : sizeof(T) == 2 ? v * sigmoid_256<256>(v) : silu(v);
 }
 
 // the weights of V channels, which stand one after another
 template <typename T, int V, int W>
-__device__ __forceinline__ void load_weights(float (&w)[W][V], const void* from, int c) {
+__device__ __forceinline__ void load_weights(float (&w)[W][V], const void* from, int c, float part) {
     Row<T, V * W> r;
     constexpr int kPart = V * W * sizeof(T) % 8 ? 1 : 8 / (int)sizeof(T);  // wide where c is a multiple of V: 8 bytes
     const T* p = static_cast<const T*>(from) + (int64_t)c * W;
@@ -56,7 +60,7 @@ __device__ __forceinline__ void load_weights(float (&w)[W][V], const void* from,
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i][j] = (float)r.v[j * W + i];
+        for (int i = 0; i < W; ++i) w[i][j] = part * (float)r.v[j * W + i];
 }
 
 // A thread takes V channels (8 bytes, or one where rows are not aligned) down
@@ -100,11 +104,11 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const __grid_constant__ 
     }
     float w[W][V], bias[V], past[W - 1][V];
     if (a.w_bf16)
-        load_weights<__nv_bfloat16, V, W>(w, a.w, c);
+        load_weights<__nv_bfloat16, V, W>(w, a.w, c, kPart<T, SILU>);
     else
-        load_weights<float, V, W>(w, a.w, c);
+        load_weights<float, V, W>(w, a.w, c, kPart<T, SILU>);
 #pragma unroll
-    for (int j = 0; j < V; ++j) bias[j] = a.bias ? a.bias[c + j] : 0.0f;
+    for (int j = 0; j < V; ++j) bias[j] = a.bias ? kPart<T, SILU> * a.bias[c + j] : 0.0f;
 
     T* y = static_cast<T*>(a.y) + first * a.y_ld + c;
     T* state = a.state ? static_cast<T*>(a.state) + (int64_t)slot * (W - 1) * a.channels + c : nullptr;
@@ -195,12 +199,12 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_consta
     const R in = *reinterpret_cast<const R*>(static_cast<const T*>(a.x) + s * a.x_ld + c);
     float w[W][V], rows[W][V];
     if (a.w_bf16)
-        load_weights<__nv_bfloat16, V, W>(w, a.w, c);
+        load_weights<__nv_bfloat16, V, W>(w, a.w, c, kPart<T, SILU>);
     else
-        load_weights<float, V, W>(w, a.w, c);
+        load_weights<float, V, W>(w, a.w, c, kPart<T, SILU>);
     float bias[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) bias[j] = a.bias ? a.bias[c + j] : 0.0f;
+    for (int j = 0; j < V; ++j) bias[j] = a.bias ? kPart<T, SILU> * a.bias[c + j] : 0.0f;
     if (slot < 0) return;
     T* state = a.state ? static_cast<T*>(a.state) + (int64_t)slot * (W - 1) * a.channels + c : nullptr;
     R old[W - 1];

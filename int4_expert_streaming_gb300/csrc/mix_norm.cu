@@ -220,6 +220,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 
             for (int d = LANES / 2; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
             factor = rsqrtf(fmaf(sum, g.part, g.c.eps));
         }
+        constexpr bool kParts = GATE && sizeof(T) == 2;  // the gate as 2^8 / (1 + e^-z) times z, and the 2^-8 here
+        if (kParts && t.gate_dev) factor *= 1.0f / 256;
         float v[CH][P];
 #pragma unroll
         for (int i = 0; i < CH; ++i)
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) gate[u][i][p].get(&z[p * kPiece]);
 #pragma unroll
-                for (int j = 0; j < P; ++j) v[i][j] *= sizeof(T) == 2 ? silu_bf16(z[j]) : silu(z[j]);
+                for (int j = 0; j < P; ++j) v[i][j] = kParts ? v[i][j] * sigmoid_256<1>(z[j]) * z[j] : v[i][j] * silu(z[j]);
             }
         }
         if (threadIdx.x / LANES + u * kPass < here) {
