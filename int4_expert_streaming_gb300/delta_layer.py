@@ -57,7 +57,7 @@ class DeltaMixer:
 
     def forward(self, x, seqs: moe.moe_seqs, y):
         """x [T, hidden] -> y [T, hidden], both bf16, on the current stream.  Rows of no sequence, or of one without a
-        slot, get nothing of use."""
+        slot, get zeros (where x is finite)."""
         T, st = x.shape[0], torch.cuda.current_stream()
         Hk, Hv, dk, dv = self.heads
         if x.shape != (T, self.hidden) or y.shape != x.shape:
@@ -74,6 +74,8 @@ class DeltaMixer:
         q, k, v = m.split([Hk * dk, Hk * dk, Hv * dv], 1)
         q, k, v = q.unflatten(1, (Hk, dk)), k.unflatten(1, (Hk, dk)), v.unflatten(1, (Hv, dv))
         moe.moe_head_norm(self.unit, q, q, x2=k, y2=k, stream=st)
+        if seqs.offsets_dev or seqs.slot_dev:  # there may be rows that the delta rule leaves as an earlier call left them
+            o.zero_()
         moe.moe_delta(q, k, v, g, beta.sigmoid(), self.state, o, dk ** -0.5, seqs, self.workspace, st)
         moe.moe_head_norm(self.gated, o, o, self.norm, p[:, self.channels:].unflatten(1, (Hv, dv)), stream=st)
         return torch.mm(o.flatten(1), self.w_out.T, out=y)
