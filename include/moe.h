@@ -516,7 +516,10 @@ int moe_combine_rows(const void* rows_dev, int64_t n_rows, int32_t rows_type, in
  *                NULL: all go on from their slots
  *   max_len      no sequence has more rows (0: not known); from 1 to 24 moe_delta needs neither its workspace nor its
  *                kernels for long runs.  Calls stay right, if slow, where it is too small
- * A sequence without rows leaves its slot as it is.  seqs = NULL: all T rows are one sequence, with slot 0.
+ * A sequence without rows leaves its slot as it is.  What is left in a slot is
+ * the state after the sequence's last row: who may have to go back to an
+ * earlier one (of drafted tokens that are not taken) copies the slots before
+ * the call, or runs the tokens that are taken again from there.  seqs = NULL: all T rows are one sequence, with slot 0.
  */
 typedef struct {
     const int32_t* offsets_dev;
@@ -605,12 +608,15 @@ typedef struct {
  *                 zeros and leaves nothing behind
  * Sequences of up to 24 rows run token by token, with the state in registers
  * and fp32 throughout.  Longer ones run in chunks of 64 tokens on the tensor
- * cores: within a chunk the updates come from one triangular system; the
- * state, the chunk's inverse and the updates enter the products as pairs of
- * fp16 numbers in units of powers of two (together about 2^-22 of the largest
- * within 16 columns of v_dim and 64 tokens)
- * and are summed in fp32; what goes only into o enters as one fp16 number.  Which of the two a sequence takes depends on its own
- * length alone (max_len being right), so its results do not depend on its batch.
+ * cores: within a chunk the updates come from one triangular system.  What the
+ * products are of (the state, the updates, the chunk's inverse, products of q
+ * and k) enters them as pairs of fp16 numbers in units of powers of two, 2^-22
+ * of a value, and 2^-38 of the largest within 16 columns of v_dim and 64
+ * tokens; sums are fp32, and the state is fp32 from chunk to chunk.  o is
+ * rounded once.  A state that is cleared in the midst of a chunk should not be
+ * more than 2^20 times what is written in the rest of it.  Which of the two a
+ * sequence takes depends on its own length alone (max_len being right), so its
+ * results do not depend on its batch.
  * A value of q, k, v, g or beta that is not finite (but for g = -inf) leaves
  * that head's o undefined from 63 tokens before it on, and its state; other heads
  * and sequences are not touched.

@@ -14,11 +14,14 @@
 //
 // Numbers enter the products as fp16.  K and Q are bf16, exact in fp16 once a
 // row is scaled by a power of two that brings its largest value to 2^14 (values
-// 2^-28 below that lose bits).  S, X, T and the updates are sums in fp32 and
-// enter as two fp16 numbers each, high and rest, together 22 bits, in units
-// that bring a bound of their values to 2^14: all 22 bits are there down to
-// 2^-16 of the bound, so the bound may be generous.  The product of two rests is
-// left out.  P T, which only goes into o, a bf16 number, is one fp16 number.
+// 2^-28 below that lose bits).  S, X, T, P, P T and the updates are sums in fp32
+// and enter as two fp16 numbers each, high and rest, together 22 bits, in units
+// that bring their largest value or a bound of it to 2^14: all 22 bits are there
+// down to 2^-16 of that, so a bound may be generous.  The product of two rests is
+// left out.  What goes into o alone has both numbers too: with the high ones
+// only, o was off by 2^-12 of |S| |q|, more than its rounding to bf16 where sums
+// cancel in it (a key that is written over).  That costs 4096 tokens with 32 heads of
+// 128 178 us instead of 165, 64 prompts of 64 257 instead of 252.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -30,8 +33,8 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kC = kDeltaChunk;
 
 // Workspace, per chunk and k head: K16 and Q16, panels of 64 columns of 128 rows
-// (K's, then Q's).  Per chunk and v head: T high over P T [128 x 64], T rest
-// [64 x 64], and the factors.  At the end the sequences (Taken).  Rows are of 128 bytes with their 16-byte pieces
+// (K's, then Q's).  Per chunk and v head: T high, P T high, T rest and P T rest
+// [64 x 64 each], and the factors.  At the end the sequences (Taken).  Rows are of 128 bytes with their 16-byte pieces
 // exchanged (piece p of row r at p ^ (r & 7)): read from shared memory without
 // conflicts.
 struct Factors {
@@ -46,7 +49,7 @@ struct Factors {
 };
 constexpr int kSquare = kC * 128;
 constexpr int kPanel = 2 * kSquare;
-constexpr int kHeadTiles = 3 * kSquare;
+constexpr int kHeadTiles = 4 * kSquare;
 constexpr int kHeadBytes = (kHeadTiles + (int)sizeof(Factors) + 127) / 128 * 128;
 
 constexpr int kSorted = 512;
@@ -68,6 +71,9 @@ __device__ __forceinline__ void ldmatrix(uint32_t (&r)[4], uint32_t at) {
 __device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void stmatrix(uint32_t at, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w0), "r"(w1), "r"(w2), "r"(w3) : "memory");
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -92,6 +98,14 @@ __device__ __forceinline__ int field(float m) { return max((int)(__float_as_uint
 __device__ __forceinline__ float up(int e) { return __uint_as_float((uint32_t)(268 - e) << 23); }    // 2^(14 - (e - 127))
 __device__ __forceinline__ float down(int e) {                                                        // 2^(e - 127 - 14)
     return e > 14 ? __uint_as_float((uint32_t)(e - 14) << 23) : 0.0f;
+}
+
+// two numbers as the high ones and what is left of them
+__device__ __forceinline__ uint32_t halved(float x, float y, uint32_t& rest) {
+    const uint32_t high = pack(x, y);
+    const float2 h = unpack(high);
+    rest = pack(x - h.x, y - h.y);
+    return high;
 }
 
 // byte of 16-byte piece p of row r, in rows of N pieces
@@ -374,7 +388,7 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
     __syncthreads();
 
     const float *gh = m.g_high[b], *gr = m.g_rest[b];
-    uint32_t P[8][2];  // of blocks up to the diagonal one, as left operands' fragments
+    uint32_t P[8][2], Pr[8][2];  // of blocks up to the diagonal one, as left operands' fragments: high numbers and rests
     float p_down[2];
     const uint32_t k_at = smem_at(m.kq[0]), q_at = smem_at(m.kq[1]);
     if (there) {
@@ -422,7 +436,7 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
             const int r = 16 * warp + (lane >> 2) + 8 * i;
             after[i] = exp2_of((gh[r] - gh[16 * warp]) + (gr[r] - gr[16 * warp]));
             beta[i] = m.beta[b][r];
-            // |q_i k_j| is at most the largest of q_i times the sum of k_j; a bound will do for 11 bits
+            // |q_i k_j| is at most the largest of q_i times the sum of k_j
             const int e = field(2.0f * m.q_top[r] * most_k);
             p_up[i] = up(e);
             p_down[i] = down(e);
@@ -483,7 +497,7 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
                         if (j + 1 + !which > r) v1 = 0;
                     }
                     if (which)
-                        P[n][i] = pack(v0, v1);
+                        P[n][i] = halved(v0, v1, Pr[n][i]);
                     else
                         *reinterpret_cast<float2*>(&m.A[b][r][j]) = make_float2(v0, v1);
                 }
@@ -576,21 +590,17 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
             const int row = ((tid & 127) >> 3) + 16 * i;
             uint32_t high[4], rest[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float u0 = v[i][2 * j] * t_up, u1 = v[i][2 * j + 1] * t_up;
-                high[j] = pack(u0, u1);
-                const float2 h = unpack(high[j]);
-                rest[j] = pack(u0 - h.x, u1 - h.y);
-            }
-            const uint4 h4 = make_uint4(high[0], high[1], high[2], high[3]);
+            for (int j = 0; j < 4; ++j) high[j] = halved(v[i][2 * j] * t_up, v[i][2 * j + 1] * t_up, rest[j]);
+            const uint4 h4 = make_uint4(high[0], high[1], high[2], high[3]), r4 = make_uint4(rest[0], rest[1], rest[2], rest[3]);
             *reinterpret_cast<uint4*>(T16 + piece_at<8>(row, p)) = h4;
+            *reinterpret_cast<uint4*>(T16 + kSquare + piece_at<8>(row, p)) = r4;
             *reinterpret_cast<uint4*>(out + piece_at<8>(row, p)) = h4;
-            *reinterpret_cast<uint4*>(out + 2 * kSquare + piece_at<8>(row, p)) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+            *reinterpret_cast<uint4*>(out + 2 * kSquare + piece_at<8>(row, p)) = r4;
         }
         if ((tid & 127) == 0) f.t = down(e), f.most_l = __uint_as_float(m.most[b]) * m.left[b];
         head_barrier(b);
         let_next_start();  // not earlier: one prompt of 4096 164 us, at the kernel's start 166
-        // P T, rows 16 warp .. +15; it goes into o only, so one fp16 of each will do
+        // P T, rows 16 warp .. +15
         const uint32_t t_at = smem_at(T16);
         float acc[8][4];
 #pragma unroll
@@ -601,14 +611,23 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
         for (int t = 0; t < 4; ++t) {
             if (t > warp) continue;
             const uint32_t l[4] = {P[2 * t][0], P[2 * t][1], P[2 * t + 1][0], P[2 * t + 1][1]};
+            const uint32_t lr[4] = {Pr[2 * t][0], Pr[2 * t][1], Pr[2 * t + 1][0], Pr[2 * t + 1][1]};
 #pragma unroll
             for (int n = 0; n <= t; ++n) {
-                uint32_t w[4];
+                uint32_t w[4], wr[4];
                 ldmatrix_trans(w, left_at<8>(t_at, 16 * t, 2 * n, lane));
-                mma_f16(acc[2 * n], l, w[0], w[1]);
-                mma_f16(acc[2 * n + 1], l, w[2], w[3]);
+                ldmatrix_trans(wr, left_at<8>(t_at + kSquare, 16 * t, 2 * n, lane));
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    mma_f16(acc[2 * n + m], lr, w[2 * m], w[2 * m + 1]);
+                    mma_f16(acc[2 * n + m], l, wr[2 * m], wr[2 * m + 1]);
+                    mma_f16(acc[2 * n + m], l, w[2 * m], w[2 * m + 1]);
+                }
             }
         }
+        // to rows of memory over T, whose last readers were before the barriers, and from there 16 bytes a thread
+        uint8_t* rows16 = reinterpret_cast<uint8_t*>(m.T[b]) + warp * 2 * 16 * 128;
+        uint32_t high[8][2], rest[8][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float largest = 0;
@@ -619,10 +638,20 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
             const int r = 16 * warp + (lane >> 2) + 8 * i, er = field(largest);
             const float by = up(er);
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
-                *reinterpret_cast<uint32_t*>(out + kSquare + piece_at<8>(r, n) + 4 * (lane & 3)) =
-                    pack(acc[n][2 * i] * by, acc[n][2 * i + 1] * by);
+            for (int n = 0; n < 8; ++n) high[n][i] = halved(acc[n][2 * i] * by, acc[n][2 * i + 1] * by, rest[n][i]);
             if ((lane & 3) == 0) f.pt[r] = down(er) * p_down[i] * (down(e) * a.c.scale);
+        }
+#pragma unroll
+        for (int n = 0; n < 8; n += 2) {
+            const uint32_t at = left_at<8>(smem_at(rows16), 0, n, lane);
+            stmatrix(at, high[n][0], high[n][1], high[n + 1][0], high[n + 1][1]);
+            stmatrix(at + 16 * 128, rest[n][0], rest[n][1], rest[n + 1][0], rest[n + 1][1]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = lane * 16; i < 16 * 128; i += 32 * 16) {
+            *reinterpret_cast<uint4*>(out + kSquare + warp * 16 * 128 + i) = *reinterpret_cast<const uint4*>(rows16 + i);
+            *reinterpret_cast<uint4*>(out + 3 * kSquare + warp * 16 * 128 + i) = *reinterpret_cast<const uint4*>(rows16 + 16 * 128 + i);
         }
     }
 }
@@ -641,10 +670,7 @@ __device__ __forceinline__ void split(Fragment& r, const float (&c0)[4], const f
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float(&c)[4] = i < 2 ? c0 : c1;
-        const float x = c[2 * (i & 1)] * f, y = c[2 * (i & 1) + 1] * f;
-        r.high[i] = pack(x, y);
-        const float2 h = unpack(r.high[i]);
-        r.rest[i] = pack(x - h.x, y - h.y);
+        r.high[i] = halved(c[2 * (i & 1)] * f, c[2 * (i & 1) + 1] * f, r.rest[i]);
     }
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
@@ -674,17 +700,20 @@ struct ChunkShape {
     static constexpr int kVPitch = kCols * 2 + 16;  // bytes of a row; the 16 keep 8 rows on different banks
     static constexpr int kHalf = PAIRS * 2 * 32;   // threads with S, and as many for o
     static constexpr int kTiles = KD / 32;         // 16 x 16 blocks of a warp's half of S^T
-    // a stage: K and Q, T high, P T and T rest, V; two of them, and of the factors three
+    // a stage: K and Q, T and P T, V; two of them, and of the factors
     static constexpr int kV = pair_bytes(KD) + kHeadTiles;
     static constexpr int kStage = kV + kC * kVPitch;
     static constexpr int kFactors = kHeadBytes - kHeadTiles;
-    // handed to the warps for o, by each warp with S, twice: the high numbers of its half of S and of its tokens' X
-    static constexpr int kHand = (kTiles + 2) * kVector;
-    // exchanged in a pair, by each warp: sums for the other's tokens, then what goes into S (high, rest); rests of X
-    static constexpr int kSwap = 4 * kVector, kRests = 2 * kVector;
-    static constexpr int kOffFactors = 2 * kStage, kOffHands = kOffFactors + 3 * kFactors;
-    static constexpr int kOffSwap = kOffHands + 2 * 2 * PAIRS * kHand, kOffRests = kOffSwap + 2 * PAIRS * kSwap;
-    static constexpr int kBytes = kOffRests + 2 * PAIRS * kRests;
+    // handed on by each warp with S: its half of S, high numbers and rests, and its tokens' X
+    static constexpr int kX = 2 * kTiles * kVector, kHand = kX + 4 * kVector;
+    // exchanged in a pair, by each warp: sums for the other's tokens, then what goes into S (high, rest)
+    static constexpr int kSwap = 4 * kVector;
+    static constexpr int kOffFactors = 2 * kStage, kOffHands = kOffFactors + 2 * kFactors;
+    static constexpr int kOffSwap = kOffHands + 2 * PAIRS * kHand;
+    static constexpr int kBytes = kOffSwap + 2 * PAIRS * kSwap;
+    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+    // barriers beside the CTA's: of a pair, and for S and X that are handed on
+    static constexpr int kPairBarrier = 1, kHandedS = 1 + PAIRS, kHandedX = 1 + 2 * PAIRS;
     // registers of a thread with S and of one for o, where the same number for both would be too few for S
     static constexpr int kMost = 168, kLeast = 88;
     static_assert(PAIRS == 2 || 2 * kHalf * 128 == kHalf * (kMost + kLeast), "registers of the launch");
@@ -700,9 +729,8 @@ __device__ __forceinline__ int group_of(int q, int g) { return q ? 1 + g : 3 * g
 // product as it stands: only K, T and K^T come from shared memory, each by
 // fragments of half the size that the other way round would need.  Between the
 // three products of a chunk the pair exchanges what both need: sums over their
-// halves of k_dim, X of their tokens, and what goes into S.  Four more warps form
-// o one chunk later, from the high numbers of S and X that they are handed, and
-// copy the tiles of the next chunk.
+// halves of k_dim, X of their tokens, and what goes into S.  As many more warps form
+// o, from the S and X that they are handed, and copy the tiles of the next chunk.
 //
 // The way from chunk to chunk bounds this where there are few sequences and
 // heads: 4096 tokens with 32 heads are 64 chunks one after another on 128 CTAs,
@@ -717,7 +745,7 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
     using Shape = ChunkShape<KD, PAIRS>;
     constexpr int kPairs = PAIRS, kCols = Shape::kCols, kHalf = Shape::kHalf, kVPitch = Shape::kVPitch;
     extern __shared__ __align__(128) uint8_t raw[];
-    __shared__ float2 units[2][2 * kPairs];                  // of S and of X
+    __shared__ float2 units[2 * kPairs];                     // of S and of X
     __shared__ float2 found[2 * kPairs];                     // by a warp for the other of its pair: largest of S and of V
     after_previous();
     constexpr int kT = Shape::kTiles, kN = 2 * kT;
@@ -736,7 +764,6 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
     const int chunks = (int)((len + kC - 1) / kC);
     const int64_t piece = taken.piece & 0x7fffffffu;
     const uint32_t base = smem_at(raw);
-    constexpr int kHands = 2 * kPairs * Shape::kHand;  // from one time's to the next
     const uint32_t hands = base + Shape::kOffHands + lane * 16;
     const int r0 = lane >> 2, c0 = 2 * (lane & 3);
 
@@ -746,121 +773,45 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
         };
         const int t = tid - kHalf;
-        // K, T, V and the factors of a chunk: what the warps with S read
-        auto fetch_s = [&](int c) {
-            if (c < chunks) {
-                const uint32_t to = base + (c & 1) * Shape::kStage;
-                const uint8_t* pair = a.ws + ((piece + c) * Hk + kh) * pair_bytes(KD);
-                const uint8_t* head = a.ws + a.q_pieces * Hk * pair_bytes(KD) + ((piece + c) * Hv + h) * kHeadBytes;
+        constexpr int kFetches = 8, kFirst = 2;
+        // Copies of chunk c: K and Q, T and P T by eighths, the factors and V with the first.  All at once hold the warp up for
+        // 1000 cycles, so they stand between the products: 4096 tokens 178 us, with half of them before the products 181.
+        auto fetch = [&](int c, int part) {
+            if (c >= chunks) return;
+            const uint32_t to = base + (c & 1) * Shape::kStage;
+            const uint8_t* pair = a.ws + ((piece + c) * Hk + kh) * pair_bytes(KD);
+            const uint8_t* head = a.ws + a.q_pieces * Hk * pair_bytes(KD) + ((piece + c) * Hv + h) * kHeadBytes;
 #pragma unroll
-                for (int n = 0; n < KD / 64; ++n)
-#pragma unroll
-                    for (int i = t * 16; i < kSquare; i += kHalf * 16) copy16(to + n * kPanel + i, pair + n * kPanel + i, true);
-#pragma unroll
-                for (int i = t * 16; i < kSquare; i += kHalf * 16) {
-                    copy16(to + pair_bytes(KD) + i, head + i, true);
-                    copy16(to + pair_bytes(KD) + 2 * kSquare + i, head + 2 * kSquare + i, true);
-                }
-                for (int i = t * 16; i < Shape::kFactors; i += kHalf * 16)
-                    copy16(base + Shape::kOffFactors + c % 3 * Shape::kFactors + i, head + kHeadTiles + i, true);
-                const int64_t row0 = lo + (int64_t)c * kC;
-#pragma unroll
-                for (int i = t; i < kC * (kCols / 8); i += kHalf) {
-                    const int r = i / (kCols / 8), d = first + i % (kCols / 8) * 8;
-                    const bool there = row0 + r < hi && d < dv;
-                    const __nv_bfloat16* from = there ? a.vr + (row0 + r) * a.v_ld + h * dv + d : a.vr;
-                    const uint32_t at = (uint32_t)(Shape::kV + r * kVPitch + (d - first) * 2);
-                    if (a.wide) {
-                        copy16(to + at, from, there);
-                    } else {
-                        *reinterpret_cast<uint4*>(raw + (c & 1) * Shape::kStage + at) =
-                            there ? eight(from, false) : make_uint4(0, 0, 0, 0);
-                    }
-                }
+            for (int i = 0; i < pair_bytes(KD) / 8; i += kHalf * 16) {
+                const int at = part * (pair_bytes(KD) / 8) + i + t * 16;
+                if (kHalf * 16 <= pair_bytes(KD) / 8 || t * 16 < pair_bytes(KD) / 8) copy16(to + at, pair + at, true);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        auto fetch_o = [&](int c) {  // Q and P T
-            if (c < chunks) {
-                const uint32_t to = base + (c & 1) * Shape::kStage + kSquare;
-                const uint8_t* pair = a.ws + ((piece + c) * Hk + kh) * pair_bytes(KD) + kSquare;
-                const uint8_t* head = a.ws + a.q_pieces * Hk * pair_bytes(KD) + ((piece + c) * Hv + h) * kHeadBytes + kSquare;
 #pragma unroll
-                for (int i = t * 16; i < kSquare; i += kHalf * 16) {
-#pragma unroll
-                    for (int n = 0; n < KD / 64; ++n) copy16(to + n * kPanel + i, pair + n * kPanel + i, true);
-                    copy16(to + pair_bytes(KD) + i, head + i, true);
-                }
+            for (int i = 0; i < kHeadTiles / 8; i += kHalf * 16) {
+                const int at = part * (kHeadTiles / 8) + i + t * 16;
+                copy16(to + pair_bytes(KD) + at, head + at, true);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        fetch_s(0);
-        fetch_o(0);
-        for (int c = 0; c <= chunks; ++c) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but Q and P T of chunk c
-            __syncthreads();  // K, T and V of chunk c are there, and what goes into o of c - 1; nobody reads K, T, V of c - 1
-            fetch_s(c + 1);
-            if (c == 0) {
-                fetch_o(1);
-                continue;
-            }
-            const int o_c = c - 1;
-            const uint32_t stage = base + (o_c & 1) * Shape::kStage, hand = hands + (o_c & 1) * kHands + 2 * p * Shape::kHand;
-            const Factors& f = *reinterpret_cast<const Factors*>(raw + Shape::kOffFactors + o_c % 3 * Shape::kFactors);
-            float o[4][4];  // of this warp's two groups of 16 tokens
+            if (part) return;
+            for (int i = t * 16; i < Shape::kFactors; i += kHalf * 16)
+                copy16(base + Shape::kOffFactors + (c & 1) * Shape::kFactors + i, head + kHeadTiles + i, true);
+            const int64_t row0 = lo + (int64_t)c * kC;
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[n][i] = 0;
-            // Q S^T, in the units of each half of k_dim, then P T X
-#pragma unroll
-            for (int part = 0; part < 3; ++part) {
-                float acc[4][4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[n][i] = 0;
-                if (part < 2) {
-#pragma unroll
-                    for (int t = 0; t < kT; ++t) {
-                        uint32_t x[4];
-                        get4(x, hand + part * Shape::kHand + t * kVector);
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            uint32_t w[4];
-                            ldmatrix(w, columns_at(stage, kC + 16 * group_of(q, g), 2 * (part * kT + t), lane));
-                            mma_f16(acc[2 * g], x, w[0], w[1]);
-                            mma_f16(acc[2 * g + 1], x, w[2], w[3]);
-                        }
-                    }
+            for (int i = t; i < kC * (kCols / 8); i += kHalf) {
+                const int r = i / (kCols / 8), d = first + i % (kCols / 8) * 8;
+                const bool there = row0 + r < hi && d < dv;
+                const __nv_bfloat16* from = there ? a.vr + (row0 + r) * a.v_ld + h * dv + d : a.vr;
+                const uint32_t at = (uint32_t)(Shape::kV + r * kVPitch + (d - first) * 2);
+                if (a.wide) {
+                    copy16(to + at, from, there);
                 } else {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        uint32_t x[4];
-                        const int owner = t == 1 || t == 2;
-                        get4(x, hand + owner * Shape::kHand + (kT + t / 2) * kVector);
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            if (group_of(q, g) < t) continue;
-                            uint32_t w[4];
-                            ldmatrix(w, right_at<8>(stage + pair_bytes(KD) + kSquare, 16 * group_of(q, g), 2 * t, lane));
-                            mma_f16(acc[2 * g], x, w[0], w[1]);
-                            mma_f16(acc[2 * g + 1], x, w[2], w[3]);
-                        }
-                    }
-                }
-                const float2 unit = units[o_c & 1][2 * p + (part < 2 ? part : 0)];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 by = *reinterpret_cast<const float2*>((part < 2 ? f.qs : f.pt) + 16 * group_of(q, n >> 1) + 8 * (n & 1) + c0);
-                    const float b0 = by.x * (part < 2 ? unit.x : unit.y), b1 = by.y * (part < 2 ? unit.x : unit.y);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[n][i] = fmaf(i & 1 ? b1 : b0, acc[n][i], o[n][i]);
+                    *reinterpret_cast<uint4*>(raw + (c & 1) * Shape::kStage + at) =
+                        there ? eight(from, false) : make_uint4(0, 0, 0, 0);
                 }
             }
-            asm volatile("bar.sync %0, %1;" ::"r"(kPairs + 1), "r"(kHalf) : "memory");  // nobody reads Q and P T of c - 1 any more
-            fetch_o(c + 1);
-            const int64_t row0 = lo + (int64_t)o_c * kC;
+        };
+        float o[4][4];  // of this warp's two groups of 16 tokens
+        auto put = [&](int c) {  // to memory
+            const int64_t row0 = lo + (int64_t)c * kC;
             const int rows = (int)(hi - row0 < kC ? hi - row0 : kC), d = first + 16 * p + c0;
             __nv_bfloat16* to = a.o + row0 * a.o_ld + h * dv + d;
 #pragma unroll
@@ -881,15 +832,90 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
                     }
                 }
             }
+        };
+        for (int i = 0; i < kFetches; ++i) fetch(0, i);
+        for (int c = 0; c < chunks; ++c) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();  // chunk c is there; nobody reads chunk c - 1 or what was handed on in it
+#pragma unroll
+            for (int i = 0; i < kFirst; ++i) fetch(c + 1, i);
+            const uint32_t stage = base + (c & 1) * Shape::kStage, hand = hands + 2 * p * Shape::kHand;
+            const Factors& f = *reinterpret_cast<const Factors*>(raw + Shape::kOffFactors + (c & 1) * Shape::kFactors);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][i] = 0;
+            // Q S^T, in the units of each half of k_dim, then P T X
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+                if (part == 0) asm volatile("bar.sync %0, 128;" ::"r"(Shape::kHandedS + p) : "memory");
+                if (part == 2) asm volatile("bar.sync %0, 128;" ::"r"(Shape::kHandedX + p) : "memory");
+                float acc[4][4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][i] = 0;
+                if (part < 2) {
+#pragma unroll
+                    for (int t = 0; t < kT; ++t) {
+                        if (kFirst + part * kT + t < kFetches) fetch(c + 1, kFirst + part * kT + t);
+                        uint32_t x[4], rest[4];
+                        get4(x, hand + part * Shape::kHand + t * kVector);
+                        get4(rest, hand + part * Shape::kHand + (kT + t) * kVector);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t w[4];
+                            ldmatrix(w, columns_at(stage, kC + 16 * group_of(q, g), 2 * (part * kT + t), lane));
+                            mma_f16(acc[2 * g], x, w[0], w[1]);
+                            mma_f16(acc[2 * g + 1], x, w[2], w[3]);
+                            mma_f16(acc[2 * g], rest, w[0], w[1]);
+                            mma_f16(acc[2 * g + 1], rest, w[2], w[3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        if (kFirst + 2 * kT + t < kFetches) fetch(c + 1, kFirst + 2 * kT + t);
+                        uint32_t x[4], rest[4];
+                        const int owner = t == 1 || t == 2;
+                        get4(x, hand + owner * Shape::kHand + Shape::kX + t / 2 * kVector);
+                        get4(rest, hand + owner * Shape::kHand + Shape::kX + (2 + t / 2) * kVector);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            if (group_of(q, g) < t) continue;
+                            const uint32_t at = right_at<8>(stage + pair_bytes(KD) + kSquare, 16 * group_of(q, g), 2 * t, lane);
+                            uint32_t w[4];
+                            ldmatrix(w, at + 2 * kSquare);
+                            mma_f16(acc[2 * g], x, w[0], w[1]);
+                            mma_f16(acc[2 * g + 1], x, w[2], w[3]);
+                            ldmatrix(w, at);
+                            mma_f16(acc[2 * g], rest, w[0], w[1]);
+                            mma_f16(acc[2 * g + 1], rest, w[2], w[3]);
+                            mma_f16(acc[2 * g], x, w[0], w[1]);
+                            mma_f16(acc[2 * g + 1], x, w[2], w[3]);
+                        }
+                    }
+                }
+                const float2 unit = units[2 * p + (part < 2 ? part : 0)];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 by = *reinterpret_cast<const float2*>((part < 2 ? f.qs : f.pt) + 16 * group_of(q, n >> 1) + 8 * (n & 1) + c0);
+                    const float b0 = by.x * (part < 2 ? unit.x : unit.y), b1 = by.y * (part < 2 ? unit.x : unit.y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[n][i] = fmaf(i & 1 ? b1 : b0, acc[n][i], o[n][i]);
+                }
+            }
+            put(c);
         }
         return;
     }
 
     if (PAIRS > 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Shape::kMost));
-    const uint32_t swap = base + Shape::kOffSwap + lane * 16, rests = base + Shape::kOffRests + lane * 16;
+    const uint32_t swap = base + Shape::kOffSwap + lane * 16;
     const uint32_t my_swap = swap + warp * Shape::kSwap, its_swap = swap + (warp ^ 1) * Shape::kSwap;
-    const uint32_t my_rests = rests + warp * Shape::kRests, its_rests = rests + (warp ^ 1) * Shape::kRests;
-    auto pair_barrier = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + p) : "memory"); };
+    const uint32_t hand = hands + warp * Shape::kHand, its_hand = hands + (warp ^ 1) * Shape::kHand;
+    auto pair_barrier = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(Shape::kPairBarrier + p) : "memory"); };
+    auto handed = [&](int barrier) { asm volatile("bar.arrive %0, 128;" ::"r"(barrier + p) : "memory"); };
     // S: rows d0, d0 + 8 of v_dim, columns k0 + 8 n (+ 1) of k_dim, in units of down(unit)
     const int d0 = first + 16 * p + r0, k0 = q * (KD / 2) + c0;
     float S[kN][4];
@@ -917,8 +943,7 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
     for (int c = 0; c < chunks; ++c) {
         __syncthreads();
         const uint32_t stage = base + (c & 1) * Shape::kStage, T_high = stage + pair_bytes(KD), T_rest = T_high + 2 * kSquare;
-        const Factors& f = *reinterpret_cast<const Factors*>(raw + Shape::kOffFactors + c % 3 * Shape::kFactors);
-        const uint32_t hand = hands + (c & 1) * kHands + warp * Shape::kHand, its_hand = hands + (c & 1) * kHands + (warp ^ 1) * Shape::kHand;
+        const Factors& f = *reinterpret_cast<const Factors*>(raw + Shape::kOffFactors + (c & 1) * Shape::kFactors);
 
         // V of this warp's tokens, turned: two groups of 16 tokens by 16 columns
         uint32_t v[2][4], bits = 0;
@@ -953,9 +978,11 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
         for (int t = 0; t < kT; ++t) {
             split(b[t], S[2 * t], S[2 * t + 1], s_up);
             put4(hand + t * kVector, b[t].high);
+            put4(hand + (kT + t) * kVector, b[t].rest);
             times_k(t, 2);
         }
-        if (lane == 0) found[warp] = make_float2(most, __uint_as_float(bits)), units[c & 1][warp].x = s_down;
+        if (lane == 0) found[warp] = make_float2(most, __uint_as_float(bits)), units[warp].x = s_down;
+        handed(Shape::kHandedS);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float send[4] = {x[4 + n][0] * s_down, x[4 + n][1] * s_down, x[4 + n][2] * s_down, x[4 + n][3] * s_down};
@@ -975,7 +1002,7 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
         const float units_by = __uint_as_float((uint32_t)(127 + min(max(unit - next, -126), 127)) << 23);
         const float grow = f.all * units_by, grow_rest = f.rest * units_by;
         const float to_l = f.t * x_down * up(next);
-        if (lane == 0) units[c & 1][warp].y = x_down;
+        if (lane == 0) units[warp].y = x_down;
         unit = next;
 
         // X = V - e^G K S^T of this warp's tokens
@@ -995,9 +1022,10 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
                 }
             }
             split(X[g], x[2 * g], x[2 * g + 1], x_up);
-            put4(hand + (kT + g) * kVector, X[g].high);
-            put4(my_rests + g * kVector, X[g].rest);
+            put4(hand + Shape::kX + g * kVector, X[g].high);
+            put4(hand + Shape::kX + (2 + g) * kVector, X[g].rest);
         }
+        handed(Shape::kHandedX);
         // U = T X of this warp's tokens, first what its own X bring: two sums a block, the second of what the rests bring
         float u[4][4], u2[4][4];
 #pragma unroll
@@ -1023,8 +1051,8 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
             Fragment theirs[2];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                get4(theirs[g].high, its_hand + (kT + g) * kVector);
-                get4(theirs[g].rest, its_rests + g * kVector);
+                get4(theirs[g].high, its_hand + Shape::kX + g * kVector);
+                get4(theirs[g].rest, its_hand + Shape::kX + (2 + g) * kVector);
             }
             times_t(1, theirs[0], group[2]);  // group 1 for 3, or 0 for 2
             if (q)
@@ -1085,7 +1113,6 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[n][i] = fmaf(S[n][i], grow, grown[n][i]);
     }
-    __syncthreads();  // for the last chunk's o
     let_next_start();  // not earlier: 8 prompts of 512 with 8 heads 45 us, at the kernel's start 49 (64 of 64 with 32: 256 and 252)
     if (state) {
 #pragma unroll

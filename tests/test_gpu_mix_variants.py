@@ -9,7 +9,7 @@ import int4_expert_streaming_gb300 as moe
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from test_gpu_mix import BF, F32, HALF, check_norm, cuda, f64, ints, rng_of, strided  # noqa: E402
+from test_gpu_mix import BF, F32, HALF, check_norm, cuda, delta_inputs, f64, ints, rng_of, run_delta, strided  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -75,27 +75,46 @@ def test_norm_of_many_heads_in_place_and_by_columns(dt, D):
 # ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("T", [20, 64, 190])
-def test_delta_keys_that_come_again(T):
+@pytest.mark.parametrize("Hv,dv", [(2, 128), (48, 64)])
+def test_delta_keys_that_come_again(T, Hv, dv):
     """Every second token asks with the key that it has just written over, by zeros with beta 1: o is far smaller than what
-    cancels in it.  In chunks S, the updates and the products of q and k enter o as numbers of 11 bits, 2^-12 of their
-    largest each: 2^-9 of scale size |q| is five times the spread of sums of 64 and 128 of them.  Token by token they are
-    fp32: sums of 128, 2^-18."""
-    rng = rng_of(T)
+    cancels in it.  In chunks three sums follow each other beside a fourth, each of up to 16 steps of the tensor core that
+    may lose 2^-23 of sums below four times the size: 2^-17 each, 2^-15 of scale size |q| together.  Token by token: sums of
+    128 in fp32, 2^-18."""
+    rng = rng_of(T, Hv)
     k = rng.standard_normal((T, 1, 128))
     k[1::2] = k[0::2]
     k = cuda(k / np.linalg.norm(k, axis=2, keepdims=True), BF)
-    v = rng.standard_normal((T, 2, 128))
+    v = rng.standard_normal((T, Hv, dv))
     v[1::2] = 0
-    v, g, beta = cuda(v, BF), torch.zeros((T, 2), device="cuda"), torch.ones((T, 2), device="cuda")
-    st, o = cuda(rng.standard_normal((1, 2, 128, 128))), torch.empty((T, 2, 128), dtype=BF, device="cuda")
-    ws = torch.empty(max(1, moe.moe_delta_workspace(T, 1, 1, 2, 128, 128)), dtype=torch.uint8, device="cuda")
-    want, state = np.zeros((T, 2, 128)), f64(st)
+    v, g, beta = cuda(v, BF), torch.zeros((T, Hv), device="cuda"), torch.ones((T, Hv), device="cuda")
+    st, o = cuda(rng.standard_normal((1, Hv, dv, 128))), torch.empty((T, Hv, dv), dtype=BF, device="cuda")
+    ws = torch.empty(max(1, moe.moe_delta_workspace(T, 1, 1, Hv, 128, dv)), dtype=torch.uint8, device="cuda")
+    want, state = np.zeros((T, Hv, dv)), f64(st)
     top = ora.delta(f64(k), f64(k), f64(v), f64(g), f64(beta), state, want, 1.0, ora.sequences(T, [0, T]))
     moe.moe_delta(k, k, v, g, beta, st, o, 1.0, workspace=ws, stream=torch.cuda.current_stream())
     torch.cuda.synchronize()
-    near = 2.0 ** -8 * 1.01 * np.abs(want) + (2.0 ** -18 if T <= 24 else 2.0 ** -9) * top[:, :, None] * 1.01
-    assert (np.abs(f64(o) - want) <= near).all()
+    near = 2.0 ** -8 * 1.01 * np.abs(want) + (2.0 ** -18 if T <= 24 else 2.0 ** -15) * top[:, :, None] * 1.01
+    assert (np.abs(f64(o) - want) <= near).all(), (np.abs(f64(o) - want) / near).max()
     assert (np.abs(f64(st) - state) <= 2.0 ** -16 * top[-1][None, :, None, None]).all()
+
+
+@pytest.mark.parametrize("lens", [[24, 7], [64, 300], [90] * 40])
+def test_delta_o_is_rounded_once(lens):
+    """All but few values are the exact ones rounded.  The sums before are off by about 2^-20 of scale size |q|, a value of o
+    is about half of that and bf16's steps are 2^-8 of it or more: one value in 2^10 is next to a border that near.  Numbers
+    of 11 bits in the sums, 2^-13 in the mean, would make it one in ten."""
+    rng = rng_of(len(lens), lens[0])
+    T, n = sum(lens), len(lens)
+    q, k, v, g, beta = delta_inputs(rng, T, 2, 4, 128, 64)
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    st, o = cuda(rng.standard_normal((n, 4, 64, 128))), torch.empty((T, 4, 64), dtype=BF, device="cuda")
+    want, ws = np.zeros((T, 4, 64)), f64(st)
+    ora.delta(f64(q), f64(k), f64(v), f64(g), f64(beta), ws, want, 0.1, ora.sequences(T, off))
+    run_delta(q, k, v, g, beta, st, o, 0.1, moe.make_seqs(n, ints(off)), T, n)
+    torch.cuda.synchronize()
+    other = int((o != cuda(want, BF)).sum())
+    assert other <= o.numel() // 100, other / o.numel()
 
 
 # ---------------------------------------------------------------------------
