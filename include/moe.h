@@ -610,9 +610,9 @@ typedef struct {
  * and fp32 throughout.  Longer ones run in chunks of 64 tokens on the tensor
  * cores: within a chunk the updates come from one triangular system.  What the
  * products are of (the state, the updates, the chunk's inverse, products of q
- * and k) enters them as pairs of fp16 numbers in units of powers of two, 2^-22
- * of a value, and 2^-38 of the largest within 16 columns of v_dim and 64
- * tokens; sums are fp32, and the state is fp32 from chunk to chunk.  o is
+ * and k) enters them as pairs of fp16 numbers in units of powers of two, good to
+ * 2^-22 of a value, or to about 2^-32 of the largest within 16 columns of v_dim
+ * and 64 tokens where that is more; sums are fp32, and the state is fp32 from chunk to chunk.  o is
  * rounded once.  A state that is cleared in the midst of a chunk should not be
  * more than 2^20 times what is written in the rest of it.  Which of the two a
  * sequence takes depends on its own length alone (max_len being right), so its

@@ -6,9 +6,11 @@
 
 namespace moe {
 
-// Rows up to which a sequence of the delta rule runs token by token.  32 heads of 128 x 128, token by token and in a
-// chunk: one run of 24 rows 15.3 and 16.6 us, of 32 rows 19.3 and 16.7; 16 runs of 24 rows 58 and 63 us, of 32 rows 75 and 64;
-// 64 runs of 24 rows 223 and 234 us, of 32 rows 291 and 237.
+// Rows up to which a sequence of the delta rule runs token by token.  In us, token by token and in a chunk, of 24 and of 32
+// rows: 32 heads of 128 x 128, one run 16.3 and 17.4, 20.7 and 17.3; 16 runs 66 and 65, 84 and 66; 64 runs 247 and 242, 319 and 243.
+// 8 heads of 128 x 128, one run 16.2 and 17.0, 20.6 and 17.0; 64 runs 67 and 66, 84 and 66.  16 heads of 64 x 96, one run 11.7 and
+// 14.7, 14.6 and 14.7; 64 runs 83 and 91, 104 and 92.  Of 64 x 64, 16 runs 17.2 and 24.3, 21.1 and 24.4, and equal at 40 rows.  So
+// smaller heads could go to 32 rows; the bound is the same for all, as a sequence's results may depend on its length alone.
 constexpr int kDeltaShort = 24;
 constexpr int kDeltaChunk = 64;
 

@@ -21,7 +21,7 @@
 // left out.  What goes into o alone has both numbers too: with the high ones
 // only, o was off by 2^-12 of |S| |q|, more than its rounding to bf16 where sums
 // cancel in it (a key that is written over).  That costs 4096 tokens with 32 heads of
-// 128 178 us instead of 165, 64 prompts of 64 257 instead of 252.
+// 128 178 us instead of 165, 64 prompts of 64 256 instead of 252.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -54,7 +54,7 @@ constexpr int kHeadBytes = (kHeadTiles + (int)sizeof(Factors) + 127) / 128 * 128
 
 constexpr int kSorted = 512;
 // A sequence as chunks_kernel takes it, in one load: lists, slot and offsets one after another cost a CTA 1 us (64 prompts of
-// 64 tokens, 32 heads: 268 us instead of 252)
+// 64 tokens, 32 heads, 256 us: 16 us more)
 struct alignas(16) Taken {
     int lo, hi, slot;  // rows; slot -1: not taken
     uint32_t piece;    // its first chunk's place; bit 31: it goes on from its slot
@@ -219,7 +219,7 @@ __device__ __forceinline__ Taken* taken_of(const DeltaArgs& a, int pair, int hea
 }
 // The sequences first .. first + kPrepare - 1 to their places.  Longest first,
 // so that their CTAs start first and the last to start are short (9001 rows in 24
-// sequences: 120 us, in their own order 129).  Above kSorted sequences, where the
+// sequences: 132 us, in their own order 141).  Above kSorted sequences, where the
 // comparisons would take longer than a chunk, they stand in their own order: no one
 // of so many is long beside the whole.
 __device__ __forceinline__ void list_sequences(const DeltaArgs& a, int first, int* lens) {
@@ -246,8 +246,8 @@ __device__ __forceinline__ void list_sequences(const DeltaArgs& a, int first, in
 // a lane a column; then T_10 and T_32, and of those the lower left quarter, by
 //   (T_11 0; T_21 T_22) with T_21 = -T_22 A_21 T_11.
 // Two heads a CTA, since they share K and Q; three CTAs an SM.  4096 tokens, 16
-// and 32 heads of 128: 48 us of the call's 164, with 51% of the issue slots and
-// 66% of shared memory's rate in use and a tenth of the time in barriers.
+// and 32 heads of 128: 52 us of the call's 178, with 48% of the issue slots and
+// 68% of shared memory's rate in use and a tenth of the time in barriers.
 template <int KD>
 __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_constant__ DeltaArgs a) {
     extern __shared__ __align__(128) uint8_t raw[];
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kPrepare, 3) prepare_kernel(const __grid_const
         }
         if ((tid & 127) == 0) f.t = down(e), f.most_l = __uint_as_float(m.most[b]) * m.left[b];
         head_barrier(b);
-        let_next_start();  // not earlier: one prompt of 4096 164 us, at the kernel's start 166
+        let_next_start();  // at the kernel's start: the same (one prompt of 4096 178 us, 24 ragged 132)
         // P T, rows 16 warp .. +15
         const uint32_t t_at = smem_at(T16);
         float acc[8][4];
@@ -734,12 +734,14 @@ __device__ __forceinline__ int group_of(int q, int g) { return q ? 1 + g : 3 * g
 //
 // The way from chunk to chunk bounds this where there are few sequences and
 // heads: 4096 tokens with 32 heads are 64 chunks one after another on 128 CTAs,
-// 115 us, 3400 cycles a chunk, of which the warps with S spend 1260 in the tensor
-// cores: K S^T 1100, X 400, U 600, its conversion 230, S 670, the rest in
-// exchanges.  Half of k_dim (half of the first and last product) saves 550.  The
-// same chunk by tcgen05 with S in tensor memory, the four products by one thread,
-// was built and took 144 us: three trips to the tensor core and back of 500 to
-// 600 cycles each, and a fence and a barrier of 230 to 450 before each.
+// 125 us, 3700 cycles a chunk: S's largest value and K S^T 1400, X 550, U 700, its
+// conversion 450, S 650.  The warps for o are at work for nearly as long: Q S^T 1500
+// beside the copies, P T X 1200.  The tensor pipe is busy for 54% of the time,
+// shared memory for 72%.  Half of k_dim (half of the first and last product) saves
+// 850.  The same chunk by tcgen05 with S in tensor memory, the four products by one
+// thread, was built when this way took 116 us, and took 144: three trips to the
+// tensor core and back of 500 to 600 cycles each, and a fence and a barrier of 230
+// to 450 before each.
 template <int KD, int PAIRS>
 __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_kernel(const __grid_constant__ DeltaArgs a) {
     using Shape = ChunkShape<KD, PAIRS>;
@@ -1113,7 +1115,7 @@ __global__ void __launch_bounds__(2 * ChunkShape<KD, PAIRS>::kHalf, 1) chunks_ke
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[n][i] = fmaf(S[n][i], grow, grown[n][i]);
     }
-    let_next_start();  // not earlier: 8 prompts of 512 with 8 heads 45 us, at the kernel's start 49 (64 of 64 with 32: 256 and 252)
+    let_next_start();  // not earlier: 64 prompts of 64 255.5 us, at the kernel's start 256.5; 24 ragged 131.8 and 132.4
     if (state) {
 #pragma unroll
         for (int n = 0; n < kN; ++n)
@@ -1147,11 +1149,13 @@ cudaError_t launch_chunked(const DeltaArgs& a, cudaStream_t st) {
     if (cudaError_t e = launch(prepare_kernel<KD>, dim3((unsigned)(a.q_pieces + (a.q.n + kPrepare - 1) / kPrepare), (unsigned)(a.c.k_heads * twos)), kPrepare, kShared,
                                st, 1, a))
         return e;
-    // Four pairs take 1.8 times as long for a chunk as two, so they pay where the CTAs of two would be more than the SMs
-    // (and are twos): 64 prompts of 64 tokens, 32 heads of 128: 252 us, two pairs 291; 16 of 256: 166 and 182; 2 of 2048:
-    // 154 and 167; one of 4096, 128 CTAs of two pairs: 252 and 166.
+    // Four pairs take 1.6 to 1.8 times as long for a chunk as two, so they pay where the CTAs of two would be more than the
+    // SMs (and are twos).  Four pairs and two, in us: 32 heads of 128, 64 prompts of 64 tokens 259 and 298, 16 of 256 182 and 195, 2 of
+    // 2048 173 and 179, one of 4096 (128 CTAs of two pairs) 286 and 178; 16 heads of 64, 8 of 512 52 and 55, 5 of 1024 (160 CTAs)
+    // 78 and 82, 4 of 1024 (128) 73 and 53.
+    constexpr int kSMs = 152;  // of a GB300
     const int64_t columns = (a.c.v_dim + 31) / 32, ctas = a.q.n * a.c.v_heads * columns;
-    return ctas > 152 && columns % 2 == 0 ? launch_chunks<KD, 4>(a, st) : launch_chunks<KD, 2>(a, st);
+    return ctas > kSMs && columns % 2 == 0 ? launch_chunks<KD, 4>(a, st) : launch_chunks<KD, 2>(a, st);
 }
 
 }  // namespace

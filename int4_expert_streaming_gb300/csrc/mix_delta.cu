@@ -12,11 +12,13 @@ constexpr unsigned kAll = 0xffffffffu;
 // Eight threads share a row of S and keep it in registers over the tokens of
 // the run, four rows each.  One token is bound by reading and writing S: its
 // loads are issued before anything else is waited for, together with the first
-// token's.  Runs are bound by issuing instructions: products go two at a time,
-// and four rows share what is unpacked of k and q.  64 sequences, 32 heads,
-// 128 x 128: one token each (256 MB of states) 42.7 us, 89% of the measured
-// copy's rate; with two rows a thread 43.7, with sixteen threads a row 50.7;
-// four tokens for each of 16 sequences 18.6, 21.7 and 24.5 us.
+// token's.  A run is a chain: its state's loads, then one token after another, of
+// about 350 instructions a warp (38% of the slots with 2.6 warps a scheduler);
+// products go two at a time, and four rows share what is unpacked of k and q.  64
+// sequences, 32 heads, 128 x 128: one token each (256 MB of states) 42.6 us, 89% of
+// the measured copy's rate; four tokens for each of 16 sequences 19.3 us, in three
+// rounds of CTAs.  Before decays near 1 had a way of their own 42.4 and 18.6, then
+// with two rows a thread 43.7 and 21.7, with sixteen threads a row 50.7 and 24.5.
 constexpr int kLanes = 8, kRows = 4;
 constexpr int kStepRows = 128 / kLanes * kRows;  // rows of S of a CTA
 
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(128) steps_kernel(const __grid_constant__ Delt
         }
     Token<KD> next;
     load(next);
-    // the next 16 tokens' rows to L1, eight threads a token: four tokens for each of 16 sequences 19.0 us, without this 19.9
+    // the next 16 tokens' rows to L1, eight threads a token: without this four tokens for each of 16 sequences take 0.8 us more
     const int ahead = 1 + threadIdx.x / 8, part = threadIdx.x % 8;
     if (ahead < hi - lo) {
         const void* line = nullptr;
@@ -117,8 +119,8 @@ __global__ void __launch_bounds__(128) steps_kernel(const __grid_constant__ Delt
     for (int tokens = (int)(hi - lo); tokens > 0; --tokens) {
         const Token<KD> in = next;
         if (tokens > 1) load(next);
-        // S <- e^g S.  Decays near 1 as S + (e^g - 1) S: one fp32 of e^-0.00001, off by the same at every token, would leave
-        // 2^-10 of S after 16384 of them
+        // S <- e^g S.  Decays near 1 as S + (e^g - 1) S: with one fp32 of e^-0.00001, off by the same at every token, S was 2^-10
+        // off after 16384 of them.  16 runs of 4 19.3 us instead of 18.6; with the sums in both branches 20.9
         const bool near = fabsf(in.g) < 0.25f;
         const float by = near ? expm1f(in.g) : expf(in.g);
         const f32x2 bys = both(by, by);
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(128) steps_kernel(const __grid_constant__ Delt
         if (lane < kRows && in_v) *o = __float2bfloat16_rn(mine);
         o += a.o_ld;
     }
-    let_next_start();  // not earlier: 16 runs of 4 18.6 us, at the kernel's start 19.2; one token 3.3 and 3.5
+    let_next_start();  // at the kernel's start 16 runs of 4 take 0.7 us more, one token 0.2
     if (state && in_v) {
 #pragma unroll
         for (int p = 0; p < kRows; ++p)

@@ -122,8 +122,10 @@ __device__ __forceinline__ void store(T* p, const float* v) {
 // come before its first write, so y may be x.  sin and cos are found once for
 // each token of a CTA, for all its heads, behind the loads.  bf16: 4096 tokens of
 // 32 gated heads of 128 17.8 us, 83% of the measured copy's rate; of 16 and 2 heads
-// of 256, 64 values of them rotated, 18.2 us, 61%: bound by issuing, 68% of the
-// slots.  Two or more pieces of work a CTA one after another cost 2 to 11% more.
+// of 256, 64 values of them rotated, 18.1 us, 61%, with 68% of the issue slots
+// used: neither is used up, and seven warps a scheduler do not cover every load's
+// latency and the barrier behind the angles.  P = 1: 4096 tokens of 16 heads of 80, 20
+// values of them rotated, 22 us (24 of them, by P = 8: 6.7).  Two or more pieces of work a CTA one after another cost 2 to 11% more.
 template <typename T, int LANES, int CH, int P, int U, int ROT, bool GATE>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && U > 1 ? (GATE ? 3 : 4) : 1)
     norm_kernel(const __grid_constant__ NormArgs g) {
